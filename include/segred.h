@@ -24,8 +24,9 @@
 extern "C" {
 #endif
 
-/* Element types of `values` (4-byte packed scalars). */
-enum segred_dtype { SEGRED_U32 = 0, SEGRED_I32 = 1, SEGRED_F32 = 2 };
+/* Element types of `values` (4-byte packed scalars; the 2-byte types are
+ * those of the matrix products and the combine calls only). */
+enum segred_dtype { SEGRED_U32 = 0, SEGRED_I32 = 1, SEGRED_F32 = 2, SEGRED_BF16 = 3, SEGRED_F16 = 4 };
 
 /* Reductions.  MEAN is float32 only. */
 enum segred_op { SEGRED_SUM = 0, SEGRED_MIN = 1, SEGRED_MAX = 2, SEGRED_MEAN = 3 };
@@ -399,6 +400,176 @@ int segred_galloping_search(const void *values, int32_t dtype, int64_t value_cou
                             const int64_t *segments, int64_t num_segments, int64_t max_query_count,
                             int32_t queries_per_tile, int64_t *out, uint32_t *validation,
                             int32_t preserve_validation, hipStream_t stream);
+
+/*
+ * Operators over ragged groups of rows: grouping rows by an index, products
+ * of each group with weights of its own and their gradients, the weighted
+ * join of the rows an entry was sent to, and a shared projection with a
+ * low-rank adapter per segment.  Types are SEGRED_F32, SEGRED_BF16 and
+ * SEGRED_F16; sums are held in float32 and every output is rounded to its
+ * type once.  None of these calls allocates memory or uses the library's own
+ * scratch: where one needs working memory the caller passes `workspace`
+ * (16-byte aligned, at least as many bytes as the matching _workspace call
+ * returns; NULL where that is 0), which is free again once the call's work
+ * has run.  So they may be captured in a HIP graph, and graphs or streams
+ * with workspaces of their own may run at once.  No atomics: results are the
+ * same bit for bit from run to run.
+ *
+ * segred_matmul -- the matrix product of each segment's rows with weights of
+ * its own: out[r] = values[v(r)] W[s] for the rows r of segment s.
+ *
+ *   values        [value_rows, k] row-major, of type `dtype`.
+ *   rows          int64 [num_rows] or NULL: v(r) = rows[r] (an entry outside
+ *                 [0, value_rows) stands for a row of zeros), or v(r) = r.
+ *   weights       W[s] is [k, m], out = x W[s]; with `transpose` nonzero it is
+ *                 [m, k], out = x W[s]^T.  (The gradient of the rows is the
+ *                 same call on the output's gradient with the other setting.)
+ *   offsets       int64 [num_segments + 1], nondecreasing; offsets[0] may be
+ *                 above 0.  They are not read on the host or checked; rows at
+ *                 or past num_rows are not touched.
+ *   num_rows      rows of `out`, and of `rows` where given.
+ *   out           [num_rows, m]; rows of no segment are left as they were.
+ *
+ * Rows and weights that hold whole 16-byte units on 16-byte boundaries are
+ * copied to LDS directly, others through registers (slower).
+ *
+ * Errors: SEGRED_ERR_INVALID_ARGUMENT for an unknown dtype, k or m < 1,
+ * negative counts, value_rows < num_rows without `rows`, a NULL pointer that
+ * is needed, misalignment (an element for values, weights and out; 8 bytes
+ * for offsets and rows), sizes past INT64_MAX bytes.  SEGRED_ERR_UNSUPPORTED
+ * for integer types, k or m above 2^24, or more than 2^36 tiles.
+ * SEGRED_ERR_HIP if a launch fails.  `out` must not overlap the inputs.  No
+ * segments or no rows enqueue nothing.
+ */
+int segred_matmul(const void *values, int32_t dtype, int64_t k, const int64_t *rows, int64_t value_rows,
+                  const void *weights, int32_t transpose, int64_t m, const int64_t *offsets,
+                  int64_t num_segments, int64_t num_rows, void *out, hipStream_t stream);
+
+/*
+ * segred_outer -- the sum of outer products of each segment's rows, the
+ * gradient of segred_matmul's weights: out[s] = sum over the rows r of
+ * segment s of left[l(r)]^T right[q(r)].
+ *
+ *   left, right   [left_count, k] and [right_count, m] of type `dtype`.
+ *   left_rows, right_rows  int64 [num_rows] or NULL, as `rows` above.
+ *   offsets       as above; segments reach no further than num_rows.
+ *   out           [num_segments, k, m] of type `out_dtype`: `dtype` or
+ *                 SEGRED_F32.  An empty segment gets zeros.  (With `dtype`
+ *                 weights [k, m]; swap left and right for [m, k].)
+ *   workspace     segred_outer_workspace(k, m, num_segments, num_rows) bytes:
+ *                 few long segments are cut into pieces whose sums are added
+ *                 in row order by a second kernel.
+ *
+ * Errors: as segred_matmul, and SEGRED_ERR_INVALID_ARGUMENT for another
+ * out_dtype or a workspace that is missing or too small.
+ */
+int segred_outer(const void *left, const int64_t *left_rows, int64_t left_count, int64_t k,
+                 const void *right, const int64_t *right_rows, int64_t right_count, int64_t m, int32_t dtype,
+                 const int64_t *offsets, int64_t num_segments, int64_t num_rows, void *out, int32_t out_dtype,
+                 void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t segred_outer_workspace(int64_t k, int64_t m, int64_t num_segments, int64_t num_rows);
+
+/*
+ * segred_group -- entries grouped by an index: the stable order that puts the
+ * entries of group 0 first, then those of group 1, and so on.
+ *
+ *   index      int64 [rows], any order.  Entries outside [0, dim_size) belong
+ *              to no group and come behind the last one.
+ *   rows       0 <= rows <= 2^31 - 1 (entries).
+ *   fanout     >= 1: entry e belongs to source row e / fanout (a token that
+ *              names `fanout` groups has that many consecutive entries).
+ *   dim_size   0 <= dim_size <= 2^31 - 2.
+ *   order      int64 [rows]: order[p] = the source row of the entry at place
+ *              p; `rows` of the products.
+ *   position   int64 [rows]: position[e] = the place of entry e, -1 for an
+ *              entry of no group; `position` of the combine calls.
+ *   offsets    int64 [dim_size + 1]: group s has the places offsets[s] ..
+ *              offsets[s + 1] - 1.
+ *   workspace  segred_group_workspace(rows, dim_size) bytes.
+ *
+ * Errors: SEGRED_ERR_INVALID_ARGUMENT for negative sizes, fanout < 1, a NULL
+ * pointer that is needed, misalignment (8 bytes; 16 for the workspace), a
+ * workspace that is missing or too small.  SEGRED_ERR_UNSUPPORTED for sizes
+ * above those given.  SEGRED_ERR_HIP if a launch fails.
+ */
+int segred_group(const int64_t *index, int64_t rows, int64_t fanout, int64_t dim_size, int64_t *order,
+                 int64_t *position, int64_t *offsets, void *workspace, int64_t workspace_bytes,
+                 hipStream_t stream);
+int64_t segred_group_workspace(int64_t rows, int64_t dim_size);
+
+/*
+ * segred_combine -- the weighted join of the rows each token was sent to:
+ * out[t] = sum over j of weights[t, j] values[position[t, j]].
+ *
+ *   values    [rows, m] of type `dtype`.
+ *   position  int64 [tokens, fanout]; entries outside [0, rows) take no part.
+ *             A row may be named more than once.
+ *   weights   float32 [tokens, fanout].
+ *   out       [tokens, m] of type `dtype`, every element written (zeros for a
+ *             token without a row).
+ *
+ * Errors: SEGRED_ERR_INVALID_ARGUMENT for an unknown dtype, m < 1, negative
+ * counts, a NULL pointer that is needed, misalignment (an element for values
+ * and out, 8 bytes for position, 4 for weights), sizes past INT64_MAX bytes.
+ * SEGRED_ERR_UNSUPPORTED for integer types or more than 2^36 workgroups.
+ * SEGRED_ERR_HIP if a launch fails.  `out` must not overlap the inputs.
+ */
+int segred_combine(const void *values, int32_t dtype, int64_t m, int64_t rows, const int64_t *position,
+                   const float *weights, int64_t tokens, int64_t fanout, void *out, hipStream_t stream);
+
+/*
+ * segred_combine_grad -- the gradient of segred_combine from that of its
+ * output: grad_values[position[t, j]] = weights[t, j] grad[t] and
+ * grad_weights[t, j] = <grad[t], values[position[t, j]]>.
+ *
+ *   grad          [tokens, m] of type `dtype`.
+ *   grad_values   [rows, m]; rows that no entry names are left as they were.
+ *                 Each row may be named once only (as segred_group's positions
+ *                 do); it is not checked.
+ *   grad_weights  float32 [tokens, fanout]; 0 for entries that take no part.
+ *   the others    as segred_combine, and the errors.
+ */
+int segred_combine_grad(const void *grad, const void *values, int32_t dtype, int64_t m, int64_t rows,
+                        const int64_t *position, const float *weights, int64_t tokens, int64_t fanout,
+                        void *grad_values, float *grad_weights, hipStream_t stream);
+
+/*
+ * segred_adapter -- a projection that all rows share with a low-rank adapter
+ * per segment (request) beside it.  For the rows of segment s, a = which[s]:
+ *   out = x W^T + scale[a] (x down[a]^T) up[a]^T      (transpose = 0, x [., k])
+ *   out = x W   + scale[a] (x up[a]) down[a]          (transpose != 0, x [., m])
+ * The second is the gradient of the first's input, from its output's.
+ *
+ *   values     [num_rows, k], or [num_rows, m] with `transpose`.
+ *   weights    W [m, k].
+ *   offsets    int64 [num_segments + 1], nondecreasing, as segred_matmul.
+ *   which      int64 [num_segments]; outside [0, adapters): no adapter.
+ *   down, up   [adapters, rank, k] and [adapters, m, rank].
+ *   scale      float32 [adapters], or NULL: 1.
+ *   out        [num_rows, m], or [num_rows, k] with `transpose`; rows of no
+ *              segment are left as they were.
+ *   low        [num_rows, rank] of type `dtype`, or NULL: the low-rank rows
+ *              scale[a] (x down[a]^T) (or scale[a] (x up[a])), zeros without
+ *              an adapter.  The gradients of the factors are sums of outer
+ *              products over the rows of an adapter: of up[a] from the output
+ *              gradient and the forward call's `low`, of down[a] from the
+ *              transposed call's `low` and x (segred_outer).
+ *   workspace  segred_adapter_workspace(rank, num_rows) bytes.
+ *
+ * The low-rank rows enter the second product in float32, or as the sum of two
+ * bf16 (2^-17 relative) for the 16-bit types.
+ *
+ * Errors: as segred_matmul; also SEGRED_ERR_INVALID_ARGUMENT for rank < 1,
+ * adapters < 0 or a workspace that is missing or too small, and
+ * SEGRED_ERR_UNSUPPORTED for rank above 2^24, adapters above 2^31 - 1 or
+ * num_rows above 2^40.
+ */
+int segred_adapter(const void *values, int32_t dtype, int64_t k, const void *weights, int64_t m,
+                   const int64_t *offsets, const int64_t *which, int64_t num_segments, int64_t num_rows,
+                   const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
+                   int32_t transpose, void *out, void *low, void *workspace, int64_t workspace_bytes,
+                   hipStream_t stream);
+int64_t segred_adapter_workspace(int64_t rank, int64_t num_rows);
 
 /* Static, host-side description of a status code (never NULL). */
 const char *segred_status_string(int status);

@@ -14,6 +14,15 @@ There is no CPU fallback: if the library is missing, calls raise.
     pos, word = galloping_search(values, queries, segments)  # lower bounds per segment
     values, count = unique(keys)                       # distinct adjacent values
     offsets, count = offsets_from_flags(start_flags)   # uint32 flags, nonzero = start
+
+Operators over ragged groups of rows (float32, bfloat16, float16):
+
+    order, position, offsets = group(choice, groups)   # choice int64 [N] or [T, k]
+    h = matmul(x, weights, offsets, rows=order)        # each group's rows by its own weights
+    y = combine(h, position, prob)                     # the weighted join per token
+    dh, dprob = combine_grad(dy, h, position, prob)
+    dw = outer(x, dh, offsets, left_rows=order)        # the gradient of the weights
+    y = adapter(x, weights, offsets, which, down, up)  # shared projection + low-rank adapter per request
 """
 from __future__ import annotations
 
@@ -29,6 +38,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libsegred.so")
 SUM, MIN, MAX, MEAN = 0, 1, 2, 3
 OPS = {"sum": SUM, "min": MIN, "max": MAX, "mean": MEAN}
 DTYPES = {torch.uint32: 0, torch.int32: 1, torch.float32: 2}
+FLOATS = {torch.float32: 2, torch.bfloat16: 3, torch.float16: 4}  # the products and combine calls
 STATUS = {0: "SEGRED_OK", 1: "SEGRED_ERR_INVALID_ARGUMENT", 2: "SEGRED_ERR_UNSUPPORTED",
           3: "SEGRED_ERR_OUT_OF_MEMORY", 4: "SEGRED_ERR_HIP", 5: "SEGRED_ERR_SCRATCH_LIMIT"}
 
@@ -77,6 +87,25 @@ def library(path: str | None = None):
             lib.segred_unique.restype = ctypes.c_int
             lib.segred_offsets_from_flags.argtypes = [vp, i64, vp, vp, vp]
             lib.segred_offsets_from_flags.restype = ctypes.c_int
+            lib.segred_matmul.argtypes = [vp, i32, i64, vp, i64, vp, i32, i64, vp, i64, i64, vp, vp]
+            lib.segred_matmul.restype = ctypes.c_int
+            lib.segred_outer.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, i64, vp, i32, vp, i64, vp]
+            lib.segred_outer.restype = ctypes.c_int
+            lib.segred_outer_workspace.argtypes = [i64, i64, i64, i64]
+            lib.segred_outer_workspace.restype = i64
+            lib.segred_group.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+            lib.segred_group.restype = ctypes.c_int
+            lib.segred_group_workspace.argtypes = [i64, i64]
+            lib.segred_group_workspace.restype = i64
+            lib.segred_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp]
+            lib.segred_combine.restype = ctypes.c_int
+            lib.segred_combine_grad.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp]
+            lib.segred_combine_grad.restype = ctypes.c_int
+            lib.segred_adapter.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, i32, vp, vp,
+                                           vp, i64, vp]
+            lib.segred_adapter.restype = ctypes.c_int
+            lib.segred_adapter_workspace.argtypes = [i64, i64]
+            lib.segred_adapter_workspace.restype = i64
             lib.segred_status_string.argtypes = [ctypes.c_int]
             lib.segred_status_string.restype = ctypes.c_char_p
             lib.segred_set_shares.argtypes = [i64]
@@ -380,6 +409,262 @@ def offsets_from_flags(flags: torch.Tensor):
                                                  count.data_ptr(), _stream(flags.device))
     _check(rc, "segred_offsets_from_flags")
     return offsets, count
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Raise unless every tensor given is contiguous and on the GPU of ``first``."""
+    for name, t in others.items():
+        if t is not None and (t.device != first.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor on the GPU of the other inputs")
+
+
+def _check_index(name: str, t: torch.Tensor | None):
+    if t is not None and (t.dtype != torch.int64 or t.dim() != 1):
+        raise ValueError(f"{name} must be a 1-D int64 tensor")
+
+
+def matmul(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *, transpose: bool = False,
+           rows: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The matrix product of each segment's rows with weights of its own
+    (segred_matmul): ``out[r] = values[r] @ weights[s]`` for the rows r of
+    segment s, with ``weights[s]`` transposed first where ``transpose`` is set.
+
+    values   [N, K] float32 / bfloat16 / float16 on a GPU, contiguous.
+    weights  [S, K, M], or [S, M, K] with ``transpose``, of the same type.
+    offsets  int64 [S + 1] on the same GPU.
+    rows     optional int64 [R]: row r of the product is then made from
+             ``values[rows[r]]`` (``group``'s order); an entry outside the
+             values stands for a row of zeros.
+    Returns out [N or R, M]; rows of no segment are left as they were
+    (uninitialised when ``out`` is not given).  The gradient of the (gathered)
+    rows is ``matmul(grad, weights, offsets, transpose=not transpose)``, that
+    of the weights ``outer``.
+    """
+    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
+        raise ValueError("values must be a contiguous 2-D GPU tensor")
+    if values.dtype not in FLOATS:
+        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
+    if weights.dtype != values.dtype:
+        raise TypeError("weights must have the dtype of values")
+    _same_device(values, weights=weights, offsets=offsets, rows=rows, out=out)
+    _check_index("offsets", offsets)
+    _check_index("rows", rows)
+    s, n = offsets.numel() - 1, (values if rows is None else rows).shape[0]
+    k = values.shape[1]
+    if s < 0 or weights.dim() != 3 or weights.shape[0] != s:
+        raise ValueError("weights must be [S, K, M] (or [S, M, K] with transpose) with S + 1 offsets")
+    m, kw = (weights.shape[1], weights.shape[2]) if transpose else (weights.shape[2], weights.shape[1])
+    if kw != k:
+        raise ValueError(f"values have {k} features and weights take {kw}")
+    if out is None:
+        out = torch.empty((n, m), dtype=values.dtype, device=values.device)
+    elif out.shape != (n, m) or out.dtype != values.dtype:
+        raise ValueError("out must be [rows, M] of the dtype of values")
+    with torch.cuda.device(values.device):
+        rc = library().segred_matmul(values.data_ptr(), FLOATS[values.dtype], k,
+                                     rows.data_ptr() if rows is not None else None, values.shape[0],
+                                     weights.data_ptr(), int(bool(transpose)), m, offsets.data_ptr(), s, n,
+                                     out.data_ptr(), _stream(values.device))
+    _check(rc, "segred_matmul")
+    return out
+
+
+def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, left_rows: torch.Tensor | None = None,
+          right_rows: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+          out: torch.Tensor | None = None) -> torch.Tensor:
+    """The sum of outer products of each segment's rows (segred_outer):
+    ``out[s] = sum over r of left[r].T @ right[r]``, [S, K, M].
+
+    left, right  [*, K] and [*, M] float32 / bfloat16 / float16 on a GPU,
+                 contiguous and of one type.
+    offsets      int64 [S + 1] on the same GPU; an empty segment gives zeros.
+    left_rows, right_rows  optional int64 [R]: gather that side's rows.
+    out_dtype    the inputs' type (default) or float32.
+    """
+    if not left.is_cuda or not left.is_contiguous() or left.dim() != 2 or right.dim() != 2:
+        raise ValueError("left and right must be contiguous 2-D GPU tensors")
+    if left.dtype not in FLOATS:
+        raise TypeError(f"left dtype {left.dtype} is not float32, bfloat16 or float16")
+    if right.dtype != left.dtype:
+        raise TypeError("right must have the dtype of left")
+    _same_device(left, right=right, offsets=offsets, left_rows=left_rows, right_rows=right_rows, out=out)
+    _check_index("offsets", offsets)
+    _check_index("left_rows", left_rows)
+    _check_index("right_rows", right_rows)
+    s = offsets.numel() - 1
+    n = (left if left_rows is None else left_rows).shape[0]
+    if (right if right_rows is None else right_rows).shape[0] != n or s < 0:
+        raise ValueError("left and right need the same number of rows, and offsets S + 1 entries")
+    k, m = left.shape[1], right.shape[1]
+    odt = out_dtype or (left.dtype if out is None else out.dtype)
+    if odt not in (left.dtype, torch.float32):
+        raise TypeError("out_dtype must be the dtype of left or float32")
+    if out is None:
+        out = torch.empty((s, k, m), dtype=odt, device=left.device)
+    elif out.shape != (s, k, m) or out.dtype != odt:
+        raise ValueError("out must be [S, K, M] of out_dtype")
+    need = library().segred_outer_workspace(k, m, s, n)
+    work = torch.empty(need, dtype=torch.uint8, device=left.device) if need else None
+    with torch.cuda.device(left.device):
+        rc = library().segred_outer(left.data_ptr(), left_rows.data_ptr() if left_rows is not None else None,
+                                    left.shape[0], k, right.data_ptr(),
+                                    right_rows.data_ptr() if right_rows is not None else None, right.shape[0], m,
+                                    FLOATS[left.dtype], offsets.data_ptr(), s, n, out.data_ptr(), FLOATS[odt],
+                                    work.data_ptr() if need else None, need, _stream(left.device))
+    _check(rc, "segred_outer")
+    return out
+
+
+def group(index: torch.Tensor, dim_size: int):
+    """Rows grouped by an index (segred_group).
+
+    index  int64 [N], or [T, k] where each row names k groups.
+    Returns (order, position, offsets), all int64: ``order`` [N] or [T * k]
+    holds the rows of group 0, then of group 1, and so on, each group's in
+    increasing order; ``position``, shaped as ``index``, the place of each
+    entry in ``order``; ``offsets`` [dim_size + 1] where each group begins.
+    Entries outside [0, dim_size) come behind the last group, at position -1.
+    """
+    if not index.is_cuda or index.dtype != torch.int64 or index.dim() not in (1, 2) or not index.is_contiguous():
+        raise ValueError("index must be a contiguous 1-D or 2-D int64 GPU tensor")
+    dim_size = int(dim_size)
+    if dim_size < 0:
+        raise ValueError("dim_size must be >= 0")
+    n, dev = index.numel(), index.device
+    fanout = max(index.shape[1], 1) if index.dim() == 2 else 1
+    order = torch.empty(n, dtype=torch.int64, device=dev)
+    position = torch.empty_like(index)
+    offsets = torch.empty(dim_size + 1, dtype=torch.int64, device=dev)
+    lib = library()
+    need = lib.segred_group_workspace(n, dim_size)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with torch.cuda.device(dev):
+        rc = lib.segred_group(index.data_ptr(), n, fanout, dim_size, order.data_ptr(), position.data_ptr(),
+                              offsets.data_ptr(), work.data_ptr() if need else None, need, _stream(dev))
+    _check(rc, "segred_group")
+    return order, position, offsets
+
+
+def _check_combine(values, position, weights):
+    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
+        raise ValueError("values must be a contiguous 2-D GPU tensor")
+    if values.dtype not in FLOATS:
+        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
+    if position.dtype != torch.int64 or position.dim() != 2:
+        raise ValueError("position must be an int64 [T, k] tensor")
+    if weights.dtype != torch.float32 or weights.shape != position.shape:
+        raise ValueError("weights must be a float32 tensor of the shape of position")
+    if values.shape[1] < 1:
+        raise ValueError("values has an empty feature dimension")
+
+
+def combine(values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor, *,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """The weighted join of the rows a token was sent to (segred_combine):
+    ``out[t] = sum over j of weights[t, j] * values[position[t, j]]``.
+
+    values    [N, M] float32 / bfloat16 / float16 on a GPU, contiguous.
+    position  int64 [T, k] (``group``'s); entries outside the values take no part.
+    weights   float32 [T, k].
+    Returns out [T, M] of the values' type.
+    """
+    _check_combine(values, position, weights)
+    _same_device(values, position=position, weights=weights, out=out)
+    (n, m), (t, k) = values.shape, position.shape
+    if out is None:
+        out = torch.empty((t, m), dtype=values.dtype, device=values.device)
+    elif out.shape != (t, m) or out.dtype != values.dtype:
+        raise ValueError("out must be [T, M] of the dtype of values")
+    with torch.cuda.device(values.device):
+        rc = library().segred_combine(values.data_ptr(), FLOATS[values.dtype], m, n, position.data_ptr(),
+                                      weights.data_ptr(), t, k, out.data_ptr(), _stream(values.device))
+    _check(rc, "segred_combine")
+    return out
+
+
+def combine_grad(grad: torch.Tensor, values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor, *,
+                 out: torch.Tensor | None = None):
+    """The gradient of ``combine`` (segred_combine_grad) from ``grad`` [T, M].
+
+    Returns (grad_values [N, M], grad_weights float32 [T, k]).  Each row may be
+    named once only; rows that ``position`` does not name are left as they were
+    (uninitialised when ``out`` is not given)."""
+    _check_combine(values, position, weights)
+    _same_device(values, grad=grad, position=position, weights=weights, out=out)
+    (n, m), (t, k) = values.shape, position.shape
+    if grad.shape != (t, m) or grad.dtype != values.dtype:
+        raise ValueError("grad must be [T, M] of the dtype of values")
+    if out is None:
+        out = torch.empty_like(values)
+    elif out.shape != values.shape or out.dtype != values.dtype:
+        raise ValueError("out must have the shape and dtype of values")
+    grad_weights = torch.empty_like(weights)
+    with torch.cuda.device(values.device):
+        rc = library().segred_combine_grad(grad.data_ptr(), values.data_ptr(), FLOATS[values.dtype], m, n,
+                                           position.data_ptr(), weights.data_ptr(), t, k, out.data_ptr(),
+                                           grad_weights.data_ptr(), _stream(values.device))
+    _check(rc, "segred_combine_grad")
+    return out, grad_weights
+
+
+def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, which: torch.Tensor,
+            down: torch.Tensor, up: torch.Tensor, *, scale: torch.Tensor | None = None, transpose: bool = False,
+            want_low: bool = False, out: torch.Tensor | None = None):
+    """A projection that all rows share with a low-rank adapter per segment
+    beside it (segred_adapter): for the rows of segment s and a = which[s],
+    ``x @ weights.T + scale[a] * (x @ down[a].T) @ up[a].T``, or with
+    ``transpose`` (the gradient of x, from that of the output)
+    ``x @ weights + scale[a] * (x @ up[a]) @ down[a]``.
+
+    values    [N, K] ([N, M] with ``transpose``) float32 / bfloat16 / float16
+              on a GPU, contiguous.
+    weights   [M, K]; down [L, r, K]; up [L, M, r], of the same type.
+    offsets   int64 [S + 1]; which int64 [S], outside [0, L): no adapter.
+    scale     optional float32 [L].
+    want_low  also return the low-rank rows [N, r]: ``outer`` of the output's
+              gradient and these gives the gradient of up, ``outer`` of the
+              transposed call's and x that of down (rows grouped by adapter).
+    Rows of no segment are left as they were in ``out`` (uninitialised when it
+    is not given; likewise the low-rank rows).
+    """
+    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
+        raise ValueError("values must be a contiguous 2-D GPU tensor")
+    if values.dtype not in FLOATS:
+        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
+    if weights.dtype != values.dtype or down.dtype != values.dtype or up.dtype != values.dtype:
+        raise TypeError("weights, down and up must have the dtype of values")
+    _same_device(values, weights=weights, offsets=offsets, which=which, down=down, up=up, scale=scale, out=out)
+    _check_index("offsets", offsets)
+    _check_index("which", which)
+    if weights.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise ValueError("weights must be [M, K], down [L, r, K] and up [L, M, r]")
+    (m, k), (count, r, _) = weights.shape, down.shape
+    if down.shape[2] != k or up.shape != (count, m, r):
+        raise ValueError("weights must be [M, K], down [L, r, K] and up [L, M, r]")
+    s, n = offsets.numel() - 1, values.shape[0]
+    if s < 0 or which.numel() != s:
+        raise ValueError("which needs one entry per segment and offsets one more")
+    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (count,)):
+        raise ValueError("scale must be a float32 [L] tensor")
+    have, give = (m, k) if transpose else (k, m)
+    if values.shape[1] != have:
+        raise ValueError(f"values have {values.shape[1]} features and the projection takes {have}")
+    if out is None:
+        out = torch.empty((n, give), dtype=values.dtype, device=values.device)
+    elif out.shape != (n, give) or out.dtype != values.dtype:
+        raise ValueError("out must be [N, outputs] of the dtype of values")
+    low = torch.empty((n, r), dtype=values.dtype, device=values.device) if want_low else None
+    lib = library()
+    need = lib.segred_adapter_workspace(r, n)
+    work = torch.empty(need, dtype=torch.uint8, device=values.device) if need else None
+    with torch.cuda.device(values.device):
+        rc = lib.segred_adapter(values.data_ptr(), FLOATS[values.dtype], k, weights.data_ptr(), m, offsets.data_ptr(),
+                                which.data_ptr(), s, n, down.data_ptr(), up.data_ptr(),
+                                scale.data_ptr() if scale is not None else None, count, r, int(bool(transpose)),
+                                out.data_ptr(), low.data_ptr() if want_low else None,
+                                work.data_ptr() if need else None, need, _stream(values.device))
+    _check(rc, "segred_adapter")
+    return (out, low) if want_low else out
 
 
 def set_shares(shares: int):

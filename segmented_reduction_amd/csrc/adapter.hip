@@ -1,0 +1,457 @@
+// adapter.hip -- a projection that all rows share with a low-rank adapter per
+// segment beside it: out[r] = x[r] W + scale_a (x[r] A_a) B_a, a the adapter
+// of r's segment.
+//
+// Two kernels.  adapter_low computes u = scale (x A) per segment, 32 ranks a
+// workgroup, the contraction split over its waves.  adapter_main computes
+// x W over tiles of rows that may span many segments and goes on, in the same
+// accumulators, with one step per adapter met in the tile: u's rows of that
+// adapter (zeros for the others) times B_a.  So x and W are read once, out is
+// written once, and each adapter costs a few steps.
+//
+// u is kept in more bits than the inputs have: for 16-bit inputs as the sum of
+// two bf16 (2^-17 relative), stored as [hi 32 | lo 32] per 32 ranks, so that
+// one step multiplies both halves by the same 32 ranks of B.  float16 B is
+// split the same way, because u may leave float16's range.
+#include <algorithm>
+
+#include "internal.hpp"
+#include "tile.hpp"
+
+namespace segred {
+
+struct AdapterArgs {
+    const char *values;   // [N, K]
+    const char *weights;  // [M, K] (row form) or [K, M] (col form)
+    const char *first;    // [L, R, K] or [L, K, R]
+    const char *second;   // [L, M, R] or [L, R, M]
+    const int64_t *offsets, *which;
+    const float *scale;   // [L] or null
+    int64_t S, N, K, M, L, R;
+    int64_t slots, mtiles, ntiles, blocks;  // blocks: ceil(R / 32)
+    char *u;              // [N, blocks * 128 bytes]
+    int32_t *ids;         // [N] adapter of each row, -1: none
+    char *low;            // [N, R] or null
+    char *out;
+    int vec;
+};
+
+constexpr int kRankBlock = 32;
+
+template <typename T, int MT, int NW, int STAGES, bool B_COL, bool DIRECT>
+__global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
+    constexpr int BM = 16 * MT, BN = kRankBlock, NT = 2;
+    constexpr int kLg = __builtin_ctz(BM);
+    using AStage = RowStage<T, BM, 64, DIRECT>;
+    using BRow = RowStage<T, BN, 64, DIRECT>;
+    using BCol = ColStage<T, BN, 64, DIRECT>;
+    constexpr int kABytes = AStage::kBytes;
+    constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[NW * STAGES * kStageBytes];
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.slots * a.blocks);
+    if (id >= a.slots * a.blocks) return;
+    const int64_t slot = id / a.blocks, block = id - slot * a.blocks;
+    const int r0 = (int)block * kRankBlock;
+    const int64_t s = slot_segment(a.offsets, a.S, kLg, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, kLg)) << kLg);
+    const int64_t end = min(a.offsets[s + 1], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)BM, end - row0);
+    const int64_t adapter = a.which[s];
+    const bool has = adapter >= 0 && adapter < a.L;
+    if (block == 0)
+        for (int r = threadIdx.x; r < rows; r += 64 * NW) a.ids[row0 + r] = has ? (int32_t)adapter : -1;
+    const int K = (int)a.K, R = (int)a.R;
+    if (!has) {
+        if (a.low)
+            for (int i = threadIdx.x; i < rows * kRankBlock; i += 64 * NW)
+                if (r0 + i % kRankBlock < R)
+                    reinterpret_cast<T *>(a.low)[(row0 + i / kRankBlock) * R + r0 + i % kRankBlock] = (T)0.f;
+        return;
+    }
+
+    AStage sa;
+    sa.init(0, lane, K, [&](int r) -> const char * {
+        return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+    });
+    const char *w = a.first + adapter * a.K * a.R * (int64_t)sizeof(T);
+    BRow sbr;
+    BCol sbc;
+    uint64_t wp[BCol::kLoads];
+    int wleft[BCol::kLoads];
+    if constexpr (B_COL) {
+#pragma unroll
+        for (int i = 0; i < BCol::kLoads; ++i) {
+            const int n = r0 + BCol::col(i, 0, lane);
+            wp[i] = (uint64_t)(w + (BCol::row(i, 0, lane) * a.R + n) * (int64_t)sizeof(T));
+            wleft[i] = R - n;
+        }
+    } else {
+        sbr.init(0, lane, K, [&](int r) -> const char * {
+            return r0 + r < R ? w + (r0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    }
+    f32x4 acc[MT][NT] = {};
+    const int steps = (K + kStep<T> - 1) / kStep<T>;
+    wave_steps<STAGES, DIRECT, kLoads, kStageBytes>(
+        lds + wave * STAGES * kStageBytes, wave * steps / NW, (wave + 1) * steps / NW,
+        [&](int t, bool live, lds_char *buf) {
+            const int k0 = live ? t * kStep<T> : K;
+            sa.issue(buf, 0, k0);
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.R * sizeof(T);
+                sbc.issue(
+                    buf + kABytes, 0, [&](int i) { return wp[i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, 0, lane) < K ? wleft[i] : 0; });
+            } else {
+                sbr.issue(buf + kABytes, 0, k0);
+            }
+        },
+        [&](lds_char *buf) {
+            sa.commit(buf, 0, lane);
+            if constexpr (B_COL) sbc.commit(buf + kABytes, 0, lane);
+            else sbr.commit(buf + kABytes, 0, lane);
+        },
+        [&](int, const lds_char *buf) {
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, lane);
+        });
+    const float scale = a.scale ? a.scale[adapter] : 1.f;
+    join_waves<NW, MT, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
+        if (r >= rows) return;
+        sum *= scale;
+        char *u = a.u + ((row0 + r) * a.blocks + block) * 128;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<f32x4 *>(u + c * 4) = sum;
+        } else {
+            bf16x4 hi, lo;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                hi[j] = (__bf16)sum[j];
+                lo[j] = (__bf16)(sum[j] - (float)hi[j]);
+            }
+            *reinterpret_cast<bf16x4 *>(u + c * 2) = hi;
+            *reinterpret_cast<bf16x4 *>(u + 64 + c * 2) = lo;
+        }
+        if (a.low) store_quad<T>(reinterpret_cast<T *>(a.low) + (row0 + r) * R, r0 + c, R, sum, false);
+    });
+}
+
+// The steps of an output tile after those of x W: rows of u against the
+// adapters met in the tile.
+template <typename T, int BM, int BN, int THREADS, bool B_COL, bool DIRECT>
+struct AdapterSteps {
+    using AS = RowStage<T, BM, THREADS, DIRECT>;
+    using BR = RowStage<T, BN, THREADS, DIRECT>;
+    using BC = ColStage<T, BN, THREADS, DIRECT>;
+    uint64_t up[AS::kLoads];
+    int rid[AS::kLoads];
+
+    __device__ __forceinline__ void init(const AdapterArgs &a, const int *s_ids, int64_t row0, int wave, int lane) {
+        const int unit = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+        for (int i = 0; i < AS::kLoads; ++i) {
+            const int r = AS::group(i, wave) * 8 + (lane >> 3);
+            rid[i] = s_ids[r];
+            up[i] = (uint64_t)(a.u + (row0 + r) * a.blocks * 128 + unit * 16);
+        }
+    }
+    __device__ __forceinline__ void issue(AS &sa, BR &sbr, BC &sbc, const AdapterArgs &a, lds_char *buf, int adapter,
+                                          int block, int64_t n0, int wave, int lane) {
+        const uint64_t zeros = (uint64_t)zero_unit();
+#pragma unroll
+        for (int i = 0; i < AS::kLoads; ++i) {
+            const bool mine = rid[i] == adapter;
+            const uint64_t q = up[i] + (uint64_t)block * 128;
+            if constexpr (DIRECT) load_to_lds(mine ? q : zeros, buf + AS::group(i, wave) * 1024);
+            else sa.v[i] = load_unit<T>(q, mine ? kUnit<T> : 0);
+        }
+        lds_char *bb = buf + AS::kBytes;
+        const char *w = a.second + (int64_t)adapter * a.M * a.R * (int64_t)sizeof(T);
+        const int R = (int)a.R, M = (int)a.M;
+        constexpr int kMask = kRankBlock - 1;
+        if constexpr (B_COL) {
+            auto rank = [&](int i) { return block * kRankBlock + (BC::row(i, wave, lane) & kMask); };
+            sbc.issue(
+                bb, wave,
+                [&](int i) { return (uint64_t)(w + (rank(i) * a.M + n0 + BC::col(i, wave, lane)) * (int64_t)sizeof(T)); },
+                [&](int i) { return rank(i) < R ? M - (int)n0 - BC::col(i, wave, lane) : 0; });
+        } else {
+            const int rank = block * kRankBlock + ((((lane & 7) ^ (lane >> 3)) * kUnit<T>) & kMask);
+#pragma unroll
+            for (int i = 0; i < BR::kLoads; ++i) {
+                const int64_t n = n0 + BR::group(i, wave) * 8 + (lane >> 3);
+                const uint64_t q = (uint64_t)(w + (n * a.R + rank) * (int64_t)sizeof(T));
+                const int left = n < a.M ? R - rank : 0;
+                if constexpr (DIRECT) load_to_lds(left > 0 ? q : zeros, bb + BR::group(i, wave) * 1024);
+                else sbr.v[i] = load_unit<T>(q, left);
+            }
+        }
+    }
+};
+
+// Products of an adapter step: bf16 halves of u against B's two bf16 halves.
+template <int MT, int NT, bool B_COL, int BW>
+__device__ __forceinline__ void split_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
+                                               int n0, int lane) {
+    bf16x8 hi[NT], lo[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        u32x4 b;
+        if constexpr (B_COL) b = col_frag<_Float16, BW>(lb, n0 + 16 * j, 0, lane);
+        else b = row_frag(lb, n0 + 16 * j, 0, lane);
+        const f16x8 h = __builtin_bit_cast(f16x8, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            hi[j][e] = (__bf16)(float)h[e];
+            lo[j][e] = (__bf16)((float)h[e] - (float)hi[j][e]);
+        }
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const bf16x8 a = __builtin_bit_cast(bf16x8, row_frag(la, m0 + 16 * i, ks, lane));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[j], a, acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[j], a, acc[i][j], 0, 0, 0);
+            }
+        }
+}
+
+// Fills s_ids (adapter of each tile row, -1: none) and s_list (the adapters
+// met, in row order); returns their number.  All threads must call it.
+template <int BM, int THREADS>
+__device__ __forceinline__ int tile_adapters(const AdapterArgs &a, int64_t row0, int rows, int *s_ids, int *s_list,
+                                             int *s_count) {
+    const int tid = threadIdx.x;
+    for (int r = tid; r < BM; r += THREADS) s_ids[r] = r < rows ? a.ids[row0 + r] : -1;
+    if (tid == 0) *s_count = 0;
+    __syncthreads();
+    if (tid < 64) {  // one wave walks the rows, 64 at a time
+        int n = 0;
+        for (int b = 0; b < BM; b += 64) {
+            const int r = b + tid;
+            const int id = r < BM ? s_ids[r] : -1;
+            bool first = id >= 0 && (r == 0 || s_ids[r - 1] != id);
+            if (first)
+                for (int q = 0; q < r - 1 && first; ++q) first = s_ids[q] != id;
+            const uint64_t m = ballot(first);
+            if (first) s_list[n + popc64(m & ((uint64_t(1) << tid) - 1))] = id;
+            n += popc64(m);
+        }
+        if (tid == 0) *s_count = n;
+    }
+    __syncthreads();
+    return *s_count;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool B_COL, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    using Steps = AdapterSteps<T, BM, BN, kThreads, B_COL, DIRECT>;
+    using AStage = typename Steps::AS;
+    using BRow = typename Steps::BR;
+    using BCol = typename Steps::BC;
+    constexpr int kABytes = AStage::kBytes;
+    constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kStageBytes];
+    __shared__ int s_ids[BM], s_list[BM], s_count;
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t total = a.mtiles * a.ntiles;
+    const int64_t id = xcd_tile(total);
+    if (id >= total) return;
+    constexpr int kGroup = 4;
+    const int64_t group = id / (kGroup * a.ntiles), in_group = id - group * kGroup * a.ntiles;
+    const int64_t gm = min((int64_t)kGroup, a.mtiles - group * kGroup);
+    const int64_t row0 = a.offsets[0] + (group * kGroup + in_group % gm) * BM;
+    const int64_t n0 = in_group / gm * BN;
+    const int64_t end = min(a.offsets[a.S], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)BM, end - row0);
+    const int K = (int)a.K;
+    const int met = tile_adapters<BM, kThreads>(a, row0, rows, s_ids, s_list, &s_count);
+
+    AStage sa;
+    sa.init(wave, lane, K, [&](int r) -> const char * {
+        return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+    });
+    BRow sbr;
+    BCol sbc;
+    uint64_t wp[BCol::kLoads];
+    int wleft[BCol::kLoads];
+    if constexpr (B_COL) {
+#pragma unroll
+        for (int i = 0; i < BCol::kLoads; ++i) {
+            const int64_t n = n0 + BCol::col(i, wave, lane);
+            wp[i] = (uint64_t)(a.weights + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+            wleft[i] = (int)(a.M - n);
+        }
+    } else {
+        sbr.init(wave, lane, K, [&](int r) -> const char * {
+            return n0 + r < a.M ? a.weights + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    }
+    Steps extra;
+    extra.init(a, s_ids, row0, wave, lane);
+    const int base = (K + kStep<T> - 1) / kStep<T>, blocks = (int)a.blocks;
+    const int steps = base + met * blocks;
+    auto issue = [&](int t, lds_char *buf) {
+        if (t < base) {
+            const int k0 = t * kStep<T>;
+            sa.issue(buf, wave, k0);
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                sbc.issue(
+                    buf + kABytes, wave, [&](int i) { return wp[i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
+            } else {
+                sbr.issue(buf + kABytes, wave, k0);
+            }
+        } else {
+            const int e = (t - base) / blocks;
+            extra.issue(sa, sbr, sbc, a, buf, __builtin_amdgcn_readfirstlane(s_list[e]), (t - base) - e * blocks, n0,
+                        wave, lane);
+        }
+    };
+    auto commit = [&](lds_char *buf) {
+        sa.commit(buf, wave, lane);
+        if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
+        else sbr.commit(buf + kABytes, wave, lane);
+    };
+
+    f32x4 acc[MT][NT] = {};
+    const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+    issue(0, lds);
+    commit(lds);
+    for (int t = 0; t < steps; ++t) {
+        wait_and_meet<0>();
+        lds_char *next = lds + ((t + 1) & 1) * kStageBytes;
+        if (t + 1 < steps) issue(t + 1, next);
+        const lds_char *buf = lds + (t & 1) * kStageBytes;
+        if (__is_same(T, _Float16) && t >= base)
+            split_products<MT, NT, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+        else
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+        if (t + 1 < steps) commit(next);
+    }
+
+    T *out = reinterpret_cast<T *>(a.out);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int r = m_w + 16 * i + (lane & 15);
+        if (r < rows) {
+            T *row = out + (row0 + r) * a.M;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+        }
+    }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+int adapter_main_launch(AdapterArgs a, bool b_col, hipStream_t st) {
+    a.mtiles = (a.N + BM - 1) / BM;
+    a.ntiles = (a.M + BN - 1) / BN;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    constexpr int kThreads = 64 * WM * WN;
+    if (b_col) timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, true, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    else timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, false, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+template <typename T, int MT, bool DIRECT>
+int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
+    constexpr int NW = 4, STAGES = DIRECT ? 3 : 2;
+    a.slots = (a.N >> __builtin_ctz(16 * MT)) + a.S;
+    dim3 grid;
+    if (!tile_grid(a.slots * a.blocks, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (b_col) timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, true, DIRECT>), grid, dim3(64 * NW), 0, st, a);
+    else timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, false, DIRECT>), grid, dim3(64 * NW), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+template <typename T>
+int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool main_direct, hipStream_t st) {
+    int rc = low_direct ? adapter_low_launch<T, 1, true>(a, b_col, st) : adapter_low_launch<T, 1, false>(a, b_col, st);
+    if (rc != SEGRED_OK) return rc;
+    if (!main_direct) return adapter_main_launch<T, 64, 64, 2, 2, false>(a, b_col, st);
+    if constexpr (sizeof(T) == 2)
+        if (a.N >= 1024 && a.M >= 256) return adapter_main_launch<T, 256, 256, 2, 4, true>(a, b_col, st);
+    return adapter_main_launch<T, 64, 64, 2, 2, true>(a, b_col, st);
+}
+
+size_t adapter_ids_bytes(int64_t rows) { return ((size_t)rows * 4 + 255) & ~size_t(255); }
+
+}  // namespace segred
+
+using namespace segred;
+
+extern "C" int64_t segred_adapter_workspace(int64_t rank, int64_t num_rows) {
+    if (rank < 1 || rank > kMaxWidth || num_rows < 1 || num_rows > (int64_t(1) << 40)) return 0;
+    return (int64_t)adapter_ids_bytes(num_rows) + num_rows * ((rank + kRankBlock - 1) / kRankBlock) * 128;
+}
+
+extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, const void *weights, int64_t m,
+                              const int64_t *offsets, const int64_t *which, int64_t num_segments, int64_t num_rows,
+                              const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
+                              int32_t transpose, void *out, void *low, void *workspace, int64_t workspace_bytes,
+                              hipStream_t stream) {
+    const int64_t e = float_size(dtype);
+    if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (k < 1 || m < 1 || rank < 1 || adapters < 0 || num_segments < 0 || num_rows < 0) return SEGRED_ERR_INVALID_ARGUMENT;
+    const bool some = num_segments > 0 && num_rows > 0;
+    if (some && (!values || !weights || !offsets || !which || !out || (adapters > 0 && (!down || !up))))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (e == 0 || k > kMaxWidth || m > kMaxWidth || rank > kMaxWidth || adapters > INT32_MAX || num_rows > (int64_t(1) << 40))
+        return SEGRED_ERR_UNSUPPORTED;
+    if (!aligned(values, e) || !aligned(weights, e) || !aligned(out, e) || !aligned(down, e) || !aligned(up, e) ||
+        !aligned(low, e) || !aligned(scale, 4) || !aligned(offsets, 8) || !aligned(which, 8) || !aligned(workspace, 16))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (too_large(num_rows, k, 4) || too_large(num_rows, m, 4) || too_large(num_rows, rank, 4) ||
+        too_large(adapters, k * rank, 4) || too_large(adapters, m * rank, 4))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!some) return SEGRED_OK;
+    const int64_t need = segred_adapter_workspace(rank, num_rows);
+    if (!workspace || workspace_bytes < need) return SEGRED_ERR_INVALID_ARGUMENT;
+
+    AdapterArgs a{};
+    a.values = static_cast<const char *>(values);
+    a.weights = static_cast<const char *>(weights);
+    // forward: down is [L, R, K] and up [L, M, R]; transposed, from [N, M] to
+    // [N, K]: up is the first factor, [L, M, R], and down the second
+    a.first = static_cast<const char *>(transpose ? up : down);
+    a.second = static_cast<const char *>(transpose ? down : up);
+    a.offsets = offsets;
+    a.which = which;
+    a.scale = scale;
+    a.S = num_segments;
+    a.N = num_rows;
+    a.K = transpose ? m : k;
+    a.M = transpose ? k : m;
+    a.L = adapters;
+    a.R = rank;
+    a.blocks = (rank + kRankBlock - 1) / kRankBlock;
+    a.ids = static_cast<int32_t *>(workspace);
+    a.u = static_cast<char *>(workspace) + adapter_ids_bytes(num_rows);
+    a.low = static_cast<char *>(low);
+    a.out = static_cast<char *>(out);
+    a.vec = (a.M % 4 == 0 && aligned(out, 4 * e)) ? 1 : 0;
+    auto units = [&](const void *p, int64_t width) { return (width * e) % 16 == 0 && aligned(p, 16); };
+    const bool x = units(values, a.K);
+    const bool low_direct = x && units(a.first, transpose ? rank : k);
+    const bool main_direct = x && units(weights, k) && units(a.second, transpose ? k : rank);
+    switch (dtype) {
+    case SEGRED_BF16: return adapter_dispatch<__bf16>(a, transpose != 0, low_direct, main_direct, stream);
+    case SEGRED_F16: return adapter_dispatch<_Float16>(a, transpose != 0, low_direct, main_direct, stream);
+    default: return adapter_dispatch<float>(a, transpose != 0, low_direct, main_direct, stream);
+    }
+}

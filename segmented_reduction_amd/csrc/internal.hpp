@@ -70,6 +70,17 @@ inline void timed_launch_ggl(bool streaming, F kernel, dim3 grid, dim3 block, ui
 // Process-wide share override (0 = default).
 int64_t shares_override();
 
+// Bytes of an element of the products' types, 0 for the others.
+inline int64_t float_size(int32_t dtype) {
+    return dtype == SEGRED_F32 ? 4 : dtype == SEGRED_BF16 || dtype == SEGRED_F16 ? 2 : 0;
+}
+// Widest rows of the products (element offsets inside a row are 32-bit).
+constexpr int64_t kMaxWidth = int64_t(1) << 24;
+// Whether a * b * c (all >= 0, c > 0) passes INT64_MAX.
+inline bool too_large(int64_t a, int64_t b, int64_t c) {
+    return a > 0 && b > 0 && (b > INT64_MAX / c || a > INT64_MAX / (b * c));
+}
+
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 }  // namespace segred

@@ -1,0 +1,295 @@
+// matmul.hip -- the matrix product of each segment's rows with weights of its
+// own: out[r] = values[r] W[s] for the rows r of segment s.
+#include <algorithm>
+
+#include "internal.hpp"
+#include "tile.hpp"
+
+namespace segred {
+
+struct MatmulArgs {
+    const char *values;
+    const int64_t *rows;  // row of `values` behind each row, or null
+    int64_t value_rows;
+    const char *weights;
+    const int64_t *offsets;
+    int64_t S, N, K, M;
+    int64_t slots, ntiles;
+    void *out;
+    int vec;
+};
+
+constexpr int kSlotGroup = 4;  // row tiles that walk the column tiles together
+
+// One BM x BN tile of one segment per workgroup.
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    constexpr int kLg = __builtin_ctz(BM);
+    using AStage = RowStage<T, BM, kThreads, DIRECT>;
+    using BRow = RowStage<T, BN, kThreads, DIRECT>;
+    using BCol = ColStage<T, BN, kThreads, DIRECT>;
+    constexpr int kABytes = AStage::kBytes;
+    constexpr int kBBytes = B_COL ? BCol::kBytes : BRow::kBytes;
+    constexpr int kStageBytes = kABytes + kBBytes;
+    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    static_assert(DIRECT || STAGES == 2, "units that pass through registers use two buffers");
+    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes];
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return;
+    const int64_t group = id / (kSlotGroup * a.ntiles), in_group = id - group * kSlotGroup * a.ntiles;
+    const int64_t gm = min((int64_t)kSlotGroup, a.slots - group * kSlotGroup);
+    const int64_t slot = group * kSlotGroup + in_group % gm;
+    const int64_t n0 = in_group / gm * BN;
+
+    const int64_t s = slot_segment(a.offsets, a.S, kLg, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, kLg)) << kLg);
+    const int64_t end = min(a.offsets[s + 1], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)BM, end - row0);
+
+    AStage sa;
+    const int K = (int)a.K;
+    sa.init(wave, lane, K, [&](int r) -> const char * {
+        if (r >= rows) return nullptr;
+        int64_t v = row0 + r;
+        if (a.rows) v = a.rows[v];
+        if (v < 0 || v >= a.value_rows) return nullptr;
+        return a.values + v * a.K * (int64_t)sizeof(T);
+    });
+    const char *w = a.weights + s * a.K * a.M * (int64_t)sizeof(T);
+    BRow sbr;
+    BCol sbc;
+    uint64_t wp[BCol::kLoads];
+    int wleft[BCol::kLoads];
+    if constexpr (B_COL) {
+#pragma unroll
+        for (int i = 0; i < BCol::kLoads; ++i) {
+            const int64_t n = n0 + BCol::col(i, wave, lane);
+            wp[i] = (uint64_t)(w + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+            wleft[i] = (int)(a.M - n);
+        }
+    } else {
+        sbr.init(wave, lane, K, [&](int r) -> const char * {
+            return n0 + r < a.M ? w + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    }
+    auto issue = [&](int t, lds_char *buf) {
+        const int k0 = t * kStep<T>;
+        sa.issue(buf, wave, k0);
+        if constexpr (B_COL) {
+            const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+            sbc.issue(
+                buf + kABytes, wave, [&](int i) { return wp[i] + step; },
+                [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
+        } else {
+            sbr.issue(buf + kABytes, wave, k0);
+        }
+    };
+    auto commit = [&](lds_char *buf) {
+        sa.commit(buf, wave, lane);
+        if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
+        else sbr.commit(buf + kABytes, wave, lane);
+    };
+
+    f32x4 acc[MT][NT] = {};
+    const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+    const int steps = (K + kStep<T> - 1) / kStep<T>;
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
+        int cur = 0, fill = STAGES - 1;
+        for (int t = 0; t < steps; ++t) {
+            wait_and_meet<(STAGES - 2) * kLoads>();
+            issue(t + STAGES - 1, lds + fill * kStageBytes);
+            const lds_char *buf = lds + cur * kStageBytes;
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+        }
+        // the last loads write zeros into LDS; they must land before it is given away
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    } else {
+        issue(0, lds);
+        commit(lds);
+        for (int t = 0; t < steps; ++t) {
+            __syncthreads();
+            if (t + 1 < steps) issue(t + 1, lds);
+            const lds_char *buf = lds + (t & 1) * kStageBytes;
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+            if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
+        }
+    }
+
+    T *out = reinterpret_cast<T *>(a.out);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int r = m_w + 16 * i + (lane & 15);
+        if (r < rows) {
+            T *row = out + (row0 + r) * a.M;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+        }
+    }
+}
+
+// Few rows per segment: 16 rows x 16 NT columns per workgroup, the
+// contraction split over its NW waves.
+template <typename T, int NT, int NW, int STAGES, bool B_COL>
+__global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
+    using AStage = RowStage<T, 16, 64, true>;
+    using BRow = RowStage<T, 16 * NT, 64, true>;
+    using BCol = ColStage<T, 16 * NT, 64, true>;
+    constexpr int kABytes = AStage::kBytes;
+    constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[NW * STAGES * kStageBytes];
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return;
+    const int64_t slot = id / a.ntiles, n0 = (id - slot * a.ntiles) * (16 * NT);
+    const int64_t s = slot_segment(a.offsets, a.S, 4, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, 4)) << 4);
+    const int64_t end = min(a.offsets[s + 1], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)16, end - row0);
+    const int K = (int)a.K;
+
+    AStage sa;
+    sa.init(0, lane, K, [&](int r) -> const char * {
+        if (r >= rows) return nullptr;
+        int64_t v = row0 + r;
+        if (a.rows) v = a.rows[v];
+        if (v < 0 || v >= a.value_rows) return nullptr;
+        return a.values + v * a.K * (int64_t)sizeof(T);
+    });
+    const char *w = a.weights + s * a.K * a.M * (int64_t)sizeof(T);
+    BRow sbr;
+    BCol sbc;
+    uint64_t wp[BCol::kLoads];
+    int wleft[BCol::kLoads];
+    if constexpr (B_COL) {
+#pragma unroll
+        for (int i = 0; i < BCol::kLoads; ++i) {
+            const int64_t n = n0 + BCol::col(i, 0, lane);
+            wp[i] = (uint64_t)(w + (BCol::row(i, 0, lane) * a.M + n) * (int64_t)sizeof(T));
+            wleft[i] = (int)(a.M - n);
+        }
+    } else {
+        sbr.init(0, lane, K, [&](int r) -> const char * {
+            return n0 + r < a.M ? w + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    }
+    f32x4 acc[1][NT] = {};
+    const int steps = (K + kStep<T> - 1) / kStep<T>;
+    wave_steps<STAGES, true, kLoads, kStageBytes>(
+        lds + wave * STAGES * kStageBytes, wave * steps / NW, (wave + 1) * steps / NW,
+        [&](int t, bool live, lds_char *buf) {
+            const int k0 = live ? t * kStep<T> : K;
+            sa.issue(buf, 0, k0);
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                sbc.issue(
+                    buf + kABytes, 0, [&](int i) { return wp[i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, 0, lane) < K ? wleft[i] : 0; });
+            } else {
+                sbr.issue(buf + kABytes, 0, k0);
+            }
+        },
+        [](lds_char *) {},
+        [&](int, const lds_char *buf) {
+            step_products<T, 1, NT, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, lane);
+        });
+    T *out = reinterpret_cast<T *>(a.out);
+    join_waves<NW, 1, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
+        if (r < rows) store_quad<T>(out + (row0 + r) * a.M, n0 + c, a.M, sum, a.vec != 0);
+    });
+}
+
+template <typename T, int NT, int NW, int STAGES>
+int matmul_few_launch(MatmulArgs a, bool b_col, hipStream_t st) {
+    a.slots = (a.N >> 4) + a.S;
+    a.ntiles = (a.M + 16 * NT - 1) / (16 * NT);
+    dim3 grid;
+    if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (b_col) timed_launch_ggl(true, (seg_matmul_few<T, NT, NW, STAGES, true>), grid, dim3(64 * NW), 0, st, a);
+    else timed_launch_ggl(true, (seg_matmul_few<T, NT, NW, STAGES, false>), grid, dim3(64 * NW), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
+int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
+    a.slots = (a.N >> __builtin_ctz(BM)) + a.S;
+    a.ntiles = (a.M + BN - 1) / BN;
+    dim3 grid;
+    if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    constexpr int kThreads = 64 * WM * WN;
+    if (b_col)
+        timed_launch_ggl(true, (seg_matmul<T, BM, BN, WM, WN, STAGES, true, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    else
+        timed_launch_ggl(true, (seg_matmul<T, BM, BN, WM, WN, STAGES, false, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+// Tile by the mean number of rows per segment.
+template <typename T>
+int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st) {
+    const int64_t mean = a.N / a.S;
+    if (!direct) {
+        if (mean <= 32) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
+        return matmul_launch<T, 128, 128, 2, 2, 2, false>(a, b_col, st);
+    }
+    if (mean <= 16) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
+    if (mean <= 32) return matmul_launch<T, 16, 128, 1, 4, 4, true>(a, b_col, st);
+    if (mean <= 96) return matmul_launch<T, 64, 128, 2, 2, 3, true>(a, b_col, st);
+    if constexpr (sizeof(T) == 2)
+        if (mean >= 384 && a.M > 128) return matmul_launch<T, 256, 256, 2, 4, 2, true>(a, b_col, st);
+    return matmul_launch<T, 128, 128, 2, 2, 2, true>(a, b_col, st);
+}
+
+}  // namespace segred
+
+using namespace segred;
+
+extern "C" int segred_matmul(const void *values, int32_t dtype, int64_t k, const int64_t *rows, int64_t value_rows,
+                             const void *weights, int32_t transpose, int64_t m, const int64_t *offsets,
+                             int64_t num_segments, int64_t num_rows, void *out, hipStream_t stream) {
+    const int64_t e = float_size(dtype);
+    if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (k < 1 || m < 1 || value_rows < 0 || num_segments < 0 || num_rows < 0) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!rows && value_rows < num_rows) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments > 0 && num_rows > 0 && (!values || !weights || !offsets || !out)) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (e == 0 || k > kMaxWidth || m > kMaxWidth) return SEGRED_ERR_UNSUPPORTED;
+    if (!aligned(values, e) || !aligned(weights, e) || !aligned(out, e) || !aligned(offsets, 8) || !aligned(rows, 8))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (too_large(value_rows, k, 4) || too_large(num_rows, m, 4) || too_large(num_segments, k * m, 4))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments == 0 || num_rows == 0) return SEGRED_OK;
+
+    MatmulArgs a{};
+    a.values = static_cast<const char *>(values);
+    a.rows = rows;
+    a.value_rows = value_rows;
+    a.weights = static_cast<const char *>(weights);
+    a.offsets = offsets;
+    a.S = num_segments;
+    a.N = num_rows;
+    a.K = k;
+    a.M = m;
+    a.out = out;
+    a.vec = (m % 4 == 0 && aligned(out, 4 * e)) ? 1 : 0;
+    const int64_t along = transpose ? k : m;  // the weights' contiguous axis
+    const bool direct = (k * e) % 16 == 0 && (along * e) % 16 == 0 && aligned(values, 16) && aligned(weights, 16);
+    switch (dtype) {
+    case SEGRED_BF16: return matmul_dispatch<__bf16>(a, !transpose, direct, stream);
+    case SEGRED_F16: return matmul_dispatch<_Float16>(a, !transpose, direct, stream);
+    default: return matmul_dispatch<float>(a, !transpose, direct, stream);
+    }
+}

@@ -1,0 +1,412 @@
+// tile.hpp -- matrix-core tiles shared by the products over segments: how an
+// operand tile lies in LDS, how it gets there, and how the waves multiply it.
+//
+// A workgroup computes a BM x BN tile of out = A B with a contraction axis k
+// that it walks in steps of kStep<T> elements (128 bytes).  One step of an
+// operand is staged in LDS in one of two forms:
+//
+//   row form   the operand's rows run along k in memory (x, and weights
+//              applied transposed): LDS row r holds the 128 bytes of row r.
+//              The 16-byte unit u of a row lies at place u ^ (r & 7), so that
+//              the 16 lanes of a fragment read, which ask for the same unit
+//              of 16 consecutive rows, spread over all banks.
+//   col form   the operand's rows run across k (weights applied from the
+//              right, both operands of a sum of outer products): LDS row k
+//              holds the W elements of step row k.  Blocks of 16 elements lie
+//              at place block ^ col_swizzle(k), for the same reason.
+//
+// Fragments follow v_mfma_f32_16x16x32_{bf16,f16} (a lane holds 8 consecutive
+// k of one row) and v_mfma_f32_16x16x4_f32 (one k; four of them are fed from
+// one 16-byte unit, so k is visited in another order, the same for both
+// operands).  A 16-bit fragment in col form is read with
+// ds_read_b64_tr_b16, which transposes 4 x 16 elements among 16 lanes.
+//
+// The first MFMA operand is B's fragment and the second A's, so that a lane
+// ends up with four consecutive columns of one output row and stores them as
+// one unit.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "wave.hpp"
+
+namespace segred {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(1))) const void global_void;
+
+template <typename T> constexpr int kStep = 128 / (int)sizeof(T);  // k elements of one step
+template <typename T> constexpr int kUnit = 16 / (int)sizeof(T);   // elements of a 16-byte unit
+
+// What a load beyond the operand's edge reads instead.
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ const char *zero_unit() { return reinterpret_cast<const char *>(&kZeros); }
+
+// 16 bytes per lane from global memory to LDS at `dst` + 16 * lane (dst is
+// wave-uniform), without passing through registers.
+__device__ __forceinline__ void load_to_lds(uint64_t src, lds_char *dst) {
+    __builtin_amdgcn_global_load_lds((global_void *)src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// Up to `n` leading elements of a 16-byte unit at any element boundary; the
+// others are zero and not touched (n <= 0: nothing is read).
+template <typename T>
+__device__ __forceinline__ u32x4 load_unit(uint64_t addr, int n) {
+    const char *src = reinterpret_cast<const char *>(addr);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (n >= kUnit<T>) {
+        __builtin_memcpy(&v, __builtin_assume_aligned(src, sizeof(T)), 16);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) v[j] = reinterpret_cast<const uint32_t *>(src)[j];
+    } else {
+        const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = 2 * j < n ? s[2 * j] : 0u, hi = 2 * j + 1 < n ? s[2 * j + 1] : 0u;
+            v[j] = lo | hi << 16;
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------- staging
+//
+// A stage object belongs to one thread and moves that thread's units of one
+// operand.  DIRECT: global_load_lds, for operands whose rows start on 16-byte
+// boundaries and hold whole units.  Otherwise the units pass through
+// registers (`v`) and commit() writes them after the step's products.
+
+// Row form: ROWS x 128 bytes, 8 rows per wave and load.
+template <typename T, int ROWS, int THREADS, bool DIRECT>
+struct RowStage {
+    static constexpr int kWaves = THREADS / 64;
+    static constexpr int kLoads = (ROWS / 8 + kWaves - 1) / kWaves;
+    static constexpr int kBytes = ROWS * 128;
+    uint64_t p[kLoads];  // address of this lane's unit of the row's first step
+    int left[kLoads];    // elements of the row from there on; <= 0: a row of zeros
+    u32x4 v[DIRECT ? 1 : kLoads];
+
+    // Row group of load i.  With fewer groups than waves the surplus waves
+    // fetch a group again (the same bytes to the same place), so that every
+    // wave has the same number of loads in flight.
+    static __device__ __forceinline__ int group(int i, int wave) { return (i * kWaves + wave) % (ROWS / 8); }
+
+    // row_ptr(r): start of tile row r, or null for a row of zeros.
+    template <typename F>
+    __device__ __forceinline__ void init(int wave, int lane, int K, F row_ptr) {
+        const int unit = ((lane & 7) ^ (lane >> 3)) * kUnit<T>;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const char *q = row_ptr(group(i, wave) * 8 + (lane >> 3));
+            p[i] = (uint64_t)q + (uint64_t)unit * sizeof(T);
+            left[i] = q ? K - unit : 0;
+        }
+    }
+    // The step that starts at element k0 of each row.
+    __device__ __forceinline__ void issue(lds_char *lds, int wave, int k0) {
+        const uint64_t zeros = (uint64_t)zero_unit();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint64_t q = p[i] + (uint64_t)k0 * sizeof(T);
+            if constexpr (DIRECT) {
+                load_to_lds(k0 < left[i] ? q : zeros, lds + group(i, wave) * 1024);
+            } else {
+                v[i] = load_unit<T>(q, left[i] - k0);
+            }
+        }
+    }
+    __device__ __forceinline__ void commit(lds_char *lds, int wave, int lane) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + group(i, wave) * 1024 + lane * 16) = v[i];
+        }
+    }
+};
+
+// Swizzle of the 16-element blocks of LDS row k in col form.
+template <typename T, int W>
+__device__ __forceinline__ int col_swizzle(int k) {
+    constexpr int kMask = (W / 16 < 8 ? W / 16 : 8) - 1;
+    static_assert((W / 16 & (W / 16 - 1)) == 0, "power of two blocks");
+    if constexpr (sizeof(T) == 2) return ((k & 3) | ((k >> 3) & 1) << 2) & kMask;
+    return ((k >> 2) & 3) & kMask;
+}
+
+// Col form: kStep<T> rows of W elements.
+template <typename T, int W, int THREADS, bool DIRECT>
+struct ColStage {
+    static constexpr int kWaves = THREADS / 64;
+    static constexpr int kUnits = W / kUnit<T>;                         // per LDS row
+    static constexpr int kGroups = kStep<T> * W * (int)sizeof(T) / 1024;  // wave loads of a step
+    static constexpr int kLoads = (kGroups + kWaves - 1) / kWaves;
+    static constexpr int kBytes = kStep<T> * W * (int)sizeof(T);
+    static constexpr int kSub = 16 / kUnit<T>;  // units of a block
+    u32x4 v[DIRECT ? 1 : kLoads];
+
+    static __device__ __forceinline__ int group(int i, int wave) { return (i * kWaves + wave) % kGroups; }
+    // Step row and element column of load i of this lane.
+    static __device__ __forceinline__ int row(int i, int wave, int lane) {
+        return (group(i, wave) * 64 + lane) / kUnits;
+    }
+    static __device__ __forceinline__ int col(int i, int wave, int lane) {
+        const int place = (group(i, wave) * 64 + lane) % kUnits;
+        const int block = (place / kSub) ^ col_swizzle<T, W>(row(i, wave, lane));
+        return (block * kSub + place % kSub) * kUnit<T>;
+    }
+    // src(i): address of load i's unit; left(i): how many elements of its row
+    // exist from there on (<= 0: none, zeros instead).
+    template <typename F, typename G>
+    __device__ __forceinline__ void issue(lds_char *lds, int wave, F src, G left) {
+        const uint64_t zeros = (uint64_t)zero_unit();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if constexpr (DIRECT) load_to_lds(left(i) > 0 ? src(i) : zeros, lds + group(i, wave) * 1024);
+            else v[i] = load_unit<T>(src(i), left(i));
+        }
+    }
+    __device__ __forceinline__ void commit(lds_char *lds, int wave, int lane) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + group(i, wave) * 1024 + lane * 16) = v[i];
+        }
+    }
+};
+
+// --------------------------------------------------------------- fragments
+
+// 8 k of one row (or 4 for float): k = 32 * ks + 8 * (lane / 16) + 0..7
+// (16 * ks + 4 * (lane / 16) + 0..3), row = r0 + lane % 16.
+__device__ __forceinline__ u32x4 row_frag(const lds_char *lds, int r0, int ks, int lane) {
+    const int off = (r0 + (lane & 15)) * 128 + (((ks * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
+    return *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(lds + off);
+}
+
+template <typename T, int W>
+__device__ __forceinline__ u32x4 col_frag(const lds_char *lds, int c0, int ks, int lane) {
+    constexpr int kRow = W * (int)sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        union {
+            s16x4 h[2];
+            u32x4 v;
+        } f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = ks * 32 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
+            const int off = k * kRow + (((c0 >> 4) ^ col_swizzle<T, W>(k)) << 5) + (lane & 3) * 8;
+            f.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(const_cast<lds_char *>(lds) + off));
+        }
+        return f.v;
+    } else {
+        u32x4 f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = ks * 16 + (lane >> 4) * 4 + j;
+            const int off = k * kRow + (((c0 >> 4) ^ col_swizzle<T, W>(k)) << 6) + (lane & 15) * 4;
+            f[j] = *reinterpret_cast<const __attribute__((address_space(3))) uint32_t *>(lds + off);
+        }
+        return f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4 mma(u32x4 b, u32x4 a, f32x4 c) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[j]), __uint_as_float(a[j]), c, 0, 0, 0);
+        return c;
+    } else if constexpr (__is_same(T, __bf16)) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+    }
+}
+
+// One step of a wave's MT x NT tile of 16 x 16 blocks: rows from m0, columns
+// from n0 of the workgroup's tile.
+template <typename T, int MT, int NT, bool A_COL, int AW, bool B_COL, int BW>
+__device__ __forceinline__ void step_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
+                                              int n0, int lane) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        u32x4 a[MT], b[NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if constexpr (A_COL) a[i] = col_frag<T, AW>(la, m0 + 16 * i, ks, lane);
+            else a[i] = row_frag(la, m0 + 16 * i, ks, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if constexpr (B_COL) b[j] = col_frag<T, BW>(lb, n0 + 16 * j, ks, lane);
+            else b[j] = row_frag(lb, n0 + 16 * j, ks, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = mma<T>(b[j], a[i], acc[i][j]);
+    }
+}
+
+// ------------------------------------------------------------- wave's own
+//
+// With few rows a workgroup's waves split the contraction instead of the
+// tile: each wave walks its steps [t0, t1) through LDS buffers of its own,
+// without meeting the others, and the accumulators are added at the end.
+
+// Waits until at most N of this wave's loads are in flight and its LDS reads
+// are done.
+template <int N>
+__device__ __forceinline__ void wait_own() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// issue(t, live, buf): start step t (zeros where not live); commit(buf): write
+// units held in registers; products(t, buf).
+template <int STAGES, bool DIRECT, int LOADS, int BYTES, typename I, typename C, typename P>
+__device__ __forceinline__ void wave_steps(lds_char *lds, int t0, int t1, I issue, C commit, P products) {
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) issue(t0 + i, t0 + i < t1, lds + i * BYTES);
+        int cur = 0, fill = STAGES - 1;
+        for (int t = t0; t < t1; ++t) {
+            wait_own<(STAGES - 2) * LOADS>();
+            issue(t + STAGES - 1, t + STAGES - 1 < t1, lds + fill * BYTES);
+            products(t, lds + cur * BYTES);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+        }
+        wait_own<0>();  // the last loads write zeros into LDS
+    } else {
+        if (t0 < t1) {
+            issue(t0, true, lds);
+            commit(lds);
+        }
+        for (int t = t0; t < t1; ++t) {
+            wave_lds_sync();
+            if (t + 1 < t1) issue(t + 1, true, lds);
+            products(t, lds + ((t - t0) & 1) * BYTES);
+            wave_lds_sync();
+            if (t + 1 < t1) commit(lds + ((t + 1 - t0) & 1) * BYTES);
+        }
+    }
+}
+
+// Adds the waves' accumulators in wave order and gives each quad of columns
+// to one thread: out(row, column, sum).  `lds` is the workgroup's, at least
+// NW * MT * NT KiB, and may be the step buffers.
+template <int NW, int MT, int NT, typename F>
+__device__ __forceinline__ void join_waves(lds_char *lds, const f32x4 (&acc)[MT][NT], int wave, int lane, F out) {
+    typedef __attribute__((address_space(3))) f32x4 lds_quad;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<lds_quad *>(lds + ((wave * MT + i) * NT + j) * 1024 + lane * 16) = acc[i][j];
+    __syncthreads();
+    for (int q = wave * 64 + lane; q < MT * NT * 64; q += NW * 64) {
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            sum += *reinterpret_cast<const lds_quad *>(lds + w * MT * NT * 1024 + q * 16);
+        const int block = q >> 6, l = q & 63;
+        out(block / NT * 16 + (l & 15), block % NT * 16 + (l >> 4) * 4, sum);
+    }
+}
+
+// ------------------------------------------------------------------ output
+
+// Four consecutive elements from column n of a row of `width` elements, each
+// rounded to T once.  VEC: the row starts on a 4-element boundary and its
+// width is a multiple of 4.
+template <typename T>
+__device__ __forceinline__ void store_quad(T *row, int64_t n, int64_t width, f32x4 c, bool vec) {
+    if (vec) {
+        if (n < width) {
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<f32x4 *>(row + n) = c;
+            } else {
+                typedef __attribute__((ext_vector_type(4))) T T4;
+                T4 q;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = (T)c[j];
+                *reinterpret_cast<T4 *>(row + n) = q;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < width) row[n + j] = (T)c[j];
+    }
+}
+
+// ------------------------------------------------------------- tile places
+
+// Waits until at most N of this wave's loads are in flight and meets the
+// other waves.  (A workgroup fence would wait for all of them.)
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The launch grid of `total` tiles and the tile index of a workgroup.  A
+// dimension of the grid may not pass 2^32 threads, so long grids are folded.
+constexpr int64_t kGridFold = int64_t(1) << 20;
+inline bool tile_grid(int64_t total, dim3 &grid) {
+    const int64_t y = (total + kGridFold - 1) / kGridFold;
+    if (y > 65535) return false;
+    grid = dim3((unsigned)(y > 1 ? kGridFold : total), (unsigned)y);
+    return true;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; this maps the launch index to a
+// tile index such that each XCD (with an L2 of its own) owns one contiguous
+// range of tiles.
+__device__ __forceinline__ int64_t xcd_tile(int64_t total) {
+    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (id >= total) return total;
+    const int64_t q = total >> 3, r = total & 7, x = id & 7, i = id >> 3;
+    return x * q + (x < r ? x : r) + i;
+}
+
+// The rows of segment s are cut into slots of 2^lg rows from the segment's
+// start.  Slot keys need no table: segment s owns the slots from
+// key(s) = (offsets[s] - offsets[0]) / 2^lg + s up to key(s + 1), which are at
+// least ceil(len / 2^lg) and at least one; what is over is empty.  There are
+// (offsets[S] - offsets[0]) / 2^lg + S slots in all.
+__device__ __forceinline__ int64_t slot_key(const int64_t *offsets, int64_t s, int lg) {
+    return ((offsets[s] - offsets[0]) >> lg) + s;
+}
+
+// The segment of `slot`, found with 64 probes a round (every lane must call it).
+__device__ __forceinline__ int64_t slot_segment(const int64_t *offsets, int64_t S, int lg, int64_t slot, int lane) {
+    int64_t lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int64_t d = (hi - lo + 63) >> 6;
+        const int64_t s = lo + lane * d;
+        bool below = false;
+        if (s < hi) below = slot_key(offsets, s, lg) <= slot;
+        const int n = popc64(ballot(below));
+        lo += (n > 0 ? n - 1 : 0) * d;
+        hi = hi < lo + d ? hi : lo + d;
+    }
+    return readfirst(lo);
+}
+
+}  // namespace segred
