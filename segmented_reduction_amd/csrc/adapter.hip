@@ -56,8 +56,8 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
     if (id >= a.slots * a.blocks) return;
     const int64_t slot = id / a.blocks, block = id - slot * a.blocks;
     const int r0 = (int)block * kRankBlock;
-    const int64_t s = slot_segment(a.offsets, a.S, kLg, slot, lane);
-    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, kLg)) << kLg);
+    const int64_t s = tight_segment(a.offsets, a.S, kLg, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - tight_key(a.offsets, s, kLg)) << kLg);
     const int64_t end = min(a.offsets[s + 1], a.N);
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)BM, end - row0);
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
             else sbr.commit(buf + kABytes, 0, lane);
         },
         [&](int, const lds_char *buf) {
-            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, lane);
+            step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, MT, NT, lane);
         });
     const float scale = a.scale ? a.scale[adapter] : 1.f;
     join_waves<NW, MT, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
@@ -268,11 +268,9 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     const int64_t total = a.mtiles * a.ntiles;
     const int64_t id = xcd_tile(total);
     if (id >= total) return;
-    constexpr int kGroup = 4;
-    const int64_t group = id / (kGroup * a.ntiles), in_group = id - group * kGroup * a.ntiles;
-    const int64_t gm = min((int64_t)kGroup, a.mtiles - group * kGroup);
-    const int64_t row0 = a.offsets[0] + (group * kGroup + in_group % gm) * BM;
-    const int64_t n0 = in_group / gm * BN;
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    const int64_t row0 = a.offsets[0] + at.m * BM;
+    const int64_t n0 = at.n * BN;
     const int64_t end = min(a.offsets[a.S], a.N);
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)BM, end - row0);
@@ -339,7 +337,7 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
         if (__is_same(T, _Float16) && t >= base)
             split_products<MT, NT, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
         else
-            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+            step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, MT, NT, lane);
         if (t + 1 < steps) commit(next);
     }
 
@@ -354,6 +352,180 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
                 store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
         }
     }
+}
+
+// Many rows: AH * 128 rows x 256 columns per workgroup, in phases (16-bit
+// types, whole units).
+template <typename T, int AH, bool B_COL>
+__global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a) {
+    using AStage = RowStage<T, kHalf, kPhaseThreads, true>;
+    using BRow = RowStage<T, kHalf, kPhaseThreads, true>;
+    using BCol = ColStage<T, kHalf, kPhaseThreads, true>;
+    constexpr int BM = AH * kHalf;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    __shared__ int s_ids[BM], s_list[BM], s_count;
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t total = a.mtiles * a.ntiles;
+    const int64_t id = xcd_tile(total);
+    if (id >= total) return;
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    const int64_t row0 = a.offsets[0] + at.m * BM;
+    const int64_t n0 = at.n * (2 * kHalf);
+    const int64_t end = min(a.offsets[a.S], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)BM, end - row0);
+    const int K = (int)a.K, R = (int)a.R;
+    const int met = tile_adapters<BM, kPhaseThreads>(a, row0, rows, s_ids, s_list, &s_count);
+
+    AStage sa[AH];
+#pragma unroll
+    for (int h = 0; h < AH; ++h)
+        sa[h].init(wave, lane, K, [&](int r) -> const char * {
+            r += h * kHalf;
+            return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    BRow sbr[2];
+    BCol sbc;
+    uint64_t wp[2][BCol::kLoads];
+    int wleft[2][BCol::kLoads];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (B_COL) {
+#pragma unroll
+            for (int i = 0; i < BCol::kLoads; ++i) {
+                const int64_t n = n0 + h * kHalf + BCol::col(i, wave, lane);
+                wp[h][i] = (uint64_t)(a.weights + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+                wleft[h][i] = (int)(a.M - n);
+            }
+        } else {
+            sbr[h].init(wave, lane, K, [&](int r) -> const char * {
+                const int64_t n = n0 + h * kHalf + r;
+                return n < a.M ? a.weights + n * a.K * (int64_t)sizeof(T) : nullptr;
+            });
+        }
+    }
+    f32x4 acc[2][2][4][2] = {};
+    phase_steps<T, AH, false, B_COL>(
+        acc, lds, (K + kStep<T> - 1) / kStep<T>, wave, lane,
+        [&](int h, int t, lds_char *place) { sa[h].issue(place, wave, t * kStep<T>); },
+        [&](int h, int t, lds_char *place) {
+            const int k0 = t * kStep<T>;
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                sbc.issue(
+                    place, wave, [&](int i) { return wp[h][i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[h][i] : 0; });
+            } else {
+                sbr[h].issue(place, wave, k0);
+            }
+        },
+        [](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); },
+        [](int) {});
+    __syncthreads();
+
+    // the adapters met in the tile, 32 ranks a step
+    const int blocks = (int)a.blocks, extra = met * blocks;
+    const int unit = (lane & 7) ^ (lane >> 3);
+    auto adapter_of = [&](int t, int &block) {
+        const int e = t / blocks;
+        block = t - e * blocks;
+        return __builtin_amdgcn_readfirstlane(s_list[e]);
+    };
+    auto fetch_u = [&](int h, int t, lds_char *place) {
+        int block = 0;
+        const int adapter = t < extra ? adapter_of(t, block) : -2;  // past the last step: zeros
+#pragma unroll
+        for (int i = 0; i < AStage::kLoads; ++i) {
+            const int g = AStage::group(i, wave), r = h * kHalf + g * 8 + (lane >> 3);
+            const uint64_t q = (uint64_t)(a.u + ((row0 + r) * a.blocks + block) * 128 + unit * 16);
+            load_to_lds(s_ids[r] == adapter ? q : (uint64_t)zero_unit(), place + g * 1024);
+        }
+    };
+    auto fetch_second = [&](int h, int t, lds_char *place) {
+        int block = 0;
+        const int adapter = t < extra ? adapter_of(t, block) : -1;
+        const int have = adapter >= 0 ? R - block * kRankBlock : 0;  // ranks of this step
+        const char *w = a.second + ((int64_t)max(adapter, 0) * a.M * a.R) * (int64_t)sizeof(T);
+        constexpr int kMask = kRankBlock - 1;
+        if constexpr (B_COL) {
+            auto rank = [&](int i) { return BCol::row(i, wave, lane) & kMask; };
+            auto col = [&](int i) { return n0 + h * kHalf + BCol::col(i, wave, lane); };
+            sbc.issue(
+                place, wave,
+                [&](int i) { return (uint64_t)(w + ((block * kRankBlock + rank(i)) * a.M + col(i)) * (int64_t)sizeof(T)); },
+                [&](int i) { return rank(i) < have ? (int)(a.M - col(i)) : 0; });
+        } else {
+            const int rank = (unit * kUnit<T>) & kMask;
+#pragma unroll
+            for (int i = 0; i < BRow::kLoads; ++i) {
+                const int g = BRow::group(i, wave);
+                const int64_t n = n0 + h * kHalf + g * 8 + (lane >> 3);
+                const uint64_t q = (uint64_t)(w + (n * a.R + block * kRankBlock + rank) * (int64_t)sizeof(T));
+                load_to_lds(n < a.M && rank < have ? q : (uint64_t)zero_unit(), place + g * 1024);
+            }
+        }
+    };
+    auto products = [&](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) {
+        if constexpr (__is_same(T, _Float16)) {
+            // bf16 halves of u against the two bf16 that a float16 is the sum
+            // of; y[.][1] holds the same ranks again, so wait for it here
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f16x8 h = __builtin_bit_cast(f16x8, y[j][0]);
+                bf16x8 hi, lo;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    hi[e] = (__bf16)(float)h[e];
+                    lo[e] = (__bf16)((float)h[e] - (float)hi[e]);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bf16x8 v = __builtin_bit_cast(bf16x8, x[i][ks]);
+                        c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, v, c[i][j], 0, 0, 0);
+                        c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, v, c[i][j], 0, 0, 0);
+                    }
+            }
+        } else {
+            quadrant<T>(c, x, y);
+        }
+    };
+    if (extra > 0)
+        phase_steps<T, AH, false, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products, [](int) {});
+
+    T *out = reinterpret_cast<T *>(a.out);
+#pragma unroll
+    for (int p = 0; p < AH; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = phase_row(p, i, wave) + (lane & 15);
+            if (r >= rows) continue;
+            T *row = out + (row0 + r) * a.M;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    store_quad<T>(row, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, a.M, acc[p][q][i][j], a.vec != 0);
+        }
+}
+
+template <typename T, int AH>
+int adapter_many_launch(AdapterArgs a, bool b_col, hipStream_t st) {
+    a.mtiles = (a.N + AH * kHalf - 1) / (AH * kHalf);
+    a.ntiles = (a.M + 2 * kHalf - 1) / (2 * kHalf);
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if constexpr (AH == 1)
+        if (b_col) {
+            timed_launch_ggl(true, (adapter_main_many<T, 1, true>), grid, dim3(kPhaseThreads), 0, st, a);
+            return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+        }
+    timed_launch_ggl(true, (adapter_main_many<T, AH, false>), grid, dim3(kPhaseThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
@@ -371,7 +543,7 @@ int adapter_main_launch(AdapterArgs a, bool b_col, hipStream_t st) {
 template <typename T, int MT, bool DIRECT>
 int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     constexpr int NW = 4, STAGES = DIRECT ? 3 : 2;
-    a.slots = (a.N >> __builtin_ctz(16 * MT)) + a.S;
+    a.slots = tight_slots(a.N, a.S, __builtin_ctz(16 * MT));
     dim3 grid;
     if (!tile_grid(a.slots * a.blocks, grid)) return SEGRED_ERR_UNSUPPORTED;
     if (b_col) timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, true, DIRECT>), grid, dim3(64 * NW), 0, st, a);
@@ -385,7 +557,13 @@ int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool mai
     if (rc != SEGRED_OK) return rc;
     if (!main_direct) return adapter_main_launch<T, 64, 64, 2, 2, false>(a, b_col, st);
     if constexpr (sizeof(T) == 2)
-        if (a.N >= 1024 && a.M >= 256) return adapter_main_launch<T, 256, 256, 2, 4, true>(a, b_col, st);
+        if (a.N >= 512 && a.M >= 256) {
+            // a tile of 256 rows takes about 7/4 of one of 128; whole rounds of 256 CUs
+            const int64_t nt = (a.M + 255) / 256;
+            const int64_t one = ((a.N + 127) / 128 * nt + 255) / 256, two = ((a.N + 255) / 256 * nt + 255) / 256;
+            if (b_col || 4 * one < 7 * two) return adapter_many_launch<T, 1>(a, b_col, st);
+            return adapter_many_launch<T, 2>(a, b_col, st);
+        }
     return adapter_main_launch<T, 64, 64, 2, 2, true>(a, b_col, st);
 }
 

@@ -1,6 +1,7 @@
 // matmul.hip -- the matrix product of each segment's rows with weights of its
 // own: out[r] = values[r] W[s] for the rows r of segment s.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
@@ -18,8 +19,6 @@ struct MatmulArgs {
     void *out;
     int vec;
 };
-
-constexpr int kSlotGroup = 4;  // row tiles that walk the column tiles together
 
 // One BM x BN tile of one segment per workgroup.
 template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
@@ -41,13 +40,12 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t id = xcd_tile(a.slots * a.ntiles);
     if (id >= a.slots * a.ntiles) return;
-    const int64_t group = id / (kSlotGroup * a.ntiles), in_group = id - group * kSlotGroup * a.ntiles;
-    const int64_t gm = min((int64_t)kSlotGroup, a.slots - group * kSlotGroup);
-    const int64_t slot = group * kSlotGroup + in_group % gm;
-    const int64_t n0 = in_group / gm * BN;
+    const TilePlace at = tile_place(id, a.slots, a.ntiles);
+    const int64_t slot = at.m;
+    const int64_t n0 = at.n * BN;
 
-    const int64_t s = slot_segment(a.offsets, a.S, kLg, slot, lane);
-    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, kLg)) << kLg);
+    const int64_t s = tight_segment(a.offsets, a.S, kLg, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - tight_key(a.offsets, s, kLg)) << kLg);
     const int64_t end = min(a.offsets[s + 1], a.N);
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)BM, end - row0);
@@ -97,45 +95,160 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
     };
 
     f32x4 acc[MT][NT] = {};
-    const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+    constexpr bool kDeal = kDealt<T>;
+    constexpr int MS = kDeal ? 16 * WM : 16, NS = kDeal ? 16 * WN : 16;
+    const int m_w = wave / WN * (kDeal ? 16 : 16 * MT), n_w = wave % WN * (kDeal ? 16 : 16 * NT);
+    const int mv = blocks_inside(rows, m_w, MS, MT), nv = blocks_inside(a.M - n0, n_w, NS, NT);
     const int steps = (K + kStep<T> - 1) / kStep<T>;
-    if constexpr (DIRECT) {
+    auto walk = [&](auto full) {
+        auto products = [&](const lds_char *buf) {
+            step_products<T, decltype(full)::value, MT, NT, MS, NS, false, BM, B_COL, BN>(
+                acc, buf, buf + kABytes, m_w, n_w, mv, nv, lane);
+        };
+        if constexpr (DIRECT) {
 #pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
-        int cur = 0, fill = STAGES - 1;
-        for (int t = 0; t < steps; ++t) {
-            wait_and_meet<(STAGES - 2) * kLoads>();
-            issue(t + STAGES - 1, lds + fill * kStageBytes);
-            const lds_char *buf = lds + cur * kStageBytes;
-            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
-            cur = cur + 1 == STAGES ? 0 : cur + 1;
-            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
+            int cur = 0, fill = STAGES - 1;
+            for (int t = 0; t < steps; ++t) {
+                wait_and_meet<(STAGES - 2) * kLoads>();
+                issue(t + STAGES - 1, lds + fill * kStageBytes);
+                products(lds + cur * kStageBytes);
+                cur = cur + 1 == STAGES ? 0 : cur + 1;
+                fill = fill + 1 == STAGES ? 0 : fill + 1;
+            }
+            // the last loads write zeros into LDS; they must land before it is given away
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+            issue(0, lds);
+            commit(lds);
+            for (int t = 0; t < steps; ++t) {
+                __syncthreads();
+                if (t + 1 < steps) issue(t + 1, lds);
+                products(lds + (t & 1) * kStageBytes);
+                if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
+            }
         }
-        // the last loads write zeros into LDS; they must land before it is given away
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    } else {
-        issue(0, lds);
-        commit(lds);
-        for (int t = 0; t < steps; ++t) {
-            __syncthreads();
-            if (t + 1 < steps) issue(t + 1, lds);
-            const lds_char *buf = lds + (t & 1) * kStageBytes;
-            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
-            if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
-        }
-    }
+    };
+    if (!kDeal || (rows == BM && a.M - n0 >= BN)) walk(std::true_type{});
+    else if constexpr (kDeal) walk(std::false_type{});
 
     T *out = reinterpret_cast<T *>(a.out);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int r = m_w + 16 * i + (lane & 15);
+        const int r = m_w + MS * i + (lane & 15);
         if (r < rows) {
             T *row = out + (row0 + r) * a.M;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+                store_quad<T>(row, n0 + n_w + NS * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
         }
     }
+}
+
+// Many rows per segment: AH * 128 rows x 256 columns per workgroup, in phases.
+// A tile of at most 128 rows walks the steps of one half only.
+template <typename T, int AH, bool B_COL>
+__global__ __launch_bounds__(kPhaseThreads) void seg_matmul_many(MatmulArgs a) {
+    using AStage = RowStage<T, kHalf, kPhaseThreads, true>;
+    using BRow = RowStage<T, kHalf, kPhaseThreads, true>;
+    using BCol = ColStage<T, kHalf, kPhaseThreads, true>;
+    constexpr int kLg = AH == 2 ? 8 : 7;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return;
+    const TilePlace at = tile_place(id, a.slots, a.ntiles);
+    const int64_t slot = at.m;
+    const int64_t n0 = at.n * (2 * kHalf);
+    const int64_t s = tight_segment(a.offsets, a.S, kLg, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - tight_key(a.offsets, s, kLg)) << kLg);
+    const int64_t end = min(a.offsets[s + 1], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)(AH * kHalf), end - row0), K = (int)a.K;
+
+    AStage sa[AH];
+#pragma unroll
+    for (int h = 0; h < AH; ++h)
+        sa[h].init(wave, lane, K, [&](int r) -> const char * {
+            r += h * kHalf;
+            if (r >= rows) return nullptr;
+            int64_t v = row0 + r;
+            if (a.rows) v = a.rows[v];
+            if (v < 0 || v >= a.value_rows) return nullptr;
+            return a.values + v * a.K * (int64_t)sizeof(T);
+        });
+    const char *w = a.weights + s * a.K * a.M * (int64_t)sizeof(T);
+    BRow sbr[2];
+    BCol sbc;
+    uint64_t wp[2][BCol::kLoads];
+    int wleft[2][BCol::kLoads];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (B_COL) {
+#pragma unroll
+            for (int i = 0; i < BCol::kLoads; ++i) {
+                const int64_t n = n0 + h * kHalf + BCol::col(i, wave, lane);
+                wp[h][i] = (uint64_t)(w + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+                wleft[h][i] = (int)(a.M - n);
+            }
+        } else {
+            sbr[h].init(wave, lane, K, [&](int r) -> const char * {
+                const int64_t n = n0 + h * kHalf + r;
+                return n < a.M ? w + n * a.K * (int64_t)sizeof(T) : nullptr;
+            });
+        }
+    }
+    f32x4 acc[2][2][4][2] = {};
+    auto fetch_a = [&](int h, int t, lds_char *place) { sa[h].issue(place, wave, t * kStep<T>); };
+    auto fetch_b = [&](int h, int t, lds_char *place) {
+        const int k0 = t * kStep<T>;
+        if constexpr (B_COL) {
+            const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+            sbc.issue(
+                place, wave, [&](int i) { return wp[h][i] + step; },
+                [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[h][i] : 0; });
+        } else {
+            sbr[h].issue(place, wave, k0);
+        }
+    };
+    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+    const int steps = (K + kStep<T> - 1) / kStep<T>;
+    if (AH == 2 && rows > kHalf)
+        phase_steps<T, AH, false, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products, [](int) {});
+    else
+        phase_steps<T, 1, false, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products, [](int) {});
+
+    T *out = reinterpret_cast<T *>(a.out);
+#pragma unroll
+    for (int p = 0; p < AH; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = phase_row(p, i, wave) + (lane & 15);
+            if (r >= rows) continue;
+            T *row = out + (row0 + r) * a.M;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    store_quad<T>(row, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, a.M, acc[p][q][i][j], a.vec != 0);
+        }
+}
+
+template <typename T, int AH>
+int matmul_many_launch(MatmulArgs a, bool b_col, hipStream_t st) {
+    a.slots = tight_slots(a.N, a.S, AH == 2 ? 8 : 7);
+    a.ntiles = (a.M + 2 * kHalf - 1) / (2 * kHalf);
+    dim3 grid;
+    if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if constexpr (AH == 1)
+        if (b_col) {
+            timed_launch_ggl(true, (seg_matmul_many<T, 1, true>), grid, dim3(kPhaseThreads), 0, st, a);
+            return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+        }
+    timed_launch_ggl(true, (seg_matmul_many<T, AH, false>), grid, dim3(kPhaseThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 // Few rows per segment: 16 rows x 16 NT columns per workgroup, the
@@ -155,8 +268,8 @@ __global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
     const int64_t id = xcd_tile(a.slots * a.ntiles);
     if (id >= a.slots * a.ntiles) return;
     const int64_t slot = id / a.ntiles, n0 = (id - slot * a.ntiles) * (16 * NT);
-    const int64_t s = slot_segment(a.offsets, a.S, 4, slot, lane);
-    const int64_t row0 = a.offsets[s] + ((slot - slot_key(a.offsets, s, 4)) << 4);
+    const int64_t s = tight_segment(a.offsets, a.S, 4, slot, lane);
+    const int64_t row0 = a.offsets[s] + ((slot - tight_key(a.offsets, s, 4)) << 4);
     const int64_t end = min(a.offsets[s + 1], a.N);
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)16, end - row0);
@@ -205,7 +318,7 @@ __global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
         },
         [](lds_char *) {},
         [&](int, const lds_char *buf) {
-            step_products<T, 1, NT, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, lane);
+            step_products<T, true, 1, NT, 16, 16, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, 1, NT, lane);
         });
     T *out = reinterpret_cast<T *>(a.out);
     join_waves<NW, 1, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
@@ -215,7 +328,7 @@ __global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
 
 template <typename T, int NT, int NW, int STAGES>
 int matmul_few_launch(MatmulArgs a, bool b_col, hipStream_t st) {
-    a.slots = (a.N >> 4) + a.S;
+    a.slots = tight_slots(a.N, a.S, 4);
     a.ntiles = (a.M + 16 * NT - 1) / (16 * NT);
     dim3 grid;
     if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
@@ -226,7 +339,7 @@ int matmul_few_launch(MatmulArgs a, bool b_col, hipStream_t st) {
 
 template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
 int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
-    a.slots = (a.N >> __builtin_ctz(BM)) + a.S;
+    a.slots = tight_slots(a.N, a.S, __builtin_ctz(BM));
     a.ntiles = (a.M + BN - 1) / BN;
     dim3 grid;
     if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
@@ -238,20 +351,43 @@ int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
-// Tile by the mean number of rows per segment.
+// The kernel for a call, by its mean rows per segment and the number of tiles.
+// Times in us of bfloat16 products of 64 segments, 2,048 x 2,048, whose mean
+// rows are given (uneven; weights from HBM; "row" is a transposed weight):
+//
+//   mean          4    16    32    64   128   256   512
+//   few         101   133   214   378                     row
+//   64 x 128    139   131   137   160   183   273   452   row
+//   256 x 256               153   154   168   225   343   row
+//   128 x 256               153   153   175   234   367   row
+//   few         112   153   230   380                     col
+//   64 x 128    110   104   111   145   185   292   488   col
+//   128 x 256               195   167   198   290   479   col
+//
+// and with few tiles (8 segments, 2,048 x 1,024): 64 x 128 takes 24 us at 256
+// rows and 51 at 1,024, 128 x 256 takes 34 and 67, 256 x 256 49 and 53.
+constexpr int64_t kFewRows = 8, kManyRows = 96, kManyColRows = 256, kManyTiles = 1536;
 template <typename T>
 int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st) {
     const int64_t mean = a.N / a.S;
     if (!direct) {
-        if (mean <= 32) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
-        return matmul_launch<T, 128, 128, 2, 2, 2, false>(a, b_col, st);
+        if (mean <= 2 * kFewRows) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
+        return matmul_launch<T, 64, 128, 2, 2, 2, false>(a, b_col, st);
     }
-    if (mean <= 16) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
-    if (mean <= 32) return matmul_launch<T, 16, 128, 1, 4, 4, true>(a, b_col, st);
-    if (mean <= 96) return matmul_launch<T, 64, 128, 2, 2, 3, true>(a, b_col, st);
-    if constexpr (sizeof(T) == 2)
-        if (mean >= 384 && a.M > 128) return matmul_launch<T, 256, 256, 2, 4, 2, true>(a, b_col, st);
-    return matmul_launch<T, 128, 128, 2, 2, 2, true>(a, b_col, st);
+    if (mean <= kFewRows) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
+    if constexpr (sizeof(T) == 2) {
+        // 64 x 128 tiles, half a tile more per segment for its end
+        const int64_t tiles = (a.N / 64 + a.S / 2) * ((a.M + 127) / 128);
+        if (a.K >= 256 && a.M > 128 && tiles >= kManyTiles && mean >= (b_col ? kManyColRows : kManyRows)) {
+            // a tile of 256 rows takes about 7/4 of one of 128; whole rounds of 256 CUs
+            const int64_t nt = (a.M + 255) / 256;
+            const int64_t one = ((a.N / 128 + a.S / 2) * nt + 255) / 256, two = ((a.N / 256 + a.S / 2) * nt + 255) / 256;
+            if (b_col || 4 * one < 7 * two) return matmul_many_launch<T, 1>(a, b_col, st);
+            return matmul_many_launch<T, 2>(a, b_col, st);
+        }
+        return matmul_launch<T, 64, 128, 2, 2, 2, true>(a, b_col, st);
+    }
+    return matmul_launch<T, 64, 64, 2, 2, 2, true>(a, b_col, st);
 }
 
 }  // namespace segred

@@ -2,11 +2,14 @@
 // out[s] = sum over the rows r of segment s of left[r]^T right[r], the
 // gradient of the weights of a product over segments.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
 
 namespace segred {
+
+constexpr int64_t kWhole = int64_t(1) << 62;  // more rows than there are
 
 struct OuterArgs {
     const char *left, *right;
@@ -15,11 +18,91 @@ struct OuterArgs {
     const int64_t *offsets;
     int64_t S, N, K, M;
     int64_t slots, mtiles, ntiles;
-    int lg;         // a slot is 2^lg rows of a segment
+    int64_t step;   // a slot is this many rows of a segment, or the whole segment (kWhole)
     void *out;      // T or float [S, K, M]
     float *partial;  // [slots, K, M], when a segment may have more than one slot
     int out_f32, vec;
 };
+
+// What a workgroup computes: a tile of one slot's sum.
+struct OuterPlace {
+    int64_t s, slot, row0, rows, m0, n0;
+    bool work;  // false: nothing to store
+};
+
+// A tile's work grows with its segment's rows, so where every segment is one
+// slot, up to 64 long ones are taken longest first and the longest tiles do not
+// begin last (8,192 rows in 8 uneven segments of 2,560 x 1,024: 184 -> 88 us).
+// Up to 16 segments are spread over all XCDs (workgroups are dealt to these in
+// turn), each with one contiguous range of the segment's tiles; more are dealt
+// to the XCDs forth and back, whole, so that the rows of a segment are read into
+// one L2 only.  Short segments are left in their order: finding the rank takes
+// about half a microsecond.
+constexpr int kRanked = 64, kSpread = 16, kRankedRows = 256;
+__host__ __device__ inline bool outer_ranked(const OuterArgs &a) {
+    return a.step == kWhole && a.S <= kRanked && a.N >= a.S * kRankedRows;
+}
+__device__ __forceinline__ OuterPlace outer_place(const OuterArgs &a, int bm, int bn, int lane) {
+    OuterPlace o{};
+    const int64_t per = a.mtiles * a.ntiles;
+    int64_t tile, piece = 0;
+    if (outer_ranked(a)) {
+        const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        int64_t rank;
+        if (a.S <= kSpread) {
+            rank = id / per;
+            const int64_t in = id - rank * per, q = per >> 3, r = per & 7, x = in & 7;
+            tile = x * q + (x < r ? x : r) + (in >> 3);
+        } else {
+            const int64_t x = id & 7, i = id >> 3, turn = i / per;
+            rank = turn * 8 + (turn & 1 ? 7 - x : x);
+            tile = i - turn * per;
+        }
+        if (rank >= a.S) return o;
+        // length (cut off at 2^25) and lane in one word, all different
+        const int64_t len = lane < a.S ? a.offsets[lane + 1] - a.offsets[lane] : -1;
+        const uint32_t word = len < 0 ? 63u - lane : (uint32_t)min(len, (int64_t)(1 << 25) - 1) << 6 | (63u - lane);
+        int above = 0;
+        for (int i = 0; i < (int)a.S; ++i) above += (uint32_t)__builtin_amdgcn_readlane((int)word, i) > word ? 1 : 0;
+        o.s = __builtin_ctzll(ballot(lane < a.S && above == (int)rank));
+        o.slot = o.s;
+    } else {
+        const int64_t total = a.slots * per, id = xcd_tile(total);
+        if (id >= total) return o;
+        o.slot = id / per;
+        tile = id - o.slot * per;
+        if (a.step == kWhole) {
+            o.s = o.slot;
+        } else {
+            o.s = slot_segment(a.S, o.slot, lane, [&](int64_t s) { return slot_key(a.offsets, s, a.step); });
+            piece = o.slot - slot_key(a.offsets, o.s, a.step);
+        }
+    }
+    const TilePlace p = tile_place(tile, a.mtiles, a.ntiles);
+    o.m0 = p.m * bm;
+    o.n0 = p.n * bn;
+    o.row0 = a.offsets[o.s] + piece * (a.step == kWhole ? 0 : a.step);
+    const int64_t end = min(a.offsets[o.s + 1], a.N);
+    o.rows = o.row0 < 0 ? 0 : max((int64_t)0, min(a.step, end - o.row0));
+    o.work = o.rows > 0 || (piece == 0 && !a.partial);
+    return o;
+}
+// Workgroups of that order.
+int64_t outer_tiles(const OuterArgs &a) {
+    const int64_t per = a.mtiles * a.ntiles;
+    return (outer_ranked(a) && a.S > kSpread ? (a.S + 7) / 8 * 8 : a.slots) * per;
+}
+
+// Four sums of row r from column n: a partial one of the slot, or the result.
+template <typename T>
+__device__ __forceinline__ void outer_store(const OuterArgs &a, int64_t s, int64_t slot, int64_t r, int64_t n, f32x4 c) {
+    if (a.partial)
+        store_quad<float>(a.partial + (slot * a.K + r) * a.M, n, a.M, c, a.vec != 0);
+    else if (a.out_f32)
+        store_quad<float>(static_cast<float *>(a.out) + (s * a.K + r) * a.M, n, a.M, c, a.vec != 0);
+    else
+        store_quad<T>(static_cast<T *>(a.out) + (s * a.K + r) * a.M, n, a.M, c, a.vec != 0);
+}
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
@@ -32,18 +115,9 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
     lds_char *lds = (lds_char *)lds_mem;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t total = a.slots * a.mtiles * a.ntiles;
-    const int64_t id = xcd_tile(total);
-    if (id >= total) return;
-    const int64_t slot = id / (a.mtiles * a.ntiles), tile = id - slot * a.mtiles * a.ntiles;
-    const int64_t m0 = tile / a.ntiles * BM, n0 = tile % a.ntiles * BN;
-
-    const int64_t s = slot_segment(a.offsets, a.S, a.lg, slot, lane);
-    const int64_t piece = slot - slot_key(a.offsets, s, a.lg);
-    const int64_t row0 = a.offsets[s] + (piece << a.lg);
-    const int64_t end = min(a.offsets[s + 1], a.N);
-    const int64_t rows = row0 < 0 ? 0 : max((int64_t)0, min(int64_t(1) << a.lg, end - row0));
-    if (rows == 0 && (piece > 0 || a.partial)) return;
+    const OuterPlace at = outer_place(a, BM, BN, lane);
+    if (!at.work) return;
+    const int64_t s = at.s, slot = at.slot, row0 = at.row0, rows = at.rows, m0 = at.m0, n0 = at.n0;
 
     SA sa;
     SB sb;
@@ -76,9 +150,12 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
     };
 
     f32x4 acc[MT][NT] = {};
-    const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+    constexpr bool kDeal = kDealt<T>;
+    constexpr int MS = kDeal ? 16 * WM : 16, NS = kDeal ? 16 * WN : 16;
+    const int m_w = wave / WN * (kDeal ? 16 : 16 * MT), n_w = wave % WN * (kDeal ? 16 : 16 * NT);
+    const int mv = blocks_inside(a.K - m0, m_w, MS, MT), nv = blocks_inside(a.M - n0, n_w, NS, NT);
     const int64_t steps = (rows + kStep<T> - 1) / kStep<T>;
-    if (steps > 0) {
+    auto walk = [&](auto full) {
         fetch(0);
         issue(lds);
         fetch(kStep<T>);
@@ -91,56 +168,174 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
                 fetch((t + 2) * kStep<T>);
             }
             const lds_char *buf = lds + (t & 1) * kStageBytes;
-            step_products<T, MT, NT, true, BM, true, BN>(acc, buf, buf + SA::kBytes, m_w, n_w, lane);
+            step_products<T, decltype(full)::value, MT, NT, MS, NS, true, BM, true, BN>(
+                acc, buf, buf + SA::kBytes, m_w, n_w, mv, nv, lane);
             if (t + 1 < steps) commit(next);
         }
+    };
+    if (steps > 0) {
+        if (!kDeal || (a.K - m0 >= BM && a.M - n0 >= BN)) walk(std::true_type{});
+        else if constexpr (kDeal) walk(std::false_type{});
     }
 
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int64_t r = m0 + m_w + 16 * i + (lane & 15);
+        const int64_t r = m0 + m_w + MS * i + (lane & 15);
         if (r >= a.K) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int64_t n = n0 + n_w + 16 * j + (lane >> 4) * 4;
-            if (a.partial)
-                store_quad<float>(a.partial + (slot * a.K + r) * a.M, n, a.M, acc[i][j], a.vec != 0);
-            else if (a.out_f32)
-                store_quad<float>(static_cast<float *>(a.out) + (s * a.K + r) * a.M, n, a.M, acc[i][j], a.vec != 0);
-            else
-                store_quad<T>(static_cast<T *>(a.out) + (s * a.K + r) * a.M, n, a.M, acc[i][j], a.vec != 0);
+            outer_store<T>(a, s, slot, r, n0 + n_w + NS * j + (lane >> 4) * 4, acc[i][j]);
         }
     }
 }
 
-// Sums the slots of each segment in slot order and rounds once.
-constexpr int kJoinThreads = 256;
+// Wide operands: 128 x 256 of the output per workgroup, in phases (16-bit
+// types, whole units).  The contraction runs over the segment's rows.  Their
+// source rows are kept in LDS as byte offsets (-1: a row of zeros), four steps
+// ahead of their fetch, so that gathered rows cost no wait.
+constexpr int kRing = 8;  // steps of source rows kept, a power of two
+
 template <typename T>
-__global__ __launch_bounds__(kJoinThreads) void outer_join(OuterArgs a) {
-    const int64_t cells = a.K * a.M;
-    const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
-    if (i >= a.S * cells) return;
-    const int64_t s = i / cells, c = i - s * cells;
-    const int64_t begin = a.offsets[s], len = min(a.offsets[s + 1], a.N) - begin;
-    const int64_t n = begin < 0 || len <= 0 ? 0 : ((len - 1) >> a.lg) + 1;
-    const float *p = a.partial + slot_key(a.offsets, s, a.lg) * cells + c;
-    float sum = 0.f;
-    for (int64_t j = 0; j < n; ++j) sum += p[j * cells];
-    if (a.out_f32) static_cast<float *>(a.out)[i] = sum;
-    else static_cast<T *>(a.out)[i] = (T)sum;
+__global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
+    using Stage = ColStage<T, kHalf, kPhaseThreads, true>;
+    constexpr int kRows = kStep<T>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    __shared__ int64_t s_rows[2][kRing][kRows];  // left, right
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const OuterPlace at = outer_place(a, kHalf, 2 * kHalf, lane);
+    if (!at.work) return;
+    const int64_t s = at.s, slot = at.slot, row0 = at.row0, rows = at.rows, m0 = at.m0, n0 = at.n0;
+
+    // Byte offset of the source row of step row r.
+    auto source = [&](const int64_t *index, int64_t count, int64_t width, int64_t r) -> int64_t {
+        if (r >= rows) return -1;
+        const int64_t v = index ? index[row0 + r] : row0 + r;
+        return v >= 0 && v < count ? v * width * (int64_t)sizeof(T) : -1;
+    };
+    auto left_source = [&](int64_t r) { return source(a.left_rows, a.left_count, a.K, r); };
+    auto right_source = [&](int64_t r) { return source(a.right_rows, a.right_count, a.M, r); };
+    for (int i = threadIdx.x; i < 4 * kRows; i += kPhaseThreads) {
+        s_rows[0][i / kRows][i % kRows] = left_source(i);
+        s_rows[1][i / kRows][i % kRows] = right_source(i);
+    }
+    int64_t ahead = -1;  // of step t + 4, held by waves 0 (left) and 1 (right)
+    if (wave == 0) ahead = left_source(4 * kRows + lane);
+    if (wave == 1) ahead = right_source(4 * kRows + lane);
+    __syncthreads();
+
+    auto fetch = [&](int side, int h, int t, lds_char *place, const char *base, int64_t width, int64_t c0) {
+        const char *col[Stage::kLoads];
+        int left[Stage::kLoads];
+#pragma unroll
+        for (int i = 0; i < Stage::kLoads; ++i) {
+            const int64_t off = s_rows[side][t & (kRing - 1)][Stage::row(i, wave, lane)];
+            const int64_t c = c0 + h * kHalf + Stage::col(i, wave, lane);
+            col[i] = base + off + c * (int64_t)sizeof(T);
+            left[i] = off >= 0 ? (int)(width - c) : 0;
+        }
+        Stage st;
+        st.issue(place, wave, [&](int i) { return (uint64_t)col[i]; }, [&](int i) { return left[i]; });
+    };
+    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+    f32x4 acc[2][2][4][2] = {};
+    const int64_t steps = (rows + kRows - 1) / kRows;
+    if (steps > 0)
+        phase_steps<T, 1, true, true>(
+            acc, lds, (int)steps, wave, lane,
+            [&](int h, int t, lds_char *place) { fetch(0, h, t, place, a.left, a.K, m0); },
+            [&](int h, int t, lds_char *place) { fetch(1, h, t, place, a.right, a.M, n0); }, products,
+            [&](int t) {
+                if (wave < 2) {
+                    s_rows[wave][(t + 4) & (kRing - 1)][lane] = ahead;
+                    const int64_t r = (int64_t)(t + 5) * kRows + lane;
+                    ahead = wave == 0 ? left_source(r) : right_source(r);
+                }
+            });
+
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = m0 + phase_row(0, i, wave) + (lane & 15);
+        if (r >= a.K) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                outer_store<T>(a, s, slot, r, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, acc[0][q][i][j]);
+    }
 }
 
-// Rows of a slot: a whole segment where the tiles of all segments fill the
-// device; else enough pieces that they do.
-constexpr int64_t kOuterTiles = 512;
-constexpr int kOuterTile = 128;
-int outer_lg(int64_t k, int64_t m, int64_t S, int64_t N) {
-    const int64_t per = ((k + kOuterTile - 1) / kOuterTile) * ((m + kOuterTile - 1) / kOuterTile);
-    if (S * per >= kOuterTiles || N <= 512) return 62;
-    const int64_t want = std::max<int64_t>(512, N * per / kOuterTiles);
-    int lg = 9;
-    while ((int64_t(1) << lg) < want) ++lg;
-    return lg;
+// Adds the slots of each segment and rounds once.  PARTS threads share a cell:
+// thread p adds the slots p, p + PARTS, ... in that order, then the parts are
+// added in order, so that few cells with many slots still read with many
+// threads.  (300,000 rows in 5 segments, 64 x 96 each, about 60 slots a
+// segment: 33 us with one part; 100 segments of 256 x 256 with about two slots
+// each: 49 us with one, 133 us with 8.)
+constexpr int kJoinThreads = 256, kJoinParts = 8;
+template <typename T, int PARTS>
+__global__ __launch_bounds__(kJoinThreads) void outer_join(OuterArgs a) {
+    constexpr int kCells = kJoinThreads / PARTS;
+    __shared__ float s_part[PARTS][kCells];
+    const int64_t cells = a.K * a.M;
+    const int part = threadIdx.x / kCells, cell = threadIdx.x % kCells;
+    const int64_t i = (int64_t)blockIdx.x * kCells + cell;
+    float sum = 0.f;
+    if (i < a.S * cells) {
+        const int64_t s = i / cells, c = i - s * cells;
+        const int64_t begin = a.offsets[s], len = min(a.offsets[s + 1], a.N) - begin;
+        const int64_t n = begin < 0 || len <= 0 ? 0 : (len - 1) / a.step + 1;
+        const float *p = a.partial + slot_key(a.offsets, s, a.step) * cells + c;
+#pragma unroll 4
+        for (int64_t j = part; j < n; j += PARTS) sum += p[j * cells];
+    }
+    if constexpr (PARTS > 1) {
+        s_part[part][cell] = sum;
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int q = 1; q < PARTS; ++q) sum += s_part[q][cell];
+    }
+    if (i < a.S * cells) {
+        if (a.out_f32) static_cast<float *>(a.out)[i] = sum;
+        else static_cast<T *>(a.out)[i] = (T)sum;
+    }
+}
+
+// Tile and rows of a slot.  Where the segments' tiles of 128 x 128 give every
+// CU one, a slot is a whole segment; else the tiles are smaller and the
+// segments are cut into slots of at least kSlotRows rows, as many as the
+// device holds workgroups at a time (3 of 64 x 128 or 4 of 64 x 64 a CU).
+struct OuterPlan {
+    bool small;  // 64 x 64, or
+    bool wide;   // 64 x 128, where that holds the whole sum
+    int64_t step;
+};
+constexpr int64_t kCus = 256, kSlotRows = 256;
+OuterPlan outer_plan(int64_t k, int64_t m, int64_t S, int64_t N) {
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((k + bm - 1) / bm) * ((m + bn - 1) / bn); };
+    OuterPlan p{false, false, kWhole};
+    if (S >= kCus || S * tiles(128, 128) >= kCus) return p;
+    p.small = true;
+    p.wide = k <= 64 && m > 64;
+    if (N <= kSlotRows) return p;
+    const int64_t per = tiles(64, p.wide ? 128 : 64), room = std::max<int64_t>(1, kCus * (p.wide ? 3 : 4) / per);
+    const int64_t rows = N / std::max<int64_t>(1, room - S) + 1;
+    p.step = std::max<int64_t>(kSlotRows, (rows + 63) / 64 * 64);
+    return p;
+}
+
+// Adds the slots, where there are several.
+template <typename T>
+int outer_finish(const OuterArgs &a, hipStream_t st) {
+    if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
+    if (!a.partial) return SEGRED_OK;
+    const bool shared = a.slots >= kJoinParts * a.S;
+    const int64_t cells = shared ? kJoinThreads / kJoinParts : kJoinThreads;
+    const unsigned wgs = (unsigned)((a.S * a.K * a.M + cells - 1) / cells);
+    if (shared) timed_launch_ggl(false, (outer_join<T, kJoinParts>), dim3(wgs), dim3(kJoinThreads), 0, st, a);
+    else timed_launch_ggl(false, (outer_join<T, 1>), dim3(wgs), dim3(kJoinThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
@@ -148,23 +343,35 @@ int outer_launch(OuterArgs a, bool direct, hipStream_t st) {
     a.mtiles = (a.K + BM - 1) / BM;
     a.ntiles = (a.M + BN - 1) / BN;
     dim3 grid;
-    if (!tile_grid(a.slots * a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
     constexpr int kThreads = 64 * WM * WN;
     if (direct)
         timed_launch_ggl(true, (seg_outer<T, BM, BN, WM, WN, true>), grid, dim3(kThreads), 0, st, a);
     else
         timed_launch_ggl(true, (seg_outer<T, BM, BN, WM, WN, false>), grid, dim3(kThreads), 0, st, a);
-    if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
-    if (a.partial) {
-        const int64_t wgs = (a.S * a.K * a.M + kJoinThreads - 1) / kJoinThreads;
-        timed_launch_ggl(false, outer_join<T>, dim3((unsigned)wgs), dim3(kJoinThreads), 0, st, a);
-        if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
-    }
-    return SEGRED_OK;
+    return outer_finish<T>(a, st);
 }
 
 template <typename T>
-int outer_dispatch(const OuterArgs &a, bool direct, hipStream_t st) {
+int outer_many_launch(OuterArgs a, hipStream_t st) {
+    a.mtiles = (a.K + kHalf - 1) / kHalf;
+    a.ntiles = (a.M + 2 * kHalf - 1) / (2 * kHalf);
+    dim3 grid;
+    if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(true, seg_outer_many<T>, grid, dim3(kPhaseThreads), 0, st, a);
+    return outer_finish<T>(a, st);
+}
+
+template <typename T>
+int outer_dispatch(const OuterArgs &a, const OuterPlan &p, bool direct, hipStream_t st) {
+    if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
+    if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
+    // 128 x 256 in phases from two such tiles for every CU and eight steps a
+    // segment on: 16,384 rows in 8 segments of 4,096 x 4,096 take 876 us against
+    // 933, but 8,192 rows in 64 segments of 1,024 x 1,024 107 us against 72
+    if constexpr (sizeof(T) == 2)
+        if (direct && a.S * ((a.K + 127) / 128) * ((a.M + 255) / 256) >= 2 * kCus && a.N >= a.S * 512)
+            return outer_many_launch<T>(a, st);
     return outer_launch<T, 128, 128, 2, 2>(a, direct, st);
 }
 
@@ -175,9 +382,8 @@ using namespace segred;
 extern "C" int64_t segred_outer_workspace(int64_t k, int64_t m, int64_t num_segments, int64_t num_rows) {
     if (k < 1 || m < 1 || num_segments < 1 || num_rows < 0 || k > kMaxWidth || m > kMaxWidth) return 0;
     if (too_large(num_segments, k * m, 4)) return 0;
-    const int lg = outer_lg(k, m, num_segments, num_rows);
-    if (lg == 62) return 0;
-    return ((num_rows >> lg) + num_segments) * k * m * 4;
+    const int64_t step = outer_plan(k, m, num_segments, num_rows).step;
+    return step == kWhole ? 0 : (num_rows / step + num_segments) * k * m * 4;
 }
 
 extern "C" int segred_outer(const void *left, const int64_t *left_rows, int64_t left_count, int64_t k,
@@ -214,16 +420,17 @@ extern "C" int segred_outer(const void *left, const int64_t *left_rows, int64_t 
     a.N = num_rows;
     a.K = k;
     a.M = m;
-    a.lg = outer_lg(k, m, num_segments, num_rows);
-    a.slots = (num_rows >> a.lg) + num_segments;
+    const OuterPlan plan = outer_plan(k, m, num_segments, num_rows);
+    a.step = plan.step;
+    a.slots = num_rows / a.step + num_segments;
     a.out = out;
     a.out_f32 = out_dtype == SEGRED_F32;
     a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
     a.vec = (m % 4 == 0 && aligned(out, 4 * oe)) ? 1 : 0;
     const bool direct = (k * e) % 16 == 0 && (m * e) % 16 == 0 && aligned(left, 16) && aligned(right, 16);
     switch (dtype) {
-    case SEGRED_BF16: return outer_dispatch<__bf16>(a, direct, stream);
-    case SEGRED_F16: return outer_dispatch<_Float16>(a, direct, stream);
-    default: return outer_dispatch<float>(a, direct, stream);
+    case SEGRED_BF16: return outer_dispatch<__bf16>(a, plan, direct, stream);
+    case SEGRED_F16: return outer_dispatch<_Float16>(a, plan, direct, stream);
+    default: return outer_dispatch<float>(a, plan, direct, stream);
     }
 }

@@ -238,30 +238,235 @@ __device__ __forceinline__ f32x4 mma(u32x4 b, u32x4 a, f32x4 c) {
     }
 }
 
-// One step of a wave's MT x NT tile of 16 x 16 blocks: rows from m0, columns
-// from n0 of the workgroup's tile.
-template <typename T, int MT, int NT, bool A_COL, int AW, bool B_COL, int BW>
+// One step of a wave's MT x NT blocks of 16 x 16 of the workgroup's tile: rows
+// m0 + MS * i and columns n0 + NS * j.  Unless FULL, only the first mv block
+// rows and nv block columns are multiplied (wave-uniform): the others lie past
+// the edge.
+template <typename T, bool FULL, int MT, int NT, int MS, int NS, bool A_COL, int AW, bool B_COL, int BW>
 __device__ __forceinline__ void step_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
-                                              int n0, int lane) {
+                                              int n0, int mv, int nv, int lane) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         u32x4 a[MT], b[NT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            if constexpr (A_COL) a[i] = col_frag<T, AW>(la, m0 + 16 * i, ks, lane);
-            else a[i] = row_frag(la, m0 + 16 * i, ks, lane);
+            if (!FULL && i >= mv) continue;
+            if constexpr (A_COL) a[i] = col_frag<T, AW>(la, m0 + MS * i, ks, lane);
+            else a[i] = row_frag(la, m0 + MS * i, ks, lane);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if constexpr (B_COL) b[j] = col_frag<T, BW>(lb, n0 + 16 * j, ks, lane);
-            else b[j] = row_frag(lb, n0 + 16 * j, ks, lane);
+            if (!FULL && j >= nv) continue;
+            if constexpr (B_COL) b[j] = col_frag<T, BW>(lb, n0 + NS * j, ks, lane);
+            else b[j] = row_frag(lb, n0 + NS * j, ks, lane);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i) {
+            if (!FULL && i >= mv) continue;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[i][j] = mma<T>(b[j], a[i], acc[i][j]);
+            for (int j = 0; j < NT; ++j)
+                if (FULL || j < nv) acc[i][j] = mma<T>(b[j], a[i], acc[i][j]);
+        }
     }
 }
+
+// How a workgroup's blocks go to its waves.  float blocks are dealt in turn,
+// and a tile that crosses the edge skips those past it: the matrix rate of
+// float is a sixteenth of the 16-bit types', so that is what such a tile waits
+// for.  The 16-bit types keep neighbouring blocks together and multiply zeros:
+// the skipping branches cost more than they save (128 x 128 tiles of a product
+// of 8192^3 in bfloat16: 1,446 us without, 5,451 us with them).
+template <typename T> constexpr bool kDealt = sizeof(T) == 4;
+
+// Blocks of a wave that lie before the edge: `left` rows (columns) from the
+// tile's start, the wave's first block at `first`, the others `stride` apart.
+__device__ __forceinline__ int blocks_inside(int64_t left, int first, int stride, int most) {
+    const int n = (int)(min(left, (int64_t)1 << 20) - first + stride - 1) / stride;
+    return n < 0 ? 0 : n > most ? most : n;
+}
+
+// ------------------------------------------------------------------- waits
+
+// Waits until at most N of this wave's loads are in flight and meets the
+// other waves.  (A workgroup fence would wait for all of them.)
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The launch grid of `total` tiles and the tile index of a workgroup.  A
+// dimension of the grid may not pass 2^32 threads, so long grids are folded.
+constexpr int64_t kGridFold = int64_t(1) << 20;
+inline bool tile_grid(int64_t total, dim3 &grid) {
+    const int64_t y = (total + kGridFold - 1) / kGridFold;
+    if (y > 65535) return false;
+    grid = dim3((unsigned)(y > 1 ? kGridFold : total), (unsigned)y);
+    return true;
+}
+
+// ------------------------------------------------------------- in phases
+//
+// The large tiles of the 16-bit types: 256 columns by AH * 128 rows, 8 waves,
+// 2 by 4.  Each operand's step is cut into halves of 128 rows (columns), and a
+// wave owns 64 x 32 of each quadrant.  A step takes one phase per quadrant, in
+// an order that changes one half at a time; a phase first moves data
+// (fragments of the half that changes, from LDS; a half of a later step, from
+// memory into a place that has been read) and then multiplies.  Waves 4..7,
+// which share the SIMDs with waves 0..3, run one barrier behind, so that on
+// each SIMD one wave multiplies while the other moves data.
+//
+//   AH = 2     reads    fetches    multiplies      places: two steps
+//     0        A0(t)    A1(t+1)    A0 B0
+//     1        B1(t)    B0(t+2)    A0 B1
+//     2        A1(t)    A0(t+2)    A1 B1
+//     3        B0(t+1)  B1(t+2)    A1 B0
+//
+//   AH = 1     reads           fetches            multiplies   three steps
+//     0        A0(t)           A0(t+2)            A0 B0
+//     1        B1(t), B0(t+1)  B1(t+2), B0(t+3)   A0 B1
+//
+// A half is read one phase after every wave has waited for it; the loads
+// issued since (2 per half and thread) may be in flight.  A half's place is
+// filled again two phases after it was read, when the wave that reads last has
+// multiplied what it read.  The loads past the last step fetch zeros.
+constexpr int kHalf = 128;
+constexpr int kPhaseThreads = 512;
+constexpr int kHalfBytes = kHalf * 128;
+constexpr int kPhaseLds = 9 * kHalfBytes;  // two steps of A0 A1 B0 B1, or three of A0 B0 B1
+
+template <bool COL, typename T>
+__device__ __forceinline__ u32x4 half_frag(const lds_char *lds, int r0, int ks, int lane) {
+    if constexpr (COL) return col_frag<T, kHalf>(lds, r0, ks, lane);
+    else return row_frag(lds, r0, ks, lane);
+}
+
+// The products of a phase: c += a b over the step's two k halves.
+template <typename T>
+__device__ __forceinline__ void quadrant(f32x4 (&c)[4][2], const u32x4 (&a)[4][2], const u32x4 (&b)[2][2]) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) c[i][j] = mma<T>(b[j][ks], a[i][ks], c[i][j]);
+}
+
+// fetch_a(h, t, place) and fetch_b(h, t, place) start half h of step t (two
+// loads per thread; zeros past the last step); products(t, c, a, b) are a
+// phase's; tick(t) is called once a step.  acc[a][b] are the quadrants.
+template <typename T, int AH, bool A_COL, bool B_COL, typename FA, typename FB, typename P, typename K>
+__device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *lds, int steps, int wave, int lane,
+                                            FA fetch_a, FB fetch_b, P products, K tick) {
+    static_assert(sizeof(T) == 2, "16-bit types");
+    const int ma = (wave >> 2) * 64, nb = (wave & 3) * 32;
+    u32x4 a[4][2], b0[2][2], b1[2][2];
+    auto read_a = [&](const lds_char *p) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i][ks] = half_frag<A_COL, T>(p, ma + 16 * i, ks, lane);
+    };
+    auto read_b = [&](u32x4 (&b)[2][2], const lds_char *p) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) b[j][ks] = half_frag<B_COL, T>(p, nb + 16 * j, ks, lane);
+    };
+    auto multiply = [&](int t, f32x4 (&c)[4][2], const u32x4 (&b)[2][2]) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        products(t, c, a, b);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#define SEGRED_MEET(N)                                                      \
+    __builtin_amdgcn_sched_barrier(0);                                      \
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+
+    if constexpr (AH == 2) {
+        auto place_a = [&](int h, int t) { return lds + ((t & 1) * 4 + h) * kHalfBytes; };
+        auto place_b = [&](int h, int t) { return lds + ((t & 1) * 4 + 2 + h) * kHalfBytes; };
+        u32x4 b0_next[2][2];
+        fetch_b(0, 0, place_b(0, 0));
+        fetch_a(0, 0, place_a(0, 0));
+        fetch_b(1, 0, place_b(1, 0));
+        fetch_a(1, 0, place_a(1, 0));
+        fetch_b(0, 1, place_b(0, 1));
+        fetch_a(0, 1, place_a(0, 1));
+        fetch_b(1, 1, place_b(1, 1));
+        wait_and_meet<10>();
+        read_b(b0, place_b(0, 0));
+        wait_and_meet<10>();
+        if (wave >= 4) asm volatile("s_barrier" ::: "memory");
+        for (int t = 0; t < steps; ++t) {
+            tick(t);
+            read_a(place_a(0, t));
+            fetch_a(1, t + 1, place_a(1, t + 1));
+            SEGRED_MEET(10)
+            multiply(t, acc[0][0], b0);
+
+            read_b(b1, place_b(1, t));
+            fetch_b(0, t + 2, place_b(0, t));
+            SEGRED_MEET(10)
+            multiply(t, acc[0][1], b1);
+
+            read_a(place_a(1, t));
+            fetch_a(0, t + 2, place_a(0, t));
+            SEGRED_MEET(10)
+            multiply(t, acc[1][1], b1);
+
+            read_b(b0_next, place_b(0, t + 1));
+            fetch_b(1, t + 2, place_b(1, t));
+            SEGRED_MEET(10)
+            multiply(t, acc[1][0], b0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) b0[j][ks] = b0_next[j][ks];
+        }
+    } else {
+        constexpr int kStepBytes = 3 * kHalfBytes;  // A0 B0 B1
+        fetch_b(0, 0, lds + kHalfBytes);
+        fetch_a(0, 0, lds);
+        fetch_b(1, 0, lds + 2 * kHalfBytes);
+        fetch_b(0, 1, lds + kStepBytes + kHalfBytes);
+        fetch_a(0, 1, lds + kStepBytes);
+        fetch_b(1, 1, lds + kStepBytes + 2 * kHalfBytes);
+        fetch_b(0, 2, lds + 2 * kStepBytes + kHalfBytes);
+        wait_and_meet<10>();
+        read_b(b0, lds + kHalfBytes);
+        wait_and_meet<10>();
+        if (wave >= 4) asm volatile("s_barrier" ::: "memory");
+        lds_char *now = lds, *next = lds + kStepBytes, *after = lds + 2 * kStepBytes;
+        for (int t = 0; t < steps; ++t) {
+            tick(t);
+            read_a(now);
+            fetch_a(0, t + 2, after);
+            SEGRED_MEET(8)
+            multiply(t, acc[0][0], b0);
+
+            read_b(b0, next + kHalfBytes);  // before b1, whose arrival then implies b0's
+            read_b(b1, now + 2 * kHalfBytes);
+            fetch_b(1, t + 2, after + 2 * kHalfBytes);
+            fetch_b(0, t + 3, now + kHalfBytes);
+            SEGRED_MEET(10)
+            multiply(t, acc[0][1], b1);
+            lds_char *const first = now;
+            now = next;
+            next = after;
+            after = first;
+        }
+    }
+#undef SEGRED_MEET
+    if (wave < 4) asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the zeros past the last step
+}
+
+// Row and column of quadrant (a, b)'s 16 x 16 block (i, j) in the tile.
+__device__ __forceinline__ int phase_row(int a, int i, int wave) { return a * kHalf + (wave >> 2) * 64 + 16 * i; }
+__device__ __forceinline__ int phase_col(int b, int j, int wave) { return b * kHalf + (wave & 3) * 32 + 16 * j; }
 
 // ------------------------------------------------------------- wave's own
 //
@@ -358,23 +563,6 @@ __device__ __forceinline__ void store_quad(T *row, int64_t n, int64_t width, f32
 
 // ------------------------------------------------------------- tile places
 
-// Waits until at most N of this wave's loads are in flight and meets the
-// other waves.  (A workgroup fence would wait for all of them.)
-template <int N>
-__device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// The launch grid of `total` tiles and the tile index of a workgroup.  A
-// dimension of the grid may not pass 2^32 threads, so long grids are folded.
-constexpr int64_t kGridFold = int64_t(1) << 20;
-inline bool tile_grid(int64_t total, dim3 &grid) {
-    const int64_t y = (total + kGridFold - 1) / kGridFold;
-    if (y > 65535) return false;
-    grid = dim3((unsigned)(y > 1 ? kGridFold : total), (unsigned)y);
-    return true;
-}
-
 // Workgroups are dealt to the 8 XCDs in turn; this maps the launch index to a
 // tile index such that each XCD (with an L2 of its own) owns one contiguous
 // range of tiles.
@@ -385,28 +573,54 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t total) {
     return x * q + (x < r ? x : r) + i;
 }
 
-// The rows of segment s are cut into slots of 2^lg rows from the segment's
-// start.  Slot keys need no table: segment s owns the slots from
-// key(s) = (offsets[s] - offsets[0]) / 2^lg + s up to key(s + 1), which are at
-// least ceil(len / 2^lg) and at least one; what is over is empty.  There are
-// (offsets[S] - offsets[0]) / 2^lg + S slots in all.
-__device__ __forceinline__ int64_t slot_key(const int64_t *offsets, int64_t s, int lg) {
-    return ((offsets[s] - offsets[0]) >> lg) + s;
+// Row tile and column tile of tile `id` of mt x nt: groups of 4 row tiles walk
+// the column tiles together, so that the 32 tiles an XCD works on at a time
+// share 4 row strips and 8 column strips.
+struct TilePlace {
+    int64_t m, n;
+};
+__device__ __forceinline__ TilePlace tile_place(int64_t id, int64_t mt, int64_t nt) {
+    const int64_t group = id / (4 * nt), in = id - group * 4 * nt;
+    const int64_t gm = min((int64_t)4, mt - group * 4);
+    return {group * 4 + in % gm, in / gm};
 }
 
-// The segment of `slot`, found with 64 probes a round (every lane must call it).
-__device__ __forceinline__ int64_t slot_segment(const int64_t *offsets, int64_t S, int lg, int64_t slot, int lane) {
+// The rows of segment s are cut into slots of `step` rows from the segment's
+// start.  Slot keys need no table: segment s owns the slots from
+// key(s) = (offsets[s] - offsets[0]) / step + s up to key(s + 1), which are at
+// least ceil(len / step) and at least one; what is over is empty.  There are
+// (offsets[S] - offsets[0]) / step + S slots in all.
+__device__ __forceinline__ int64_t slot_key(const int64_t *offsets, int64_t s, int64_t step) {
+    return (offsets[s] - offsets[0]) / step + s;
+}
+
+// The same with fewer empty slots, for calls that need none for an empty
+// segment, and for steps of 2^lg rows:
+// key(s) = (offsets[s] - offsets[0] + s (2^lg - 1)) / 2^lg, which still grows
+// by at least ceil(len / 2^lg).  tight_slots() of them in all.
+__device__ __forceinline__ int64_t tight_key(const int64_t *offsets, int64_t s, int lg) {
+    return (offsets[s] - offsets[0] + (s << lg) - s) >> lg;
+}
+inline int64_t tight_slots(int64_t rows, int64_t segments, int lg) { return (rows + (segments << lg) - segments) >> lg; }
+
+// The segment of `slot`, found with 64 probes a round (every lane must call
+// it): the last one whose key is not above it.
+template <typename K>
+__device__ __forceinline__ int64_t slot_segment(int64_t S, int64_t slot, int lane, K key) {
     int64_t lo = 0, hi = S;
     while (hi - lo > 1) {
         const int64_t d = (hi - lo + 63) >> 6;
         const int64_t s = lo + lane * d;
         bool below = false;
-        if (s < hi) below = slot_key(offsets, s, lg) <= slot;
+        if (s < hi) below = key(s) <= slot;
         const int n = popc64(ballot(below));
         lo += (n > 0 ? n - 1 : 0) * d;
         hi = hi < lo + d ? hi : lo + d;
     }
     return readfirst(lo);
+}
+__device__ __forceinline__ int64_t tight_segment(const int64_t *offsets, int64_t S, int lg, int64_t slot, int lane) {
+    return slot_segment(S, slot, lane, [&](int64_t s) { return tight_key(offsets, s, lg); });
 }
 
 }  // namespace segred
