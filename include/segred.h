@@ -554,7 +554,8 @@ int segred_combine_grad(const void *grad, const void *values, int32_t dtype, int
  *              products over the rows of an adapter: of up[a] from the output
  *              gradient and the forward call's `low`, of down[a] from the
  *              transposed call's `low` and x (segred_outer).
- *   workspace  segred_adapter_workspace(rank, num_rows) bytes.
+ *   workspace  segred_adapter_workspace(dtype, m, adapters, rank, num_rows)
+ *              bytes.
  *
  * The low-rank rows enter the second product in float32, or as the sum of two
  * bf16 (2^-17 relative) for the 16-bit types.
@@ -569,7 +570,7 @@ int segred_adapter(const void *values, int32_t dtype, int64_t k, const void *wei
                    const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
                    int32_t transpose, void *out, void *low, void *workspace, int64_t workspace_bytes,
                    hipStream_t stream);
-int64_t segred_adapter_workspace(int64_t rank, int64_t num_rows);
+int64_t segred_adapter_workspace(int32_t dtype, int64_t m, int64_t adapters, int64_t rank, int64_t num_rows);
 
 /* Static, host-side description of a status code (never NULL). */
 const char *segred_status_string(int status);

@@ -24,10 +24,12 @@ struct AdapterArgs {
     const char *values;   // [N, K]
     const char *weights;  // [M, K] (row form) or [K, M] (col form)
     const char *first;    // [L, R, K] or [L, K, R]
-    const char *second;   // [L, M, R] or [L, R, M]
+    const char *second;   // [L, M, R2] or [L, R, M]
     const int64_t *offsets, *which;
     const float *scale;   // [L] or null
     int64_t S, N, K, M, L, R;
+    int64_t R2;           // ranks between rows of `second`: R, or more where it is a copy
+    const char *copy_from;  // the caller's second factor, where `second` is a copy of it
     int64_t slots, mtiles, ntiles, blocks;  // blocks: ceil(R / 32)
     char *u;              // [N, blocks * 128 bytes]
     int32_t *ids;         // [N] adapter of each row, -1: none
@@ -37,6 +39,27 @@ struct AdapterArgs {
 };
 
 constexpr int kRankBlock = 32;
+
+// Rows of the second factor that do not hold whole 16-byte units are copied,
+// with zeros behind them, for the adapters that some segment has: by the
+// workgroups of its first segment, kCopyRows rows each.
+constexpr int kCopyRows = 512;
+template <typename T>
+__device__ __forceinline__ void copy_second(const AdapterArgs &a, int64_t wg, int threads) {
+    const int64_t per = (a.M + kCopyRows - 1) / kCopyRows, s = wg / per, m0 = (wg - s * per) * kCopyRows;
+    const int64_t adapter = a.which[s];
+    if (adapter < 0 || adapter >= a.L) return;
+    const int lane = threadIdx.x & 63;
+    for (int64_t q = 0; q < s; q += 64)
+        if (ballot(q + lane < s && a.which[q + lane] == adapter) != 0) return;
+    const int R = (int)a.R, R2 = (int)a.R2, rows = (int)min((int64_t)kCopyRows, a.M - m0);
+    const T *from = reinterpret_cast<const T *>(a.copy_from) + (adapter * a.M + m0) * R;
+    T *to = reinterpret_cast<T *>(const_cast<char *>(a.second)) + (adapter * a.M + m0) * R2;
+    for (int i = threadIdx.x; i < rows * R2; i += threads) {
+        const int r = i / R2, c = i - r * R2;
+        to[i] = c < R ? from[r * R + c] : (T)0.f;
+    }
+}
 
 template <typename T, int MT, int NW, int STAGES, bool B_COL, bool DIRECT>
 __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
@@ -52,8 +75,13 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
     lds_char *lds = (lds_char *)lds_mem;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t launch = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (launch >= a.slots * a.blocks) {
+        if (a.copy_from && launch < a.slots * a.blocks + a.S * ((a.M + kCopyRows - 1) / kCopyRows))
+            copy_second<T>(a, launch - a.slots * a.blocks, 64 * NW);
+        return;
+    }
     const int64_t id = xcd_tile(a.slots * a.blocks);
-    if (id >= a.slots * a.blocks) return;
     const int64_t slot = id / a.blocks, block = id - slot * a.blocks;
     const int r0 = (int)block * kRankBlock;
     const int64_t s = tight_segment(a.offsets, a.S, kLg, slot, lane);
@@ -118,7 +146,8 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
         },
         [&](int, const lds_char *buf) {
             step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, MT, NT, lane);
-        });
+        },
+        [] {});
     const float scale = a.scale ? a.scale[adapter] : 1.f;
     join_waves<NW, MT, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
         if (r >= rows) return;
@@ -170,7 +199,7 @@ struct AdapterSteps {
             else sa.v[i] = load_unit<T>(q, mine ? kUnit<T> : 0);
         }
         lds_char *bb = buf + AS::kBytes;
-        const char *w = a.second + (int64_t)adapter * a.M * a.R * (int64_t)sizeof(T);
+        const char *w = a.second + (int64_t)adapter * a.M * a.R2 * (int64_t)sizeof(T);
         const int R = (int)a.R, M = (int)a.M;
         constexpr int kMask = kRankBlock - 1;
         if constexpr (B_COL) {
@@ -184,7 +213,7 @@ struct AdapterSteps {
 #pragma unroll
             for (int i = 0; i < BR::kLoads; ++i) {
                 const int64_t n = n0 + BR::group(i, wave) * 8 + (lane >> 3);
-                const uint64_t q = (uint64_t)(w + (n * a.R + rank) * (int64_t)sizeof(T));
+                const uint64_t q = (uint64_t)(w + (n * a.R2 + rank) * (int64_t)sizeof(T));
                 const int left = n < a.M ? R - rank : 0;
                 if constexpr (DIRECT) load_to_lds(left > 0 ? q : zeros, bb + BR::group(i, wave) * 1024);
                 else sbr.v[i] = load_unit<T>(q, left);
@@ -235,13 +264,14 @@ __device__ __forceinline__ int tile_adapters(const AdapterArgs &a, int64_t row0,
     if (tid < 64) {  // one wave walks the rows, 64 at a time
         int n = 0;
         for (int b = 0; b < BM; b += 64) {
-            const int r = b + tid;
-            const int id = r < BM ? s_ids[r] : -1;
-            bool first = id >= 0 && (r == 0 || s_ids[r - 1] != id);
-            if (first)
-                for (int q = 0; q < r - 1 && first; ++q) first = s_ids[q] != id;
+            const int id = b + tid < BM ? s_ids[b + tid] : -1;
+            bool first = id >= 0;
+            for (int q = 0; q < n; ++q) first = first && s_list[q] != id;
+            const int most = BM - b < 64 ? BM - b : 64;
+            for (int q = 0; q < most - 1; ++q) first = first && (q >= tid || __builtin_amdgcn_readlane(id, q) != id);
             const uint64_t m = ballot(first);
             if (first) s_list[n + popc64(m & ((uint64_t(1) << tid) - 1))] = id;
+            wave_lds_sync();
             n += popc64(m);
         }
         if (tid == 0) *s_count = n;
@@ -250,8 +280,9 @@ __device__ __forceinline__ int tile_adapters(const AdapterArgs &a, int64_t row0,
     return *s_count;
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool B_COL, bool DIRECT>
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
+    static_assert(DIRECT || STAGES == 2, "units that pass through registers use two buffers");
     constexpr int kThreads = 64 * WM * WN;
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     using Steps = AdapterSteps<T, BM, BN, kThreads, B_COL, DIRECT>;
@@ -260,7 +291,8 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     using BCol = typename Steps::BC;
     constexpr int kABytes = AStage::kBytes;
     constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kStageBytes];
+    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes];
     __shared__ int s_ids[BM], s_list[BM], s_count;
     lds_char *lds = (lds_char *)lds_mem;
 
@@ -302,7 +334,7 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     const int base = (K + kStep<T> - 1) / kStep<T>, blocks = (int)a.blocks;
     const int steps = base + met * blocks;
     auto issue = [&](int t, lds_char *buf) {
-        if (t < base) {
+        if (t < base || t >= steps) {  // past the last step: zeros
             const int k0 = t * kStep<T>;
             sa.issue(buf, wave, k0);
             if constexpr (B_COL) {
@@ -327,18 +359,33 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
 
     f32x4 acc[MT][NT] = {};
     const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
-    issue(0, lds);
-    commit(lds);
-    for (int t = 0; t < steps; ++t) {
-        wait_and_meet<0>();
-        lds_char *next = lds + ((t + 1) & 1) * kStageBytes;
-        if (t + 1 < steps) issue(t + 1, next);
-        const lds_char *buf = lds + (t & 1) * kStageBytes;
+    auto products = [&](int t, const lds_char *buf) {
         if (__is_same(T, _Float16) && t >= base)
             split_products<MT, NT, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
         else
             step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, MT, NT, lane);
-        if (t + 1 < steps) commit(next);
+    };
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
+        int cur = 0, fill = STAGES - 1;
+        for (int t = 0; t < steps; ++t) {
+            wait_and_meet<(STAGES - 2) * kLoads>();
+            issue(t + STAGES - 1, lds + fill * kStageBytes);
+            products(t, lds + cur * kStageBytes);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the zeros past the last step
+    } else {
+        issue(0, lds);
+        commit(lds);
+        for (int t = 0; t < steps; ++t) {
+            __syncthreads();
+            if (t + 1 < steps) issue(t + 1, lds);
+            products(t, lds + (t & 1) * kStageBytes);
+            if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
+        }
     }
 
     T *out = reinterpret_cast<T *>(a.out);
@@ -352,6 +399,143 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
                 store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
         }
     }
+}
+
+// Four columns from n of a row's adapter part, u B, in float32.
+template <typename T, bool B_COL>
+__device__ __forceinline__ f32x4 adapter_quad(const AdapterArgs &a, int64_t row, int adapter, int64_t n) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    const int R = (int)a.R, columns = (int)min((int64_t)4, a.M - n);
+    if (adapter < 0 || columns <= 0) return sum;
+    constexpr int U = kUnit<T>;
+    const char *u = a.u + row * a.blocks * 128;
+    const T *b = reinterpret_cast<const T *>(a.second) + (int64_t)adapter * a.M * a.R2;
+    for (int r0 = 0; r0 < R; r0 += U) {
+        const char *p = u + r0 / kRankBlock * 128 + r0 % kRankBlock * (128 / kRankBlock) / (sizeof(T) == 2 ? 2 : 1);
+        float x[U];  // zeros past the rank
+        if constexpr (sizeof(T) == 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+            for (int e = 0; e < U; ++e) x[e] = v[e];
+        } else {
+            const bf16x8 hi = *reinterpret_cast<const bf16x8 *>(p), lo = *reinterpret_cast<const bf16x8 *>(p + 64);
+#pragma unroll
+            for (int e = 0; e < U; ++e) x[e] = (float)hi[e] + (float)lo[e];
+        }
+        union Units {
+            u32x4 v;
+            T e[U];
+        };
+        if constexpr (B_COL) {
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                if (r0 + e >= R) continue;
+                Units w;
+                w.v = load_unit<T>((uint64_t)(b + (int64_t)(r0 + e) * a.M + n), columns);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = fmaf(x[e], (float)w.e[j], sum[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= columns) continue;
+                Units w;
+                w.v = load_unit<T>((uint64_t)(b + (n + j) * a.R2 + r0), R - r0);
+#pragma unroll
+                for (int e = 0; e < U; ++e) sum[j] = fmaf(x[e], (float)w.e[e], sum[j]);
+            }
+        }
+    }
+    return sum;
+}
+
+// Few rows: 16 MT rows x 16 columns per workgroup, whose waves split the
+// contraction of x W.  The adapters' part, for which every row may have an
+// adapter of its own, is added per element instead of in steps: 64 rows with 64
+// adapters of rank 16 beside 4,096 x 4,096 took 18 us in steps.
+template <typename T, int MT, int NW, int STAGES, bool B_COL>
+__global__ __launch_bounds__(64 * NW) void adapter_main_few(AdapterArgs a) {
+    static_assert(MT <= NW, "a quad of columns per thread");
+    constexpr int BM = 16 * MT, BN = 16;
+    using AStage = RowStage<T, BM, 64, true>;
+    using BRow = RowStage<T, BN, 64, true>;
+    using BCol = ColStage<T, BN, 64, true>;
+    constexpr int kABytes = AStage::kBytes;
+    constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[NW * STAGES * kStageBytes];
+    lds_char *lds = (lds_char *)lds_mem;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.mtiles * a.ntiles);
+    if (id >= a.mtiles * a.ntiles) return;
+    const int64_t n0 = id / a.mtiles * BN;  // row tiles of the same columns of W together
+    const int64_t row0 = a.offsets[0] + id % a.mtiles * BM;
+    const int64_t end = min(a.offsets[a.S], a.N);
+    if (row0 >= end || row0 < 0) return;
+    const int rows = (int)min((int64_t)BM, end - row0), K = (int)a.K;
+
+    AStage sa;
+    sa.init(0, lane, K, [&](int r) -> const char * {
+        return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+    });
+    BRow sbr;
+    BCol sbc;
+    uint64_t wp[BCol::kLoads];
+    int wleft[BCol::kLoads];
+    if constexpr (B_COL) {
+#pragma unroll
+        for (int i = 0; i < BCol::kLoads; ++i) {
+            const int64_t n = n0 + BCol::col(i, 0, lane);
+            wp[i] = (uint64_t)(a.weights + (BCol::row(i, 0, lane) * a.M + n) * (int64_t)sizeof(T));
+            wleft[i] = (int)(a.M - n);
+        }
+    } else {
+        sbr.init(0, lane, K, [&](int r) -> const char * {
+            return n0 + r < a.M ? a.weights + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+        });
+    }
+    f32x4 acc[MT][1] = {}, extra = {0.f, 0.f, 0.f, 0.f};
+    const int steps = (K + kStep<T> - 1) / kStep<T>;
+    wave_steps<STAGES, true, kLoads, kStageBytes>(
+        lds + wave * STAGES * kStageBytes, wave * steps / NW, (wave + 1) * steps / NW,
+        [&](int t, bool live, lds_char *buf) {
+            const int k0 = live ? t * kStep<T> : steps * kStep<T>;
+            sa.issue(buf, 0, k0);
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                sbc.issue(
+                    buf + kABytes, 0, [&](int i) { return wp[i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, 0, lane) < K ? wleft[i] : 0; });
+            } else {
+                sbr.issue(buf + kABytes, 0, k0);
+            }
+        },
+        [](lds_char *) {},
+        [&](int, const lds_char *buf) {
+            step_products<T, true, MT, 1, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, MT, 1, lane);
+        },
+        [&] {
+            // this thread's quad in join_waves()
+            const int r = wave * 16 + (lane & 15);
+            if (wave < MT && r < rows)
+                extra = adapter_quad<T, B_COL>(a, row0 + r, a.ids[row0 + r], n0 + (lane >> 4) * 4);
+        });
+    T *out = reinterpret_cast<T *>(a.out);
+    join_waves<NW, MT, 1>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
+        if (r < rows) store_quad<T>(out + (row0 + r) * a.M, n0 + c, a.M, sum + extra, a.vec != 0);
+    });
+}
+
+template <typename T, int MT, int NW, int STAGES>
+int adapter_few_launch(AdapterArgs a, bool b_col, hipStream_t st) {
+    a.mtiles = (a.N + 16 * MT - 1) / (16 * MT);
+    a.ntiles = (a.M + 15) / 16;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (b_col) timed_launch_ggl(true, (adapter_main_few<T, MT, NW, STAGES, true>), grid, dim3(64 * NW), 0, st, a);
+    else timed_launch_ggl(true, (adapter_main_few<T, MT, NW, STAGES, false>), grid, dim3(64 * NW), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 // Many rows: AH * 128 rows x 256 columns per workgroup, in phases (16-bit
@@ -447,7 +631,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
         int block = 0;
         const int adapter = t < extra ? adapter_of(t, block) : -1;
         const int have = adapter >= 0 ? R - block * kRankBlock : 0;  // ranks of this step
-        const char *w = a.second + ((int64_t)max(adapter, 0) * a.M * a.R) * (int64_t)sizeof(T);
+        const char *w = a.second + ((int64_t)max(adapter, 0) * a.M * a.R2) * (int64_t)sizeof(T);
         constexpr int kMask = kRankBlock - 1;
         if constexpr (B_COL) {
             auto rank = [&](int i) { return BCol::row(i, wave, lane) & kMask; };
@@ -462,7 +646,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
             for (int i = 0; i < BRow::kLoads; ++i) {
                 const int g = BRow::group(i, wave);
                 const int64_t n = n0 + h * kHalf + g * 8 + (lane >> 3);
-                const uint64_t q = (uint64_t)(w + (n * a.R + block * kRankBlock + rank) * (int64_t)sizeof(T));
+                const uint64_t q = (uint64_t)(w + (n * a.R2 + block * kRankBlock + rank) * (int64_t)sizeof(T));
                 load_to_lds(n < a.M && rank < have ? q : (uint64_t)zero_unit(), place + g * 1024);
             }
         }
@@ -528,54 +712,84 @@ int adapter_many_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
 int adapter_main_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     a.mtiles = (a.N + BM - 1) / BM;
     a.ntiles = (a.M + BN - 1) / BN;
     dim3 grid;
     if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
     constexpr int kThreads = 64 * WM * WN;
-    if (b_col) timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, true, DIRECT>), grid, dim3(kThreads), 0, st, a);
-    else timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, false, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    if (b_col) timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, STAGES, true, DIRECT>), grid, dim3(kThreads), 0, st, a);
+    else timed_launch_ggl(true, (adapter_main<T, BM, BN, WM, WN, STAGES, false, DIRECT>), grid, dim3(kThreads), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 template <typename T, int MT, bool DIRECT>
 int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
-    constexpr int NW = 4, STAGES = DIRECT ? 3 : 2;
+    constexpr int NW = 8, STAGES = DIRECT ? 3 : 2;
     a.slots = tight_slots(a.N, a.S, __builtin_ctz(16 * MT));
     dim3 grid;
-    if (!tile_grid(a.slots * a.blocks, grid)) return SEGRED_ERR_UNSUPPORTED;
+    const int64_t copies = a.copy_from ? a.S * ((a.M + kCopyRows - 1) / kCopyRows) : 0;
+    if (!tile_grid(a.slots * a.blocks + copies, grid)) return SEGRED_ERR_UNSUPPORTED;
     if (b_col) timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, true, DIRECT>), grid, dim3(64 * NW), 0, st, a);
     else timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, false, DIRECT>), grid, dim3(64 * NW), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+constexpr int64_t kAdapterFew = 128;  // rows up to which waves split the contraction
 template <typename T>
 int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool main_direct, hipStream_t st) {
     int rc = low_direct ? adapter_low_launch<T, 1, true>(a, b_col, st) : adapter_low_launch<T, 1, false>(a, b_col, st);
     if (rc != SEGRED_OK) return rc;
-    if (!main_direct) return adapter_main_launch<T, 64, 64, 2, 2, false>(a, b_col, st);
-    if constexpr (sizeof(T) == 2)
-        if (a.N >= 512 && a.M >= 256) {
-            // a tile of 256 rows takes about 7/4 of one of 128; whole rounds of 256 CUs
-            const int64_t nt = (a.M + 255) / 256;
-            const int64_t one = ((a.N + 127) / 128 * nt + 255) / 256, two = ((a.N + 255) / 256 * nt + 255) / 256;
-            if (b_col || 4 * one < 7 * two) return adapter_many_launch<T, 1>(a, b_col, st);
+    if (main_direct && a.N <= kAdapterFew) {
+        if (a.N <= 16) return adapter_few_launch<T, 1, 8, 4>(a, b_col, st);
+        if (a.N <= 32) return adapter_few_launch<T, 2, 8, 3>(a, b_col, st);
+        if (a.N <= 48) return adapter_few_launch<T, 3, 4, 4>(a, b_col, st);
+        return adapter_few_launch<T, 4, 4, 3>(a, b_col, st);
+    }
+    if (!main_direct) return adapter_main_launch<T, 64, 64, 2, 2, 2, false>(a, b_col, st);
+    if constexpr (sizeof(T) == 2) {
+        // tiles of 128 x 256 in phases where there is one for every second CU
+        // (bfloat16, 2,048 x 2,048: 1,024 rows take 44 us in phases against 33
+        // in 64 x 64, 4,096 rows 55 against 91); 256 rows where that saves a
+        // round of 256 CUs, such a tile taking about 7/4 of one of 128
+        const int64_t nt = (a.M + 255) / 256, t1 = (a.N + 127) / 128 * nt, t2 = (a.N + 255) / 256 * nt;
+        if (a.M >= 256 && t1 >= 128) {
+            if (b_col || 4 * ((t1 + 255) / 256) < 7 * ((t2 + 255) / 256)) return adapter_many_launch<T, 1>(a, b_col, st);
             return adapter_many_launch<T, 2>(a, b_col, st);
         }
-    return adapter_main_launch<T, 64, 64, 2, 2, true>(a, b_col, st);
+    }
+    return adapter_main_launch<T, 64, 64, 2, 2, 3, true>(a, b_col, st);
 }
 
-size_t adapter_ids_bytes(int64_t rows) { return ((size_t)rows * 4 + 255) & ~size_t(255); }
+// Working memory: the rows' adapters, the low-rank rows, and a copy of the
+// second factor with whole units where its rows hold none.
+struct AdapterSpace {
+    size_t ids, low, copy;
+    int64_t ranks;  // between rows of the copy
+};
+AdapterSpace adapter_space(int64_t e, int64_t m, int64_t adapters, int64_t rank, int64_t rows) {
+    auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
+    AdapterSpace s{};
+    s.ids = up((size_t)rows * 4);
+    s.low = up((size_t)rows * ((rank + kRankBlock - 1) / kRankBlock) * 128);
+    s.ranks = (rank * e + 15) / 16 * 16 / e;
+    s.copy = (rank * e) % 16 == 0 ? 0 : (size_t)(adapters * m * s.ranks * e);
+    return s;
+}
 
 }  // namespace segred
 
 using namespace segred;
 
-extern "C" int64_t segred_adapter_workspace(int64_t rank, int64_t num_rows) {
-    if (rank < 1 || rank > kMaxWidth || num_rows < 1 || num_rows > (int64_t(1) << 40)) return 0;
-    return (int64_t)adapter_ids_bytes(num_rows) + num_rows * ((rank + kRankBlock - 1) / kRankBlock) * 128;
+extern "C" int64_t segred_adapter_workspace(int32_t dtype, int64_t m, int64_t adapters, int64_t rank, int64_t num_rows) {
+    const int64_t e = float_size(dtype);
+    if (e == 0 || m < 1 || adapters < 0 || rank < 1 || num_rows < 1 || m > kMaxWidth || rank > kMaxWidth ||
+        adapters > INT32_MAX || num_rows > (int64_t(1) << 40) || too_large(num_rows, rank + 64, 4) ||
+        too_large(adapters, m * (rank + 8), 4))
+        return 0;
+    const AdapterSpace s = adapter_space(e, m, adapters, rank, num_rows);
+    return (int64_t)(s.ids + s.low + s.copy);
 }
 
 extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, const void *weights, int64_t m,
@@ -595,10 +809,10 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
         !aligned(low, e) || !aligned(scale, 4) || !aligned(offsets, 8) || !aligned(which, 8) || !aligned(workspace, 16))
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (too_large(num_rows, k, 4) || too_large(num_rows, m, 4) || too_large(num_rows, rank, 4) ||
-        too_large(adapters, k * rank, 4) || too_large(adapters, m * rank, 4))
+        too_large(num_rows, rank + 64, 4) || too_large(adapters, k * rank, 4) || too_large(adapters, m * (rank + 8), 4))
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (!some) return SEGRED_OK;
-    const int64_t need = segred_adapter_workspace(rank, num_rows);
+    const int64_t need = segred_adapter_workspace(dtype, m, adapters, rank, num_rows);
     if (!workspace || workspace_bytes < need) return SEGRED_ERR_INVALID_ARGUMENT;
 
     AdapterArgs a{};
@@ -619,14 +833,21 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
     a.R = rank;
     a.blocks = (rank + kRankBlock - 1) / kRankBlock;
     a.ids = static_cast<int32_t *>(workspace);
-    a.u = static_cast<char *>(workspace) + adapter_ids_bytes(num_rows);
+    const AdapterSpace space = adapter_space(e, m, adapters, rank, num_rows);
+    a.u = static_cast<char *>(workspace) + space.ids;
+    a.R2 = rank;
+    if (!transpose && space.copy > 0 && num_rows > kAdapterFew) {
+        a.copy_from = a.second;
+        a.second = a.u + space.low;
+        a.R2 = space.ranks;
+    }
     a.low = static_cast<char *>(low);
     a.out = static_cast<char *>(out);
     a.vec = (a.M % 4 == 0 && aligned(out, 4 * e)) ? 1 : 0;
     auto units = [&](const void *p, int64_t width) { return (width * e) % 16 == 0 && aligned(p, 16); };
     const bool x = units(values, a.K);
     const bool low_direct = x && units(a.first, transpose ? rank : k);
-    const bool main_direct = x && units(weights, k) && units(a.second, transpose ? k : rank);
+    const bool main_direct = x && units(weights, k) && (num_rows <= kAdapterFew || units(a.second, transpose ? k : a.R2));
     switch (dtype) {
     case SEGRED_BF16: return adapter_dispatch<__bf16>(a, transpose != 0, low_direct, main_direct, stream);
     case SEGRED_F16: return adapter_dispatch<_Float16>(a, transpose != 0, low_direct, main_direct, stream);

@@ -319,7 +319,8 @@ __global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
         [](lds_char *) {},
         [&](int, const lds_char *buf) {
             step_products<T, true, 1, NT, 16, 16, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, 1, NT, lane);
-        });
+        },
+        [] {});
     T *out = reinterpret_cast<T *>(a.out);
     join_waves<NW, 1, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
         if (r < rows) store_quad<T>(out + (row0 + r) * a.M, n0 + c, a.M, sum, a.vec != 0);
@@ -364,9 +365,16 @@ int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
 //   64 x 128    110   104   111   145   185   292   488   col
 //   128 x 256               195   167   198   290   479   col
 //
-// and with few tiles (8 segments, 2,048 x 1,024): 64 x 128 takes 24 us at 256
-// rows and 51 at 1,024, 128 x 256 takes 34 and 67, 256 x 256 49 and 53.
-constexpr int64_t kFewRows = 8, kManyRows = 96, kManyColRows = 256, kManyTiles = 1536;
+// and with few tiles (8 segments, 2,048 x 1,024): 64 x 64 with three buffers
+// takes 14 us at 64 rows, 23 at 256 and 59 at 1,024, 64 x 128 22, 24 and 52,
+// 128 x 256 34 and 67 at 256 and 1,024, 256 x 256 49 and 53.
+// float (64 segments, 2,048 x 2,048; "row" and "col" are near each other):
+//
+//   mean          4    16    64   256   512
+//   few         187   243   673  2457
+//   32 x 64     210   277   508  1412  2629
+//   64 x 64     231   252   580  1464  2610
+constexpr int64_t kFewRows = 8, kManyRows = 96, kManyColRows = 256, kManyTiles = 1536, kFewTiles = 512;
 template <typename T>
 int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st) {
     const int64_t mean = a.N / a.S;
@@ -385,8 +393,10 @@ int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st
             if (b_col || 4 * one < 7 * two) return matmul_many_launch<T, 1>(a, b_col, st);
             return matmul_many_launch<T, 2>(a, b_col, st);
         }
+        if ((a.N / 64 + a.S / 2) * ((a.M + 63) / 64) <= kFewTiles) return matmul_launch<T, 64, 64, 2, 2, 3, true>(a, b_col, st);
         return matmul_launch<T, 64, 128, 2, 2, 2, true>(a, b_col, st);
     }
+    if (mean <= 96) return matmul_launch<T, 32, 64, 1, 4, 4, true>(a, b_col, st);
     return matmul_launch<T, 64, 64, 2, 2, 2, true>(a, b_col, st);
 }
 

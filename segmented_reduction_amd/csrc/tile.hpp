@@ -482,12 +482,14 @@ __device__ __forceinline__ void wait_own() {
 }
 
 // issue(t, live, buf): start step t (zeros where not live); commit(buf): write
-// units held in registers; products(t, buf).
-template <int STAGES, bool DIRECT, int LOADS, int BYTES, typename I, typename C, typename P>
-__device__ __forceinline__ void wave_steps(lds_char *lds, int t0, int t1, I issue, C commit, P products) {
+// units held in registers; products(t, buf); meanwhile(): what can be done
+// while the first steps arrive.
+template <int STAGES, bool DIRECT, int LOADS, int BYTES, typename I, typename C, typename P, typename M>
+__device__ __forceinline__ void wave_steps(lds_char *lds, int t0, int t1, I issue, C commit, P products, M meanwhile) {
     if constexpr (DIRECT) {
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) issue(t0 + i, t0 + i < t1, lds + i * BYTES);
+        meanwhile();
         int cur = 0, fill = STAGES - 1;
         for (int t = t0; t < t1; ++t) {
             wait_own<(STAGES - 2) * LOADS>();
@@ -502,6 +504,7 @@ __device__ __forceinline__ void wave_steps(lds_char *lds, int t0, int t1, I issu
             issue(t0, true, lds);
             commit(lds);
         }
+        meanwhile();
         for (int t = t0; t < t1; ++t) {
             wave_lds_sync();
             if (t + 1 < t1) issue(t + 1, true, lds);

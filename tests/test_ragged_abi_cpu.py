@@ -126,5 +126,7 @@ def test_workspaces():
     assert lib.segred_outer_workspace(4096, 4096, 8, 10000) == 0  # enough tiles without pieces
     assert lib.segred_outer_workspace(64, 96, 5, 300000) > 0
     assert lib.segred_outer_workspace(0, 96, 5, 300000) == 0 and lib.segred_outer_workspace(64, 96, 0, 10) == 0
-    assert lib.segred_adapter_workspace(16, 48) >= 48 * (4 + 128)
-    assert lib.segred_adapter_workspace(0, 48) == 0 and lib.segred_adapter_workspace(8, 0) == 0
+    assert 48 * (4 + 128) <= lib.segred_adapter_workspace(3, 4096, 32, 16, 48) < 48 * (4 + 128) + 512
+    assert lib.segred_adapter_workspace(3, 4096, 32, 12, 48) >= 48 * (4 + 128) + 32 * 4096 * 16 * 2
+    assert lib.segred_adapter_workspace(3, 64, 2, 0, 48) == 0 and lib.segred_adapter_workspace(3, 64, 2, 8, 0) == 0
+    assert lib.segred_adapter_workspace(0, 64, 2, 8, 8) == 0
