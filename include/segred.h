@@ -431,7 +431,10 @@ int segred_galloping_search(const void *values, int32_t dtype, int64_t value_cou
  *   out           [num_rows, m]; rows of no segment are left as they were.
  *
  * Rows and weights that hold whole 16-byte units on 16-byte boundaries are
- * copied to LDS directly, others through registers (slower).
+ * copied to LDS directly, others through registers (slower).  Larger float32
+ * calls form each product from three bf16 parts of either factor, exact to
+ * about 2^-22 of it like a product rounded to float32; values below 2^-102 may
+ * lose bits there (less than 2^-125 each), infinities and NaN do not.
  *
  * Errors: SEGRED_ERR_INVALID_ARGUMENT for an unknown dtype, k or m < 1,
  * negative counts, value_rows < num_rows without `rows`, a NULL pointer that

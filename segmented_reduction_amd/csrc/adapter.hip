@@ -145,7 +145,7 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
             else sbr.commit(buf + kABytes, 0, lane);
         },
         [&](int, const lds_char *buf) {
-            step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, MT, NT, lane);
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, lane);
         },
         [] {});
     const float scale = a.scale ? a.scale[adapter] : 1.f;
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
         if (__is_same(T, _Float16) && t >= base)
             split_products<MT, NT, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
         else
-            step_products<T, true, MT, NT, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, MT, NT, lane);
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
     };
     if constexpr (DIRECT) {
 #pragma unroll
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(64 * NW) void adapter_main_few(AdapterArgs a) {
         },
         [](lds_char *) {},
         [&](int, const lds_char *buf) {
-            step_products<T, true, MT, 1, 16, 16, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, MT, 1, lane);
+            step_products<T, MT, 1, false, BM, B_COL, BN>(acc, buf, buf + kABytes, 0, 0, lane);
         },
         [&] {
             // this thread's quad in join_waves()

@@ -1,7 +1,6 @@
 // matmul.hip -- the matrix product of each segment's rows with weights of its
 // own: out[r] = values[r] W[s] for the rows r of segment s.
 #include <algorithm>
-#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
@@ -20,90 +19,109 @@ struct MatmulArgs {
     int vec;
 };
 
-// One BM x BN tile of one segment per workgroup.
-template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
-    constexpr int kThreads = 64 * WM * WN;
-    constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+// A tile of one segment: rows row0 .. row0 + rows - 1, columns from n0.
+struct MatmulPlace {
+    int64_t s, row0, n0;
+    int rows;  // 0: nothing to do
+};
+template <int BM, int BN>
+__device__ __forceinline__ MatmulPlace matmul_place(const MatmulArgs &a, int lane) {
     constexpr int kLg = __builtin_ctz(BM);
+    MatmulPlace p{0, 0, 0, 0};
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return p;
+    const TilePlace at = tile_place(id, a.slots, a.ntiles);
+    p.s = tight_segment(a.offsets, a.S, kLg, at.m, lane);
+    p.n0 = at.n * BN;
+    p.row0 = a.offsets[p.s] + ((at.m - tight_key(a.offsets, p.s, kLg)) << kLg);
+    const int64_t end = min(a.offsets[p.s + 1], a.N);
+    if (p.row0 < end && p.row0 >= 0) p.rows = (int)min((int64_t)BM, end - p.row0);
+    return p;
+}
+
+// Start of the values row behind tile row r, or null for a row of zeros.
+__device__ __forceinline__ const char *matmul_row(const MatmulArgs &a, const MatmulPlace &p, int r, int64_t row_bytes) {
+    if (r >= p.rows) return nullptr;
+    int64_t v = p.row0 + r;
+    if (a.rows) v = a.rows[v];
+    return v >= 0 && v < a.value_rows ? a.values + v * row_bytes : nullptr;
+}
+
+// Stores a wave's neighbouring blocks.
+template <typename T, int MT, int NT>
+__device__ __forceinline__ void matmul_store(const MatmulArgs &a, const MatmulPlace &p, const f32x4 (&acc)[MT][NT],
+                                             int m_w, int n_w, int lane) {
+    T *out = reinterpret_cast<T *>(a.out);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int r = m_w + 16 * i + (lane & 15);
+        if (r < p.rows) {
+            T *row = out + (p.row0 + r) * a.M;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                store_quad<T>(row, p.n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+        }
+    }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
+struct MatmulTile {
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     using AStage = RowStage<T, BM, kThreads, DIRECT>;
     using BRow = RowStage<T, BN, kThreads, DIRECT>;
     using BCol = ColStage<T, BN, kThreads, DIRECT>;
-    constexpr int kABytes = AStage::kBytes;
-    constexpr int kBBytes = B_COL ? BCol::kBytes : BRow::kBytes;
-    constexpr int kStageBytes = kABytes + kBBytes;
-    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    static constexpr int kABytes = AStage::kBytes;
+    static constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    static constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    static constexpr int kLds = STAGES * kStageBytes;
     static_assert(DIRECT || STAGES == 2, "units that pass through registers use two buffers");
-    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes];
-    lds_char *lds = (lds_char *)lds_mem;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t id = xcd_tile(a.slots * a.ntiles);
-    if (id >= a.slots * a.ntiles) return;
-    const TilePlace at = tile_place(id, a.slots, a.ntiles);
-    const int64_t slot = at.m;
-    const int64_t n0 = at.n * BN;
-
-    const int64_t s = tight_segment(a.offsets, a.S, kLg, slot, lane);
-    const int64_t row0 = a.offsets[s] + ((slot - tight_key(a.offsets, s, kLg)) << kLg);
-    const int64_t end = min(a.offsets[s + 1], a.N);
-    if (row0 >= end || row0 < 0) return;
-    const int rows = (int)min((int64_t)BM, end - row0);
-
-    AStage sa;
-    const int K = (int)a.K;
-    sa.init(wave, lane, K, [&](int r) -> const char * {
-        if (r >= rows) return nullptr;
-        int64_t v = row0 + r;
-        if (a.rows) v = a.rows[v];
-        if (v < 0 || v >= a.value_rows) return nullptr;
-        return a.values + v * a.K * (int64_t)sizeof(T);
-    });
-    const char *w = a.weights + s * a.K * a.M * (int64_t)sizeof(T);
-    BRow sbr;
-    BCol sbc;
-    uint64_t wp[BCol::kLoads];
-    int wleft[BCol::kLoads];
-    if constexpr (B_COL) {
-#pragma unroll
-        for (int i = 0; i < BCol::kLoads; ++i) {
-            const int64_t n = n0 + BCol::col(i, wave, lane);
-            wp[i] = (uint64_t)(w + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
-            wleft[i] = (int)(a.M - n);
-        }
-    } else {
-        sbr.init(wave, lane, K, [&](int r) -> const char * {
-            return n0 + r < a.M ? w + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
-        });
-    }
-    auto issue = [&](int t, lds_char *buf) {
-        const int k0 = t * kStep<T>;
-        sa.issue(buf, wave, k0);
+    static __device__ __forceinline__ void run(const MatmulArgs &a, const MatmulPlace &p, lds_char *lds, int wave, int lane) {
+        AStage sa;
+        const int K = (int)a.K;
+        const int64_t n0 = p.n0;
+        sa.init(wave, lane, K, [&](int r) { return matmul_row(a, p, r, a.K * (int64_t)sizeof(T)); });
+        const char *w = a.weights + p.s * a.K * a.M * (int64_t)sizeof(T);
+        BRow sbr;
+        BCol sbc;
+        uint64_t wp[BCol::kLoads];
+        int wleft[BCol::kLoads];
         if constexpr (B_COL) {
-            const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
-            sbc.issue(
-                buf + kABytes, wave, [&](int i) { return wp[i] + step; },
-                [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
+#pragma unroll
+            for (int i = 0; i < BCol::kLoads; ++i) {
+                const int64_t n = n0 + BCol::col(i, wave, lane);
+                wp[i] = (uint64_t)(w + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+                wleft[i] = (int)(a.M - n);
+            }
         } else {
-            sbr.issue(buf + kABytes, wave, k0);
+            sbr.init(wave, lane, K, [&](int r) -> const char * {
+                return n0 + r < a.M ? w + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+            });
         }
-    };
-    auto commit = [&](lds_char *buf) {
-        sa.commit(buf, wave, lane);
-        if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
-        else sbr.commit(buf + kABytes, wave, lane);
-    };
+        auto issue = [&](int t, lds_char *buf) {
+            const int k0 = t * kStep<T>;
+            sa.issue(buf, wave, k0);
+            if constexpr (B_COL) {
+                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                sbc.issue(
+                    buf + kABytes, wave, [&](int i) { return wp[i] + step; },
+                    [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
+            } else {
+                sbr.issue(buf + kABytes, wave, k0);
+            }
+        };
+        auto commit = [&](lds_char *buf) {
+            sa.commit(buf, wave, lane);
+            if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
+            else sbr.commit(buf + kABytes, wave, lane);
+        };
 
-    f32x4 acc[MT][NT] = {};
-    constexpr bool kDeal = kDealt<T>;
-    constexpr int MS = kDeal ? 16 * WM : 16, NS = kDeal ? 16 * WN : 16;
-    const int m_w = wave / WN * (kDeal ? 16 : 16 * MT), n_w = wave % WN * (kDeal ? 16 : 16 * NT);
-    const int mv = blocks_inside(rows, m_w, MS, MT), nv = blocks_inside(a.M - n0, n_w, NS, NT);
-    const int steps = (K + kStep<T> - 1) / kStep<T>;
-    auto walk = [&](auto full) {
+        f32x4 acc[MT][NT] = {};
+        const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+        const int steps = (K + kStep<T> - 1) / kStep<T>;
         auto products = [&](const lds_char *buf) {
-            step_products<T, decltype(full)::value, MT, NT, MS, NS, false, BM, B_COL, BN>(
-                acc, buf, buf + kABytes, m_w, n_w, mv, nv, lane);
+            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
         };
         if constexpr (DIRECT) {
 #pragma unroll
@@ -128,21 +146,101 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
                 if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
             }
         }
-    };
-    if (!kDeal || (rows == BM && a.M - n0 >= BN)) walk(std::true_type{});
-    else if constexpr (kDeal) walk(std::false_type{});
+        matmul_store<T, MT, NT>(a, p, acc, m_w, n_w, lane);
+    }
+};
 
-    T *out = reinterpret_cast<T *>(a.out);
+// One BM x BN tile of one segment per workgroup.
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
+    using Tile = MatmulTile<T, BM, BN, WM, WN, STAGES, B_COL, DIRECT>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const MatmulPlace p = matmul_place<BM, BN>(a, lane);
+    if (p.rows > 0) Tile::run(a, p, (lds_char *)lds_mem, wave, lane);
+}
+
+// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// computed again with float products.
+constexpr int kSplitThreads = 256;
+template <int BM, int BN, bool B_COL, bool WHOLE>
+__global__ __launch_bounds__(kSplitThreads) void seg_matmul_split(MatmulArgs a) {
+    using Plain = MatmulTile<float, 64, 64, 2, 2, 2, B_COL, false>;
+    using SA = SplitStage<BM, kSplitThreads, false, WHOLE>;
+    using SB = SplitStage<BN, kSplitThreads, B_COL, WHOLE>;
+    constexpr int MT = BM / 32, NT = BN / 32, kSplitLds = 3 * (SA::kPlane + SB::kPlane);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kSplitLds > Plain::kLds ? kSplitLds : Plain::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const MatmulPlace p = matmul_place<BM, BN>(a, lane);
+    if (p.rows == 0) return;
+
+    const int K = (int)a.K, M = (int)a.M;
+    SA sa;
+    SB sb;
+    uint64_t ap[SA::kParts], bp[SB::kParts];
+    int aleft[SA::kParts], bleft[SB::kParts];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = m_w + MS * i + (lane & 15);
-        if (r < rows) {
-            T *row = out + (row0 + r) * a.M;
+    for (int i = 0; i < SA::kParts; ++i) {
+        const char *q = matmul_row(a, p, SA::row(i, tid), a.K * 4);
+        ap[i] = (uint64_t)(q + SA::at(i, tid) * 4);
+        aleft[i] = q ? K - SA::at(i, tid) : 0;
+    }
+    const char *w = a.weights + p.s * a.K * a.M * 4;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                store_quad<T>(row, n0 + n_w + NS * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+    for (int i = 0; i < SB::kParts; ++i) {
+        const int64_t r = SB::row(i, tid), c = SB::at(i, tid);
+        if constexpr (B_COL) {
+            bp[i] = (uint64_t)(w + (r * a.M + p.n0 + c) * 4);
+            bleft[i] = (int)(a.M - p.n0 - c);
+        } else {
+            bp[i] = (uint64_t)(w + ((p.n0 + r) * a.K + c) * 4);
+            bleft[i] = p.n0 + r < a.M ? K - (int)c : 0;
         }
     }
+    f32x4 acc[MT][NT] = {};
+    float bad = 0.f;
+    const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
+    split_steps(
+        (K + kSplitK - 1) / kSplitK,
+        [&](int64_t t) {
+            const int k0 = (int)t * kSplitK;
+            sa.issue([&](int i) { return ap[i] + (uint64_t)k0 * 4; }, [&](int i) { return aleft[i] - k0; });
+            if constexpr (B_COL)
+                sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * M * 4; },
+                         [&](int i) { return k0 + SB::row(i, tid) < K ? bleft[i] : 0; });
+            else
+                sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * 4; }, [&](int i) { return bleft[i] - k0; });
+        },
+        [&] {
+            sa.commit(lds, tid, bad);
+            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+        },
+        [&] { split_step<MT, NT, false, BM, B_COL, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
+    if (__syncthreads_or(bad != 0.f)) {
+        for (int r = 0; r < p.rows; r += 64)
+            for (int c = 0; c < BN && p.n0 + c < a.M; c += 64) {
+                const MatmulPlace q{p.s, p.row0 + r, p.n0 + c, min(64, p.rows - r)};
+                __syncthreads();
+                Plain::run(a, q, lds, wave, lane);
+            }
+        return;
+    }
+    matmul_store<float, MT, NT>(a, p, acc, m_w, n_w, lane);
+}
+
+template <int BM, int BN>
+int matmul_split_launch(MatmulArgs a, bool b_col, hipStream_t st) {
+    a.slots = tight_slots(a.N, a.S, __builtin_ctz(BM));
+    a.ntiles = (a.M + BN - 1) / BN;
+    dim3 grid;
+    if (a.slots > INT64_MAX / a.ntiles || !tile_grid(a.slots * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    const bool whole = a.K % 8 == 0 && (!b_col || a.M % 8 == 0);
+    if (b_col && whole) timed_launch_ggl(true, (seg_matmul_split<BM, BN, true, true>), grid, dim3(kSplitThreads), 0, st, a);
+    else if (b_col) timed_launch_ggl(true, (seg_matmul_split<BM, BN, true, false>), grid, dim3(kSplitThreads), 0, st, a);
+    else if (whole) timed_launch_ggl(true, (seg_matmul_split<BM, BN, false, true>), grid, dim3(kSplitThreads), 0, st, a);
+    else timed_launch_ggl(true, (seg_matmul_split<BM, BN, false, false>), grid, dim3(kSplitThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
 // Many rows per segment: AH * 128 rows x 256 columns per workgroup, in phases.
@@ -318,7 +416,7 @@ __global__ __launch_bounds__(64 * NW) void seg_matmul_few(MatmulArgs a) {
         },
         [](lds_char *) {},
         [&](int, const lds_char *buf) {
-            step_products<T, true, 1, NT, 16, 16, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, 1, NT, lane);
+            step_products<T, 1, NT, false, 16, B_COL, 16 * NT>(acc, buf, buf + kABytes, 0, 0, lane);
         },
         [] {});
     T *out = reinterpret_cast<T *>(a.out);
@@ -368,24 +466,33 @@ int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
 // and with few tiles (8 segments, 2,048 x 1,024): 64 x 64 with three buffers
 // takes 14 us at 64 rows, 23 at 256 and 59 at 1,024, 64 x 128 22, 24 and 52,
 // 128 x 256 34 and 67 at 256 and 1,024, 256 x 256 49 and 53.
-// float (64 segments, 2,048 x 2,048; "row" and "col" are near each other):
+// float (64 segments, 2,048 x 2,048; "row" and "col" are near each other),
+// the last line in bf16 parts:
 //
-//   mean          4    16    64   256   512
-//   few         187   243   673  2457
-//   32 x 64     210   277   508  1412  2629
-//   64 x 64     231   252   580  1464  2610
+//   mean          4    16    32    64   256   512
+//   few         187   243
+//   32 x 64     209   242   322   470  1412  2629
+//   64 x 128    239   242   272   371   952  1728
+//
+// and with few tiles (8 segments, 2,048 x 1,024): 32 x 64 takes 46 us at 64 rows
+// and 124 at 256, 64 x 128 83 and 106.
 constexpr int64_t kFewRows = 8, kManyRows = 96, kManyColRows = 256, kManyTiles = 1536, kFewTiles = 512;
+constexpr int64_t kSplitRows = 24, kSplitTiles = 224;
 template <typename T>
 int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st) {
     const int64_t mean = a.N / a.S;
-    if (!direct) {
-        if (mean <= 2 * kFewRows) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
-        return matmul_launch<T, 64, 128, 2, 2, 2, false>(a, b_col, st);
-    }
-    if (mean <= kFewRows) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
-    if constexpr (sizeof(T) == 2) {
-        // 64 x 128 tiles, half a tile more per segment for its end
-        const int64_t tiles = (a.N / 64 + a.S / 2) * ((a.M + 127) / 128);
+    // 64 x 128 tiles, half a tile more per segment for its end
+    const int64_t tiles = (a.N / 64 + a.S / 2) * ((a.M + 127) / 128);
+    if constexpr (sizeof(T) == 4) {
+        if (direct && mean <= kFewRows) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
+        if (direct && (mean <= kSplitRows || tiles < kSplitTiles))
+            return matmul_launch<T, 32, 64, 1, 4, 4, true>(a, b_col, st);
+        if (mean <= kSplitRows) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
+        return matmul_split_launch<64, 128>(a, b_col, st);
+    } else {
+        if (!direct && mean <= 2 * kFewRows) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
+        if (!direct) return matmul_launch<T, 64, 128, 2, 2, 2, false>(a, b_col, st);
+        if (mean <= kFewRows) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
         if (a.K >= 256 && a.M > 128 && tiles >= kManyTiles && mean >= (b_col ? kManyColRows : kManyRows)) {
             // a tile of 256 rows takes about 7/4 of one of 128; whole rounds of 256 CUs
             const int64_t nt = (a.M + 255) / 256;
@@ -396,8 +503,6 @@ int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st
         if ((a.N / 64 + a.S / 2) * ((a.M + 63) / 64) <= kFewTiles) return matmul_launch<T, 64, 64, 2, 2, 3, true>(a, b_col, st);
         return matmul_launch<T, 64, 128, 2, 2, 2, true>(a, b_col, st);
     }
-    if (mean <= 96) return matmul_launch<T, 32, 64, 1, 4, 4, true>(a, b_col, st);
-    return matmul_launch<T, 64, 64, 2, 2, 2, true>(a, b_col, st);
 }
 
 }  // namespace segred

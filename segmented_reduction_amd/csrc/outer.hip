@@ -2,7 +2,6 @@
 // out[s] = sum over the rows r of segment s of left[r]^T right[r], the
 // gradient of the weights of a product over segments.
 #include <algorithm>
-#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
@@ -104,62 +103,74 @@ __device__ __forceinline__ void outer_store(const OuterArgs &a, int64_t s, int64
         store_quad<T>(static_cast<T *>(a.out) + (s * a.K + r) * a.M, n, a.M, c, a.vec != 0);
 }
 
+// Byte offset of the source row behind row r of a slot, -1: a row of zeros.
+__device__ __forceinline__ int64_t outer_source(const OuterPlace &at, const int64_t *index, int64_t count,
+                                                int64_t row_bytes, int64_t r) {
+    if (r >= at.rows) return -1;
+    const int64_t v = index ? index[at.row0 + r] : at.row0 + r;
+    return v >= 0 && v < count ? v * row_bytes : -1;
+}
+
+// Stores a wave's neighbouring blocks.
+template <typename T, int MT, int NT>
+__device__ __forceinline__ void outer_blocks(const OuterArgs &a, const OuterPlace &at, const f32x4 (&acc)[MT][NT],
+                                             int m_w, int n_w, int lane) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t r = at.m0 + m_w + 16 * i + (lane & 15);
+        if (r >= a.K) continue;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            outer_store<T>(a, at.s, at.slot, r, at.n0 + n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+    }
+}
+
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
-    constexpr int kThreads = 64 * WM * WN;
-    constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+struct OuterTile {
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     using SA = ColStage<T, BM, kThreads, DIRECT>;
     using SB = ColStage<T, BN, kThreads, DIRECT>;
-    constexpr int kStageBytes = SA::kBytes + SB::kBytes;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kStageBytes];
-    lds_char *lds = (lds_char *)lds_mem;
+    static constexpr int kStageBytes = SA::kBytes + SB::kBytes;
+    static constexpr int kLds = 2 * kStageBytes;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const OuterPlace at = outer_place(a, BM, BN, lane);
-    if (!at.work) return;
-    const int64_t s = at.s, slot = at.slot, row0 = at.row0, rows = at.rows, m0 = at.m0, n0 = at.n0;
-
-    SA sa;
-    SB sb;
-    int64_t ia[SA::kLoads], ib[SB::kLoads];  // source row of the next step's units, -1: none
-    auto fetch = [&](int64_t k0) {
+    static __device__ __forceinline__ void run(const OuterArgs &a, const OuterPlace &at, lds_char *lds, int wave, int lane) {
+        const int64_t m0 = at.m0, n0 = at.n0, lb = a.K * (int64_t)sizeof(T), rb = a.M * (int64_t)sizeof(T);
+        SA sa;
+        SB sb;
+        int64_t ia[SA::kLoads], ib[SB::kLoads];  // source rows of the next step's units
+        auto fetch = [&](int64_t k0) {
 #pragma unroll
-        for (int i = 0; i < SA::kLoads; ++i) {
-            const int64_t r = k0 + SA::row(i, wave, lane);
-            ia[i] = r < rows ? (a.left_rows ? a.left_rows[row0 + r] : row0 + r) : -1;
-        }
+            for (int i = 0; i < SA::kLoads; ++i)
+                ia[i] = outer_source(at, a.left_rows, a.left_count, lb, k0 + SA::row(i, wave, lane));
 #pragma unroll
-        for (int i = 0; i < SB::kLoads; ++i) {
-            const int64_t r = k0 + SB::row(i, wave, lane);
-            ib[i] = r < rows ? (a.right_rows ? a.right_rows[row0 + r] : row0 + r) : -1;
-        }
-    };
-    auto issue = [&](lds_char *buf) {
-        sa.issue(
-            buf, wave,
-            [&](int i) { return (uint64_t)(a.left + (ia[i] * a.K + m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-            [&](int i) { return ia[i] >= 0 && ia[i] < a.left_count ? (int)(a.K - m0) - SA::col(i, wave, lane) : 0; });
-        sb.issue(
-            buf + SA::kBytes, wave,
-            [&](int i) { return (uint64_t)(a.right + (ib[i] * a.M + n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-            [&](int i) { return ib[i] >= 0 && ib[i] < a.right_count ? (int)(a.M - n0) - SB::col(i, wave, lane) : 0; });
-    };
-    auto commit = [&](lds_char *buf) {
-        sa.commit(buf, wave, lane);
-        sb.commit(buf + SA::kBytes, wave, lane);
-    };
+            for (int i = 0; i < SB::kLoads; ++i)
+                ib[i] = outer_source(at, a.right_rows, a.right_count, rb, k0 + SB::row(i, wave, lane));
+        };
+        auto issue = [&](lds_char *buf) {
+            sa.issue(
+                buf, wave,
+                [&](int i) { return (uint64_t)(a.left + ia[i] + (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T)); },
+                [&](int i) { return ia[i] >= 0 ? (int)(a.K - m0) - SA::col(i, wave, lane) : 0; });
+            sb.issue(
+                buf + SA::kBytes, wave,
+                [&](int i) { return (uint64_t)(a.right + ib[i] + (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T)); },
+                [&](int i) { return ib[i] >= 0 ? (int)(a.M - n0) - SB::col(i, wave, lane) : 0; });
+        };
+        auto commit = [&](lds_char *buf) {
+            sa.commit(buf, wave, lane);
+            sb.commit(buf + SA::kBytes, wave, lane);
+        };
 
-    f32x4 acc[MT][NT] = {};
-    constexpr bool kDeal = kDealt<T>;
-    constexpr int MS = kDeal ? 16 * WM : 16, NS = kDeal ? 16 * WN : 16;
-    const int m_w = wave / WN * (kDeal ? 16 : 16 * MT), n_w = wave % WN * (kDeal ? 16 : 16 * NT);
-    const int mv = blocks_inside(a.K - m0, m_w, MS, MT), nv = blocks_inside(a.M - n0, n_w, NS, NT);
-    const int64_t steps = (rows + kStep<T> - 1) / kStep<T>;
-    auto walk = [&](auto full) {
-        fetch(0);
-        issue(lds);
-        fetch(kStep<T>);
-        commit(lds);
+        f32x4 acc[MT][NT] = {};
+        const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+        const int64_t steps = (at.rows + kStep<T> - 1) / kStep<T>;
+        if (steps > 0) {
+            fetch(0);
+            issue(lds);
+            fetch(kStep<T>);
+            commit(lds);
+        }
         for (int64_t t = 0; t < steps; ++t) {
             wait_and_meet<0>();
             lds_char *next = lds + ((t + 1) & 1) * kStageBytes;
@@ -168,25 +179,82 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
                 fetch((t + 2) * kStep<T>);
             }
             const lds_char *buf = lds + (t & 1) * kStageBytes;
-            step_products<T, decltype(full)::value, MT, NT, MS, NS, true, BM, true, BN>(
-                acc, buf, buf + SA::kBytes, m_w, n_w, mv, nv, lane);
+            step_products<T, MT, NT, true, BM, true, BN>(acc, buf, buf + SA::kBytes, m_w, n_w, lane);
             if (t + 1 < steps) commit(next);
         }
-    };
-    if (steps > 0) {
-        if (!kDeal || (a.K - m0 >= BM && a.M - n0 >= BN)) walk(std::true_type{});
-        else if constexpr (kDeal) walk(std::false_type{});
+        outer_blocks<T, MT, NT>(a, at, acc, m_w, n_w, lane);
     }
+};
 
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
+    using Tile = OuterTile<T, BM, BN, WM, WN, DIRECT>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const OuterPlace at = outer_place(a, BM, BN, lane);
+    if (at.work) Tile::run(a, at, (lds_char *)lds_mem, wave, lane);
+}
+
+// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// computed again with float products.
+// (Three workgroups a CU: 300,000 rows in 5 segments, 64 x 96 each, take 57 us
+// against 76 with the two that the registers would allow otherwise.)
+constexpr int kSplitThreads = 256;
+template <int BM, int BN, bool WHOLE>
+__global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a) {
+    using Plain = OuterTile<float, 64, 64, 2, 2, false>;
+    using SA = SplitStage<BM, kSplitThreads, true, WHOLE>;
+    using SB = SplitStage<BN, kSplitThreads, true, WHOLE>;
+    constexpr int MT = BM / 32, NT = BN / 32, kSplitLds = 3 * (SA::kPlane + SB::kPlane);
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kSplitLds > Plain::kLds ? kSplitLds : Plain::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const OuterPlace at = outer_place(a, BM, BN, lane);
+    if (!at.work) return;
+
+    SA sa;
+    SB sb;
+    int64_t ia[SA::kParts], ib[SB::kParts];  // source rows of the next step's parts
+    auto fetch = [&](int64_t k0) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t r = m0 + m_w + MS * i + (lane & 15);
-        if (r >= a.K) continue;
+        for (int i = 0; i < SA::kParts; ++i)
+            ia[i] = outer_source(at, a.left_rows, a.left_count, a.K * 4, k0 + SA::row(i, tid));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            outer_store<T>(a, s, slot, r, n0 + n_w + NS * j + (lane >> 4) * 4, acc[i][j]);
-        }
+        for (int i = 0; i < SB::kParts; ++i)
+            ib[i] = outer_source(at, a.right_rows, a.right_count, a.M * 4, k0 + SB::row(i, tid));
+    };
+    f32x4 acc[MT][NT] = {};
+    float bad = 0.f;
+    const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
+    const char *left = a.left + at.m0 * 4, *right = a.right + at.n0 * 4;
+    const int kleft = (int)(a.K - at.m0), mleft = (int)(a.M - at.n0);
+    fetch(0);
+    split_steps(
+        (at.rows + kSplitK - 1) / kSplitK,
+        [&](int64_t t) {
+            sa.issue([&](int i) { return (uint64_t)(left + ia[i] + SA::at(i, tid) * 4); },
+                     [&](int i) { return ia[i] >= 0 ? kleft - SA::at(i, tid) : 0; });
+            sb.issue([&](int i) { return (uint64_t)(right + ib[i] + SB::at(i, tid) * 4); },
+                     [&](int i) { return ib[i] >= 0 ? mleft - SB::at(i, tid) : 0; });
+            fetch((t + 1) * kSplitK);
+        },
+        [&] {
+            sa.commit(lds, tid, bad);
+            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+        },
+        [&] { split_step<MT, NT, true, BM, true, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
+    if (__syncthreads_or(bad != 0.f)) {
+        OuterPlace q = at;
+        for (int r = 0; r < BM && at.m0 + r < a.K; r += 64)
+            for (int c = 0; c < BN && at.n0 + c < a.M; c += 64) {
+                q.m0 = at.m0 + r;
+                q.n0 = at.n0 + c;
+                __syncthreads();
+                Plain::run(a, q, lds, wave, lane);
+            }
+        return;
     }
+    outer_blocks<float, MT, NT>(a, at, acc, m_w, n_w, lane);
 }
 
 // Wide operands: 128 x 256 of the output per workgroup, in phases (16-bit
@@ -206,16 +274,10 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const OuterPlace at = outer_place(a, kHalf, 2 * kHalf, lane);
     if (!at.work) return;
-    const int64_t s = at.s, slot = at.slot, row0 = at.row0, rows = at.rows, m0 = at.m0, n0 = at.n0;
+    const int64_t s = at.s, slot = at.slot, rows = at.rows, m0 = at.m0, n0 = at.n0;
 
-    // Byte offset of the source row of step row r.
-    auto source = [&](const int64_t *index, int64_t count, int64_t width, int64_t r) -> int64_t {
-        if (r >= rows) return -1;
-        const int64_t v = index ? index[row0 + r] : row0 + r;
-        return v >= 0 && v < count ? v * width * (int64_t)sizeof(T) : -1;
-    };
-    auto left_source = [&](int64_t r) { return source(a.left_rows, a.left_count, a.K, r); };
-    auto right_source = [&](int64_t r) { return source(a.right_rows, a.right_count, a.M, r); };
+    auto left_source = [&](int64_t r) { return outer_source(at, a.left_rows, a.left_count, a.K * (int64_t)sizeof(T), r); };
+    auto right_source = [&](int64_t r) { return outer_source(at, a.right_rows, a.right_count, a.M * (int64_t)sizeof(T), r); };
     for (int i = threadIdx.x; i < 4 * kRows; i += kPhaseThreads) {
         s_rows[0][i / kRows][i % kRows] = left_source(i);
         s_rows[1][i / kRows][i % kRows] = right_source(i);
@@ -362,17 +424,34 @@ int outer_many_launch(OuterArgs a, hipStream_t st) {
     return outer_finish<T>(a, st);
 }
 
+template <int BM, int BN>
+int outer_split_launch(OuterArgs a, hipStream_t st) {
+    a.mtiles = (a.K + BM - 1) / BM;
+    a.ntiles = (a.M + BN - 1) / BN;
+    dim3 grid;
+    if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (a.K % 8 == 0 && a.M % 8 == 0)
+        timed_launch_ggl(true, (seg_outer_split<BM, BN, true>), grid, dim3(kSplitThreads), 0, st, a);
+    else
+        timed_launch_ggl(true, (seg_outer_split<BM, BN, false>), grid, dim3(kSplitThreads), 0, st, a);
+    return outer_finish<float>(a, st);
+}
+
 template <typename T>
 int outer_dispatch(const OuterArgs &a, const OuterPlan &p, bool direct, hipStream_t st) {
-    if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
-    if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
-    // 128 x 256 in phases from two such tiles for every CU and eight steps a
-    // segment on: 16,384 rows in 8 segments of 4,096 x 4,096 take 876 us against
-    // 933, but 8,192 rows in 64 segments of 1,024 x 1,024 107 us against 72
-    if constexpr (sizeof(T) == 2)
+    if constexpr (sizeof(T) == 4) {
+        if (p.small && !p.wide) return outer_split_launch<64, 64>(a, st);
+        return outer_split_launch<64, 128>(a, st);
+    } else {
+        if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
+        if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
+        // 128 x 256 in phases from two such tiles for every CU and eight steps a
+        // segment on: 16,384 rows in 8 segments of 4,096 x 4,096 take 876 us
+        // against 933, but 8,192 rows in 64 segments of 1,024 x 1,024 107 against 72
         if (direct && a.S * ((a.K + 127) / 128) * ((a.M + 255) / 256) >= 2 * kCus && a.N >= a.S * 512)
             return outer_many_launch<T>(a, st);
-    return outer_launch<T, 128, 128, 2, 2>(a, direct, st);
+        return outer_launch<T, 128, 128, 2, 2>(a, direct, st);
+    }
 }
 
 }  // namespace segred

@@ -49,9 +49,9 @@ template <typename T> constexpr int kStep = 128 / (int)sizeof(T);  // k elements
 template <typename T> constexpr int kUnit = 16 / (int)sizeof(T);   // elements of a 16-byte unit
 
 // What a load beyond the operand's edge reads instead.
-__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
+__device__ const u32x4 kZeros[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
 
-__device__ __forceinline__ const char *zero_unit() { return reinterpret_cast<const char *>(&kZeros); }
+__device__ __forceinline__ const char *zero_unit() { return reinterpret_cast<const char *>(&kZeros[0]); }
 
 // 16 bytes per lane from global memory to LDS at `dst` + 16 * lane (dst is
 // wave-uniform), without passing through registers.
@@ -59,23 +59,34 @@ __device__ __forceinline__ void load_to_lds(uint64_t src, lds_char *dst) {
     __builtin_amdgcn_global_load_lds((global_void *)src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
 }
 
+// 16 bytes at any element boundary.  (As global memory: a flat load would also
+// be waited for by every LDS read behind it.)
+template <typename T>
+__device__ __forceinline__ u32x4 load_whole(uint64_t addr) {
+    typedef u32x4 __attribute__((aligned(2))) unit2;
+    typedef u32x4 __attribute__((aligned(4))) unit4;
+    if constexpr (sizeof(T) == 2) return *(__attribute__((address_space(1))) const unit2 *)addr;
+    return *(__attribute__((address_space(1))) const unit4 *)addr;
+}
+
 // Up to `n` leading elements of a 16-byte unit at any element boundary; the
 // others are zero and not touched (n <= 0: nothing is read).
 template <typename T>
 __device__ __forceinline__ u32x4 load_unit(uint64_t addr, int n) {
-    const char *src = reinterpret_cast<const char *>(addr);
+    typedef __attribute__((address_space(1))) const uint32_t global_u32;
+    typedef __attribute__((address_space(1))) const uint16_t global_u16;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (n >= kUnit<T>) {
-        __builtin_memcpy(&v, __builtin_assume_aligned(src, sizeof(T)), 16);
+        v = load_whole<T>(addr);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < n) v[j] = reinterpret_cast<const uint32_t *>(src)[j];
+        for (int j = 0; j < 3; ++j)
+            if (j < n) v[j] = ((global_u32 *)addr)[j];
     } else {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = 2 * j < n ? s[2 * j] : 0u, hi = 2 * j + 1 < n ? s[2 * j + 1] : 0u;
+            const uint32_t lo = 2 * j < n ? ((global_u16 *)addr)[2 * j] : 0u;
+            const uint32_t hi = 2 * j + 1 < n ? ((global_u16 *)addr)[2 * j + 1] : 0u;
             v[j] = lo | hi << 16;
         }
     }
@@ -238,51 +249,29 @@ __device__ __forceinline__ f32x4 mma(u32x4 b, u32x4 a, f32x4 c) {
     }
 }
 
-// One step of a wave's MT x NT blocks of 16 x 16 of the workgroup's tile: rows
-// m0 + MS * i and columns n0 + NS * j.  Unless FULL, only the first mv block
-// rows and nv block columns are multiplied (wave-uniform): the others lie past
-// the edge.
-template <typename T, bool FULL, int MT, int NT, int MS, int NS, bool A_COL, int AW, bool B_COL, int BW>
+// One step of a wave's MT x NT neighbouring blocks of 16 x 16: rows from m0,
+// columns from n0 of the workgroup's tile.
+template <typename T, int MT, int NT, bool A_COL, int AW, bool B_COL, int BW>
 __device__ __forceinline__ void step_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
-                                              int n0, int mv, int nv, int lane) {
+                                              int n0, int lane) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         u32x4 a[MT], b[NT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            if (!FULL && i >= mv) continue;
-            if constexpr (A_COL) a[i] = col_frag<T, AW>(la, m0 + MS * i, ks, lane);
-            else a[i] = row_frag(la, m0 + MS * i, ks, lane);
+            if constexpr (A_COL) a[i] = col_frag<T, AW>(la, m0 + 16 * i, ks, lane);
+            else a[i] = row_frag(la, m0 + 16 * i, ks, lane);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if (!FULL && j >= nv) continue;
-            if constexpr (B_COL) b[j] = col_frag<T, BW>(lb, n0 + NS * j, ks, lane);
-            else b[j] = row_frag(lb, n0 + NS * j, ks, lane);
+            if constexpr (B_COL) b[j] = col_frag<T, BW>(lb, n0 + 16 * j, ks, lane);
+            else b[j] = row_frag(lb, n0 + 16 * j, ks, lane);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (!FULL && i >= mv) continue;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (FULL || j < nv) acc[i][j] = mma<T>(b[j], a[i], acc[i][j]);
-        }
+            for (int j = 0; j < NT; ++j) acc[i][j] = mma<T>(b[j], a[i], acc[i][j]);
     }
-}
-
-// How a workgroup's blocks go to its waves.  float blocks are dealt in turn,
-// and a tile that crosses the edge skips those past it: the matrix rate of
-// float is a sixteenth of the 16-bit types', so that is what such a tile waits
-// for.  The 16-bit types keep neighbouring blocks together and multiply zeros:
-// the skipping branches cost more than they save (128 x 128 tiles of a product
-// of 8192^3 in bfloat16: 1,446 us without, 5,451 us with them).
-template <typename T> constexpr bool kDealt = sizeof(T) == 4;
-
-// Blocks of a wave that lie before the edge: `left` rows (columns) from the
-// tile's start, the wave's first block at `first`, the others `stride` apart.
-__device__ __forceinline__ int blocks_inside(int64_t left, int first, int stride, int most) {
-    const int n = (int)(min(left, (int64_t)1 << 20) - first + stride - 1) / stride;
-    return n < 0 ? 0 : n > most ? most : n;
 }
 
 // ------------------------------------------------------------------- waits
@@ -302,6 +291,137 @@ inline bool tile_grid(int64_t total, dim3 &grid) {
     if (y > 65535) return false;
     grid = dim3((unsigned)(y > 1 ? kGridFold : total), (unsigned)y);
     return true;
+}
+
+// ------------------------------------------------------- float in three bf16
+//
+// v_mfma_f32_16x16x4_f32 runs at a sixteenth of the 16-bit rate, so a float
+// product is made of 16-bit ones: x = h + m + l exactly, h the leading 8 bits
+// of x (cut off), m and l the remainders rounded to bf16, and
+//   x y = h h' + (h m' + m h') + (h l' + m m' + l h') + ...
+// with what is left out (m l', l m', l l') below 2^-22 |x y|, about the
+// rounding of a product to float.  Six products at 16 times the rate.  bf16 has
+// float's exponents, but the matrix cores take parts below 2^-126 for zero, so
+// that values below 2^-102 lose bits (less than 2^-125 each).  An infinity has no such parts: whoever splits one
+// (or a NaN) notes it, and the tile is computed again with float products, so
+// that infinities and NaN come out as float arithmetic gives them.
+//
+// A step is 32 k.  It passes through registers, is split on its way into LDS
+// and lies there as three planes in the forms of the 16-bit types (row form
+// with rows of 64 bytes: unit u of row r at place u ^ (r >> 2 & 3)).
+constexpr int kSplitK = 32;
+
+struct Split {
+    u32x4 h, m, l;
+};
+// Splits eight floats; `bad` becomes NaN where one is infinite or NaN.
+__device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b, float &bad) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    Split s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x0 = j < 2 ? a[2 * j] : b[2 * j - 4], x1 = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+        const uint32_t t0 = x0 & 0xffff0000u, t1 = x1 & 0xffff0000u;
+        const float r0 = __uint_as_float(x0) - __uint_as_float(t0), r1 = __uint_as_float(x1) - __uint_as_float(t1);
+        const uint32_t m = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{r0, r1}), bf16x2));
+        const float q0 = r0 - __uint_as_float(m << 16), q1 = r1 - __uint_as_float(m & 0xffff0000u);
+        s.h[j] = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
+        s.m[j] = m;
+        s.l[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{q0, q1}), bf16x2));
+        bad = fmaf(q0, 0.f, bad);
+        bad = fmaf(q1, 0.f, bad);
+    }
+    return s;
+}
+
+// One operand's step in registers: W rows (or columns) of 32 k, eight
+// neighbouring floats at a time.  COL: W neighbours of one k, else 32 k of one
+// row.  WHOLE: rows hold whole parts, so that each is there or not.
+template <int W, int THREADS, bool COL, bool WHOLE>
+struct SplitStage {
+    static constexpr int kParts = W * 4 / THREADS;  // of eight floats, per thread
+    static constexpr int kPlane = W * 64;           // bytes
+    static_assert(kParts >= 1 && W * 4 % THREADS == 0, "whole parts");
+    u32x4 v[kParts][2];
+
+    // Row (k if COL) and first element inside it of part i.
+    static __device__ __forceinline__ int row(int i, int tid) { return (i * THREADS + tid) / (COL ? W / 8 : 4); }
+    static __device__ __forceinline__ int at(int i, int tid) { return (i * THREADS + tid) % (COL ? W / 8 : 4) * 8; }
+    // src(i): address of part i; left(i): floats of its row from there on.
+    template <typename F, typename G>
+    __device__ __forceinline__ void issue(F src, G left) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if constexpr (WHOLE) {
+                const uint64_t q = left(i) > 0 ? src(i) : (uint64_t)zero_unit();
+                v[i][0] = load_whole<float>(q);
+                v[i][1] = load_whole<float>(q + 16);
+            } else {
+                v[i][0] = load_unit<float>(src(i), left(i));
+                v[i][1] = load_unit<float>(src(i) + 16, left(i) - 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void commit(lds_char *lds, int tid, float &bad) const {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int r = row(i, tid), c = at(i, tid);
+            int off;
+            if constexpr (COL) off = r * W * 2 + (((c >> 4) ^ col_swizzle<__bf16, W>(r)) << 5) + (c & 8) * 2;
+            else off = r * 64 + (((c >> 3) ^ ((r >> 2) & 3)) << 4);
+            const Split s = split_unit(v[i][0], v[i][1], bad);
+            typedef __attribute__((address_space(3))) u32x4 lds_unit;
+            *reinterpret_cast<lds_unit *>(lds + off) = s.h;
+            *reinterpret_cast<lds_unit *>(lds + kPlane + off) = s.m;
+            *reinterpret_cast<lds_unit *>(lds + 2 * kPlane + off) = s.l;
+        }
+    }
+};
+
+template <bool COL, int W>
+__device__ __forceinline__ u32x4 split_frag(const lds_char *plane, int r0, int lane) {
+    if constexpr (COL) return col_frag<__bf16, W>(plane, r0, 0, lane);
+    const int off = (r0 + (lane & 15)) * 64 + (((lane >> 4) ^ ((lane >> 2) & 3)) << 4);
+    return *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(plane + off);
+}
+
+// One step of a wave's MT x NT neighbouring blocks, the small terms first.
+template <int MT, int NT, bool A_COL, int AW, bool B_COL, int BW>
+__device__ __forceinline__ void split_step(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0, int n0,
+                                           int lane) {
+    u32x4 a[3][MT];
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) a[p][i] = split_frag<A_COL, AW>(la + p * AW * 64, m0 + 16 * i, lane);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        u32x4 b[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) b[p] = split_frag<B_COL, BW>(lb + p * BW * 64, n0 + 16 * j, lane);
+#pragma unroll
+        for (int q = 0; q < 6; ++q) {
+            constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i][j] = mma<__bf16>(b[kB[q]], a[kA[q]][i], acc[i][j]);
+        }
+    }
+}
+
+// Walks the steps of a tile: issue(t) loads into registers, commit() writes
+// them, products() multiplies.  One buffer; a second workgroup on the CU works
+// through the waits.
+template <typename I, typename C, typename P>
+__device__ __forceinline__ void split_steps(int64_t steps, I issue, C commit, P products) {
+    if (steps > 0) issue(0);
+    for (int64_t t = 0; t < steps; ++t) {
+        commit();
+        __syncthreads();
+        if (t + 1 < steps) issue(t + 1);
+        products();
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------- in phases

@@ -53,7 +53,7 @@ def matmul(values, weights, off, transpose=False, rows=None, fill=0.0):
         x = torch.where(ok[:, None], x[rows.clamp(0, max(x.shape[0] - 1, 0))], 0.0)
     w = weights.double()
     w = w.transpose(1, 2) if transpose else w
-    out = torch.full((x.shape[0], w.shape[2]), fill, dtype=torch.float64)
+    out = torch.full((x.shape[0], w.shape[2]), fill, dtype=torch.float64, device=x.device)
     mag = torch.zeros_like(out)
     o = off.tolist()
     for s, (a, b) in enumerate(zip(o[:-1], o[1:])):

@@ -135,6 +135,80 @@ def test_infinity_and_nan_of_a_row_stay_in_it():
         assert not bad.any()
 
 
+def _same_specials(got, ref, mag, n, what, lost):
+    """NaN and infinities where the 64-bit form has them, the rest within the
+    bound.  Where the terms' magnitudes pass float's range, a float sum may
+    pass it on the way, in any order of its own: nothing is asked there.
+    `lost`: the parts that a value is split into (x = h + m + l) count as zero
+    below 2^-126, the smallest normal bf16, so that a term x w is off by less
+    than 2^-125 (|x| + |w|): the sum of |x| + |w| over the terms."""
+    within = ~(mag > torch.finfo(torch.float32).max) | ~torch.isfinite(ref)
+    got, ref, mag, lost = got.cpu()[within], ref[within], mag[within], lost[within]
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+    inf = torch.isinf(ref)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf].double(), ref[inf]), what
+    fine = torch.isfinite(ref)
+    ru.assert_close(got[fine], ref[fine], mag[fine], n, what, more=2.0 ** -125 * lost[fine])
+
+
+@pytest.mark.parametrize("m", [512, 500])
+def test_float_specials_in_large_calls(m):
+    """float32 products made of bf16 parts: infinities, NaN, the largest and
+    the smallest values come out as float arithmetic gives them."""
+    g = ru.gen(m)
+    off = ru.offsets([700, 0, 500, 900, 300, 600, 512, 488])
+    n, k = int(off[-1]), 96
+    x, w = ru.randn(g, n, k), ru.randn(g, 8, k, m)
+    x[5, 3], x[800, 90], x[1500, 0] = float("inf"), float("nan"), float("-inf")
+    w[6, 7, 11] = float("inf")
+    x[2000] = x[2200] = torch.finfo(torch.float32).max
+    w[4] *= 1e-30  # segment 4 has row 2200: large times small
+    x[2500] *= 1e-30
+    x[2501] *= 1e-38
+    ru.say(f"float specials m={m}")
+    out = sr().matmul(x.cuda(), w.cuda(), off.cuda())
+    ref, mag = ru.matmul(x, w, off)
+    lost = ru.matmul(x, torch.ones_like(w), off)[1] + ru.matmul(torch.ones_like(x), w, off)[1]
+    _same_specials(out, ref, mag, k, "matmul", lost)
+    out = sr().matmul(x.cuda(), w.transpose(1, 2).contiguous().cuda(), off.cuda(), transpose=True)
+    _same_specials(out, ref, mag, k, "matmul transposed", lost)
+    y = ru.randn(g, n, m)
+    y[5, 8] = float("nan")
+    x[2000] = x[2200] = 1.0
+    dw = sr().outer(x.cuda(), y.cuda(), off.cuda())
+    ref, mag = ru.outer(x, y, off)
+    lost = ru.outer(x, torch.ones_like(y), off)[1] + ru.outer(torch.ones_like(x), y, off)[1]
+    _same_specials(dw, ref, mag, 900, "outer", lost)
+    dw = sr().outer(x[:, :24].contiguous().cuda(), y[:, :40].contiguous().cuda(), off.cuda())
+    ref, mag = ru.outer(x[:, :24], y[:, :40], off)
+    _same_specials(dw, ref, mag, 900, "outer, in pieces", lost[:, :24, :40])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,segments,k,m", [(3000, 4, 320, 512), (3000, 4, 331, 515), (6000, 3, 264, 1024),
+                                               (1500, 40, 128, 640), (2100, 70, 72, 136), (5000, 12, 520, 1032)])
+def test_larger_calls(kind, rows, segments, k, m):
+    """Sizes at which the larger tiles are taken, both layouts, gathered and not, against 64 bits on the GPU."""
+    t, g = ru.TYPES[kind], ru.gen(rows + k)
+    cuts = torch.randint(0, rows + 1, (segments - 1,), generator=g).sort().values.tolist()
+    off = torch.tensor([0, *cuts, rows])
+    x, y = ru.randn(g, rows, k, dtype=t), ru.randn(g, rows, m, dtype=t)
+    w = ru.randn(g, segments, k, m, dtype=t)
+    idx = torch.randint(0, rows, (rows,), generator=g)
+    ru.say(f"larger {kind} N={rows} S={segments} k={k} m={m}")
+    s = sr()
+    for rows_t in (None, idx):
+        ref, mag = ru.matmul(x.cuda(), w.cuda(), off, rows=None if rows_t is None else rows_t.cuda())
+        ref, mag = ref.cpu(), mag.cpu()
+        cuda_idx = None if rows_t is None else rows_t.cuda()
+        ru.assert_close(s.matmul(x.cuda(), w.cuda(), off.cuda(), rows=cuda_idx), ref, mag, k, "matmul")
+        wt = w.transpose(1, 2).contiguous().cuda()
+        ru.assert_close(s.matmul(x.cuda(), wt, off.cuda(), rows=cuda_idx, transpose=True), ref, mag, k, "transposed")
+    longest = int((off[1:] - off[:-1]).max())
+    ref, mag = ru.outer(x.cuda(), y.cuda(), off, left_rows=idx.cuda())
+    ru.assert_close(s.outer(x.cuda(), y.cuda(), off.cuda(), left_rows=idx.cuda()), ref.cpu(), mag.cpu(), longest, "outer")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_unaligned_bases(kind):
     """Inputs and output that start off a 16-byte boundary give the same results."""
