@@ -31,17 +31,23 @@ struct GroupArgs {
     int64_t *position;                     // last pass, where there is one or there are more than two
     uint32_t *where;                       // place of each input of this pass (two passes)
     int64_t *offsets;                      // where there is one pass
-    uint32_t *hist;                        // [digits][tiles]
+    uint32_t *hist;                        // [tiles][digits] where few, else [digits][tiles]
     uint32_t *totals;                      // [digits]
     uint32_t rows, dim, tiles, fanout;
     int shift, bits;
     int first, last;
+    int few;  // few tiles: group_place adds up their counts itself
 };
 
 constexpr int kGroupThreads = 256;
 constexpr int kGroupWaves = kGroupThreads / 64;
-constexpr int kGroupSteps = 16;  // entries per lane
-constexpr int kGroupTile = kGroupThreads * kGroupSteps;
+// Entries per lane of a tile.  Short ones up to 65,536 entries, so that there
+// are tiles for more CUs.  Where tiles and digits are few a workgroup adds up
+// the counts of the tiles before its own, which saves the launch of the scan:
+// 32,768 entries of 64 groups take 13 us in 32 tiles and two launches, 23 in 8
+// tiles and three; but of 2,000 groups 40 against 31.
+constexpr int kGroupShort = 4, kGroupLong = 16;
+constexpr int64_t kGroupShortRows = 65536, kGroupFewTiles = 64, kGroupFewCounts = 32768;
 constexpr int kGroupMaxBits = 11;
 constexpr uint32_t kNoPlace = 0xffffffffu;
 
@@ -89,24 +95,24 @@ __device__ __forceinline__ void digit_bases(const uint32_t *totals, int digits, 
 }
 
 // Entries of each digit in each tile.
-template <int BITS>
+template <int BITS, int STEPS>
 __global__ __launch_bounds__(kGroupThreads) void group_count(GroupArgs a) {
     extern __shared__ uint32_t s_count[];  // [waves][digits]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    constexpr int digits = 1 << BITS;
+    constexpr int digits = 1 << BITS, kTile = kGroupThreads * STEPS;
     for (int i = threadIdx.x; i < kGroupWaves * digits; i += kGroupThreads) s_count[i] = 0;
     __syncthreads();
     uint32_t *mine = s_count + wave * digits;
     const uint32_t tile = (uint32_t)xcd_tile(a.tiles);
-    const uint32_t first = tile * kGroupTile + wave * 64 * kGroupSteps;
-    uint32_t key[kGroupSteps];
+    const uint32_t first = tile * kTile + wave * 64 * STEPS;
+    uint32_t key[STEPS];
 #pragma unroll
-    for (int i = 0; i < kGroupSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const uint32_t e = first + i * 64 + lane;
         key[i] = e < a.rows ? (a.first ? group_key(a.index[e], a.dim) : a.keys_in[e]) : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < kGroupSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const bool valid = first + i * 64 + lane < a.rows;
         const uint32_t d = (key[i] >> a.shift) & (digits - 1);
         const uint64_t same = same_digit<BITS>(d, valid);
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_count(GroupArgs a) {
         uint32_t n = 0;
 #pragma unroll
         for (int w = 0; w < kGroupWaves; ++w) n += s_count[w * digits + d];
-        a.hist[(size_t)d * a.tiles + tile] = n;
+        a.hist[a.few ? (size_t)tile * digits + d : (size_t)d * a.tiles + tile] = n;
     }
 }
 
@@ -149,31 +155,48 @@ __global__ __launch_bounds__(kGroupThreads) void group_scan(GroupArgs a) {
 }
 
 // Moves each entry to its place in this pass's order.
-template <int BITS>
+template <int BITS, int STEPS>
 __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
     extern __shared__ uint32_t s_count[];  // [waves][digits], [digits] bases, [digits] places, [tile] keys, [tile] entries
     __shared__ int64_t s_tmp[2 * kGroupWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    constexpr int digits = 1 << BITS;
+    constexpr int digits = 1 << BITS, kTile = kGroupThreads * STEPS;
     uint32_t *s_base = s_count + kGroupWaves * digits, *s_place = s_base + digits;
-    uint32_t *s_key = s_place + digits, *s_entry = s_key + kGroupTile;
+    uint32_t *s_key = s_place + digits, *s_entry = s_key + kTile;
     for (int i = threadIdx.x; i < kGroupWaves * digits; i += kGroupThreads) s_count[i] = 0;
-    digit_bases<kGroupThreads>(a.totals, digits, s_base, s_tmp);
     const uint32_t tile = (uint32_t)xcd_tile(a.tiles);
+    if (a.few) {
+        for (int d = threadIdx.x; d < digits; d += kGroupThreads) {
+            uint32_t before = 0, n = 0;
+#pragma unroll 8
+            for (uint32_t t = 0; t < a.tiles; ++t) {
+                const uint32_t c = a.hist[(size_t)t * digits + d];
+                before += t < tile ? c : 0u;
+                n += c;
+            }
+            s_base[d] = n;
+            s_place[d] = before;  // until the digits of this tile are known
+            if (a.last && tile == 0) a.totals[d] = n;
+        }
+        __syncthreads();
+        digit_bases<kGroupThreads>(s_base, digits, s_base, s_tmp);
+    } else {
+        digit_bases<kGroupThreads>(a.totals, digits, s_base, s_tmp);
+    }
     if (a.offsets && tile == 0)  // one pass: the digits are the groups
         for (uint32_t d = threadIdx.x; d <= a.dim; d += kGroupThreads) a.offsets[d] = s_base[d];
     uint32_t *mine = s_count + wave * digits;
-    const uint32_t begin = tile * kGroupTile, first = begin + wave * 64 * kGroupSteps;
-    const int have = (int)min((uint32_t)kGroupTile, a.rows - begin);
-    uint32_t key[kGroupSteps], entry[kGroupSteps], rank[kGroupSteps];
+    const uint32_t begin = tile * kTile, first = begin + wave * 64 * STEPS;
+    const int have = (int)min((uint32_t)kTile, a.rows - begin);
+    uint32_t key[STEPS], entry[STEPS], rank[STEPS];
 #pragma unroll
-    for (int i = 0; i < kGroupSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const uint32_t e = first + i * 64 + lane;
         key[i] = e < a.rows ? (a.first ? group_key(a.index[e], a.dim) : a.keys_in[e]) : 0u;
         entry[i] = e < a.rows && !a.first ? a.entries_in[e] : e;
     }
 #pragma unroll
-    for (int i = 0; i < kGroupSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const bool valid = first + i * 64 + lane < a.rows;
         const uint32_t d = (key[i] >> a.shift) & (digits - 1);
         const uint64_t same = same_digit<BITS>(d, valid);
@@ -194,8 +217,8 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
             s_count[w * digits + d] = n;
             n += c;
         }
+        s_base[d] += a.few ? s_place[d] : a.hist[(size_t)d * a.tiles + tile];
         s_place[d] = n;
-        s_base[d] += a.hist[(size_t)d * a.tiles + tile];
     }
     __syncthreads();
     digit_bases<kGroupThreads>(s_place, digits, s_place, s_tmp);
@@ -203,7 +226,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
     for (int d = threadIdx.x; d < digits; d += kGroupThreads) s_base[d] -= s_place[d];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kGroupSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const uint32_t e = first + i * 64 + lane;
         if (e >= a.rows) continue;
         const uint32_t d = (key[i] >> a.shift) & (digits - 1);
@@ -258,11 +281,12 @@ __global__ __launch_bounds__(kGroupThreads) void group_bounds(GroupArgs a, const
     offsets[s] = lo;
 }
 
-// Few entries and few groups: one workgroup, one launch.  Each wave counts
+// Few entries and few groups: one workgroup, one launch (8,192 entries of 256
+// groups take 14 us so and 13 in tiles).  Each wave counts
 // its stretch, the counts are scanned over (digit, wave), and a second walk
 // over the stretch places the entries.
-constexpr int kGroupSmallRows = 8192;
-constexpr int kGroupSmallDim = 1023;
+constexpr int kGroupSmallRows = 4096;
+constexpr int kGroupSmallDim = 2047;
 template <int THREADS, int BITS>
 __global__ __launch_bounds__(THREADS) void group_small(GroupArgs a) {
     constexpr int kWaves = THREADS / 64;
@@ -330,7 +354,7 @@ void for_bits(int bits, F f) {
 
 struct GroupPlan {
     bool small;
-    int passes, bits;
+    int passes, bits, steps;
     int64_t tiles;
     size_t hist, totals, pairs, bytes;  // bytes of each part (pairs: of one array of a pass)
 };
@@ -343,7 +367,8 @@ GroupPlan group_plan(int64_t rows, int64_t dim) {
     p.bits = (bits + p.passes - 1) / p.passes;
     p.small = rows <= kGroupSmallRows && dim <= kGroupSmallDim;
     if (p.small) return p;
-    p.tiles = (rows + kGroupTile - 1) / kGroupTile;
+    p.steps = rows <= kGroupShortRows ? kGroupShort : kGroupLong;
+    p.tiles = (rows + kGroupThreads * p.steps - 1) / (kGroupThreads * p.steps);
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     p.hist = up((size_t)p.tiles * 4 << p.bits);
     p.totals = up(size_t(4) << p.bits);
@@ -409,9 +434,10 @@ extern "C" int segred_group(const int64_t *index, int64_t rows, int64_t fanout, 
     a.hist = reinterpret_cast<uint32_t *>(w);
     a.totals = reinterpret_cast<uint32_t *>(w + p.hist);
     a.tiles = (uint32_t)p.tiles;
+    a.few = p.tiles <= kGroupFewTiles && p.tiles << p.bits <= kGroupFewCounts;
     auto array = [&](int i) { return reinterpret_cast<uint32_t *>(w + p.hist + p.totals + i * p.pairs); };
     const unsigned digits = 1u << p.bits;
-    const size_t count_lds = kGroupWaves * digits * 4, place_lds = count_lds + 2 * digits * 4 + 2 * kGroupTile * 4;
+    const size_t count_lds = kGroupWaves * digits * 4, place_lds = count_lds + 2 * digits * 4 + 2 * kGroupThreads * p.steps * 4;
     a.position = position;
     for (int pass = 0; pass < p.passes; ++pass) {
         a.shift = pass * p.bits;
@@ -432,11 +458,13 @@ extern "C" int segred_group(const int64_t *index, int64_t rows, int64_t fanout, 
         }
         for_bits(p.bits, [&](auto bits) {
             constexpr int kBits = decltype(bits)::value;
-            timed_launch_ggl(true, group_count<kBits>, dim3((unsigned)p.tiles), dim3(kGroupThreads), (unsigned)count_lds,
-                             stream, a);
-            timed_launch_ggl(false, group_scan, dim3(digits), dim3(kGroupThreads), 0, stream, a);
-            timed_launch_ggl(true, group_place<kBits>, dim3((unsigned)p.tiles), dim3(kGroupThreads), (unsigned)place_lds,
-                             stream, a);
+            const bool small_tile = p.steps == kGroupShort;
+            const dim3 grid((unsigned)p.tiles), block(kGroupThreads);
+            if (small_tile) timed_launch_ggl(true, (group_count<kBits, kGroupShort>), grid, block, (unsigned)count_lds, stream, a);
+            else timed_launch_ggl(true, (group_count<kBits, kGroupLong>), grid, block, (unsigned)count_lds, stream, a);
+            if (!a.few) timed_launch_ggl(false, group_scan, dim3(digits), block, 0, stream, a);
+            if (small_tile) timed_launch_ggl(true, (group_place<kBits, kGroupShort>), grid, block, (unsigned)place_lds, stream, a);
+            else timed_launch_ggl(true, (group_place<kBits, kGroupLong>), grid, block, (unsigned)place_lds, stream, a);
         });
         if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
     }

@@ -9,7 +9,9 @@ pytestmark = pytest.mark.gpu
 # (entries, groups, fanout): one launch, one digit pass, several passes; the borders between them
 CASES = [(0, 10, 1), (1, 1, 1), (7, 3, 1), (10, 0, 1), (1000, 64, 8), (1024, 64, 2), (1025, 1023, 1), (8192, 1023, 8),
          (8193, 5, 1), (50000, 255, 4), (50000, 256, 1), (70001, 1023, 1), (70001, 1024, 1), (5, 100000, 1),
-         (300000, 250000, 1), (12288, 1, 3), (20000, 2 ** 21, 1)]
+         (300000, 250000, 1), (12288, 1, 3), (20000, 2 ** 21, 1),
+         (4096, 2047, 8), (4097, 2047, 1), (4000, 2048, 1), (65536, 64, 8), (65537, 64, 1), (65536, 2000, 1),
+         (262144, 100, 4), (270000, 100, 2), (270000, 1500, 1), (30000, 2 ** 22 + 5, 1)]
 
 
 @pytest.mark.parametrize("entries,groups,fanout", CASES)
