@@ -388,15 +388,24 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
         }
     }
 
-    T *out = reinterpret_cast<T *>(a.out);
+    T *out = reinterpret_cast<T *>(a.out) + row0 * a.M;
+    if constexpr (sizeof(T) == 2) {
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = m_w + 16 * i + (lane & 15);
-        if (r < rows) {
-            T *row = out + (row0 + r) * a.M;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                store_quad<T>(row, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+                tile_put<T, BN>(lds, m_w + 16 * i + (lane & 15), n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+        __syncthreads();
+        tile_out<T, BM, BN, kThreads>(lds, out, rows, n0, a.M, a.vec != 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int r = m_w + 16 * i + (lane & 15);
+            if (r < rows)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    store_quad<T>(out + r * a.M, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
         }
     }
 }
@@ -681,20 +690,20 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     if (extra > 0)
         phase_steps<T, AH, false, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products, [](int) {});
 
-    T *out = reinterpret_cast<T *>(a.out);
+    __syncthreads();
+    constexpr int BN = 2 * kHalf;
 #pragma unroll
     for (int p = 0; p < AH; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = phase_row(p, i, wave) + (lane & 15);
-            if (r >= rows) continue;
-            T *row = out + (row0 + r) * a.M;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    store_quad<T>(row, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, a.M, acc[p][q][i][j], a.vec != 0);
-        }
+                    tile_put<T, BN>(lds, phase_row(p, i, wave) + (lane & 15), phase_col(q, j, wave) + (lane >> 4) * 4,
+                                    acc[p][q][i][j]);
+    __syncthreads();
+    tile_out<T, BM, BN, kPhaseThreads>(lds, reinterpret_cast<T *>(a.out) + row0 * a.M, rows, n0, a.M, a.vec != 0);
 }
 
 template <typename T, int AH>
@@ -843,7 +852,7 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
     }
     a.low = static_cast<char *>(low);
     a.out = static_cast<char *>(out);
-    a.vec = (a.M % 4 == 0 && aligned(out, 4 * e)) ? 1 : 0;
+    a.vec = ((a.M * e) % 16 == 0 && aligned(out, 16)) ? 1 : 0;
     auto units = [&](const void *p, int64_t width) { return (width * e) % 16 == 0 && aligned(p, 16); };
     const bool x = units(values, a.K);
     const bool low_direct = x && units(a.first, transpose ? rank : k);

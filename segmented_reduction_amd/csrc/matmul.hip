@@ -16,7 +16,7 @@ struct MatmulArgs {
     int64_t S, N, K, M;
     int64_t slots, ntiles;
     void *out;
-    int vec;
+    int vec;  // rows of `out` hold whole 16-byte units on 16-byte boundaries
 };
 
 // A tile of one segment: rows row0 .. row0 + rows - 1, columns from n0.
@@ -47,19 +47,29 @@ __device__ __forceinline__ const char *matmul_row(const MatmulArgs &a, const Mat
     return v >= 0 && v < a.value_rows ? a.values + v * row_bytes : nullptr;
 }
 
-// Stores a wave's neighbouring blocks.
-template <typename T, int MT, int NT>
+// Stores a wave's neighbouring blocks; 16-bit ones through LDS, which the
+// workgroup's waves have finished reading when they meet here.
+template <typename T, int BM, int BN, int THREADS, int MT, int NT>
 __device__ __forceinline__ void matmul_store(const MatmulArgs &a, const MatmulPlace &p, const f32x4 (&acc)[MT][NT],
-                                             int m_w, int n_w, int lane) {
-    T *out = reinterpret_cast<T *>(a.out);
+                                             lds_char *lds, int m_w, int n_w, int lane) {
+    T *out = reinterpret_cast<T *>(a.out) + p.row0 * a.M;
+    if constexpr (sizeof(T) == 2) {
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = m_w + 16 * i + (lane & 15);
-        if (r < p.rows) {
-            T *row = out + (p.row0 + r) * a.M;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                store_quad<T>(row, p.n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+                tile_put<T, BN>(lds, m_w + 16 * i + (lane & 15), n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+        __syncthreads();
+        tile_out<T, BM, BN, THREADS>(lds, out, p.rows, p.n0, a.M, a.vec != 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int r = m_w + 16 * i + (lane & 15);
+            if (r < p.rows)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    store_quad<T>(out + r * a.M, p.n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
         }
     }
 }
@@ -146,7 +156,7 @@ struct MatmulTile {
                 if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
             }
         }
-        matmul_store<T, MT, NT>(a, p, acc, m_w, n_w, lane);
+        matmul_store<T, BM, BN, kThreads>(a, p, acc, lds, m_w, n_w, lane);
     }
 };
 
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(kSplitThreads) void seg_matmul_split(MatmulArgs a) 
             }
         return;
     }
-    matmul_store<float, MT, NT>(a, p, acc, m_w, n_w, lane);
+    matmul_store<float, BM, BN, kSplitThreads>(a, p, acc, lds, m_w, n_w, lane);
 }
 
 template <int BM, int BN>
@@ -318,20 +328,20 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_matmul_many(MatmulArgs a) {
     else
         phase_steps<T, 1, false, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products, [](int) {});
 
-    T *out = reinterpret_cast<T *>(a.out);
+    __syncthreads();
+    constexpr int BN = 2 * kHalf;
 #pragma unroll
     for (int p = 0; p < AH; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = phase_row(p, i, wave) + (lane & 15);
-            if (r >= rows) continue;
-            T *row = out + (row0 + r) * a.M;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    store_quad<T>(row, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, a.M, acc[p][q][i][j], a.vec != 0);
-        }
+                    tile_put<T, BN>(lds, phase_row(p, i, wave) + (lane & 15), phase_col(q, j, wave) + (lane >> 4) * 4,
+                                    acc[p][q][i][j]);
+    __syncthreads();
+    tile_out<T, AH * kHalf, BN, kPhaseThreads>(lds, reinterpret_cast<T *>(a.out) + row0 * a.M, rows, n0, a.M, a.vec != 0);
 }
 
 template <typename T, int AH>
@@ -535,7 +545,7 @@ extern "C" int segred_matmul(const void *values, int32_t dtype, int64_t k, const
     a.K = k;
     a.M = m;
     a.out = out;
-    a.vec = (m % 4 == 0 && aligned(out, 4 * e)) ? 1 : 0;
+    a.vec = ((m * e) % 16 == 0 && aligned(out, 16)) ? 1 : 0;
     const int64_t along = transpose ? k : m;  // the weights' contiguous axis
     const bool direct = (k * e) % 16 == 0 && (along * e) % 16 == 0 && aligned(values, 16) && aligned(weights, 16);
     switch (dtype) {
