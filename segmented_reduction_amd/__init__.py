@@ -411,33 +411,43 @@ def offsets_from_flags(flags: torch.Tensor):
     return offsets, count
 
 
-def _launch(fn, what: str, device: torch.device, *args):
-    """Call ``fn`` with ``args`` and the device's current stream, on that device.
+def _launch(fn, what: str, index: int, *args):
+    """Call ``fn`` with ``args`` and the current stream of GPU ``index``, on that GPU.
 
     The decoding calls take a few microseconds on the GPU, so the host side is
     kept short: the device is switched only where it is not the current one,
     and the stream handle is asked for without building a Stream object (0.1
     us instead of 1.9)."""
-    index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise SegredError(rc, what)
 
 
-def _same_device(first: torch.Tensor, **others):
-    """Raise unless every tensor given is contiguous and on the GPU of ``first``."""
-    for name, t in others.items():
-        if t is not None and (t.device != first.device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous tensor on the GPU of the other inputs")
+def _floats(name: str, t: torch.Tensor):
+    """(GPU index, dtype code) of a contiguous [*, features] tensor of the products' types."""
+    index = t.get_device()
+    if index < 0 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D GPU tensor")
+    code = FLOATS.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} dtype {t.dtype} is not float32, bfloat16 or float16")
+    return index, code
 
 
-def _check_index(name: str, t: torch.Tensor | None):
-    if t is not None and (t.dtype != torch.int64 or t.dim() != 1):
-        raise ValueError(f"{name} must be a 1-D int64 tensor")
+def _beside(index: int, name: str, t: torch.Tensor):
+    """Raise unless ``t`` is contiguous and on GPU ``index``."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the GPU of the other inputs")
+
+
+def _rows(index: int, name: str, t: torch.Tensor):
+    """Raise unless ``t`` is a contiguous 1-D int64 tensor on GPU ``index``."""
+    if t.get_device() != index or t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int64 tensor on the GPU of the other inputs")
 
 
 def matmul(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *, transpose: bool = False,
@@ -457,17 +467,18 @@ def matmul(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *
     rows is ``matmul(grad, weights, offsets, transpose=not transpose)``, that
     of the weights ``outer``.
     """
-    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
-        raise ValueError("values must be a contiguous 2-D GPU tensor")
-    if values.dtype not in FLOATS:
-        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
+    dev, code = _floats("values", values)
     if weights.dtype != values.dtype:
         raise TypeError("weights must have the dtype of values")
-    _same_device(values, weights=weights, offsets=offsets, rows=rows, out=out)
-    _check_index("offsets", offsets)
-    _check_index("rows", rows)
-    s, n = offsets.numel() - 1, (values if rows is None else rows).shape[0]
-    k = values.shape[1]
+    _beside(dev, "weights", weights)
+    _rows(dev, "offsets", offsets)
+    count, k = values.shape
+    s = offsets.shape[0] - 1
+    if rows is None:
+        n = count
+    else:
+        _rows(dev, "rows", rows)
+        n = rows.shape[0]
     if s < 0 or weights.dim() != 3 or weights.shape[0] != s:
         raise ValueError("weights must be [S, K, M] (or [S, M, K] with transpose) with S + 1 offsets")
     m, kw = (weights.shape[1], weights.shape[2]) if transpose else (weights.shape[2], weights.shape[1])
@@ -475,11 +486,13 @@ def matmul(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *
         raise ValueError(f"values have {k} features and weights take {kw}")
     if out is None:
         out = torch.empty((n, m), dtype=values.dtype, device=values.device)
-    elif out.shape != (n, m) or out.dtype != values.dtype:
-        raise ValueError("out must be [rows, M] of the dtype of values")
-    _launch((_lib or library()).segred_matmul, "segred_matmul", values.device, values.data_ptr(),
-            FLOATS[values.dtype], k, rows.data_ptr() if rows is not None else None, values.shape[0],
-            weights.data_ptr(), 1 if transpose else 0, m, offsets.data_ptr(), s, n, out.data_ptr())
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (n, m) or out.dtype != values.dtype:
+            raise ValueError("out must be [rows, M] of the dtype of values")
+    _launch((_lib or library()).segred_matmul, "segred_matmul", dev, values.data_ptr(), code, k,
+            rows.data_ptr() if rows is not None else None, count, weights.data_ptr(), 1 if transpose else 0, m,
+            offsets.data_ptr(), s, n, out.data_ptr())
     return out
 
 
@@ -495,17 +508,16 @@ def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, lef
     left_rows, right_rows  optional int64 [R]: gather that side's rows.
     out_dtype    the inputs' type (default) or float32.
     """
-    if not left.is_cuda or not left.is_contiguous() or left.dim() != 2 or right.dim() != 2:
-        raise ValueError("left and right must be contiguous 2-D GPU tensors")
-    if left.dtype not in FLOATS:
-        raise TypeError(f"left dtype {left.dtype} is not float32, bfloat16 or float16")
+    dev, code = _floats("left", left)
     if right.dtype != left.dtype:
         raise TypeError("right must have the dtype of left")
-    _same_device(left, right=right, offsets=offsets, left_rows=left_rows, right_rows=right_rows, out=out)
-    _check_index("offsets", offsets)
-    _check_index("left_rows", left_rows)
-    _check_index("right_rows", right_rows)
-    s = offsets.numel() - 1
+    _floats("right", right)
+    _beside(dev, "right", right)
+    _rows(dev, "offsets", offsets)
+    for name, index in (("left_rows", left_rows), ("right_rows", right_rows)):
+        if index is not None:
+            _rows(dev, name, index)
+    s = offsets.shape[0] - 1
     n = (left if left_rows is None else left_rows).shape[0]
     if (right if right_rows is None else right_rows).shape[0] != n or s < 0:
         raise ValueError("left and right need the same number of rows, and offsets S + 1 entries")
@@ -515,15 +527,17 @@ def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, lef
         raise TypeError("out_dtype must be the dtype of left or float32")
     if out is None:
         out = torch.empty((s, k, m), dtype=odt, device=left.device)
-    elif out.shape != (s, k, m) or out.dtype != odt:
-        raise ValueError("out must be [S, K, M] of out_dtype")
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (s, k, m) or out.dtype != odt:
+            raise ValueError("out must be [S, K, M] of out_dtype")
     lib = _lib or library()
     need = lib.segred_outer_workspace(k, m, s, n)
     work = torch.empty(need, dtype=torch.uint8, device=left.device) if need else None
-    _launch(lib.segred_outer, "segred_outer", left.device, left.data_ptr(),
+    _launch(lib.segred_outer, "segred_outer", dev, left.data_ptr(),
             left_rows.data_ptr() if left_rows is not None else None, left.shape[0], k, right.data_ptr(),
-            right_rows.data_ptr() if right_rows is not None else None, right.shape[0], m, FLOATS[left.dtype],
-            offsets.data_ptr(), s, n, out.data_ptr(), FLOATS[odt], work.data_ptr() if need else None, need)
+            right_rows.data_ptr() if right_rows is not None else None, right.shape[0], m, code, offsets.data_ptr(), s, n,
+            out.data_ptr(), FLOATS[odt], work.data_ptr() if need else None, need)
     return out
 
 
@@ -537,35 +551,34 @@ def group(index: torch.Tensor, dim_size: int):
     entry in ``order``; ``offsets`` [dim_size + 1] where each group begins.
     Entries outside [0, dim_size) come behind the last group, at position -1.
     """
-    if not index.is_cuda or index.dtype != torch.int64 or index.dim() not in (1, 2) or not index.is_contiguous():
+    dev = index.get_device()
+    if dev < 0 or index.dtype != torch.int64 or index.dim() not in (1, 2) or not index.is_contiguous():
         raise ValueError("index must be a contiguous 1-D or 2-D int64 GPU tensor")
     dim_size = int(dim_size)
     if dim_size < 0:
         raise ValueError("dim_size must be >= 0")
-    n, dev = index.numel(), index.device
+    n, device = index.numel(), index.device
     fanout = max(index.shape[1], 1) if index.dim() == 2 else 1
-    order = torch.empty(n, dtype=torch.int64, device=dev)
+    order = torch.empty(n, dtype=torch.int64, device=device)
     position = torch.empty_like(index)
-    offsets = torch.empty(dim_size + 1, dtype=torch.int64, device=dev)
+    offsets = torch.empty(dim_size + 1, dtype=torch.int64, device=device)
     lib = _lib or library()
     need = lib.segred_group_workspace(n, dim_size)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _launch(lib.segred_group, "segred_group", dev, index.data_ptr(), n, fanout, dim_size, order.data_ptr(),
             position.data_ptr(), offsets.data_ptr(), work.data_ptr() if need else None, need)
     return order, position, offsets
 
 
 def _check_combine(values, position, weights):
-    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
-        raise ValueError("values must be a contiguous 2-D GPU tensor")
-    if values.dtype not in FLOATS:
-        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
-    if position.dtype != torch.int64 or position.dim() != 2:
-        raise ValueError("position must be an int64 [T, k] tensor")
-    if weights.dtype != torch.float32 or weights.shape != position.shape:
-        raise ValueError("weights must be a float32 tensor of the shape of position")
-    if values.shape[1] < 1:
-        raise ValueError("values has an empty feature dimension")
+    """(GPU index, dtype code) of the tensors that both combine calls take."""
+    dev, code = _floats("values", values)
+    if position.get_device() != dev or position.dtype != torch.int64 or position.dim() != 2 or not position.is_contiguous():
+        raise ValueError("position must be a contiguous int64 [T, k] tensor on the GPU of values")
+    if (weights.get_device() != dev or weights.dtype != torch.float32 or weights.shape != position.shape
+            or not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous float32 tensor of the shape of position, on its GPU")
+    return dev, code
 
 
 def combine(values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor, *,
@@ -578,15 +591,16 @@ def combine(values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
     weights   float32 [T, k].
     Returns out [T, M] of the values' type.
     """
-    _check_combine(values, position, weights)
-    _same_device(values, position=position, weights=weights, out=out)
+    dev, code = _check_combine(values, position, weights)
     (n, m), (t, k) = values.shape, position.shape
     if out is None:
         out = torch.empty((t, m), dtype=values.dtype, device=values.device)
-    elif out.shape != (t, m) or out.dtype != values.dtype:
-        raise ValueError("out must be [T, M] of the dtype of values")
-    _launch((_lib or library()).segred_combine, "segred_combine", values.device, values.data_ptr(),
-            FLOATS[values.dtype], m, n, position.data_ptr(), weights.data_ptr(), t, k, out.data_ptr())
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (t, m) or out.dtype != values.dtype:
+            raise ValueError("out must be [T, M] of the dtype of values")
+    _launch((_lib or library()).segred_combine, "segred_combine", dev, values.data_ptr(), code, m, n,
+            position.data_ptr(), weights.data_ptr(), t, k, out.data_ptr())
     return out
 
 
@@ -597,19 +611,20 @@ def combine_grad(grad: torch.Tensor, values: torch.Tensor, position: torch.Tenso
     Returns (grad_values [N, M], grad_weights float32 [T, k]).  Each row may be
     named once only; rows that ``position`` does not name are left as they were
     (uninitialised when ``out`` is not given)."""
-    _check_combine(values, position, weights)
-    _same_device(values, grad=grad, position=position, weights=weights, out=out)
+    dev, code = _check_combine(values, position, weights)
+    _beside(dev, "grad", grad)
     (n, m), (t, k) = values.shape, position.shape
     if grad.shape != (t, m) or grad.dtype != values.dtype:
         raise ValueError("grad must be [T, M] of the dtype of values")
     if out is None:
         out = torch.empty_like(values)
-    elif out.shape != values.shape or out.dtype != values.dtype:
-        raise ValueError("out must have the shape and dtype of values")
+    else:
+        _beside(dev, "out", out)
+        if out.shape != values.shape or out.dtype != values.dtype:
+            raise ValueError("out must have the shape and dtype of values")
     grad_weights = torch.empty_like(weights)
-    _launch((_lib or library()).segred_combine_grad, "segred_combine_grad", values.device, grad.data_ptr(),
-            values.data_ptr(), FLOATS[values.dtype], m, n, position.data_ptr(), weights.data_ptr(), t, k,
-            out.data_ptr(), grad_weights.data_ptr())
+    _launch((_lib or library()).segred_combine_grad, "segred_combine_grad", dev, grad.data_ptr(), values.data_ptr(),
+            code, m, n, position.data_ptr(), weights.data_ptr(), t, k, out.data_ptr(), grad_weights.data_ptr())
     return out, grad_weights
 
 
@@ -633,38 +648,42 @@ def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, 
     Rows of no segment are left as they were in ``out`` (uninitialised when it
     is not given; likewise the low-rank rows).
     """
-    if not values.is_cuda or not values.is_contiguous() or values.dim() != 2:
-        raise ValueError("values must be a contiguous 2-D GPU tensor")
-    if values.dtype not in FLOATS:
-        raise TypeError(f"values dtype {values.dtype} is not float32, bfloat16 or float16")
+    dev, code = _floats("values", values)
     if weights.dtype != values.dtype or down.dtype != values.dtype or up.dtype != values.dtype:
         raise TypeError("weights, down and up must have the dtype of values")
-    _same_device(values, weights=weights, offsets=offsets, which=which, down=down, up=up, scale=scale, out=out)
-    _check_index("offsets", offsets)
-    _check_index("which", which)
+    _beside(dev, "weights", weights)
+    _beside(dev, "down", down)
+    _beside(dev, "up", up)
+    _rows(dev, "offsets", offsets)
+    _rows(dev, "which", which)
     if weights.dim() != 2 or down.dim() != 3 or up.dim() != 3:
         raise ValueError("weights must be [M, K], down [L, r, K] and up [L, M, r]")
-    (m, k), (count, r, _) = weights.shape, down.shape
-    if down.shape[2] != k or up.shape != (count, m, r):
+    (m, k), (count, r, kd) = weights.shape, down.shape
+    if kd != k or up.shape != (count, m, r):
         raise ValueError("weights must be [M, K], down [L, r, K] and up [L, M, r]")
-    s, n = offsets.numel() - 1, values.shape[0]
-    if s < 0 or which.numel() != s:
+    s, (n, width) = offsets.shape[0] - 1, values.shape
+    if s < 0 or which.shape[0] != s:
         raise ValueError("which needs one entry per segment and offsets one more")
-    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (count,)):
-        raise ValueError("scale must be a float32 [L] tensor")
+    if scale is not None:
+        _beside(dev, "scale", scale)
+        if scale.dtype != torch.float32 or scale.shape != (count,):
+            raise ValueError("scale must be a float32 [L] tensor")
     have, give = (m, k) if transpose else (k, m)
-    if values.shape[1] != have:
-        raise ValueError(f"values have {values.shape[1]} features and the projection takes {have}")
+    if width != have:
+        raise ValueError(f"values have {width} features and the projection takes {have}")
+    device = values.device
     if out is None:
-        out = torch.empty((n, give), dtype=values.dtype, device=values.device)
-    elif out.shape != (n, give) or out.dtype != values.dtype:
-        raise ValueError("out must be [N, outputs] of the dtype of values")
-    low = torch.empty((n, r), dtype=values.dtype, device=values.device) if want_low else None
+        out = torch.empty((n, give), dtype=values.dtype, device=device)
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (n, give) or out.dtype != values.dtype:
+            raise ValueError("out must be [N, outputs] of the dtype of values")
+    low = torch.empty((n, r), dtype=values.dtype, device=device) if want_low else None
     lib = _lib or library()
-    need = lib.segred_adapter_workspace(FLOATS[values.dtype], m, count, r, n)
-    work = torch.empty(need, dtype=torch.uint8, device=values.device) if need else None
-    _launch(lib.segred_adapter, "segred_adapter", values.device, values.data_ptr(), FLOATS[values.dtype], k,
-            weights.data_ptr(), m, offsets.data_ptr(), which.data_ptr(), s, n, down.data_ptr(), up.data_ptr(),
+    need = lib.segred_adapter_workspace(code, m, count, r, n)
+    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _launch(lib.segred_adapter, "segred_adapter", dev, values.data_ptr(), code, k, weights.data_ptr(), m,
+            offsets.data_ptr(), which.data_ptr(), s, n, down.data_ptr(), up.data_ptr(),
             scale.data_ptr() if scale is not None else None, count, r, 1 if transpose else 0, out.data_ptr(),
             low.data_ptr() if want_low else None, work.data_ptr() if need else None, need)
     return (out, low) if want_low else out

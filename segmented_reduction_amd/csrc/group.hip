@@ -10,8 +10,10 @@
 // are runs, and consecutive tiles go to one XCD, whose L2 joins the ends of
 // their runs.  An entry's place after two passes is read through the places of
 // the first (both written in order, and read along as many fronts as there are
-// digits) instead of being scattered: 4 million entries of 250,000 groups took
-// 304 us with scattered places and unordered tiles.
+// digits) instead of being scattered: 4 million entries of 250,000 groups take
+// 114 us, and took 304 with scattered places and unordered tiles.  What bounds
+// it is the wait between the steps of a tile (counts, scan, places: each a round
+// trip through LDS and a barrier), not the memory: 98 MB, 0.9 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -39,15 +41,19 @@ struct GroupArgs {
     int few;  // few tiles: group_place adds up their counts itself
 };
 
-constexpr int kGroupThreads = 256;
+constexpr int kGroupThreads = 512;
 constexpr int kGroupWaves = kGroupThreads / 64;
-// Entries per lane of a tile.  Short ones up to 65,536 entries, so that there
-// are tiles for more CUs.  Where tiles and digits are few a workgroup adds up
-// the counts of the tiles before its own, which saves the launch of the scan:
-// 32,768 entries of 64 groups take 13 us in 32 tiles and two launches, 23 in 8
-// tiles and three; but of 2,000 groups 40 against 31.
-constexpr int kGroupShort = 4, kGroupLong = 16;
-constexpr int64_t kGroupShortRows = 65536, kGroupFewTiles = 64, kGroupFewCounts = 32768;
+// Entries per lane of a tile, 1,024 or 4,096 entries in all (tiles of 256 lanes
+// and 16 entries each: 128 us for 4 million entries of 100,000 groups instead
+// of 111).  Short ones up to 262,144 entries, so that there are tiles for more
+// CUs: 35 us against 43 there for 100,000 groups and 15 against 19 for 500, but
+// 1,048,576 entries of 1,000 groups take 34 against 26.  Where tiles and digits
+// are few a workgroup adds up the counts of the tiles before its own, which
+// saves the launch of the scan: 32,768 entries of 64 groups take 13 us in 32
+// tiles and two launches, 23 in 8 tiles and three; but of 2,000 groups 40
+// against 31.
+constexpr int kGroupShort = 2, kGroupLong = 8;
+constexpr int64_t kGroupShortRows = 262144, kGroupFewTiles = 64, kGroupFewCounts = 32768;
 constexpr int kGroupMaxBits = 11;
 constexpr uint32_t kNoPlace = 0xffffffffu;
 
