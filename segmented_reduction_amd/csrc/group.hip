@@ -11,15 +11,17 @@
 // their runs.  An entry's place after two passes is read through the places of
 // the first (both written in order, and read along as many fronts as there are
 // digits) instead of being scattered: 4 million entries of 250,000 groups take
-// 114 us, and took 304 with scattered places and unordered tiles.  What bounds
-// it is the wait between the steps of a tile (counts, scan, places: each a round
-// trip through LDS and a barrier), not the memory: 98 MB, 0.9 TB/s.
+// 93 us, and took 304 with scattered places and unordered tiles.  Their 98 MB of
+// input and output would take 21.  What bounds a move (21 us) is the work per
+// entry in the vector units (the lanes of its digit, its rank, three passages
+// through LDS); the places (24 us) are bound by the cache, which serves
+// each of the scattered reads with a line of its own.
 #include <algorithm>
 #include <type_traits>
 
 #include "internal.hpp"
-#include "scan.hpp"
 #include "tile.hpp"
+#include "wave.hpp"
 
 namespace segred {
 
@@ -44,17 +46,19 @@ struct GroupArgs {
 constexpr int kGroupThreads = 512;
 constexpr int kGroupWaves = kGroupThreads / 64;
 // Entries per lane of a tile, 1,024 or 4,096 entries in all (tiles of 256 lanes
-// and 16 entries each: 128 us for 4 million entries of 100,000 groups instead
-// of 111).  Short ones up to 262,144 entries, so that there are tiles for more
-// CUs: 35 us against 43 there for 100,000 groups and 15 against 19 for 500, but
-// 1,048,576 entries of 1,000 groups take 34 against 26.  Where tiles and digits
+// and 16 entries each: 108 us for 4 million entries of 100,000 groups instead
+// of 90).  Short ones up to 262,144 entries, so that there are tiles for more
+// CUs: 33 us against 41 there for 100,000 groups and 16 against 18 for 500, but
+// 1,048,576 entries of 1,000 groups take 29 against 23.  Where tiles and digits
 // are few a workgroup adds up the counts of the tiles before its own, which
-// saves the launch of the scan: 32,768 entries of 64 groups take 13 us in 32
-// tiles and two launches, 23 in 8 tiles and three; but of 2,000 groups 40
-// against 31.
+// saves the launch of the scan: 32,768 entries of 64 groups take 13 us so and
+// 17 with it; but of 2,000 groups 25 against 18.
 constexpr int kGroupShort = 2, kGroupLong = 8;
 constexpr int64_t kGroupShortRows = 262144, kGroupFewTiles = 64, kGroupFewCounts = 32768;
 constexpr int kGroupMaxBits = 11;
+// Entries per lane where places are read through two passes (4 million entries
+// of 250,000 groups: 4 are 4 us faster than 1, 8 no faster).
+constexpr int kGroupEach = 4;
 constexpr uint32_t kNoPlace = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t group_key(int64_t v, uint32_t dim) {
@@ -64,23 +68,66 @@ __device__ __forceinline__ uint32_t group_key(int64_t v, uint32_t dim) {
 // Lanes of the wave whose digit of BITS bits equals this lane's.
 template <int BITS>
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid) {
-    uint64_t m = ballot(valid);
+    const uint64_t m = ballot(valid);
     uint32_t lo = (uint32_t)m, hi = (uint32_t)(m >> 32);
 #pragma unroll
     for (int b = 0; b < BITS; ++b) {
-        const uint32_t not_set = ((digit >> b) & 1) - 1;  // all ones where the bit is 0
-        const uint64_t with = ballot(not_set == 0);
-        lo &= (uint32_t)with ^ not_set;
-        hi &= (uint32_t)(with >> 32) ^ not_set;
+        const uint32_t set = (uint32_t)((int32_t)(digit << (31 - b)) >> 31);  // all ones where the bit is 1
+        const uint64_t with = ballot(set != 0);
+        // m & ~(with ^ set), one instruction
+        lo = __builtin_amdgcn_bitop3_b32(lo, (uint32_t)with, set, 0x90);
+        hi = __builtin_amdgcn_bitop3_b32(hi, (uint32_t)(with >> 32), set, 0x90);
     }
     return (uint64_t)hi << 32 | lo;
 }
 
-// Exclusive offsets of `digits` totals into s_base (all threads of the group).
-// `totals` may be s_base itself.
+// Keys of the wave's entries first, first + 64 ...: all loads are under way
+// before the first is waited for, so entries behind the last read that one.
+template <int STEPS>
+__device__ __forceinline__ void load_keys(const GroupArgs &a, uint32_t first, uint32_t (&key)[STEPS]) {
+    if (a.first) {
+        int64_t v[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) v[i] = a.index[min(first + i * 64, a.rows - 1)];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) key[i] = group_key(v[i], a.dim);
+    } else {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) key[i] = a.keys_in[min(first + i * 64, a.rows - 1)];
+    }
+}
+
+// Sum of v over the threads before this one (all threads of the group), and
+// over all of them.  s_tmp holds an entry per wave, free again after the next
+// barrier.
 template <int THREADS>
-__device__ __forceinline__ void digit_bases(const uint32_t *totals, int digits, uint32_t *s_base, int64_t *s_tmp) {
-    constexpr int kPer = (1 << kGroupMaxBits) / THREADS > 0 ? (1 << kGroupMaxBits) / THREADS : 1;
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *s_tmp, uint32_t &total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t x = v;
+    x += dpp32<kDppRowShr1>(0, x);
+    x += dpp32<kDppRowShr2>(0, x);
+    x += dpp32<kDppRowShr4>(0, x);
+    x += dpp32<kDppRowShr8>(0, x);
+    x += dpp32<kDppRowBcast15, 0xA>(0, x);
+    x += dpp32<kDppRowBcast31, 0xC>(0, x);
+    if (lane == 63) s_tmp[wave] = x;
+    __syncthreads();
+    uint32_t before = x - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        const uint32_t n = s_tmp[w];
+        before += w < wave ? n : 0u;
+        total += n;
+    }
+    return before;
+}
+
+// Exclusive offsets of `digits` totals, at most MAX, into s_base (all threads
+// of the group).  `totals` may be s_base itself.
+template <int THREADS, int MAX>
+__device__ __forceinline__ void digit_bases(const uint32_t *totals, int digits, uint32_t *s_base, uint32_t *s_tmp) {
+    constexpr int kPer = MAX / THREADS > 0 ? MAX / THREADS : 1;
     uint32_t v[kPer];
     uint32_t sum = 0;
 #pragma unroll
@@ -89,8 +136,8 @@ __device__ __forceinline__ void digit_bases(const uint32_t *totals, int digits, 
         v[j] = d < digits ? totals[d] : 0u;
         sum += v[j];
     }
-    int64_t total;
-    uint32_t base = (uint32_t)(block_inclusive_scan<THREADS, false>((int64_t)sum, s_tmp, total) - sum);
+    uint32_t total;
+    uint32_t base = sum_before<THREADS>(sum, s_tmp, total);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int d = threadIdx.x * kPer + j;
@@ -112,11 +159,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_count(GroupArgs a) {
     const uint32_t tile = (uint32_t)xcd_tile(a.tiles);
     const uint32_t first = tile * kTile + wave * 64 * STEPS;
     uint32_t key[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const uint32_t e = first + i * 64 + lane;
-        key[i] = e < a.rows ? (a.first ? group_key(a.index[e], a.dim) : a.keys_in[e]) : 0u;
-    }
+    load_keys<STEPS>(a, first + lane, key);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const bool valid = first + i * 64 + lane < a.rows;
@@ -136,7 +179,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_count(GroupArgs a) {
 
 // Exclusive scan over the tiles of each digit (one workgroup per digit).
 __global__ __launch_bounds__(kGroupThreads) void group_scan(GroupArgs a) {
-    __shared__ int64_t s_tmp[2 * kGroupWaves];
+    __shared__ uint32_t s_tmp[kGroupWaves];
     constexpr int kPer = 4;
     uint32_t *row = a.hist + (size_t)blockIdx.x * a.tiles;
     uint32_t running = 0;
@@ -148,28 +191,33 @@ __global__ __launch_bounds__(kGroupThreads) void group_scan(GroupArgs a) {
             v[j] = t + j < a.tiles ? row[t + j] : 0u;
             sum += v[j];
         }
-        int64_t total;
-        uint32_t base = running + (uint32_t)(block_inclusive_scan<kGroupThreads, false>((int64_t)sum, s_tmp, total) - sum);
+        uint32_t total;
+        uint32_t base = running + sum_before<kGroupThreads>(sum, s_tmp, total);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if (t + j < a.tiles) row[t + j] = base;
             base += v[j];
         }
-        running += (uint32_t)total;
+        running += total;
+        __syncthreads();
     }
     if (threadIdx.x == 0) a.totals[blockIdx.x] = running;
 }
 
-// Moves each entry to its place in this pass's order.
+// Moves each entry to its place in this pass's order.  Counts within a tile have
+// 16 bits, and keys and entries pass through the same part of LDS one after the
+// other, so that a CU holds four workgroups of 512 digits (its 32 waves).
 template <int BITS, int STEPS>
 __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
-    extern __shared__ uint32_t s_count[];  // [waves][digits], [digits] bases, [digits] places, [tile] keys, [tile] entries
-    __shared__ int64_t s_tmp[2 * kGroupWaves];
+    extern __shared__ uint32_t s_base[];  // [digits] bases, [digits] places, [tile] keys or entries, [waves][digits] counts
+    __shared__ uint32_t s_tmp[kGroupWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     constexpr int digits = 1 << BITS, kTile = kGroupThreads * STEPS;
-    uint32_t *s_base = s_count + kGroupWaves * digits, *s_place = s_base + digits;
-    uint32_t *s_key = s_place + digits, *s_entry = s_key + kTile;
-    for (int i = threadIdx.x; i < kGroupWaves * digits; i += kGroupThreads) s_count[i] = 0;
+    static_assert(kTile < 65536, "the counts of a tile have 16 bits");
+    uint32_t *s_place = s_base + digits, *s_item = s_place + digits;
+    uint16_t *s_count = reinterpret_cast<uint16_t *>(s_item + kTile);
+    for (int i = threadIdx.x; i < kGroupWaves * digits / 2; i += kGroupThreads)
+        reinterpret_cast<uint32_t *>(s_count)[i] = 0;
     const uint32_t tile = (uint32_t)xcd_tile(a.tiles);
     if (a.few) {
         for (int d = threadIdx.x; d < digits; d += kGroupThreads) {
@@ -185,21 +233,23 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
             if (a.last && tile == 0) a.totals[d] = n;
         }
         __syncthreads();
-        digit_bases<kGroupThreads>(s_base, digits, s_base, s_tmp);
+        digit_bases<kGroupThreads, digits>(s_base, digits, s_base, s_tmp);
     } else {
-        digit_bases<kGroupThreads>(a.totals, digits, s_base, s_tmp);
+        digit_bases<kGroupThreads, digits>(a.totals, digits, s_base, s_tmp);
     }
     if (a.offsets && tile == 0)  // one pass: the digits are the groups
         for (uint32_t d = threadIdx.x; d <= a.dim; d += kGroupThreads) a.offsets[d] = s_base[d];
-    uint32_t *mine = s_count + wave * digits;
+    uint16_t *mine = s_count + wave * digits;
     const uint32_t begin = tile * kTile, first = begin + wave * 64 * STEPS;
     const int have = (int)min((uint32_t)kTile, a.rows - begin);
     uint32_t key[STEPS], entry[STEPS], rank[STEPS];
+    load_keys<STEPS>(a, first + lane, key);
+    if (a.first) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const uint32_t e = first + i * 64 + lane;
-        key[i] = e < a.rows ? (a.first ? group_key(a.index[e], a.dim) : a.keys_in[e]) : 0u;
-        entry[i] = e < a.rows && !a.first ? a.entries_in[e] : e;
+        for (int i = 0; i < STEPS; ++i) entry[i] = first + i * 64 + lane;
+    } else {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) entry[i] = a.entries_in[min(first + i * 64 + lane, a.rows - 1)];
     }
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -210,7 +260,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
         const uint32_t seen = mine[d];
         rank[i] = seen + before;
         wave_lds_sync();
-        if (valid && before == 0) mine[d] = seen + popc64(same);
+        if (valid && before == 0) mine[d] = (uint16_t)(seen + popc64(same));
         wave_lds_sync();
     }
     __syncthreads();
@@ -220,14 +270,14 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
 #pragma unroll
         for (int w = 0; w < kGroupWaves; ++w) {
             const uint32_t c = s_count[w * digits + d];
-            s_count[w * digits + d] = n;
+            s_count[w * digits + d] = (uint16_t)n;
             n += c;
         }
         s_base[d] += a.few ? s_place[d] : a.hist[(size_t)d * a.tiles + tile];
         s_place[d] = n;
     }
     __syncthreads();
-    digit_bases<kGroupThreads>(s_place, digits, s_place, s_tmp);
+    digit_bases<kGroupThreads, digits>(s_place, digits, s_place, s_tmp);
     // s_base: what turns a place in the tile into one in the order
     for (int d = threadIdx.x; d < digits; d += kGroupThreads) s_base[d] -= s_place[d];
     __syncthreads();
@@ -237,22 +287,37 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
         if (e >= a.rows) continue;
         const uint32_t d = (key[i] >> a.shift) & (digits - 1);
         const uint32_t at = s_place[d] + mine[d] + rank[i];
-        s_key[at] = key[i];
-        s_entry[at] = entry[i];
+        rank[i] = at;
+        s_item[at] = key[i];
         const uint32_t to = s_base[d] + at;
         if (a.where) a.where[e] = a.last && key[i] >= a.dim ? kNoPlace : to;
         else if (a.first && a.last) a.position[e] = key[i] < a.dim ? (int64_t)to : -1;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < have; i += kGroupThreads) {
-        const uint32_t k = s_key[i], entry = s_entry[i];
-        const uint32_t to = s_base[(k >> a.shift) & (digits - 1)] + i;
-        if (a.keys_out) a.keys_out[to] = k;
+    uint32_t to[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int at = i * kGroupThreads + threadIdx.x;
+        if (at >= have) continue;
+        key[i] = s_item[at];
+        to[i] = s_base[(key[i] >> a.shift) & (digits - 1)] + at;
+        if (a.keys_out) a.keys_out[to[i]] = key[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        if (first + i * 64 + lane < a.rows) s_item[rank[i]] = entry[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int at = i * kGroupThreads + threadIdx.x;
+        if (at >= have) continue;
+        const uint32_t from = s_item[at];
         if (a.last) {
-            a.order[to] = a.fanout > 1 ? entry / a.fanout : entry;
-            if (!a.where && !a.first) a.position[entry] = k < a.dim ? (int64_t)to : -1;
+            a.order[to[i]] = a.fanout > 1 ? from / a.fanout : from;
+            if (!a.where && !a.first) a.position[from] = key[i] < a.dim ? (int64_t)to[i] : -1;
         } else {
-            a.entries_out[to] = entry;
+            a.entries_out[to[i]] = from;
         }
     }
 }
@@ -263,16 +328,26 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(GroupArgs a) {
 __global__ __launch_bounds__(kGroupThreads) void group_bounds(GroupArgs a, const uint32_t *where, int64_t *offsets,
                                                               int64_t *position, uint32_t place_wgs) {
     if (blockIdx.x < place_wgs) {
-        const uint32_t e = (uint32_t)xcd_tile(place_wgs) * kGroupThreads + threadIdx.x;
-        if (e >= a.rows) return;
-        const uint32_t to = a.where[where[e]];
-        position[e] = to == kNoPlace ? -1 : (int64_t)to;
+        const uint32_t first = (uint32_t)xcd_tile(place_wgs) * kGroupThreads * kGroupEach + threadIdx.x;
+        uint32_t at[kGroupEach], to[kGroupEach];
+#pragma unroll
+        for (int i = 0; i < kGroupEach; ++i) {
+            const uint32_t e = first + i * kGroupThreads;
+            at[i] = e < a.rows ? where[e] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kGroupEach; ++i) to[i] = a.where[at[i]];
+#pragma unroll
+        for (int i = 0; i < kGroupEach; ++i) {
+            const uint32_t e = first + i * kGroupThreads;
+            if (e < a.rows) position[e] = to[i] == kNoPlace ? -1 : (int64_t)to[i];
+        }
         return;
     }
     __shared__ uint32_t s_base[(1 << kGroupMaxBits) + 1];
-    __shared__ int64_t s_tmp[2 * kGroupWaves];
+    __shared__ uint32_t s_tmp[kGroupWaves];
     const int digits = 1 << a.bits;
-    digit_bases<kGroupThreads>(a.totals, digits, s_base, s_tmp);
+    digit_bases<kGroupThreads, 1 << kGroupMaxBits>(a.totals, digits, s_base, s_tmp);
     if (threadIdx.x == 0) s_base[digits] = a.rows;
     __syncthreads();
     const uint64_t s = (uint64_t)(blockIdx.x - place_wgs) * kGroupThreads + threadIdx.x;
@@ -297,7 +372,7 @@ template <int THREADS, int BITS>
 __global__ __launch_bounds__(THREADS) void group_small(GroupArgs a) {
     constexpr int kWaves = THREADS / 64;
     extern __shared__ uint32_t s_count[];  // [waves][digits], [digits] totals, [digits] bases
-    __shared__ int64_t s_tmp[2 * kWaves];
+    __shared__ uint32_t s_tmp[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int digits = (int)a.dim + 1;
     uint32_t *s_total = s_count + kWaves * digits, *s_base = s_total + digits;
@@ -322,7 +397,7 @@ __global__ __launch_bounds__(THREADS) void group_small(GroupArgs a) {
         s_total[d] = n;
     }
     __syncthreads();
-    digit_bases<THREADS>(s_total, digits, s_base, s_tmp);
+    digit_bases<THREADS, 1 << BITS>(s_total, digits, s_base, s_tmp);
     for (int d = threadIdx.x; d < digits; d += THREADS) {
         uint32_t at = s_base[d];
         a.offsets[d] = at;
@@ -443,7 +518,8 @@ extern "C" int segred_group(const int64_t *index, int64_t rows, int64_t fanout, 
     a.few = p.tiles <= kGroupFewTiles && p.tiles << p.bits <= kGroupFewCounts;
     auto array = [&](int i) { return reinterpret_cast<uint32_t *>(w + p.hist + p.totals + i * p.pairs); };
     const unsigned digits = 1u << p.bits;
-    const size_t count_lds = kGroupWaves * digits * 4, place_lds = count_lds + 2 * digits * 4 + 2 * kGroupThreads * p.steps * 4;
+    const size_t count_lds = kGroupWaves * digits * 4;
+    const size_t place_lds = kGroupWaves * digits * 2 + 2 * digits * 4 + kGroupThreads * p.steps * 4;
     a.position = position;
     for (int pass = 0; pass < p.passes; ++pass) {
         a.shift = pass * p.bits;
@@ -476,7 +552,7 @@ extern "C" int segred_group(const int64_t *index, int64_t rows, int64_t fanout, 
     }
     if (p.passes > 1) {
         const uint32_t bounds = (uint32_t)((dim_size + kGroupThreads) / kGroupThreads);
-        const uint32_t places = p.passes == 2 ? (a.rows + kGroupThreads - 1) / kGroupThreads : 0;
+        const uint32_t places = p.passes == 2 ? (a.rows + kGroupThreads * kGroupEach - 1) / (kGroupThreads * kGroupEach) : 0;
         timed_launch_ggl(false, group_bounds, dim3(bounds + places), dim3(kGroupThreads), 0, stream, a,
                          (const uint32_t *)array(3), offsets, position, places);
         if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
