@@ -227,23 +227,25 @@ template <int MT, int NT, bool B_COL, int BW>
 __device__ __forceinline__ void split_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
                                                int n0, int lane) {
     bf16x8 hi[NT], lo[NT];
+    u32x4 b[1][NT];
+    if constexpr (B_COL) col_frags<_Float16, BW>(b, lb, n0, lane);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        u32x4 b;
-        if constexpr (B_COL) b = col_frag<_Float16, BW>(lb, n0 + 16 * j, 0, lane);
-        else b = row_frag(lb, n0 + 16 * j, 0, lane);
-        const f16x8 h = __builtin_bit_cast(f16x8, b);
+        if constexpr (!B_COL) b[0][j] = row_frag(lb, n0 + 16 * j, 0, lane);
+        const f16x8 h = __builtin_bit_cast(f16x8, b[0][j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             hi[j][e] = (__bf16)(float)h[e];
             lo[j][e] = (__bf16)((float)h[e] - (float)hi[j][e]);
         }
     }
+    u32x4 u[2][MT];
+    row_frags(u, la, m0, lane);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const bf16x8 a = __builtin_bit_cast(bf16x8, row_frag(la, m0 + 16 * i, ks, lane));
+            const bf16x8 a = __builtin_bit_cast(bf16x8, u[ks][i]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[j], a, acc[i][j], 0, 0, 0);
@@ -292,8 +294,10 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     constexpr int kABytes = AStage::kBytes;
     constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
     constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
-    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes];
-    __shared__ int s_ids[BM], s_list[BM], s_count;
+    // one array: beside a second the compiler's reads of LDS wait for all loads
+    // into it, also for those of later steps
+    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes + (2 * BM + 1) * sizeof(int)];
+    int *s_ids = reinterpret_cast<int *>(lds_mem + STAGES * kStageBytes), *s_list = s_ids + BM, *s_count = s_list + BM;
     lds_char *lds = (lds_char *)lds_mem;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)BM, end - row0);
     const int K = (int)a.K;
-    const int met = tile_adapters<BM, kThreads>(a, row0, rows, s_ids, s_list, &s_count);
+    const int met = tile_adapters<BM, kThreads>(a, row0, rows, s_ids, s_list, s_count);
 
     AStage sa;
     sa.init(wave, lane, K, [&](int r) -> const char * {
@@ -555,8 +559,10 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     using BRow = RowStage<T, kHalf, kPhaseThreads, true>;
     using BCol = ColStage<T, kHalf, kPhaseThreads, true>;
     constexpr int BM = AH * kHalf;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
-    __shared__ int s_ids[BM], s_list[BM], s_count;
+    // one array: beside a second the compiler's reads of LDS wait for all loads
+    // into it, also for those of later steps
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds + (2 * BM + 1) * sizeof(int)];
+    int *s_ids = reinterpret_cast<int *>(lds_mem + kPhaseLds), *s_list = s_ids + BM, *s_count = s_list + BM;
     lds_char *lds = (lds_char *)lds_mem;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -570,7 +576,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     if (row0 >= end || row0 < 0) return;
     const int rows = (int)min((int64_t)BM, end - row0);
     const int K = (int)a.K, R = (int)a.R;
-    const int met = tile_adapters<BM, kPhaseThreads>(a, row0, rows, s_ids, s_list, &s_count);
+    const int met = tile_adapters<BM, kPhaseThreads>(a, row0, rows, s_ids, s_list, s_count);
 
     AStage sa[AH];
 #pragma unroll
@@ -614,7 +620,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
                 sbr[h].issue(place, wave, k0);
             }
         },
-        [](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); },
+        [](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); },
         [](int) {});
     __syncthreads();
 
@@ -660,14 +666,14 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
             }
         }
     };
-    auto products = [&](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) {
+    auto products = [&](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) {
         if constexpr (__is_same(T, _Float16)) {
             // bf16 halves of u against the two bf16 that a float16 is the sum
-            // of; y[.][1] holds the same ranks again, so wait for it here
+            // of; y[1] holds the same ranks again, so wait for it here
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const f16x8 h = __builtin_bit_cast(f16x8, y[j][0]);
+                const f16x8 h = __builtin_bit_cast(f16x8, y[0][j]);
                 bf16x8 hi, lo;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -678,7 +684,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const bf16x8 v = __builtin_bit_cast(bf16x8, x[i][ks]);
+                        const bf16x8 v = __builtin_bit_cast(bf16x8, x[ks][i]);
                         c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, v, c[i][j], 0, 0, 0);
                         c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, v, c[i][j], 0, 0, 0);
                     }

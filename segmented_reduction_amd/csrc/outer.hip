@@ -103,12 +103,26 @@ __device__ __forceinline__ void outer_store(const OuterArgs &a, int64_t s, int64
         store_quad<T>(static_cast<T *>(a.out) + (s * a.K + r) * a.M, n, a.M, c, a.vec != 0);
 }
 
-// Byte offset of the source row behind row r of a slot, -1: a row of zeros.
-__device__ __forceinline__ int64_t outer_source(const OuterPlace &at, const int64_t *index, int64_t count,
-                                                int64_t row_bytes, int64_t r) {
-    if (r >= at.rows) return -1;
-    const int64_t v = index ? index[at.row0 + r] : at.row0 + r;
-    return v >= 0 && v < count ? v * row_bytes : -1;
+// The loads of the source rows of rows row(0), row(1) ... of a slot, if they are
+// gathered.  Behind its last row they read that one again: in branches each
+// load would be waited for by itself.
+template <int N, typename R>
+__device__ __forceinline__ void outer_ask(int64_t (&v)[N], const OuterPlace &at, const int64_t *index, R row) {
+    if (!index) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = index[at.row0 + min((int64_t)row(i), at.rows - 1)];
+}
+
+// What they become: byte offsets, -1: a row of zeros.
+template <int N, typename R>
+__device__ __forceinline__ void outer_offsets(int64_t (&v)[N], const OuterPlace &at, const int64_t *index, int64_t count,
+                                              int64_t row_bytes, R row) {
+    if (!index) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = at.row0 + row(i);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = row(i) < at.rows && v[i] >= 0 && v[i] < count ? v[i] * row_bytes : -1;
 }
 
 // Stores a wave's neighbouring blocks.
@@ -140,22 +154,25 @@ struct OuterTile {
         SB sb;
         int64_t ia[SA::kLoads], ib[SB::kLoads];  // source rows of the next step's units
         auto fetch = [&](int64_t k0) {
-#pragma unroll
-            for (int i = 0; i < SA::kLoads; ++i)
-                ia[i] = outer_source(at, a.left_rows, a.left_count, lb, k0 + SA::row(i, wave, lane));
-#pragma unroll
-            for (int i = 0; i < SB::kLoads; ++i)
-                ib[i] = outer_source(at, a.right_rows, a.right_count, rb, k0 + SB::row(i, wave, lane));
+            outer_ask(ia, at, a.left_rows, [&](int i) { return k0 + SA::row(i, wave, lane); });
+            outer_ask(ib, at, a.right_rows, [&](int i) { return k0 + SB::row(i, wave, lane); });
         };
-        auto issue = [&](lds_char *buf) {
+        auto issue = [&](int64_t k0, lds_char *buf) {
+            int64_t oa[SA::kLoads], ob[SB::kLoads];
+#pragma unroll
+            for (int i = 0; i < SA::kLoads; ++i) oa[i] = ia[i];
+#pragma unroll
+            for (int i = 0; i < SB::kLoads; ++i) ob[i] = ib[i];
+            outer_offsets(oa, at, a.left_rows, a.left_count, lb, [&](int i) { return k0 + SA::row(i, wave, lane); });
+            outer_offsets(ob, at, a.right_rows, a.right_count, rb, [&](int i) { return k0 + SB::row(i, wave, lane); });
             sa.issue(
                 buf, wave,
-                [&](int i) { return (uint64_t)(a.left + ia[i] + (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-                [&](int i) { return ia[i] >= 0 ? (int)(a.K - m0) - SA::col(i, wave, lane) : 0; });
+                [&](int i) { return (uint64_t)(a.left + oa[i] + (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T)); },
+                [&](int i) { return oa[i] >= 0 ? (int)(a.K - m0) - SA::col(i, wave, lane) : 0; });
             sb.issue(
                 buf + SA::kBytes, wave,
-                [&](int i) { return (uint64_t)(a.right + ib[i] + (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-                [&](int i) { return ib[i] >= 0 ? (int)(a.M - n0) - SB::col(i, wave, lane) : 0; });
+                [&](int i) { return (uint64_t)(a.right + ob[i] + (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T)); },
+                [&](int i) { return ob[i] >= 0 ? (int)(a.M - n0) - SB::col(i, wave, lane) : 0; });
         };
         auto commit = [&](lds_char *buf) {
             sa.commit(buf, wave, lane);
@@ -167,7 +184,7 @@ struct OuterTile {
         const int64_t steps = (at.rows + kStep<T> - 1) / kStep<T>;
         if (steps > 0) {
             fetch(0);
-            issue(lds);
+            issue(0, lds);
             fetch(kStep<T>);
             commit(lds);
         }
@@ -175,7 +192,7 @@ struct OuterTile {
             wait_and_meet<0>();
             lds_char *next = lds + ((t + 1) & 1) * kStageBytes;
             if (t + 1 < steps) {
-                issue(next);
+                issue((t + 1) * kStep<T>, next);
                 fetch((t + 2) * kStep<T>);
             }
             const lds_char *buf = lds + (t & 1) * kStageBytes;
@@ -216,27 +233,26 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
     SB sb;
     int64_t ia[SA::kParts], ib[SB::kParts];  // source rows of the next step's parts
     auto fetch = [&](int64_t k0) {
-#pragma unroll
-        for (int i = 0; i < SA::kParts; ++i)
-            ia[i] = outer_source(at, a.left_rows, a.left_count, a.K * 4, k0 + SA::row(i, tid));
-#pragma unroll
-        for (int i = 0; i < SB::kParts; ++i)
-            ib[i] = outer_source(at, a.right_rows, a.right_count, a.M * 4, k0 + SB::row(i, tid));
+        outer_ask(ia, at, a.left_rows, [&](int i) { return k0 + SA::row(i, tid); });
+        outer_ask(ib, at, a.right_rows, [&](int i) { return k0 + SB::row(i, tid); });
     };
     f32x4 acc[MT][NT] = {};
     float bad = 0.f;
     const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
     const char *left = a.left + at.m0 * 4, *right = a.right + at.n0 * 4;
     const int kleft = (int)(a.K - at.m0), mleft = (int)(a.M - at.n0);
-    fetch(0);
+    if (at.rows > 0) fetch(0);
     split_steps(
         (at.rows + kSplitK - 1) / kSplitK,
         [&](int64_t t) {
+            const int64_t k0 = t * kSplitK;
+            outer_offsets(ia, at, a.left_rows, a.left_count, a.K * 4, [&](int i) { return k0 + SA::row(i, tid); });
+            outer_offsets(ib, at, a.right_rows, a.right_count, a.M * 4, [&](int i) { return k0 + SB::row(i, tid); });
             sa.issue([&](int i) { return (uint64_t)(left + ia[i] + SA::at(i, tid) * 4); },
                      [&](int i) { return ia[i] >= 0 ? kleft - SA::at(i, tid) : 0; });
             sb.issue([&](int i) { return (uint64_t)(right + ib[i] + SB::at(i, tid) * 4); },
                      [&](int i) { return ib[i] >= 0 ? mleft - SB::at(i, tid) : 0; });
-            fetch((t + 1) * kSplitK);
+            fetch(k0 + kSplitK);
         },
         [&] {
             sa.commit(lds, tid, bad);
@@ -267,8 +283,10 @@ template <typename T>
 __global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
     using Stage = ColStage<T, kHalf, kPhaseThreads, true>;
     constexpr int kRows = kStep<T>;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
-    __shared__ int64_t s_rows[2][kRing][kRows];  // left, right
+    // one array: beside a second the compiler's reads of LDS wait for all loads
+    // into it, also for those of later steps
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds + 2 * kRing * kRows * sizeof(int64_t)];
+    auto *s_rows = reinterpret_cast<int64_t (*)[kRing][kRows]>(lds_mem + kPhaseLds);  // [left, right]
     lds_char *lds = (lds_char *)lds_mem;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -276,15 +294,26 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
     if (!at.work) return;
     const int64_t s = at.s, slot = at.slot, rows = at.rows, m0 = at.m0, n0 = at.n0;
 
-    auto left_source = [&](int64_t r) { return outer_source(at, a.left_rows, a.left_count, a.K * (int64_t)sizeof(T), r); };
-    auto right_source = [&](int64_t r) { return outer_source(at, a.right_rows, a.right_count, a.M * (int64_t)sizeof(T), r); };
-    for (int i = threadIdx.x; i < 4 * kRows; i += kPhaseThreads) {
-        s_rows[0][i / kRows][i % kRows] = left_source(i);
-        s_rows[1][i / kRows][i % kRows] = right_source(i);
+    const int64_t lb = a.K * (int64_t)sizeof(T), rb = a.M * (int64_t)sizeof(T);
+    // source rows of step t + 4, held by waves 0 (left) and 1 (right) until the
+    // step after they were asked for
+    const int64_t *index = wave == 0 ? a.left_rows : a.right_rows;
+    const int64_t count = wave == 0 ? a.left_count : a.right_count, bytes = wave == 0 ? lb : rb;
+    int64_t ahead[1] = {};
+    auto ask = [&](int64_t k0) { outer_ask(ahead, at, index, [&](int) { return k0 + lane; }); };
+    if (rows > 0) {
+        for (int i = threadIdx.x; i < 4 * kRows; i += kPhaseThreads) {
+            int64_t l[1], r[1];
+            auto row = [&](int) { return (int64_t)i; };
+            outer_ask(l, at, a.left_rows, row);
+            outer_ask(r, at, a.right_rows, row);
+            outer_offsets(l, at, a.left_rows, a.left_count, lb, row);
+            outer_offsets(r, at, a.right_rows, a.right_count, rb, row);
+            s_rows[0][i / kRows][i % kRows] = l[0];
+            s_rows[1][i / kRows][i % kRows] = r[0];
+        }
+        if (wave < 2) ask(4 * kRows);
     }
-    int64_t ahead = -1;  // of step t + 4, held by waves 0 (left) and 1 (right)
-    if (wave == 0) ahead = left_source(4 * kRows + lane);
-    if (wave == 1) ahead = right_source(4 * kRows + lane);
     __syncthreads();
 
     auto fetch = [&](int side, int h, int t, lds_char *place, const char *base, int64_t width, int64_t c0) {
@@ -300,7 +329,7 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
         Stage st;
         st.issue(place, wave, [&](int i) { return (uint64_t)col[i]; }, [&](int i) { return left[i]; });
     };
-    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[4][2], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
     f32x4 acc[2][2][4][2] = {};
     const int64_t steps = (rows + kRows - 1) / kRows;
     if (steps > 0)
@@ -310,9 +339,11 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
             [&](int h, int t, lds_char *place) { fetch(1, h, t, place, a.right, a.M, n0); }, products,
             [&](int t) {
                 if (wave < 2) {
-                    s_rows[wave][(t + 4) & (kRing - 1)][lane] = ahead;
-                    const int64_t r = (int64_t)(t + 5) * kRows + lane;
-                    ahead = wave == 0 ? left_source(r) : right_source(r);
+                    const int64_t k0 = (int64_t)(t + 4) * kRows;
+                    int64_t off[1] = {ahead[0]};
+                    outer_offsets(off, at, index, count, bytes, [&](int) { return k0 + lane; });
+                    s_rows[wave][(t + 4) & (kRing - 1)][lane] = off[0];
+                    ask(k0 + kRows);
                 }
             });
 
