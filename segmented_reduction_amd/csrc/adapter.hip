@@ -741,7 +741,7 @@ int adapter_main_launch(AdapterArgs a, bool b_col, hipStream_t st) {
 
 template <typename T, int MT, bool DIRECT>
 int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
-    constexpr int NW = 8, STAGES = DIRECT ? 3 : 2;
+    constexpr int NW = DIRECT ? 4 : 8, STAGES = DIRECT ? 3 : 2;
     a.slots = tight_slots(a.N, a.S, __builtin_ctz(16 * MT));
     dim3 grid;
     const int64_t copies = a.copy_from ? a.S * ((a.M + kCopyRows - 1) / kCopyRows) : 0;
@@ -751,10 +751,20 @@ int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+constexpr int64_t kAdapterTall = 128;  // tiles of 64 rows
 constexpr int64_t kAdapterFew = 128;  // rows up to which waves split the contraction
 template <typename T>
 int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool main_direct, hipStream_t st) {
-    int rc = low_direct ? adapter_low_launch<T, 1, true>(a, b_col, st) : adapter_low_launch<T, 1, false>(a, b_col, st);
+    // x A^T in tiles of 16 rows and 32 ranks, of 64 rows where there are ranks
+    // for two tiles and enough of them.  bfloat16 beside 4,096 x 256, times of
+    // 16 and of 64: 45 us and 48 for 6,000 rows of rank 16; of rank 64, 41 and
+    // 43 for 2,048 rows, 48 and 45 for 4,096, 55 and 49 for 6,000.  (Tiles of 16
+    // rows by 4 waves, of which a CU holds two; with 8 waves the latter take 60.)
+    const bool tall = sizeof(T) == 2 && a.blocks > 1 && (a.N / 64 + a.S / 2) * a.blocks >= kAdapterTall;
+    int rc;
+    if (!low_direct) rc = adapter_low_launch<T, 1, false>(a, b_col, st);
+    else if (tall) rc = adapter_low_launch<T, sizeof(T) == 2 ? 4 : 1, true>(a, b_col, st);
+    else rc = adapter_low_launch<T, 1, true>(a, b_col, st);
     if (rc != SEGRED_OK) return rc;
     if (main_direct && a.N <= kAdapterFew) {
         if (a.N <= 16) return adapter_few_launch<T, 1, 8, 4>(a, b_col, st);
