@@ -464,18 +464,27 @@ int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
 // Times in us of bfloat16 products of 64 segments, 2,048 x 2,048, whose mean
 // rows are given (uneven; weights from HBM; "row" is a transposed weight):
 //
-//   mean          4    16    32    64   128   256   512
-//   few         101   133   214   378                     row
-//   64 x 128    139   131   137   160   183   273   452   row
-//   256 x 256               153   154   168   225   343   row
-//   128 x 256               153   153   175   234   367   row
-//   few         112   153   230   380                     col
-//   64 x 128    110   104   111   145   185   292   488   col
-//   128 x 256               195   167   198   290   479   col
+//   mean          4    16    32    64    96   128   256   512
+//   few         104   141   220   384                           row
+//   64 x 128    140   130   133   151   169   188   287   436   row
+//   256 x 256   130   150   150   148   156   164   218   310   row
+//   128 x 256   151   143   140   143   161   164   225   358   row
+//   few         100   142   200   350                           col
+//   64 x 128    106   108   116   141   163   183   262   444   col
+//   128 x 256   126   120   118   122   155   160   230   387   col
 //
-// and with few tiles (8 segments, 2,048 x 1,024): 64 x 64 with three buffers
-// takes 14 us at 64 rows, 23 at 256 and 59 at 1,024, 64 x 128 22, 24 and 52,
-// 128 x 256 34 and 67 at 256 and 1,024, 256 x 256 49 and 53.
+// and with few tiles (8 segments, 2,048 x 1,024):
+//
+//   mean          8    16    64   256   512  1024
+//   few           9    10    22    56               row
+//   64 x 64      12    12    13    23    34    58   row
+//   64 x 128     20    21    21    23    32    52   row
+//   256 x 256    31    31    31    43    45    49   row
+//   few          10    11    23    59               col
+//   64 x 64      16    15    16    27    36    62   col
+//   64 x 128     20    20    21    25    34    55   col
+//   128 x 256    36    36    36    38    41    78   col
+//
 // float (64 segments, 2,048 x 2,048; "row" and "col" are near each other),
 // the last line in bf16 parts:
 //
@@ -486,7 +495,7 @@ int matmul_launch(MatmulArgs a, bool b_col, hipStream_t st) {
 //
 // and with few tiles (8 segments, 2,048 x 1,024): 32 x 64 takes 46 us at 64 rows
 // and 124 at 256, 64 x 128 83 and 106.
-constexpr int64_t kFewRows = 8, kManyRows = 96, kManyColRows = 256, kManyTiles = 1536, kFewTiles = 512;
+constexpr int64_t kFewRows = 8, kManyRows = 64, kManyTiles = 1536, kFewTiles = 512;
 constexpr int64_t kSplitRows = 24, kSplitTiles = 224;
 template <typename T>
 int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st) {
@@ -502,15 +511,16 @@ int matmul_dispatch(const MatmulArgs &a, bool b_col, bool direct, hipStream_t st
     } else {
         if (!direct && mean <= 2 * kFewRows) return matmul_launch<T, 16, 128, 1, 4, 2, false>(a, b_col, st);
         if (!direct) return matmul_launch<T, 64, 128, 2, 2, 2, false>(a, b_col, st);
-        if (mean <= kFewRows) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
-        if (a.K >= 256 && a.M > 128 && tiles >= kManyTiles && mean >= (b_col ? kManyColRows : kManyRows)) {
+        const bool few_tiles = (a.N / 64 + a.S / 2) * ((a.M + 63) / 64) <= kFewTiles;  // of 64 x 64
+        if (mean <= (few_tiles ? 2 * kFewRows : kFewRows)) return matmul_few_launch<T, 4, 4, 3>(a, b_col, st);
+        if (a.K >= 256 && a.M > 128 && tiles >= kManyTiles && mean >= kManyRows) {
             // a tile of 256 rows takes about 7/4 of one of 128; whole rounds of 256 CUs
             const int64_t nt = (a.M + 255) / 256;
             const int64_t one = ((a.N / 128 + a.S / 2) * nt + 255) / 256, two = ((a.N / 256 + a.S / 2) * nt + 255) / 256;
             if (b_col || 4 * one < 7 * two) return matmul_many_launch<T, 1>(a, b_col, st);
             return matmul_many_launch<T, 2>(a, b_col, st);
         }
-        if ((a.N / 64 + a.S / 2) * ((a.M + 63) / 64) <= kFewTiles) return matmul_launch<T, 64, 64, 2, 2, 3, true>(a, b_col, st);
+        if (few_tiles) return matmul_launch<T, 64, 64, 2, 2, 3, true>(a, b_col, st);
         return matmul_launch<T, 64, 128, 2, 2, 2, true>(a, b_col, st);
     }
 }
