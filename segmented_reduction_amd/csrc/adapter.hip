@@ -606,7 +606,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
         }
     }
     f32x4 acc[2][2][4][2] = {};
-    phase_steps<T, AH, false, B_COL>(
+    phase_steps<T, AH, B_COL>(
         acc, lds, (K + kStep<T> - 1) / kStep<T>, wave, lane,
         [&](int h, int t, lds_char *place) { sa[h].issue(place, wave, t * kStep<T>); },
         [&](int h, int t, lds_char *place) {
@@ -694,7 +694,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
         }
     };
     if (extra > 0)
-        phase_steps<T, AH, false, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products, [](int) {});
+        phase_steps<T, AH, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products, [](int) {});
 
     __syncthreads();
     constexpr int BN = 2 * kHalf;

@@ -31,7 +31,9 @@ struct OuterPlace {
 
 // A tile's work grows with its segment's rows, so where every segment is one
 // slot, up to 64 long ones are taken longest first and the longest tiles do not
-// begin last (8,192 rows in 8 uneven segments of 2,560 x 1,024: 184 -> 88 us).
+// begin last (bfloat16, 8,192 rows in 8 uneven segments of 2,560 x 1,024: 98 ->
+// 75 us; 16,384 in 32 segments of 1,024 x 1,024 whose lengths fall as i^-0.8: 117
+// -> 100; 64 segments of about the same length lose 4%).
 // Up to 16 segments are spread over all XCDs (workgroups are dealt to these in
 // turn), each with one contiguous range of the segment's tiles; more are dealt
 // to the XCDs forth and back, whole, so that the rows of a segment are read into
@@ -273,92 +275,6 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
     outer_blocks<float, MT, NT>(a, at, acc, m_w, n_w, lane);
 }
 
-// Wide operands: 128 x 256 of the output per workgroup, in phases (16-bit
-// types, whole units).  The contraction runs over the segment's rows.  Their
-// source rows are kept in LDS as byte offsets (-1: a row of zeros), four steps
-// ahead of their fetch, so that gathered rows cost no wait.
-constexpr int kRing = 8;  // steps of source rows kept, a power of two
-
-template <typename T>
-__global__ __launch_bounds__(kPhaseThreads) void seg_outer_many(OuterArgs a) {
-    using Stage = ColStage<T, kHalf, kPhaseThreads, true>;
-    constexpr int kRows = kStep<T>;
-    // one array: beside a second the compiler's reads of LDS wait for all loads
-    // into it, also for those of later steps
-    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds + 2 * kRing * kRows * sizeof(int64_t)];
-    auto *s_rows = reinterpret_cast<int64_t (*)[kRing][kRows]>(lds_mem + kPhaseLds);  // [left, right]
-    lds_char *lds = (lds_char *)lds_mem;
-
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const OuterPlace at = outer_place(a, kHalf, 2 * kHalf, lane);
-    if (!at.work) return;
-    const int64_t s = at.s, slot = at.slot, rows = at.rows, m0 = at.m0, n0 = at.n0;
-
-    const int64_t lb = a.K * (int64_t)sizeof(T), rb = a.M * (int64_t)sizeof(T);
-    // source rows of step t + 4, held by waves 0 (left) and 1 (right) until the
-    // step after they were asked for
-    const int64_t *index = wave == 0 ? a.left_rows : a.right_rows;
-    const int64_t count = wave == 0 ? a.left_count : a.right_count, bytes = wave == 0 ? lb : rb;
-    int64_t ahead[1] = {};
-    auto ask = [&](int64_t k0) { outer_ask(ahead, at, index, [&](int) { return k0 + lane; }); };
-    if (rows > 0) {
-        for (int i = threadIdx.x; i < 4 * kRows; i += kPhaseThreads) {
-            int64_t l[1], r[1];
-            auto row = [&](int) { return (int64_t)i; };
-            outer_ask(l, at, a.left_rows, row);
-            outer_ask(r, at, a.right_rows, row);
-            outer_offsets(l, at, a.left_rows, a.left_count, lb, row);
-            outer_offsets(r, at, a.right_rows, a.right_count, rb, row);
-            s_rows[0][i / kRows][i % kRows] = l[0];
-            s_rows[1][i / kRows][i % kRows] = r[0];
-        }
-        if (wave < 2) ask(4 * kRows);
-    }
-    __syncthreads();
-
-    auto fetch = [&](int side, int h, int t, lds_char *place, const char *base, int64_t width, int64_t c0) {
-        const char *col[Stage::kLoads];
-        int left[Stage::kLoads];
-#pragma unroll
-        for (int i = 0; i < Stage::kLoads; ++i) {
-            const int64_t off = s_rows[side][t & (kRing - 1)][Stage::row(i, wave, lane)];
-            const int64_t c = c0 + h * kHalf + Stage::col(i, wave, lane);
-            col[i] = base + off + c * (int64_t)sizeof(T);
-            left[i] = off >= 0 ? (int)(width - c) : 0;
-        }
-        Stage st;
-        st.issue(place, wave, [&](int i) { return (uint64_t)col[i]; }, [&](int i) { return left[i]; });
-    };
-    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
-    f32x4 acc[2][2][4][2] = {};
-    const int64_t steps = (rows + kRows - 1) / kRows;
-    if (steps > 0)
-        phase_steps<T, 1, true, true>(
-            acc, lds, (int)steps, wave, lane,
-            [&](int h, int t, lds_char *place) { fetch(0, h, t, place, a.left, a.K, m0); },
-            [&](int h, int t, lds_char *place) { fetch(1, h, t, place, a.right, a.M, n0); }, products,
-            [&](int t) {
-                if (wave < 2) {
-                    const int64_t k0 = (int64_t)(t + 4) * kRows;
-                    int64_t off[1] = {ahead[0]};
-                    outer_offsets(off, at, index, count, bytes, [&](int) { return k0 + lane; });
-                    s_rows[wave][(t + 4) & (kRing - 1)][lane] = off[0];
-                    ask(k0 + kRows);
-                }
-            });
-
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = m0 + phase_row(0, i, wave) + (lane & 15);
-        if (r >= a.K) continue;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                outer_store<T>(a, s, slot, r, n0 + phase_col(q, j, wave) + (lane >> 4) * 4, acc[0][q][i][j]);
-    }
-}
-
 // Adds the slots of each segment and rounds once.  PARTS threads share a cell:
 // thread p adds the slots p, p + PARTS, ... in that order, then the parts are
 // added in order, so that few cells with many slots still read with many
@@ -445,16 +361,6 @@ int outer_launch(OuterArgs a, bool direct, hipStream_t st) {
     return outer_finish<T>(a, st);
 }
 
-template <typename T>
-int outer_many_launch(OuterArgs a, hipStream_t st) {
-    a.mtiles = (a.K + kHalf - 1) / kHalf;
-    a.ntiles = (a.M + 2 * kHalf - 1) / (2 * kHalf);
-    dim3 grid;
-    if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
-    timed_launch_ggl(true, seg_outer_many<T>, grid, dim3(kPhaseThreads), 0, st, a);
-    return outer_finish<T>(a, st);
-}
-
 template <int BM, int BN>
 int outer_split_launch(OuterArgs a, hipStream_t st) {
     a.mtiles = (a.K + BM - 1) / BM;
@@ -476,11 +382,6 @@ int outer_dispatch(const OuterArgs &a, const OuterPlan &p, bool direct, hipStrea
     } else {
         if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
         if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
-        // 128 x 256 in phases from two such tiles for every CU and eight steps a
-        // segment on: 16,384 rows in 8 segments of 4,096 x 4,096 take 876 us
-        // against 933, but 8,192 rows in 64 segments of 1,024 x 1,024 107 against 72
-        if (direct && a.S * ((a.K + 127) / 128) * ((a.M + 255) / 256) >= 2 * kCus && a.N >= a.S * 512)
-            return outer_many_launch<T>(a, st);
         return outer_launch<T, 128, 128, 2, 2>(a, direct, st);
     }
 }

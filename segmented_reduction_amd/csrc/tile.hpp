@@ -525,13 +525,6 @@ constexpr int kPhaseThreads = 512;
 constexpr int kHalfBytes = kHalf * 128;
 constexpr int kPhaseLds = 9 * kHalfBytes;  // two steps of A0 A1 B0 B1, or three of A0 B0 B1
 
-// Fragments of N neighbouring blocks of a half.
-template <bool COL, typename T, int N>
-__device__ __forceinline__ void half_frags(u32x4 (&f)[2][N], const lds_char *lds, int r0, int lane) {
-    if constexpr (COL) col_frags<T, kHalf>(f, lds, r0, lane);
-    else row_frags(f, lds, r0, lane);
-}
-
 // The products of a phase: c += a b over the step's two k halves.
 template <typename T>
 __device__ __forceinline__ void quadrant(f32x4 (&c)[4][2], const u32x4 (&a)[2][4], const u32x4 (&b)[2][2]) {
@@ -546,14 +539,17 @@ __device__ __forceinline__ void quadrant(f32x4 (&c)[4][2], const u32x4 (&a)[2][4
 // fetch_a(h, t, place) and fetch_b(h, t, place) start half h of step t (two
 // loads per thread; zeros past the last step); products(t, c, a, b) are a
 // phase's; tick(t) is called once a step.  acc[a][b] are the quadrants.
-template <typename T, int AH, bool A_COL, bool B_COL, typename FA, typename FB, typename P, typename K>
+template <typename T, int AH, bool B_COL, typename FA, typename FB, typename P, typename K>
 __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *lds, int steps, int wave, int lane,
                                             FA fetch_a, FB fetch_b, P products, K tick) {
     static_assert(sizeof(T) == 2, "16-bit types");
     const int ma = (wave >> 2) * 64, nb = (wave & 3) * 32;
     u32x4 a[2][4], b0[2][2], b1[2][2];
-    auto read_a = [&](const lds_char *p) { half_frags<A_COL, T>(a, p, ma, lane); };
-    auto read_b = [&](u32x4 (&b)[2][2], const lds_char *p) { half_frags<B_COL, T>(b, p, nb, lane); };
+    auto read_a = [&](const lds_char *p) { row_frags(a, p, ma, lane); };
+    auto read_b = [&](u32x4 (&b)[2][2], const lds_char *p) {
+        if constexpr (B_COL) col_frags<T, kHalf>(b, p, nb, lane);
+        else row_frags(b, p, nb, lane);
+    };
     auto multiply = [&](int t, f32x4 (&c)[4][2], const u32x4 (&b)[2][2]) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
