@@ -105,27 +105,60 @@ __device__ __forceinline__ void outer_store(const OuterArgs &a, int64_t s, int64
         store_quad<T>(static_cast<T *>(a.out) + (s * a.K + r) * a.M, n, a.M, c, a.vec != 0);
 }
 
-// The loads of the source rows of rows row(0), row(1) ... of a slot, if they are
-// gathered.  Behind its last row they read that one again: in branches each
-// load would be waited for by itself.
-template <int N, typename R>
-__device__ __forceinline__ void outer_ask(int64_t (&v)[N], const OuterPlace &at, const int64_t *index, R row) {
-    if (!index) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = index[at.row0 + min((int64_t)row(i), at.rows - 1)];
-}
+// A thread's N units per step of one operand.  row(i) is unit i's row in a step;
+// the address of a row that is not gathered moves on from step to step (two
+// thirds of the instructions of a step of 128 x 128 were addresses before).
+template <int N>
+struct OuterSide {
+    const int64_t *index;  // of the slot's first row, or null
+    uint64_t count, bytes, step_bytes;
+    uint64_t p[N];  // gathered: in row 0
+    int64_t v[N];   // gathered rows of the next step
 
-// What they become: byte offsets, -1: a row of zeros.
-template <int N, typename R>
-__device__ __forceinline__ void outer_offsets(int64_t (&v)[N], const OuterPlace &at, const int64_t *index, int64_t count,
-                                              int64_t row_bytes, R row) {
-    if (!index) {
+    // byte(i): unit i's place in a row; `step`: rows of a step.
+    template <typename R, typename B>
+    __device__ __forceinline__ void init(const OuterPlace &at, const int64_t *rows, int64_t row_count, const char *base,
+                                         int64_t row_bytes, int step, R row, B byte) {
+        index = rows ? rows + at.row0 : nullptr;
+        count = (uint64_t)row_count;
+        bytes = (uint64_t)(uint32_t)row_bytes;
+        step_bytes = bytes * step;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = at.row0 + row(i);
+        for (int i = 0; i < N; ++i)
+            p[i] = (uint64_t)(base + byte(i)) + (rows ? 0 : (uint64_t)(at.row0 + row(i)) * bytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0;
     }
+    // Starts the loads of the gathered rows of the step at row k0 with `left`
+    // rows, if it has any.  Behind the last they read that one again: in
+    // branches each load would be waited for by itself.
+    template <typename R>
+    __device__ __forceinline__ void ask(int64_t k0, int left, R row) {
+        if (!index || left <= 0) return;
+        const int64_t *from = index + k0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = row(i) < at.rows && v[i] >= 0 && v[i] < count ? v[i] * row_bytes : -1;
-}
+        for (int i = 0; i < N; ++i) v[i] = from[(uint32_t)min(row(i), left - 1)];
+    }
+    // Takes note that they have come: of both sides before either issues, and on
+    // every path, or the compiler waits again where it uses their registers,
+    // and then for all that has been issued by then.
+    __device__ __forceinline__ void settle() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+    }
+    // issue(src, ok) for the step that was asked for, or the one after the last.
+    template <typename R, typename F>
+    __device__ __forceinline__ void step(int left, R row, F issue) {
+        if (index) {
+            issue([&](int i) { return p[i] + (uint64_t)v[i] * bytes; },
+                  [&](int i) { return row(i) < left && (uint64_t)v[i] < count; });
+        } else {
+            issue([&](int i) { return p[i]; }, [&](int i) { return row(i) < left; });
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] += step_bytes;
+        }
+    }
+};
 
 // Stores a wave's neighbouring blocks.
 template <typename T, int MT, int NT>
@@ -154,27 +187,30 @@ struct OuterTile {
         const int64_t m0 = at.m0, n0 = at.n0, lb = a.K * (int64_t)sizeof(T), rb = a.M * (int64_t)sizeof(T);
         SA sa;
         SB sb;
-        int64_t ia[SA::kLoads], ib[SB::kLoads];  // source rows of the next step's units
-        auto fetch = [&](int64_t k0) {
-            outer_ask(ia, at, a.left_rows, [&](int i) { return k0 + SA::row(i, wave, lane); });
-            outer_ask(ib, at, a.right_rows, [&](int i) { return k0 + SB::row(i, wave, lane); });
+        OuterSide<SA::kLoads> left;
+        OuterSide<SB::kLoads> right;
+        auto lrow = [&](int i) { return SA::row(i, wave, lane); };
+        auto rrow = [&](int i) { return SB::row(i, wave, lane); };
+        auto lcol = [&](int i) { return (int)(a.K - m0) - SA::col(i, wave, lane); };
+        auto rcol = [&](int i) { return (int)(a.M - n0) - SB::col(i, wave, lane); };
+        left.init(at, a.left_rows, a.left_count, a.left, lb, kStep<T>, lrow,
+                  [&](int i) { return (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T); });
+        right.init(at, a.right_rows, a.right_count, a.right, rb, kStep<T>, rrow,
+                   [&](int i) { return (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T); });
+        auto rows_of = [&](int64_t t) { return (int)max(min(at.rows - t * kStep<T>, (int64_t)kStep<T>), (int64_t)0); };
+        auto ask = [&](int64_t t) {
+            left.ask(t * kStep<T>, rows_of(t), lrow);
+            right.ask(t * kStep<T>, rows_of(t), rrow);
         };
-        auto issue = [&](int64_t k0, lds_char *buf) {
-            int64_t oa[SA::kLoads], ob[SB::kLoads];
-#pragma unroll
-            for (int i = 0; i < SA::kLoads; ++i) oa[i] = ia[i];
-#pragma unroll
-            for (int i = 0; i < SB::kLoads; ++i) ob[i] = ib[i];
-            outer_offsets(oa, at, a.left_rows, a.left_count, lb, [&](int i) { return k0 + SA::row(i, wave, lane); });
-            outer_offsets(ob, at, a.right_rows, a.right_count, rb, [&](int i) { return k0 + SB::row(i, wave, lane); });
-            sa.issue(
-                buf, wave,
-                [&](int i) { return (uint64_t)(a.left + oa[i] + (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-                [&](int i) { return oa[i] >= 0 ? (int)(a.K - m0) - SA::col(i, wave, lane) : 0; });
-            sb.issue(
-                buf + SA::kBytes, wave,
-                [&](int i) { return (uint64_t)(a.right + ob[i] + (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T)); },
-                [&](int i) { return ob[i] >= 0 ? (int)(a.M - n0) - SB::col(i, wave, lane) : 0; });
+        auto issue = [&](int64_t t, lds_char *buf) {
+            left.settle();
+            right.settle();
+            left.step(rows_of(t), lrow, [&](auto src, auto ok) {
+                sa.issue(buf, wave, src, [&](int i) { return ok(i) ? lcol(i) : 0; });
+            });
+            right.step(rows_of(t), rrow, [&](auto src, auto ok) {
+                sb.issue(buf + SA::kBytes, wave, src, [&](int i) { return ok(i) ? rcol(i) : 0; });
+            });
         };
         auto commit = [&](lds_char *buf) {
             sa.commit(buf, wave, lane);
@@ -185,17 +221,17 @@ struct OuterTile {
         const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
         const int64_t steps = (at.rows + kStep<T> - 1) / kStep<T>;
         if (steps > 0) {
-            fetch(0);
+            ask(0);
             issue(0, lds);
-            fetch(kStep<T>);
+            ask(1);
             commit(lds);
         }
         for (int64_t t = 0; t < steps; ++t) {
             wait_and_meet<0>();
             lds_char *next = lds + ((t + 1) & 1) * kStageBytes;
             if (t + 1 < steps) {
-                issue((t + 1) * kStep<T>, next);
-                fetch((t + 2) * kStep<T>);
+                issue(t + 1, next);
+                ask(t + 2);
             }
             const lds_char *buf = lds + (t & 1) * kStageBytes;
             step_products<T, MT, NT, true, BM, true, BN>(acc, buf, buf + SA::kBytes, m_w, n_w, lane);
@@ -233,28 +269,37 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
 
     SA sa;
     SB sb;
-    int64_t ia[SA::kParts], ib[SB::kParts];  // source rows of the next step's parts
-    auto fetch = [&](int64_t k0) {
-        outer_ask(ia, at, a.left_rows, [&](int i) { return k0 + SA::row(i, tid); });
-        outer_ask(ib, at, a.right_rows, [&](int i) { return k0 + SB::row(i, tid); });
+    OuterSide<SA::kParts> left;
+    OuterSide<SB::kParts> right;
+    auto lrow = [&](int i) { return SA::row(i, tid); };
+    auto rrow = [&](int i) { return SB::row(i, tid); };
+    auto lcol = [&](int i) { return (int)(a.K - at.m0) - SA::at(i, tid); };
+    auto rcol = [&](int i) { return (int)(a.M - at.n0) - SB::at(i, tid); };
+    left.init(at, a.left_rows, a.left_count, a.left, a.K * 4, kSplitK, lrow,
+              [&](int i) { return (at.m0 + SA::at(i, tid)) * 4; });
+    right.init(at, a.right_rows, a.right_count, a.right, a.M * 4, kSplitK, rrow,
+               [&](int i) { return (at.n0 + SB::at(i, tid)) * 4; });
+    auto rows_of = [&](int64_t t) { return (int)max(min(at.rows - t * kSplitK, (int64_t)kSplitK), (int64_t)0); };
+    auto ask = [&](int64_t t) {
+        left.ask(t * kSplitK, rows_of(t), lrow);
+        right.ask(t * kSplitK, rows_of(t), rrow);
     };
     f32x4 acc[MT][NT] = {};
     float bad = 0.f;
     const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
-    const char *left = a.left + at.m0 * 4, *right = a.right + at.n0 * 4;
-    const int kleft = (int)(a.K - at.m0), mleft = (int)(a.M - at.n0);
-    if (at.rows > 0) fetch(0);
+    ask(0);
     split_steps(
         (at.rows + kSplitK - 1) / kSplitK,
         [&](int64_t t) {
-            const int64_t k0 = t * kSplitK;
-            outer_offsets(ia, at, a.left_rows, a.left_count, a.K * 4, [&](int i) { return k0 + SA::row(i, tid); });
-            outer_offsets(ib, at, a.right_rows, a.right_count, a.M * 4, [&](int i) { return k0 + SB::row(i, tid); });
-            sa.issue([&](int i) { return (uint64_t)(left + ia[i] + SA::at(i, tid) * 4); },
-                     [&](int i) { return ia[i] >= 0 ? kleft - SA::at(i, tid) : 0; });
-            sb.issue([&](int i) { return (uint64_t)(right + ib[i] + SB::at(i, tid) * 4); },
-                     [&](int i) { return ib[i] >= 0 ? mleft - SB::at(i, tid) : 0; });
-            fetch(k0 + kSplitK);
+            left.settle();
+            right.settle();
+            left.step(rows_of(t), lrow, [&](auto src, auto ok) {
+                sa.issue(src, [&](int i) { return ok(i) ? lcol(i) : 0; });
+            });
+            right.step(rows_of(t), rrow, [&](auto src, auto ok) {
+                sb.issue(src, [&](int i) { return ok(i) ? rcol(i) : 0; });
+            });
+            ask(t + 1);
         },
         [&] {
             sa.commit(lds, tid, bad);
