@@ -1,0 +1,155 @@
+"""Products, adapters and joins over ragged groups at their edges (GPU only):
+rows that do not exist, rows named twice, element offsets past 32 bits, many
+long requests.  Inputs are compared with plain 64-bit forms."""
+import pytest
+import torch
+
+from tests import ragged_util as ru
+from tests.test_gpu_adapter import _check
+
+pytestmark = pytest.mark.gpu
+
+
+def sr():
+    import segmented_reduction_amd
+    return segmented_reduction_amd
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("r", [40, 33])
+def test_long_requests_of_higher_rank(kind, transpose, r):
+    """Enough rows and ranks for the taller tiles of the low-rank rows; requests end inside them."""
+    _check(kind, [700, 1, 1300, 0, 63, 1500, 65, 1400, 128], 136, 264, r, transpose, count=4, seed=r)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("segments,mean,k,m", [(64, 90, 256, 256), (3, 2000, 72, 136), (2, 700, 48, 64), (260, 9, 64, 40),
+                                               (2, 700, 47, 61)])
+def test_outer_of_rows_that_may_not_exist(kind, segments, mean, k, m):
+    """Both operands gathered; a row outside the operand counts as zeros, one named twice counts twice."""
+    t, g = ru.TYPES[kind], ru.gen(segments + k)
+    lengths = torch.randint(0, 2 * mean + 1, (segments,), generator=g)
+    lengths[0] = 0
+    off = ru.offsets(lengths.tolist(), base=5)
+    n, pool = int(off[-1]) + 3, 300
+    left, right = ru.randn(g, pool, k, dtype=t), ru.randn(g, pool + 1, m, dtype=t)
+    li, ri = torch.randint(0, pool, (n,), generator=g), torch.randint(0, pool + 1, (n,), generator=g)
+    li[::13], li[1::29], ri[2::17] = -1, 2 ** 40, pool + 1
+    li[3::31], ri[5::37] = -2 ** 62, 2 ** 32
+    ru.say(f"outer, missing rows {kind} S={segments} N={n} k={k} m={m}")
+    got = sr().outer(left.cuda(), right.cuda(), off.cuda(), left_rows=li.cuda(), right_rows=ri.cuda())
+    torch.cuda.synchronize()
+
+    def rows(v, i):
+        ok = (i >= 0) & (i < v.shape[0])
+        return torch.where(ok[:, None], v[i.clamp(0, v.shape[0] - 1)], 0.0)
+
+    ref, mag = ru.outer(rows(left.double(), li), rows(right.double(), ri), off)
+    ru.assert_close(got, ref, mag, int(lengths.max()), "outer")
+
+
+def test_outer_of_a_tensor_with_itself():
+    g = ru.gen(3)
+    x = ru.randn(g, 1000, 160, dtype=torch.bfloat16)
+    off = ru.offsets([400, 0, 600])
+    ru.say("outer of one tensor")
+    xc = x.cuda()
+    got = sr().outer(xc, xc, off.cuda())
+    ref, mag = ru.outer(x, x, off)
+    ru.assert_close(got, ref, mag, 600, "outer")
+    assert torch.equal(got, got.transpose(1, 2)), "each cell and its mirror sum the same products in the same order"
+
+
+@pytest.mark.parametrize("kind,k", [("bf16", 2048), ("f32", 1030)])
+def test_inputs_past_32_bits(kind, k):
+    """Operands of more than 2^31 elements, of which the last rows are used."""
+    t, g = ru.TYPES[kind], ru.gen(k)
+    n, last, m = 2 ** 31 // k + 5000, 200, 72
+    off = ru.offsets([90, 0, 110])
+    tail = ru.randn(g, last, k, dtype=t)
+    w, y = ru.randn(g, 3, m, k, dtype=t), ru.randn(g, last, m, dtype=t)
+    ru.say(f"inputs past 32 bits {kind} {n} x {k}")
+    x = torch.zeros(n, k, dtype=t, device="cuda")
+    x[n - last:] = tail.cuda()
+    rows = torch.arange(n - last, n, device="cuda").flip(0)
+    flip = tail.flip(0)
+    ref, mag = ru.matmul(flip, w, off, True)
+    ru.assert_close(sr().matmul(x, w.cuda(), off.cuda(), transpose=True, rows=rows), ref, mag, k, "matmul")
+    ref, mag = ru.outer(flip, y, off)
+    ru.assert_close(sr().outer(x, y.cuda(), off.cuda(), left_rows=rows), ref, mag, 110, "outer")
+    # segments that begin and end at the far rows, not gathered
+    far = off + (n - last)
+    ref, mag = ru.outer(tail, y, off)
+    wide = torch.zeros(n, m, dtype=t, device="cuda")
+    wide[n - last:] = y.cuda()
+    ru.assert_close(sr().outer(x, wide, far.cuda()), ref, mag, 110, "outer of far rows")
+    weights = torch.rand(last // 2, 2, generator=g)
+    position = torch.arange(n - last, n).view(-1, 2)
+    out = sr().combine(x, position.cuda(), weights.cuda())
+    two = tail.double().view(-1, 2, k) * weights.double()[:, :, None]
+    ru.assert_close(out, two.sum(1), two.abs().sum(1), 2, "combine")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_outputs_past_32_bits(kind):
+    t, g = ru.TYPES[kind], ru.gen(8)
+    n, k, m, r = 66000, 24, 32768, 8
+    ru.say(f"outputs past 32 bits {kind} {n} x {m}")
+    x, w = ru.randn(g, n, k, dtype=t), ru.randn(g, 2, k, m, dtype=t)
+    off = torch.tensor([0, 33000, n])
+    out = sr().matmul(x.cuda(), w.cuda(), off.cuda())[-100:].clone()
+    ref, mag = ru.matmul(x[-100:], w[1:], torch.tensor([0, 100]))
+    ru.assert_close(out, ref, mag, k, "matmul")
+    down, up = ru.randn(g, 1, r, k, dtype=t), ru.randn(g, 1, m, r, dtype=t)
+    base = w[0].t().contiguous()
+    which = torch.tensor([-1, 0])
+    got = sr().adapter(x.cuda(), base.cuda(), off.cuda(), which.cuda(), down.cuda(), up.cuda())[-100:].clone()
+    ref, mag, part, _, _ = ru.adapter(x[-100:], base, torch.tensor([0, 100]), which[1:], down, up, None, False)
+    ru.assert_close(got, ref, mag, 2 * k + r, "adapter", more=0.0 if kind == "f32" else 2.0 ** -16 * part)
+
+
+@pytest.mark.parametrize("entries,groups", [(262144, 30000), (262145, 30000), (1200000, 700), (1200000, 5000000)])
+def test_group_of_many(entries, groups):
+    g = ru.gen(entries + groups)
+    index = torch.randint(-3, groups + 3, (entries,), generator=g)
+    ru.say(f"group entries={entries} groups={groups}")
+    got = sr().group(index.cuda(), groups)
+    torch.cuda.synchronize()
+    for a, b, name in zip(got, ru.group(index, groups), ("order", "position", "offsets")):
+        assert torch.equal(a.cpu(), b), name
+
+
+def test_gathered_calls_replayed():
+    """Gathered products and outer sums of more than one step, captured and replayed with other rows each time."""
+    g = ru.gen(12)
+    s = sr()
+    pool, n, k, m = 500, 3000, 256, 264
+    off = ru.offsets([900, 0, 1400, 700])
+    x, y = ru.randn(g, pool, k, dtype=torch.bfloat16), ru.randn(g, pool, m, dtype=torch.bfloat16)
+    w = ru.randn(g, 4, k, m, dtype=torch.bfloat16)
+    dev = [v.cuda() for v in (x, y, w, off)]
+    rows = torch.zeros(n, dtype=torch.int64, device="cuda")
+    ru.say("gathered calls replayed")
+
+    def work():
+        return (s.matmul(dev[0], dev[2], dev[3], rows=rows), s.outer(dev[0], dev[1], dev[3], left_rows=rows, right_rows=rows))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        work()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = work()
+    for rep in range(4):
+        rows.copy_(torch.randint(-2, pool + 2, (n,), generator=g))
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, work()):
+            assert torch.equal(a, b), rep
+        torch.cuda.synchronize()
