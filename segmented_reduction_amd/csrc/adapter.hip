@@ -260,7 +260,10 @@ template <int BM, int THREADS>
 __device__ __forceinline__ int tile_adapters(const AdapterArgs &a, int64_t row0, int rows, int *s_ids, int *s_list,
                                              int *s_count) {
     const int tid = threadIdx.x;
-    for (int r = tid; r < BM; r += THREADS) s_ids[r] = r < rows ? a.ids[row0 + r] : -1;
+    for (int r = tid; r < BM; r += THREADS) {
+        const int id = r < rows ? a.ids[row0 + r] : -1;
+        s_ids[r] = id < a.L ? id : -1;
+    }
     if (tid == 0) *s_count = 0;
     __syncthreads();
     if (tid < 64) {  // one wave walks the rows, 64 at a time
@@ -419,7 +422,7 @@ template <typename T, bool B_COL>
 __device__ __forceinline__ f32x4 adapter_quad(const AdapterArgs &a, int64_t row, int adapter, int64_t n) {
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     const int R = (int)a.R, columns = (int)min((int64_t)4, a.M - n);
-    if (adapter < 0 || columns <= 0) return sum;
+    if (adapter < 0 || adapter >= a.L || columns <= 0) return sum;
     constexpr int U = kUnit<T>;
     const char *u = a.u + row * a.blocks * 128;
     const T *b = reinterpret_cast<const T *>(a.second) + (int64_t)adapter * a.M * a.R2;

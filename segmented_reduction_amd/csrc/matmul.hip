@@ -536,7 +536,8 @@ extern "C" int segred_matmul(const void *values, int32_t dtype, int64_t k, const
     if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
     if (k < 1 || m < 1 || value_rows < 0 || num_segments < 0 || num_rows < 0) return SEGRED_ERR_INVALID_ARGUMENT;
     if (!rows && value_rows < num_rows) return SEGRED_ERR_INVALID_ARGUMENT;
-    if (num_segments > 0 && num_rows > 0 && (!values || !weights || !offsets || !out)) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments > 0 && num_rows > 0 && ((value_rows > 0 && !values) || !weights || !offsets || !out))
+        return SEGRED_ERR_INVALID_ARGUMENT;
     if (e == 0 || k > kMaxWidth || m > kMaxWidth) return SEGRED_ERR_UNSUPPORTED;
     if (!aligned(values, e) || !aligned(weights, e) || !aligned(out, e) || !aligned(offsets, 8) || !aligned(rows, 8))
         return SEGRED_ERR_INVALID_ARGUMENT;

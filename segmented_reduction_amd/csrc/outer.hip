@@ -451,7 +451,8 @@ extern "C" int segred_outer(const void *left, const int64_t *left_rows, int64_t 
     if (k < 1 || m < 1 || left_count < 0 || right_count < 0 || num_segments < 0 || num_rows < 0)
         return SEGRED_ERR_INVALID_ARGUMENT;
     if ((!left_rows && left_count < num_rows) || (!right_rows && right_count < num_rows)) return SEGRED_ERR_INVALID_ARGUMENT;
-    if (num_segments > 0 && (!offsets || !out || (num_rows > 0 && (!left || !right)))) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments > 0 && (!offsets || !out || (num_rows > 0 && ((left_count > 0 && !left) || (right_count > 0 && !right)))))
+        return SEGRED_ERR_INVALID_ARGUMENT;
     if (e == 0 || k > kMaxWidth || m > kMaxWidth) return SEGRED_ERR_UNSUPPORTED;
     if (out_dtype != dtype && out_dtype != SEGRED_F32) return SEGRED_ERR_INVALID_ARGUMENT;
     const int64_t oe = float_size(out_dtype);

@@ -153,3 +153,29 @@ def test_gathered_calls_replayed():
         for a, b in zip(outs, work()):
             assert torch.equal(a, b), rep
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("k,m", [(64, 128), (13, 7)])
+def test_no_source_rows_at_all(kind, k, m):
+    """An operand without a row, of which every row that is named is missing."""
+    t = ru.TYPES[kind]
+    s = sr()
+    none = torch.empty(0, k, dtype=t, device="cuda")
+    rows = torch.tensor([0, -1, 5], device="cuda")
+    off = torch.tensor([0, 1, 3], device="cuda")
+    ru.say(f"no source rows {kind} k={k} m={m}")
+    out = s.matmul(none, torch.ones(2, k, m, dtype=t, device="cuda"), off, rows=rows)
+    assert out.shape == (3, m) and not out.any()
+    right = torch.ones(3, m, dtype=t, device="cuda")
+    assert not s.outer(none, right, off, left_rows=rows).any()
+    assert not s.outer(right, none, off, right_rows=rows).any()
+    assert not s.combine(none, rows.view(3, 1), torch.ones(3, 1, device="cuda")).any()
+    values = torch.empty(0, m, dtype=t, device="cuda")
+    grad, part = s.combine_grad(right, values, rows.view(3, 1), torch.ones(3, 1, device="cuda"))
+    assert grad.shape == (0, m) and not part.any()
+    # an adapter call without an adapter, and one whose segments hold no row
+    x, w = torch.ones(3, k, dtype=t, device="cuda"), torch.ones(m, k, dtype=t, device="cuda")
+    down, up = torch.empty(0, 4, k, dtype=t, device="cuda"), torch.empty(0, m, 4, dtype=t, device="cuda")
+    which = torch.tensor([0, 7], device="cuda")
+    assert torch.equal(s.adapter(x, w, off, which, down, up), torch.full((3, m), float(k), dtype=t, device="cuda"))
