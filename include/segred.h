@@ -562,6 +562,9 @@ int segred_combine_grad(const void *grad, const void *values, int32_t dtype, int
  *
  * The low-rank rows enter the second product in float32, or as the sum of two
  * bf16 (2^-17 relative) for the 16-bit types.
+ * An infinity or a NaN of a row reaches that row alone, one of an adapter its
+ * rows alone.  (In the 16-bit types the adapter's part of such a row may be a
+ * NaN where the formula gives an infinity.)
  *
  * Errors: as segred_matmul; also SEGRED_ERR_INVALID_ARGUMENT for rank < 1,
  * adapters < 0 or a workspace that is missing or too small, and

@@ -14,6 +14,7 @@
 // one step multiplies both halves by the same 32 ranks of B.  float16 B is
 // split the same way, because u may leave float16's range.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
@@ -152,6 +153,9 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
     join_waves<NW, MT, NT>(lds, acc, wave, lane, [&](int r, int c, f32x4 sum) {
         if (r >= rows) return;
         sum *= scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r0 + c + j >= R) sum[j] = 0.f;  // not an infinite row's 0 * inf
         char *u = a.u + ((row0 + r) * a.blocks + block) * 128;
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<f32x4 *>(u + c * 4) = sum;
@@ -160,7 +164,8 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 hi[j] = (__bf16)sum[j];
-                lo[j] = (__bf16)(sum[j] - (float)hi[j]);
+                const float rest = sum[j] - (float)hi[j];  // NaN beside an infinity
+                lo[j] = (__bf16)(rest == rest ? rest : 0.f);
             }
             *reinterpret_cast<bf16x4 *>(u + c * 2) = hi;
             *reinterpret_cast<bf16x4 *>(u + 64 + c * 2) = lo;
@@ -254,6 +259,26 @@ __device__ __forceinline__ void split_products(f32x4 (&acc)[MT][NT], const lds_c
         }
 }
 
+// The products of an adapter's step with all rows of a tile, added where a row
+// has that adapter: elsewhere u is zero, but an infinity or a NaN of the
+// adapter would make something of it.  A lane holds columns of the rows
+// m0 + 16 i + lane % 16.
+template <typename T, int MT, int NT, bool B_COL, int BM, int BW>
+__device__ __forceinline__ void adapter_products(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0,
+                                                 int n0, int lane, const int *s_ids, int adapter) {
+    f32x4 part[MT][NT] = {};
+    if constexpr (__is_same(T, _Float16)) split_products<MT, NT, B_COL, BW>(part, la, lb, m0, n0, lane);
+    else step_products<T, MT, NT, false, BM, B_COL, BW>(part, la, lb, m0, n0, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const bool mine = s_ids[m0 + 16 * i + (lane & 15)] == adapter;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] += mine ? part[i][j][e] : 0.f;
+    }
+}
+
 // Fills s_ids (adapter of each tile row, -1: none) and s_list (the adapters
 // met, in row order); returns their number.  All threads must call it.
 template <int BM, int THREADS>
@@ -285,135 +310,259 @@ __device__ __forceinline__ int tile_adapters(const AdapterArgs &a, int64_t row0,
     return *s_count;
 }
 
+// A tile of the output; s_ids and s_list as tile_adapters leaves them.
 template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
+struct AdapterTile {
     static_assert(DIRECT || STAGES == 2, "units that pass through registers use two buffers");
-    constexpr int kThreads = 64 * WM * WN;
-    constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     using Steps = AdapterSteps<T, BM, BN, kThreads, B_COL, DIRECT>;
     using AStage = typename Steps::AS;
     using BRow = typename Steps::BR;
     using BCol = typename Steps::BC;
-    constexpr int kABytes = AStage::kBytes;
-    constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
-    constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
-    // one array: beside a second the compiler's reads of LDS wait for all loads
-    // into it, also for those of later steps
-    __shared__ __attribute__((aligned(1024))) char lds_mem[STAGES * kStageBytes + (2 * BM + 1) * sizeof(int)];
-    int *s_ids = reinterpret_cast<int *>(lds_mem + STAGES * kStageBytes), *s_list = s_ids + BM, *s_count = s_list + BM;
-    lds_char *lds = (lds_char *)lds_mem;
+    static constexpr int kABytes = AStage::kBytes;
+    static constexpr int kStageBytes = kABytes + (B_COL ? BCol::kBytes : BRow::kBytes);
+    static constexpr int kLoads = AStage::kLoads + (B_COL ? BCol::kLoads : BRow::kLoads);
+    static constexpr int kLds = STAGES * kStageBytes;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t total = a.mtiles * a.ntiles;
-    const int64_t id = xcd_tile(total);
-    if (id >= total) return;
-    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
-    const int64_t row0 = a.offsets[0] + at.m * BM;
-    const int64_t n0 = at.n * BN;
-    const int64_t end = min(a.offsets[a.S], a.N);
-    if (row0 >= end || row0 < 0) return;
-    const int rows = (int)min((int64_t)BM, end - row0);
-    const int K = (int)a.K;
-    const int met = tile_adapters<BM, kThreads>(a, row0, rows, s_ids, s_list, s_count);
-
-    AStage sa;
-    sa.init(wave, lane, K, [&](int r) -> const char * {
-        return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
-    });
-    BRow sbr;
-    BCol sbc;
-    uint64_t wp[BCol::kLoads];
-    int wleft[BCol::kLoads];
-    if constexpr (B_COL) {
-#pragma unroll
-        for (int i = 0; i < BCol::kLoads; ++i) {
-            const int64_t n = n0 + BCol::col(i, wave, lane);
-            wp[i] = (uint64_t)(a.weights + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
-            wleft[i] = (int)(a.M - n);
-        }
-    } else {
-        sbr.init(wave, lane, K, [&](int r) -> const char * {
-            return n0 + r < a.M ? a.weights + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+    static __device__ __forceinline__ void run(const AdapterArgs &a, int64_t row0, int rows, int64_t n0, int met,
+                                               const int *s_ids, const int *s_list, lds_char *lds, int wave, int lane) {
+        const int K = (int)a.K;
+        AStage sa;
+        sa.init(wave, lane, K, [&](int r) -> const char * {
+            return r < rows ? a.values + (row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
         });
-    }
-    Steps extra;
-    extra.init(a, s_ids, row0, wave, lane);
-    const int base = (K + kStep<T> - 1) / kStep<T>, blocks = (int)a.blocks;
-    const int steps = base + met * blocks;
-    auto issue = [&](int t, lds_char *buf) {
-        if (t < base || t >= steps) {  // past the last step: zeros
-            const int k0 = t * kStep<T>;
-            sa.issue(buf, wave, k0);
-            if constexpr (B_COL) {
-                const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
-                sbc.issue(
-                    buf + kABytes, wave, [&](int i) { return wp[i] + step; },
-                    [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
-            } else {
-                sbr.issue(buf + kABytes, wave, k0);
+        BRow sbr;
+        BCol sbc;
+        uint64_t wp[BCol::kLoads];
+        int wleft[BCol::kLoads];
+        if constexpr (B_COL) {
+#pragma unroll
+            for (int i = 0; i < BCol::kLoads; ++i) {
+                const int64_t n = n0 + BCol::col(i, wave, lane);
+                wp[i] = (uint64_t)(a.weights + (BCol::row(i, wave, lane) * a.M + n) * (int64_t)sizeof(T));
+                wleft[i] = (int)(a.M - n);
             }
         } else {
-            const int e = (t - base) / blocks;
-            extra.issue(sa, sbr, sbc, a, buf, __builtin_amdgcn_readfirstlane(s_list[e]), (t - base) - e * blocks, n0,
-                        wave, lane);
+            sbr.init(wave, lane, K, [&](int r) -> const char * {
+                return n0 + r < a.M ? a.weights + (n0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+            });
         }
-    };
-    auto commit = [&](lds_char *buf) {
-        sa.commit(buf, wave, lane);
-        if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
-        else sbr.commit(buf + kABytes, wave, lane);
-    };
+        Steps extra;
+        extra.init(a, s_ids, row0, wave, lane);
+        const int base = (K + kStep<T> - 1) / kStep<T>, blocks = (int)a.blocks;
+        const int steps = base + met * blocks;
+        auto issue = [&](int t, lds_char *buf) {
+            if (t < base || t >= steps) {  // past the last step: zeros
+                const int k0 = t * kStep<T>;
+                sa.issue(buf, wave, k0);
+                if constexpr (B_COL) {
+                    const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
+                    sbc.issue(
+                        buf + kABytes, wave, [&](int i) { return wp[i] + step; },
+                        [&](int i) { return k0 + BCol::row(i, wave, lane) < K ? wleft[i] : 0; });
+                } else {
+                    sbr.issue(buf + kABytes, wave, k0);
+                }
+            } else {
+                const int e = (t - base) / blocks;
+                extra.issue(sa, sbr, sbc, a, buf, __builtin_amdgcn_readfirstlane(s_list[e]), (t - base) - e * blocks, n0,
+                            wave, lane);
+            }
+        };
+        auto commit = [&](lds_char *buf) {
+            sa.commit(buf, wave, lane);
+            if constexpr (B_COL) sbc.commit(buf + kABytes, wave, lane);
+            else sbr.commit(buf + kABytes, wave, lane);
+        };
 
-    f32x4 acc[MT][NT] = {};
-    const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
-    auto products = [&](int t, const lds_char *buf) {
-        if (__is_same(T, _Float16) && t >= base)
-            split_products<MT, NT, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
-        else
-            step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
-    };
-    if constexpr (DIRECT) {
+        f32x4 acc[MT][NT] = {};
+        const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+        auto products = [&](int t, const lds_char *buf, auto extra) {
+            if constexpr (decltype(extra)::value)
+                adapter_products<T, MT, NT, B_COL, BM, BN>(acc, buf, buf + kABytes, m_w, n_w, lane, s_ids,
+                                                           s_list[(t - base) / blocks]);
+            else
+                step_products<T, MT, NT, false, BM, B_COL, BN>(acc, buf, buf + kABytes, m_w, n_w, lane);
+        };
+        if constexpr (DIRECT) {
 #pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
-        int cur = 0, fill = STAGES - 1;
-        for (int t = 0; t < steps; ++t) {
-            wait_and_meet<(STAGES - 2) * kLoads>();
-            issue(t + STAGES - 1, lds + fill * kStageBytes);
-            products(t, lds + cur * kStageBytes);
-            cur = cur + 1 == STAGES ? 0 : cur + 1;
-            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
+            int cur = 0, fill = STAGES - 1;
+            auto step = [&](int t, auto extra) {
+                wait_and_meet<(STAGES - 2) * kLoads>();
+                issue(t + STAGES - 1, lds + fill * kStageBytes);
+                products(t, lds + cur * kStageBytes, extra);
+                cur = cur + 1 == STAGES ? 0 : cur + 1;
+                fill = fill + 1 == STAGES ? 0 : fill + 1;
+            };
+            for (int t = 0; t < base; ++t) step(t, std::false_type{});
+            for (int t = base; t < steps; ++t) step(t, std::true_type{});
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the zeros past the last step
+        } else {
+            issue(0, lds);
+            commit(lds);
+            auto step = [&](int t, auto extra) {
+                __syncthreads();
+                if (t + 1 < steps) issue(t + 1, lds);
+                products(t, lds + (t & 1) * kStageBytes, extra);
+                if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
+            };
+            for (int t = 0; t < base; ++t) step(t, std::false_type{});
+            for (int t = base; t < steps; ++t) step(t, std::true_type{});
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the zeros past the last step
-    } else {
-        issue(0, lds);
-        commit(lds);
-        for (int t = 0; t < steps; ++t) {
+
+        T *out = reinterpret_cast<T *>(a.out) + row0 * a.M;
+        if constexpr (sizeof(T) == 2) {
             __syncthreads();
-            if (t + 1 < steps) issue(t + 1, lds);
-            products(t, lds + (t & 1) * kStageBytes);
-            if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
-        }
-    }
-
-    T *out = reinterpret_cast<T *>(a.out) + row0 * a.M;
-    if constexpr (sizeof(T) == 2) {
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                tile_put<T, BN>(lds, m_w + 16 * i + (lane & 15), n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
-        __syncthreads();
-        tile_out<T, BM, BN, kThreads>(lds, out, rows, n0, a.M, a.vec != 0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = m_w + 16 * i + (lane & 15);
-            if (r < rows)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    store_quad<T>(out + r * a.M, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+                    tile_put<T, BN>(lds, m_w + 16 * i + (lane & 15), n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+            __syncthreads();
+            tile_out<T, BM, BN, kThreads>(lds, out, rows, n0, a.M, a.vec != 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int r = m_w + 16 * i + (lane & 15);
+                if (r < rows)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        store_quad<T>(out + r * a.M, n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
+            }
         }
+    }
+};
+
+// The output tile of a workgroup.
+struct AdapterPlace {
+    int64_t row0, n0;
+    int rows;  // 0: nothing to do
+};
+__device__ __forceinline__ AdapterPlace adapter_place(const AdapterArgs &a, int bm, int bn) {
+    AdapterPlace p{0, 0, 0};
+    const int64_t total = a.mtiles * a.ntiles, id = xcd_tile(total);
+    if (id >= total) return p;
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    p.row0 = a.offsets[0] + at.m * bm;
+    p.n0 = at.n * bn;
+    const int64_t end = min(a.offsets[a.S], a.N);
+    if (p.row0 >= 0 && p.row0 < end) p.rows = (int)min((int64_t)bm, end - p.row0);
+    return p;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool B_COL, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
+    using Tile = AdapterTile<T, BM, BN, WM, WN, STAGES, B_COL, DIRECT>;
+    // one array: beside a second the compiler's reads of LDS wait for all loads
+    // into it, also for those of later steps
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds + (2 * BM + 1) * sizeof(int)];
+    int *s_ids = reinterpret_cast<int *>(lds_mem + Tile::kLds), *s_list = s_ids + BM, *s_count = s_list + BM;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const AdapterPlace p = adapter_place(a, BM, BN);
+    if (p.rows == 0) return;
+    const int met = tile_adapters<BM, Tile::kThreads>(a, p.row0, p.rows, s_ids, s_list, s_count);
+    Tile::run(a, p.row0, p.rows, p.n0, met, s_ids, s_list, (lds_char *)lds_mem, wave, lane);
+}
+
+// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// computed again with float products.
+constexpr int kSplitThreads = 256;
+template <int BN, bool B_COL, bool WHOLE>
+__global__ __launch_bounds__(kSplitThreads, 3) void adapter_main_split(AdapterArgs a) {
+    constexpr int BM = 64;
+    static_assert(kSplitK == kRankBlock, "a step is a block of ranks");
+    using Plain = AdapterTile<float, BM, 64, 2, 2, 2, B_COL, false>;
+    using SA = SplitStage<BM, kSplitThreads, false, WHOLE>;
+    using SB = SplitStage<BN, kSplitThreads, B_COL, WHOLE>;
+    constexpr int MT = BM / 32, NT = BN / 32, kSplitLds = 3 * (SA::kPlane + SB::kPlane);
+    constexpr int kLds = kSplitLds > Plain::kLds ? kSplitLds : Plain::kLds;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kLds + (2 * BM + 1) * sizeof(int)];
+    int *s_ids = reinterpret_cast<int *>(lds_mem + kLds), *s_list = s_ids + BM, *s_count = s_list + BM;
+    lds_char *lds = (lds_char *)lds_mem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const AdapterPlace p = adapter_place(a, BM, BN);
+    if (p.rows == 0) return;
+    const int met = tile_adapters<BM, kSplitThreads>(a, p.row0, p.rows, s_ids, s_list, s_count);
+
+    const int K = (int)a.K, M = (int)a.M, R = (int)a.R;
+    SA sa;
+    SB sb;
+    uint64_t ap[SA::kParts], bp[SB::kParts];
+    int aleft[SA::kParts], bleft[SB::kParts];
+#pragma unroll
+    for (int i = 0; i < SA::kParts; ++i) {
+        const int r = SA::row(i, tid), c = SA::at(i, tid);
+        ap[i] = (uint64_t)(a.values + ((p.row0 + r) * a.K + c) * 4);
+        aleft[i] = r < p.rows ? K - c : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < SB::kParts; ++i) {
+        const int64_t r = SB::row(i, tid), c = SB::at(i, tid);
+        if constexpr (B_COL) {
+            bp[i] = (uint64_t)(a.weights + (r * a.M + p.n0 + c) * 4);
+            bleft[i] = (int)(a.M - p.n0 - c);
+        } else {
+            bp[i] = (uint64_t)(a.weights + ((p.n0 + r) * a.K + c) * 4);
+            bleft[i] = p.n0 + r < a.M ? K - (int)c : 0;
+        }
+    }
+    const int base = (K + kSplitK - 1) / kSplitK, blocks = (int)a.blocks;
+    f32x4 acc[MT][NT] = {};
+    float bad = 0.f;
+    const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
+    split_steps(
+        base + met * blocks,
+        [&](int64_t step) {
+            const int t = (int)step;
+            if (t < base) {
+                const int k0 = t * kSplitK;
+                sa.issue([&](int i) { return ap[i] + (uint64_t)k0 * 4; }, [&](int i) { return aleft[i] - k0; });
+                if constexpr (B_COL)
+                    sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * M * 4; },
+                             [&](int i) { return k0 + SB::row(i, tid) < K ? bleft[i] : 0; });
+                else
+                    sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * 4; }, [&](int i) { return bleft[i] - k0; });
+                return;
+            }
+            const int e = (t - base) / blocks, rank = ((t - base) - e * blocks) * kRankBlock;
+            const int adapter = __builtin_amdgcn_readfirstlane(s_list[e]);
+            const char *w = a.second + (int64_t)adapter * a.M * a.R2 * 4;
+            sa.issue(
+                [&](int i) {
+                    return (uint64_t)(a.u + (p.row0 + SA::row(i, tid)) * a.blocks * 128 + (rank + SA::at(i, tid)) * 4);
+                },
+                [&](int i) { return s_ids[SA::row(i, tid)] == adapter ? 8 : 0; });
+            if constexpr (B_COL)
+                sb.template issue<false>(
+                    [&](int i) { return (uint64_t)(w + ((rank + SB::row(i, tid)) * a.M + p.n0 + SB::at(i, tid)) * 4); },
+                    [&](int i) { return rank + SB::row(i, tid) < R ? (int)(a.M - p.n0) - SB::at(i, tid) : 0; });
+            else
+                sb.template issue<false>(
+                    [&](int i) { return (uint64_t)(w + ((p.n0 + SB::row(i, tid)) * a.R2 + rank + SB::at(i, tid)) * 4); },
+                    [&](int i) { return p.n0 + SB::row(i, tid) < a.M ? R - rank - SB::at(i, tid) : 0; });
+        },
+        [&] {
+            sa.commit(lds, tid, bad);
+            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+        },
+        [&] { split_step<MT, NT, false, BM, B_COL, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
+    if (__syncthreads_or(bad != 0.f)) {
+        for (int c = 0; c < BN && p.n0 + c < a.M; c += 64) {
+            __syncthreads();
+            Plain::run(a, p.row0, p.rows, p.n0 + c, met, s_ids, s_list, lds, wave, lane);
+        }
+        return;
+    }
+    float *out = reinterpret_cast<float *>(a.out) + p.row0 * a.M;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int r = m_w + 16 * i + (lane & 15);
+        if (r < p.rows)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                store_quad<float>(out + r * a.M, p.n0 + n_w + 16 * j + (lane >> 4) * 4, a.M, acc[i][j], a.vec != 0);
     }
 }
 
@@ -554,6 +703,39 @@ int adapter_few_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+// Puts zeros in the place of infinities and NaN of eight elements.
+template <typename T>
+__device__ __forceinline__ void drop_specials(u32x4 &v, bool &dropped) {
+    constexpr uint32_t kExp = __is_same(T, _Float16) ? 0x7c007c00u : 0x7f807f80u, kOne = __is_same(T, _Float16) ? 0x04000400u : 0x00800080u;
+    uint32_t flag[4], any = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        flag[q] = ((v[q] & kExp) + kOne) & 0x80008000u;  // an exponent of all ones
+        any |= flag[q];
+    }
+    if (ballot(any != 0) != 0) {
+        dropped = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] &= ~((flag[q] >> 15) * 0xffffu);
+    }
+}
+
+// What they make of their own rows: the elements of a stored tile whose
+// adapter's part is infinite or NaN.
+template <typename T, bool B_COL, int BN, int THREADS>
+__device__ __forceinline__ void add_specials(const AdapterArgs &a, int64_t row0, int rows, int64_t n0, const int *s_ids) {
+    T *out = reinterpret_cast<T *>(a.out) + row0 * a.M;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (BN / 4); i += THREADS) {
+        const int r = i / (BN / 4);
+        const int64_t n = n0 + i % (BN / 4) * 4;
+        const f32x4 v = adapter_quad<T, B_COL>(a, row0 + r, s_ids[r], n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < a.M && !(v[j] * 0.f == 0.f)) out[r * a.M + n + j] = (T)((float)out[r * a.M + n + j] + v[j]);
+    }
+}
+
 // Many rows: AH * 128 rows x 256 columns per workgroup, in phases (16-bit
 // types, whole units).
 template <typename T, int AH, bool B_COL>
@@ -562,8 +744,8 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     using BRow = RowStage<T, kHalf, kPhaseThreads, true>;
     using BCol = ColStage<T, kHalf, kPhaseThreads, true>;
     constexpr int BM = AH * kHalf;
-    // one array: beside a second the compiler's reads of LDS wait for all loads
-    // into it, also for those of later steps
+    // one array: beside a second (__syncthreads_or has one) the compiler's reads
+    // of LDS wait for all loads into it, also for those of later steps
     __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds + (2 * BM + 1) * sizeof(int)];
     int *s_ids = reinterpret_cast<int *>(lds_mem + kPhaseLds), *s_list = s_ids + BM, *s_count = s_list + BM;
     lds_char *lds = (lds_char *)lds_mem;
@@ -623,8 +805,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
                 sbr[h].issue(place, wave, k0);
             }
         },
-        [](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); },
-        [](int) {});
+        [](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); });
     __syncthreads();
 
     // the adapters met in the tile, 32 ranks a step
@@ -669,7 +850,20 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
             }
         }
     };
-    auto products = [&](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) {
+    // Where rows differ in their adapter, without the adapters' infinities and
+    // NaN, which would reach the rows of others (added below; parts of their own
+    // as in adapter_products do not fit the registers).
+    bool mixed = met > 1, dropped = false;
+    for (int r = lane; r < rows; r += 64) mixed = mixed || s_ids[r] < 0;
+    mixed = ballot(mixed) != 0;
+    auto products = [&](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], u32x4 (&y)[2][2]) {
+        constexpr int kHalves = __is_same(T, _Float16) ? 1 : 2;
+        if (mixed) {
+#pragma unroll
+            for (int ks = 0; ks < kHalves; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) drop_specials<T>(y[ks][j], dropped);
+        }
         if constexpr (__is_same(T, _Float16)) {
             // bf16 halves of u against the two bf16 that a float16 is the sum
             // of; y[1] holds the same ranks again, so wait for it here
@@ -697,7 +891,8 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
         }
     };
     if (extra > 0)
-        phase_steps<T, AH, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products, [](int) {});
+        phase_steps<T, AH, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products);
+    if (dropped) *s_count = -1;
 
     __syncthreads();
     constexpr int BN = 2 * kHalf;
@@ -713,6 +908,10 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
                                     acc[p][q][i][j]);
     __syncthreads();
     tile_out<T, BM, BN, kPhaseThreads>(lds, reinterpret_cast<T *>(a.out) + row0 * a.M, rows, n0, a.M, a.vec != 0);
+    if (*s_count < 0) {
+        __syncthreads();
+        add_specials<T, B_COL, BN, kPhaseThreads>(a, row0, rows, n0, s_ids);
+    }
 }
 
 template <typename T, int AH>
@@ -742,6 +941,20 @@ int adapter_main_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+int adapter_split_launch(AdapterArgs a, bool b_col, hipStream_t st) {
+    constexpr int BN = 128;
+    a.mtiles = (a.N + 63) / 64;
+    a.ntiles = (a.M + BN - 1) / BN;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    const bool whole = a.K % 8 == 0 && (!b_col || a.M % 8 == 0);
+    if (b_col && whole) timed_launch_ggl(true, (adapter_main_split<BN, true, true>), grid, dim3(kSplitThreads), 0, st, a);
+    else if (b_col) timed_launch_ggl(true, (adapter_main_split<BN, true, false>), grid, dim3(kSplitThreads), 0, st, a);
+    else if (whole) timed_launch_ggl(true, (adapter_main_split<BN, false, true>), grid, dim3(kSplitThreads), 0, st, a);
+    else timed_launch_ggl(true, (adapter_main_split<BN, false, false>), grid, dim3(kSplitThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
 template <typename T, int MT, bool DIRECT>
 int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     constexpr int NW = DIRECT ? 4 : 8, STAGES = DIRECT ? 3 : 2;
@@ -754,6 +967,7 @@ int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+constexpr int64_t kAdapterSplit = 320;  // tiles of 64 x 128
 constexpr int64_t kAdapterTall = 128;  // tiles of 64 rows
 constexpr int64_t kAdapterFew = 128;  // rows up to which waves split the contraction
 template <typename T>
@@ -775,6 +989,12 @@ int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool mai
         if (a.N <= 48) return adapter_few_launch<T, 3, 4, 4>(a, b_col, st);
         return adapter_few_launch<T, 4, 4, 3>(a, b_col, st);
     }
+    // float in bf16 parts from 320 tiles of 64 x 128 on: beside 2,048 x 2,048, 105
+    // us against 97 for 1,024 rows (256 tiles), 131 against 177 for 2,048, 424
+    // against 625 for 8,192; beside 515 x 1,030, 51 against 48 for 1,024 (144) and
+    // 83 against 100 for 4,096 (576)
+    if constexpr (sizeof(T) == 4)
+        if ((a.N + 63) / 64 * ((a.M + 127) / 128) >= kAdapterSplit) return adapter_split_launch(a, b_col, st);
     if (!main_direct) return adapter_main_launch<T, 64, 64, 2, 2, 2, false>(a, b_col, st);
     if constexpr (sizeof(T) == 2) {
         // tiles of 128 x 256 in phases where there is one for every second CU

@@ -321,12 +321,12 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_matmul_many(MatmulArgs a) {
             sbr[h].issue(place, wave, k0);
         }
     };
-    auto products = [](int, f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+    auto products = [](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
     const int steps = (K + kStep<T> - 1) / kStep<T>;
     if (AH == 2 && rows > kHalf)
-        phase_steps<T, AH, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products, [](int) {});
+        phase_steps<T, AH, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products);
     else
-        phase_steps<T, 1, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products, [](int) {});
+        phase_steps<T, 1, B_COL>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products);
 
     __syncthreads();
     constexpr int BN = 2 * kHalf;

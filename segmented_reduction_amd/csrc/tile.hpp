@@ -420,11 +420,11 @@ struct SplitStage {
     static __device__ __forceinline__ int row(int i, int tid) { return (i * THREADS + tid) / (COL ? W / 8 : 4); }
     static __device__ __forceinline__ int at(int i, int tid) { return (i * THREADS + tid) % (COL ? W / 8 : 4) * 8; }
     // src(i): address of part i; left(i): floats of its row from there on.
-    template <typename F, typename G>
+    template <bool EIGHT = WHOLE, typename F, typename G>
     __device__ __forceinline__ void issue(F src, G left) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            if constexpr (WHOLE) {
+            if constexpr (EIGHT) {
                 const uint64_t q = left(i) > 0 ? src(i) : (uint64_t)zero_unit();
                 v[i][0] = load_whole<float>(q);
                 v[i][1] = load_whole<float>(q + 16);
@@ -537,11 +537,11 @@ __device__ __forceinline__ void quadrant(f32x4 (&c)[4][2], const u32x4 (&a)[2][4
 }
 
 // fetch_a(h, t, place) and fetch_b(h, t, place) start half h of step t (two
-// loads per thread; zeros past the last step); products(t, c, a, b) are a
-// phase's; tick(t) is called once a step.  acc[a][b] are the quadrants.
-template <typename T, int AH, bool B_COL, typename FA, typename FB, typename P, typename K>
+// loads per thread; zeros past the last step); products(c, a, b) are a
+// phase's.  acc[a][b] are the quadrants.
+template <typename T, int AH, bool B_COL, typename FA, typename FB, typename P>
 __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *lds, int steps, int wave, int lane,
-                                            FA fetch_a, FB fetch_b, P products, K tick) {
+                                            FA fetch_a, FB fetch_b, P products) {
     static_assert(sizeof(T) == 2, "16-bit types");
     const int ma = (wave >> 2) * 64, nb = (wave & 3) * 32;
     u32x4 a[2][4], b0[2][2], b1[2][2];
@@ -550,10 +550,10 @@ __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *
         if constexpr (B_COL) col_frags<T, kHalf>(b, p, nb, lane);
         else row_frags(b, p, nb, lane);
     };
-    auto multiply = [&](int t, f32x4 (&c)[4][2], const u32x4 (&b)[2][2]) {
+    auto multiply = [&](f32x4 (&c)[4][2], u32x4 (&b)[2][2]) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
-        products(t, c, a, b);
+        products(c, a, b);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_barrier" ::: "memory");
@@ -579,26 +579,25 @@ __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *
         wait_and_meet<10>();
         if (wave >= 4) asm volatile("s_barrier" ::: "memory");
         for (int t = 0; t < steps; ++t) {
-            tick(t);
             read_a(place_a(0, t));
             fetch_a(1, t + 1, place_a(1, t + 1));
             SEGRED_MEET(10)
-            multiply(t, acc[0][0], b0);
+            multiply(acc[0][0], b0);
 
             read_b(b1, place_b(1, t));
             fetch_b(0, t + 2, place_b(0, t));
             SEGRED_MEET(10)
-            multiply(t, acc[0][1], b1);
+            multiply(acc[0][1], b1);
 
             read_a(place_a(1, t));
             fetch_a(0, t + 2, place_a(0, t));
             SEGRED_MEET(10)
-            multiply(t, acc[1][1], b1);
+            multiply(acc[1][1], b1);
 
             read_b(b0_next, place_b(0, t + 1));
             fetch_b(1, t + 2, place_b(1, t));
             SEGRED_MEET(10)
-            multiply(t, acc[1][0], b0);
+            multiply(acc[1][0], b0);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -619,18 +618,17 @@ __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *
         if (wave >= 4) asm volatile("s_barrier" ::: "memory");
         lds_char *now = lds, *next = lds + kStepBytes, *after = lds + 2 * kStepBytes;
         for (int t = 0; t < steps; ++t) {
-            tick(t);
             read_a(now);
             fetch_a(0, t + 2, after);
             SEGRED_MEET(8)
-            multiply(t, acc[0][0], b0);
+            multiply(acc[0][0], b0);
 
             read_b(b0, next + kHalfBytes);  // before b1, whose arrival then implies b0's
             read_b(b1, now + 2 * kHalfBytes);
             fetch_b(1, t + 2, after + 2 * kHalfBytes);
             fetch_b(0, t + 3, now + kHalfBytes);
             SEGRED_MEET(10)
-            multiply(t, acc[0][1], b1);
+            multiply(acc[0][1], b1);
             lds_char *const first = now;
             now = next;
             next = after;

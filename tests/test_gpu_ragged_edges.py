@@ -179,3 +179,57 @@ def test_no_source_rows_at_all(kind, k, m):
     down, up = torch.empty(0, 4, k, dtype=t, device="cuda"), torch.empty(0, m, 4, dtype=t, device="cuda")
     which = torch.tensor([0, 7], device="cuda")
     assert torch.equal(s.adapter(x, w, off, which, down, up), torch.full((3, m), float(k), dtype=t, device="cuda"))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("k,m,r", [(640, 648, 8), (641, 643, 33), (712, 640, 64)])
+def test_large_float_adapters(k, m, r, transpose):
+    """Enough tiles for float products in bf16 parts, whole units and odd widths."""
+    _check("f32", [700, 1, 1300, 0, 63, 1500, 65, 1400, 128], k, m, r, transpose, count=4, seed=5)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_infinity_and_nan_in_large_float_adapters(transpose):
+    """They come out where 64 bits put them, and nowhere else; the other rows keep their accuracy."""
+    g = ru.gen(6)
+    k, m, r, n = 640, 648, 8, 5000
+    off, which = torch.tensor([0, 2000, 2100, n]), torch.tensor([1, -1, 0])
+    have = m if transpose else k
+    x, w = ru.randn(g, n, have), ru.randn(g, m, k, std=have ** -0.5)
+    down, up = ru.randn(g, 2, r, k, std=k ** -0.5), ru.randn(g, 2, m, r, std=r ** -0.5)
+    x[3, 5], x[2050, 0], x[4999, 17], x[1000, 3] = float("nan"), float("inf"), -float("inf"), 3e38
+    x[1000, 4] = -3e38
+    ru.say(f"large float adapter with specials transpose={transpose}")
+    got = sr().adapter(*(v.cuda() for v in (x, w, off, which, down, up)), transpose=transpose).cpu()
+    ref, mag, _, _, _ = ru.adapter(x, w, off, which, down, up, None, transpose)
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got[2050].double(), ref[2050]) and bool((got[2050].abs() == float("inf")).all())
+    plain = torch.ones(n, dtype=torch.bool)
+    plain[[3, 2050, 4999, 1000]] = False
+    ru.assert_close(got[plain], ref[plain], mag[plain], 2 * have + r, "other rows")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("rows,k,m,r", [(90, 64, 96, 8), (700, 64, 96, 40), (700, 61, 99, 5), (5000, 648, 640, 8), (6100, 136, 2048, 33)])
+def test_specials_of_an_adapter_stay_with_its_rows(kind, transpose, rows, k, m, r):
+    """Infinities and NaN in the second factor of two adapters; requests of others share their tiles."""
+    t, g = ru.TYPES[kind], ru.gen(rows + r)
+    cuts = torch.randint(0, rows + 1, (23,), generator=g).sort().values.tolist()
+    off, which = torch.tensor([0, *cuts, rows]), torch.arange(24) % 5 - 1
+    have = m if transpose else k
+    x, w = ru.randn(g, rows, have, dtype=t), ru.randn(g, m, k, dtype=t, std=have ** -0.5)
+    down, up = ru.randn(g, 4, r, k, dtype=t, std=k ** -0.5), ru.randn(g, 4, m, r, dtype=t, std=r ** -0.5)
+    second = down.transpose(1, 2) if transpose else up  # [4, outputs, r]
+    second[1, 7, r - 1], second[1, 50, 0], second[3, 40, 2] = float("nan"), float("inf"), -float("inf")
+    ru.say(f"specials of an adapter {kind} N={rows} k={k} m={m} r={r} transpose={transpose}")
+    got = sr().adapter(*(v.cuda() for v in (x, w, off, which, down.contiguous(), up)), transpose=transpose).cpu()
+    ref, mag, part, _, _ = ru.adapter(x, w, off, which, down, up, None, transpose)
+    assert torch.equal(got.isfinite(), ref.isfinite())
+    if kind == "f32":
+        assert torch.equal(got.isnan(), ref.isnan())
+    ok = ref.isfinite()
+    zero = torch.zeros((), dtype=torch.float64)
+    mag, part = torch.where(ok, mag, zero), torch.where(ok, part, zero)
+    ru.assert_close(torch.where(ok, got, torch.zeros((), dtype=t)), torch.where(ok, ref, zero), mag, 2 * have + r, "the others",
+                    more=0.0 if kind == "f32" else 2.0 ** -16 * part)
