@@ -703,36 +703,40 @@ int adapter_few_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
-// Puts zeros in the place of infinities and NaN of eight elements.
-template <typename T>
-__device__ __forceinline__ void drop_specials(u32x4 &v, bool &dropped) {
-    constexpr uint32_t kExp = __is_same(T, _Float16) ? 0x7c007c00u : 0x7f807f80u, kOne = __is_same(T, _Float16) ? 0x04000400u : 0x00800080u;
-    uint32_t flag[4], any = 0;
+// NaN where a value of c is infinite or NaN, else z.
+__device__ __forceinline__ float not_finite(f32x4 c, float z) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        flag[q] = ((v[q] & kExp) + kOne) & 0x80008000u;  // an exponent of all ones
-        any |= flag[q];
-    }
-    if (ballot(any != 0) != 0) {
-        dropped = true;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] &= ~((flag[q] >> 15) * 0xffffu);
-    }
+    for (int j = 0; j < 4; ++j) z = fmaf(c[j], 0.f, z);
+    return z;
 }
 
-// What they make of their own rows: the elements of a stored tile whose
-// adapter's part is infinite or NaN.
+// The infinities and NaN of a stored tile again, element by element, so that
+// only what the row's own adapter makes of it remains.
 template <typename T, bool B_COL, int BN, int THREADS>
-__device__ __forceinline__ void add_specials(const AdapterArgs &a, int64_t row0, int rows, int64_t n0, const int *s_ids) {
-    T *out = reinterpret_cast<T *>(a.out) + row0 * a.M;
+__device__ __forceinline__ void own_specials(const AdapterArgs &a, int64_t row0, int rows, int64_t n0, const int *s_ids) {
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * (BN / 4); i += THREADS) {
         const int r = i / (BN / 4);
-        const int64_t n = n0 + i % (BN / 4) * 4;
-        const f32x4 v = adapter_quad<T, B_COL>(a, row0 + r, s_ids[r], n);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n + j < a.M && !(v[j] * 0.f == 0.f)) out[r * a.M + n + j] = (T)((float)out[r * a.M + n + j] + v[j]);
+        const int64_t row = row0 + r, n = n0 + i % (BN / 4) * 4;
+        T *out = reinterpret_cast<T *>(a.out) + row * a.M + n;
+        bool any = false;
+        for (int j = 0; j < 4 && n + j < a.M; ++j) any = any || !((float)out[j] * 0.f == 0.f);
+        if (!any) continue;
+        const f32x4 q = adapter_quad<T, B_COL>(a, row, s_ids[r], n);
+#pragma unroll 1
+        for (int j = 0; j < 4 && n + j < a.M; ++j) {
+            if ((float)out[j] * 0.f == 0.f) continue;
+            float sum = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
+            if (sum == sum) {
+                const T *x = reinterpret_cast<const T *>(a.values) + row * a.K;
+                const T *w = reinterpret_cast<const T *>(a.weights) + (B_COL ? n + j : (n + j) * a.K);
+                float main = 0.f;
+#pragma unroll 1
+                for (int64_t k = 0; k < a.K; ++k) main = fmaf((float)x[k], (float)w[B_COL ? k * a.M : k], main);
+                sum += main;
+            }
+            out[j] = (T)sum;
+        }
     }
 }
 
@@ -850,20 +854,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
             }
         }
     };
-    // Where rows differ in their adapter, without the adapters' infinities and
-    // NaN, which would reach the rows of others (added below; parts of their own
-    // as in adapter_products do not fit the registers).
-    bool mixed = met > 1, dropped = false;
-    for (int r = lane; r < rows; r += 64) mixed = mixed || s_ids[r] < 0;
-    mixed = ballot(mixed) != 0;
-    auto products = [&](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], u32x4 (&y)[2][2]) {
-        constexpr int kHalves = __is_same(T, _Float16) ? 1 : 2;
-        if (mixed) {
-#pragma unroll
-            for (int ks = 0; ks < kHalves; ++ks)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) drop_specials<T>(y[ks][j], dropped);
-        }
+    auto products = [&](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) {
         if constexpr (__is_same(T, _Float16)) {
             // bf16 halves of u against the two bf16 that a float16 is the sum
             // of; y[1] holds the same ranks again, so wait for it here
@@ -890,9 +881,25 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
             quadrant<T>(c, x, y);
         }
     };
-    if (extra > 0)
+    if (extra > 0) {
         phase_steps<T, AH, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products);
-    if (dropped) *s_count = -1;
+        // Where rows differ in their adapter, an infinity or a NaN of one has
+        // reached the rows of others.  (Parts of their own as in
+        // adapter_products do not fit the registers; looking for these values
+        // in every step took 5% of a call.)
+        bool mixed = met > 1;
+        for (int r = lane; r < rows; r += 64) mixed = mixed || s_ids[r] < 0;
+        float bad = 0.f;
+#pragma unroll
+        for (int p = 0; p < AH; ++p)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) bad = not_finite(acc[p][q][i][j], bad);
+        if (ballot(mixed) != 0 && bad != 0.f) *s_count = -1;
+    }
 
     __syncthreads();
     constexpr int BN = 2 * kHalf;
@@ -910,7 +917,7 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     tile_out<T, BM, BN, kPhaseThreads>(lds, reinterpret_cast<T *>(a.out) + row0 * a.M, rows, n0, a.M, a.vec != 0);
     if (*s_count < 0) {
         __syncthreads();
-        add_specials<T, B_COL, BN, kPhaseThreads>(a, row0, rows, n0, s_ids);
+        own_specials<T, B_COL, BN, kPhaseThreads>(a, row0, rows, n0, s_ids);
     }
 }
 

@@ -550,7 +550,7 @@ __device__ __forceinline__ void phase_steps(f32x4 (&acc)[2][2][4][2], lds_char *
         if constexpr (B_COL) col_frags<T, kHalf>(b, p, nb, lane);
         else row_frags(b, p, nb, lane);
     };
-    auto multiply = [&](f32x4 (&c)[4][2], u32x4 (&b)[2][2]) {
+    auto multiply = [&](f32x4 (&c)[4][2], const u32x4 (&b)[2][2]) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
         products(c, a, b);
