@@ -171,10 +171,12 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
 }
 
 // The same for float, in bf16 parts; a tile that met an infinity or a NaN is
-// computed again with float products.
+// computed again with float products.  (Three workgroups a CU: 8,192 rows in 8
+// segments, 1,024 x 1,024, take 122 us against 137 with the two that the
+// registers of transposed weights would allow otherwise.)
 constexpr int kSplitThreads = 256;
 template <int BM, int BN, bool B_COL, bool WHOLE>
-__global__ __launch_bounds__(kSplitThreads) void seg_matmul_split(MatmulArgs a) {
+__global__ __launch_bounds__(kSplitThreads, 3) void seg_matmul_split(MatmulArgs a) {
     using Plain = MatmulTile<float, 64, 64, 2, 2, 2, B_COL, false>;
     using SA = SplitStage<BM, kSplitThreads, false, WHOLE>;
     using SB = SplitStage<BN, kSplitThreads, B_COL, WHOLE>;
