@@ -473,6 +473,19 @@ int segred_outer(const void *left, const int64_t *left_rows, int64_t left_count,
 int64_t segred_outer_workspace(int64_t k, int64_t m, int64_t num_segments, int64_t num_rows);
 
 /*
+ * segred_outer_mixed -- segred_outer with a type for either side: the same, or
+ * SEGRED_F32 beside SEGRED_BF16 or SEGRED_F16 (a 16-bit gradient with the
+ * float32 low-rank rows of an adapter).  The 16-bit side enters exactly, the
+ * float32 one as in larger float32 calls of segred_matmul.  `out_dtype` is one of
+ * the two or SEGRED_F32; SEGRED_ERR_UNSUPPORTED for SEGRED_BF16 beside
+ * SEGRED_F16.  The workspace and the other errors are segred_outer's.
+ */
+int segred_outer_mixed(const void *left, int32_t left_dtype, const int64_t *left_rows, int64_t left_count, int64_t k,
+                       const void *right, int32_t right_dtype, const int64_t *right_rows, int64_t right_count,
+                       int64_t m, const int64_t *offsets, int64_t num_segments, int64_t num_rows, void *out,
+                       int32_t out_dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * segred_group -- entries grouped by an index: the stable order that puts the
  * entries of group 0 first, then those of group 1, and so on.
  *
@@ -556,7 +569,9 @@ int segred_combine_grad(const void *grad, const void *values, int32_t dtype, int
  *              an adapter.  The gradients of the factors are sums of outer
  *              products over the rows of an adapter: of up[a] from the output
  *              gradient and the forward call's `low`, of down[a] from the
- *              transposed call's `low` and x (segred_outer).
+ *              transposed call's `low` and x (segred_outer).  In the 16-bit
+ *              types these rows are rounded here and the gradients once more:
+ *              segred_adapter_mixed leaves them in float32.
  *   workspace  segred_adapter_workspace(dtype, m, adapters, rank, num_rows)
  *              bytes.
  *
@@ -577,6 +592,18 @@ int segred_adapter(const void *values, int32_t dtype, int64_t k, const void *wei
                    int32_t transpose, void *out, void *low, void *workspace, int64_t workspace_bytes,
                    hipStream_t stream);
 int64_t segred_adapter_workspace(int32_t dtype, int64_t m, int64_t adapters, int64_t rank, int64_t num_rows);
+
+/*
+ * segred_adapter_mixed -- segred_adapter with a type of its own for `low`:
+ * `dtype`, or SEGRED_F32 for low-rank rows that are not rounded before
+ * segred_outer_mixed sums them up to the factors' gradients.
+ * SEGRED_ERR_INVALID_ARGUMENT for another.
+ */
+int segred_adapter_mixed(const void *values, int32_t dtype, int64_t k, const void *weights, int64_t m,
+                         const int64_t *offsets, const int64_t *which, int64_t num_segments, int64_t num_rows,
+                         const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
+                         int32_t transpose, void *out, void *low, int32_t low_dtype, void *workspace,
+                         int64_t workspace_bytes, hipStream_t stream);
 
 /* Static, host-side description of a status code (never NULL). */
 const char *segred_status_string(int status);

@@ -91,6 +91,9 @@ def library(path: str | None = None):
             lib.segred_matmul.restype = ctypes.c_int
             lib.segred_outer.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i32, vp, i64, i64, vp, i32, vp, i64, vp]
             lib.segred_outer.restype = ctypes.c_int
+            lib.segred_outer_mixed.argtypes = [vp, i32, vp, i64, i64, vp, i32, vp, i64, i64, vp, i64, i64, vp, i32, vp,
+                                               i64, vp]
+            lib.segred_outer_mixed.restype = ctypes.c_int
             lib.segred_outer_workspace.argtypes = [i64, i64, i64, i64]
             lib.segred_outer_workspace.restype = i64
             lib.segred_group.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
@@ -104,6 +107,9 @@ def library(path: str | None = None):
             lib.segred_adapter.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, i32, vp, vp,
                                            vp, i64, vp]
             lib.segred_adapter.restype = ctypes.c_int
+            lib.segred_adapter_mixed.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, i32, vp,
+                                                 vp, i32, vp, i64, vp]
+            lib.segred_adapter_mixed.restype = ctypes.c_int
             lib.segred_adapter_workspace.argtypes = [i32, i64, i64, i64, i64]
             lib.segred_adapter_workspace.restype = i64
             lib.segred_status_string.argtypes = [ctypes.c_int]
@@ -503,15 +509,21 @@ def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, lef
     ``out[s] = sum over r of left[r].T @ right[r]``, [S, K, M].
 
     left, right  [*, K] and [*, M] float32 / bfloat16 / float16 on a GPU,
-                 contiguous and of one type.
+                 contiguous and of one type; or, where ``out_dtype`` (or
+                 ``out``) says what the sums are, one of a 16-bit type, which
+                 enters exactly, and one float32 (an adapter's low-rank rows).
     offsets      int64 [S + 1] on the same GPU; an empty segment gives zeros.
     left_rows, right_rows  optional int64 [R]: gather that side's rows.
-    out_dtype    the inputs' type (default) or float32.
+    out_dtype    the inputs' type (default; either of two) or float32.
     """
     dev, code = _floats("left", left)
+    odt = out_dtype or (left.dtype if out is None else out.dtype)
     if right.dtype != left.dtype:
-        raise TypeError("right must have the dtype of left")
-    _floats("right", right)
+        if torch.float32 not in (left.dtype, right.dtype):
+            raise TypeError("right must have the dtype of left, or one of the two float32")
+        if out_dtype is None and out is None:
+            raise TypeError("right must have the dtype of left where neither out_dtype nor out is given")
+    right_code = _floats("right", right)[1]
     _beside(dev, "right", right)
     _rows(dev, "offsets", offsets)
     for name, index in (("left_rows", left_rows), ("right_rows", right_rows)):
@@ -522,9 +534,8 @@ def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, lef
     if (right if right_rows is None else right_rows).shape[0] != n or s < 0:
         raise ValueError("left and right need the same number of rows, and offsets S + 1 entries")
     k, m = left.shape[1], right.shape[1]
-    odt = out_dtype or (left.dtype if out is None else out.dtype)
-    if odt not in (left.dtype, torch.float32):
-        raise TypeError("out_dtype must be the dtype of left or float32")
+    if odt not in (left.dtype, right.dtype, torch.float32):
+        raise TypeError("out_dtype must be the dtype of left or right or float32")
     if out is None:
         out = torch.empty((s, k, m), dtype=odt, device=left.device)
     else:
@@ -534,9 +545,9 @@ def outer(left: torch.Tensor, right: torch.Tensor, offsets: torch.Tensor, *, lef
     lib = _lib or library()
     need = lib.segred_outer_workspace(k, m, s, n)
     work = torch.empty(need, dtype=torch.uint8, device=left.device) if need else None
-    _launch(lib.segred_outer, "segred_outer", dev, left.data_ptr(),
-            left_rows.data_ptr() if left_rows is not None else None, left.shape[0], k, right.data_ptr(),
-            right_rows.data_ptr() if right_rows is not None else None, right.shape[0], m, code, offsets.data_ptr(), s, n,
+    _launch(lib.segred_outer_mixed, "segred_outer", dev, left.data_ptr(), code,
+            left_rows.data_ptr() if left_rows is not None else None, left.shape[0], k, right.data_ptr(), right_code,
+            right_rows.data_ptr() if right_rows is not None else None, right.shape[0], m, offsets.data_ptr(), s, n,
             out.data_ptr(), FLOATS[odt], work.data_ptr() if need else None, need)
     return out
 
@@ -630,7 +641,7 @@ def combine_grad(grad: torch.Tensor, values: torch.Tensor, position: torch.Tenso
 
 def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, which: torch.Tensor,
             down: torch.Tensor, up: torch.Tensor, *, scale: torch.Tensor | None = None, transpose: bool = False,
-            want_low: bool = False, out: torch.Tensor | None = None):
+            want_low: bool | torch.dtype = False, out: torch.Tensor | None = None):
     """A projection that all rows share with a low-rank adapter per segment
     beside it (segred_adapter): for the rows of segment s and a = which[s],
     ``x @ weights.T + scale[a] * (x @ down[a].T) @ up[a].T``, or with
@@ -642,9 +653,12 @@ def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, 
     weights   [M, K]; down [L, r, K]; up [L, M, r], of the same type.
     offsets   int64 [S + 1]; which int64 [S], outside [0, L): no adapter.
     scale     optional float32 [L].
-    want_low  also return the low-rank rows [N, r]: ``outer`` of the output's
+    want_low  also return the low-rank rows [N, r], of this type (float32 or
+              the values'; ``True``: the values'): ``outer`` of the output's
               gradient and these gives the gradient of up, ``outer`` of the
               transposed call's and x that of down (rows grouped by adapter).
+              Rows of a 16-bit type are rounded, and the gradients once more;
+              ask for ``torch.float32`` to round the gradients alone.
     Rows of no segment are left as they were in ``out`` (uninitialised when it
     is not given; likewise the low-rank rows).
     """
@@ -678,14 +692,17 @@ def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, 
         _beside(dev, "out", out)
         if out.shape != (n, give) or out.dtype != values.dtype:
             raise ValueError("out must be [N, outputs] of the dtype of values")
-    low = torch.empty((n, r), dtype=values.dtype, device=device) if want_low else None
+    low_dtype = values.dtype if want_low is True or not want_low else want_low
+    if low_dtype not in (values.dtype, torch.float32):
+        raise TypeError("want_low must be float32 or the dtype of values")
+    low = torch.empty((n, r), dtype=low_dtype, device=device) if want_low else None
     lib = _lib or library()
     need = lib.segred_adapter_workspace(code, m, count, r, n)
     work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _launch(lib.segred_adapter, "segred_adapter", dev, values.data_ptr(), code, k, weights.data_ptr(), m,
+    _launch(lib.segred_adapter_mixed, "segred_adapter", dev, values.data_ptr(), code, k, weights.data_ptr(), m,
             offsets.data_ptr(), which.data_ptr(), s, n, down.data_ptr(), up.data_ptr(),
             scale.data_ptr() if scale is not None else None, count, r, 1 if transpose else 0, out.data_ptr(),
-            low.data_ptr() if want_low else None, work.data_ptr() if need else None, need)
+            low.data_ptr() if want_low else None, FLOATS[low_dtype], work.data_ptr() if need else None, need)
     return (out, low) if want_low else out
 
 

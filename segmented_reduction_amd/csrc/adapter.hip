@@ -35,6 +35,7 @@ struct AdapterArgs {
     char *u;              // [N, blocks * 128 bytes]
     int32_t *ids;         // [N] adapter of each row, -1: none
     char *low;            // [N, R] or null
+    int low_f32;          // of float, else of the inputs' type
     char *out;
     int vec;
 };
@@ -97,9 +98,12 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
     const int K = (int)a.K, R = (int)a.R;
     if (!has) {
         if (a.low)
-            for (int i = threadIdx.x; i < rows * kRankBlock; i += 64 * NW)
-                if (r0 + i % kRankBlock < R)
-                    reinterpret_cast<T *>(a.low)[(row0 + i / kRankBlock) * R + r0 + i % kRankBlock] = (T)0.f;
+            for (int i = threadIdx.x; i < rows * kRankBlock; i += 64 * NW) {
+                const int64_t at = (row0 + i / kRankBlock) * R + r0 + i % kRankBlock;
+                if (r0 + i % kRankBlock >= R) continue;
+                if (a.low_f32) reinterpret_cast<float *>(a.low)[at] = 0.f;
+                else reinterpret_cast<T *>(a.low)[at] = (T)0.f;
+            }
         return;
     }
 
@@ -170,7 +174,10 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
             *reinterpret_cast<bf16x4 *>(u + c * 2) = hi;
             *reinterpret_cast<bf16x4 *>(u + 64 + c * 2) = lo;
         }
-        if (a.low) store_quad<T>(reinterpret_cast<T *>(a.low) + (row0 + r) * R, r0 + c, R, sum, false);
+        if (a.low && a.low_f32)
+            store_quad<float>(reinterpret_cast<float *>(a.low) + (row0 + r) * R, r0 + c, R, sum, false);
+        else if (a.low)
+            store_quad<T>(reinterpret_cast<T *>(a.low) + (row0 + r) * R, r0 + c, R, sum, false);
     });
 }
 
@@ -1052,8 +1059,18 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
                               const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
                               int32_t transpose, void *out, void *low, void *workspace, int64_t workspace_bytes,
                               hipStream_t stream) {
+    return segred_adapter_mixed(values, dtype, k, weights, m, offsets, which, num_segments, num_rows, down, up, scale,
+                                adapters, rank, transpose, out, low, dtype, workspace, workspace_bytes, stream);
+}
+
+extern "C" int segred_adapter_mixed(const void *values, int32_t dtype, int64_t k, const void *weights, int64_t m,
+                                    const int64_t *offsets, const int64_t *which, int64_t num_segments,
+                                    int64_t num_rows, const void *down, const void *up, const float *scale,
+                                    int64_t adapters, int64_t rank, int32_t transpose, void *out, void *low,
+                                    int32_t low_dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
     const int64_t e = float_size(dtype);
     if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (low_dtype != dtype && low_dtype != SEGRED_F32) return SEGRED_ERR_INVALID_ARGUMENT;
     if (k < 1 || m < 1 || rank < 1 || adapters < 0 || num_segments < 0 || num_rows < 0) return SEGRED_ERR_INVALID_ARGUMENT;
     const bool some = num_segments > 0 && num_rows > 0;
     if (some && (!values || !weights || !offsets || !which || !out || (adapters > 0 && (!down || !up))))
@@ -1061,7 +1078,7 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
     if (e == 0 || k > kMaxWidth || m > kMaxWidth || rank > kMaxWidth || adapters > INT32_MAX || num_rows > (int64_t(1) << 40))
         return SEGRED_ERR_UNSUPPORTED;
     if (!aligned(values, e) || !aligned(weights, e) || !aligned(out, e) || !aligned(down, e) || !aligned(up, e) ||
-        !aligned(low, e) || !aligned(scale, 4) || !aligned(offsets, 8) || !aligned(which, 8) || !aligned(workspace, 16))
+        !aligned(low, float_size(low_dtype)) || !aligned(scale, 4) || !aligned(offsets, 8) || !aligned(which, 8) || !aligned(workspace, 16))
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (too_large(num_rows, k, 4) || too_large(num_rows, m, 4) || too_large(num_rows, rank, 4) ||
         too_large(num_rows, rank + 64, 4) || too_large(adapters, k * rank, 4) || too_large(adapters, m * (rank + 8), 4))
@@ -1097,6 +1114,7 @@ extern "C" int segred_adapter(const void *values, int32_t dtype, int64_t k, cons
         a.R2 = space.ranks;
     }
     a.low = static_cast<char *>(low);
+    a.low_f32 = low_dtype == SEGRED_F32;
     a.out = static_cast<char *>(out);
     a.vec = ((a.M * e) % 16 == 0 && aligned(out, 16)) ? 1 : 0;
     auto units = [&](const void *p, int64_t width) { return (width * e) % 16 == 0 && aligned(p, 16); };

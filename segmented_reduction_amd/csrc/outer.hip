@@ -2,6 +2,7 @@
 // out[s] = sum over the rows r of segment s of left[r]^T right[r], the
 // gradient of the weights of a product over segments.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "tile.hpp"
@@ -174,17 +175,20 @@ __device__ __forceinline__ void outer_blocks(const OuterArgs &a, const OuterPlac
     }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+// L and Q: the operands' types in memory, where they are not T.
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT, typename L = T, typename Q = T>
 struct OuterTile {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-    using SA = ColStage<T, BM, kThreads, DIRECT>;
-    using SB = ColStage<T, BN, kThreads, DIRECT>;
+    using SA = ColStage<T, BM, kThreads, DIRECT, L>;
+    using SB = ColStage<T, BN, kThreads, DIRECT, Q>;
     static constexpr int kStageBytes = SA::kBytes + SB::kBytes;
     static constexpr int kLds = 2 * kStageBytes;
 
+    // O: the type of a result that is not float.
+    template <typename O = T>
     static __device__ __forceinline__ void run(const OuterArgs &a, const OuterPlace &at, lds_char *lds, int wave, int lane) {
-        const int64_t m0 = at.m0, n0 = at.n0, lb = a.K * (int64_t)sizeof(T), rb = a.M * (int64_t)sizeof(T);
+        const int64_t m0 = at.m0, n0 = at.n0, lb = a.K * (int64_t)sizeof(L), rb = a.M * (int64_t)sizeof(Q);
         SA sa;
         SB sb;
         OuterSide<SA::kLoads> left;
@@ -194,9 +198,9 @@ struct OuterTile {
         auto lcol = [&](int i) { return (int)(a.K - m0) - SA::col(i, wave, lane); };
         auto rcol = [&](int i) { return (int)(a.M - n0) - SB::col(i, wave, lane); };
         left.init(at, a.left_rows, a.left_count, a.left, lb, kStep<T>, lrow,
-                  [&](int i) { return (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(T); });
+                  [&](int i) { return (m0 + SA::col(i, wave, lane)) * (int64_t)sizeof(L); });
         right.init(at, a.right_rows, a.right_count, a.right, rb, kStep<T>, rrow,
-                   [&](int i) { return (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(T); });
+                   [&](int i) { return (n0 + SB::col(i, wave, lane)) * (int64_t)sizeof(Q); });
         auto rows_of = [&](int64_t t) { return (int)max(min(at.rows - t * kStep<T>, (int64_t)kStep<T>), (int64_t)0); };
         auto ask = [&](int64_t t) {
             left.ask(t * kStep<T>, rows_of(t), lrow);
@@ -237,7 +241,7 @@ struct OuterTile {
             step_products<T, MT, NT, true, BM, true, BN>(acc, buf, buf + SA::kBytes, m_w, n_w, lane);
             if (t + 1 < steps) commit(next);
         }
-        outer_blocks<T, MT, NT>(a, at, acc, m_w, n_w, lane);
+        outer_blocks<O, MT, NT>(a, at, acc, m_w, n_w, lane);
     }
 };
 
@@ -254,13 +258,16 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
 // computed again with float products.
 // (Three workgroups a CU: 300,000 rows in 5 segments, 64 x 96 each, take 57 us
 // against 76 with the two that the registers would allow otherwise.)
+// L, Q: types of the operands; where one is of 16 bits it is not rounded
+// again, and a result that is not float has its type, O.
 constexpr int kSplitThreads = 256;
-template <int BM, int BN, bool WHOLE>
+template <int BM, int BN, bool WHOLE, typename L, typename Q>
 __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a) {
-    using Plain = OuterTile<float, 64, 64, 2, 2, false>;
-    using SA = SplitStage<BM, kSplitThreads, true, WHOLE>;
-    using SB = SplitStage<BN, kSplitThreads, true, WHOLE>;
-    constexpr int MT = BM / 32, NT = BN / 32, kSplitLds = 3 * (SA::kPlane + SB::kPlane);
+    typedef std::conditional_t<sizeof(L) == 2, L, Q> O;
+    using Plain = OuterTile<float, 64, 64, 2, 2, false, L, Q>;
+    using SA = SplitStage<BM, kSplitThreads, true, WHOLE, L>;
+    using SB = SplitStage<BN, kSplitThreads, true, WHOLE, Q>;
+    constexpr int MT = BM / 32, NT = BN / 32, kSplitLds = SA::kLds + SB::kLds;
     __shared__ __attribute__((aligned(1024))) char lds_mem[kSplitLds > Plain::kLds ? kSplitLds : Plain::kLds];
     lds_char *lds = (lds_char *)lds_mem;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -275,10 +282,10 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
     auto rrow = [&](int i) { return SB::row(i, tid); };
     auto lcol = [&](int i) { return (int)(a.K - at.m0) - SA::at(i, tid); };
     auto rcol = [&](int i) { return (int)(a.M - at.n0) - SB::at(i, tid); };
-    left.init(at, a.left_rows, a.left_count, a.left, a.K * 4, kSplitK, lrow,
-              [&](int i) { return (at.m0 + SA::at(i, tid)) * 4; });
-    right.init(at, a.right_rows, a.right_count, a.right, a.M * 4, kSplitK, rrow,
-               [&](int i) { return (at.n0 + SB::at(i, tid)) * 4; });
+    left.init(at, a.left_rows, a.left_count, a.left, a.K * (int64_t)sizeof(L), kSplitK, lrow,
+              [&](int i) { return (at.m0 + SA::at(i, tid)) * (int64_t)sizeof(L); });
+    right.init(at, a.right_rows, a.right_count, a.right, a.M * (int64_t)sizeof(Q), kSplitK, rrow,
+               [&](int i) { return (at.n0 + SB::at(i, tid)) * (int64_t)sizeof(Q); });
     auto rows_of = [&](int64_t t) { return (int)max(min(at.rows - t * kSplitK, (int64_t)kSplitK), (int64_t)0); };
     auto ask = [&](int64_t t) {
         left.ask(t * kSplitK, rows_of(t), lrow);
@@ -303,9 +310,9 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
         },
         [&] {
             sa.commit(lds, tid, bad);
-            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+            sb.commit(lds + SA::kLds, tid, bad);
         },
-        [&] { split_step<MT, NT, true, BM, true, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
+        [&] { split_step<MT, NT, true, BM, true, BN, kPlanes<L>, kPlanes<Q>>(acc, lds, lds + SA::kLds, m_w, n_w, lane); });
     if (__syncthreads_or(bad != 0.f)) {
         OuterPlace q = at;
         for (int r = 0; r < BM && at.m0 + r < a.K; r += 64)
@@ -313,11 +320,11 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
                 q.m0 = at.m0 + r;
                 q.n0 = at.n0 + c;
                 __syncthreads();
-                Plain::run(a, q, lds, wave, lane);
+                Plain::template run<O>(a, q, lds, wave, lane);
             }
         return;
     }
-    outer_blocks<float, MT, NT>(a, at, acc, m_w, n_w, lane);
+    outer_blocks<O, MT, NT>(a, at, acc, m_w, n_w, lane);
 }
 
 // Adds the slots of each segment and rounds once.  PARTS threads share a cell:
@@ -406,24 +413,29 @@ int outer_launch(OuterArgs a, bool direct, hipStream_t st) {
     return outer_finish<T>(a, st);
 }
 
-template <int BM, int BN>
+template <typename L, typename Q, int BM, int BN>
 int outer_split_launch(OuterArgs a, hipStream_t st) {
     a.mtiles = (a.K + BM - 1) / BM;
     a.ntiles = (a.M + BN - 1) / BN;
     dim3 grid;
     if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
     if (a.K % 8 == 0 && a.M % 8 == 0)
-        timed_launch_ggl(true, (seg_outer_split<BM, BN, true>), grid, dim3(kSplitThreads), 0, st, a);
+        timed_launch_ggl(true, (seg_outer_split<BM, BN, true, L, Q>), grid, dim3(kSplitThreads), 0, st, a);
     else
-        timed_launch_ggl(true, (seg_outer_split<BM, BN, false>), grid, dim3(kSplitThreads), 0, st, a);
-    return outer_finish<float>(a, st);
+        timed_launch_ggl(true, (seg_outer_split<BM, BN, false, L, Q>), grid, dim3(kSplitThreads), 0, st, a);
+    return outer_finish<std::conditional_t<sizeof(L) == 2, L, Q>>(a, st);
+}
+
+template <typename L, typename Q>
+int outer_split_dispatch(const OuterArgs &a, const OuterPlan &p, hipStream_t st) {
+    if (p.small && !p.wide) return outer_split_launch<L, Q, 64, 64>(a, st);
+    return outer_split_launch<L, Q, 64, 128>(a, st);
 }
 
 template <typename T>
 int outer_dispatch(const OuterArgs &a, const OuterPlan &p, bool direct, hipStream_t st) {
     if constexpr (sizeof(T) == 4) {
-        if (p.small && !p.wide) return outer_split_launch<64, 64>(a, st);
-        return outer_split_launch<64, 128>(a, st);
+        return outer_split_dispatch<T, T>(a, p, st);
     } else {
         if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
         if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
@@ -446,17 +458,28 @@ extern "C" int segred_outer(const void *left, const int64_t *left_rows, int64_t 
                             const void *right, const int64_t *right_rows, int64_t right_count, int64_t m,
                             int32_t dtype, const int64_t *offsets, int64_t num_segments, int64_t num_rows, void *out,
                             int32_t out_dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
-    const int64_t e = float_size(dtype);
-    if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
+    return segred_outer_mixed(left, dtype, left_rows, left_count, k, right, dtype, right_rows, right_count, m, offsets,
+                              num_segments, num_rows, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+extern "C" int segred_outer_mixed(const void *left, int32_t left_dtype, const int64_t *left_rows, int64_t left_count,
+                                  int64_t k, const void *right, int32_t right_dtype, const int64_t *right_rows,
+                                  int64_t right_count, int64_t m, const int64_t *offsets, int64_t num_segments,
+                                  int64_t num_rows, void *out, int32_t out_dtype, void *workspace,
+                                  int64_t workspace_bytes, hipStream_t stream) {
+    const int64_t le = float_size(left_dtype), re = float_size(right_dtype);
+    for (int32_t dtype : {left_dtype, right_dtype})
+        if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
     if (k < 1 || m < 1 || left_count < 0 || right_count < 0 || num_segments < 0 || num_rows < 0)
         return SEGRED_ERR_INVALID_ARGUMENT;
     if ((!left_rows && left_count < num_rows) || (!right_rows && right_count < num_rows)) return SEGRED_ERR_INVALID_ARGUMENT;
     if (num_segments > 0 && (!offsets || !out || (num_rows > 0 && ((left_count > 0 && !left) || (right_count > 0 && !right)))))
         return SEGRED_ERR_INVALID_ARGUMENT;
-    if (e == 0 || k > kMaxWidth || m > kMaxWidth) return SEGRED_ERR_UNSUPPORTED;
-    if (out_dtype != dtype && out_dtype != SEGRED_F32) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (le == 0 || re == 0 || k > kMaxWidth || m > kMaxWidth) return SEGRED_ERR_UNSUPPORTED;
+    if (left_dtype != right_dtype && left_dtype != SEGRED_F32 && right_dtype != SEGRED_F32) return SEGRED_ERR_UNSUPPORTED;
+    if (out_dtype != left_dtype && out_dtype != right_dtype && out_dtype != SEGRED_F32) return SEGRED_ERR_INVALID_ARGUMENT;
     const int64_t oe = float_size(out_dtype);
-    if (!aligned(left, e) || !aligned(right, e) || !aligned(out, oe) || !aligned(offsets, 8) || !aligned(left_rows, 8) ||
+    if (!aligned(left, le) || !aligned(right, re) || !aligned(out, oe) || !aligned(offsets, 8) || !aligned(left_rows, 8) ||
         !aligned(right_rows, 8) || !aligned(workspace, 16))
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (too_large(left_count, k, 4) || too_large(right_count, m, 4) || too_large(num_segments, k * m, 4))
@@ -484,8 +507,14 @@ extern "C" int segred_outer(const void *left, const int64_t *left_rows, int64_t 
     a.out_f32 = out_dtype == SEGRED_F32;
     a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
     a.vec = (m % 4 == 0 && aligned(out, 4 * oe)) ? 1 : 0;
-    const bool direct = (k * e) % 16 == 0 && (m * e) % 16 == 0 && aligned(left, 16) && aligned(right, 16);
-    switch (dtype) {
+    const bool direct = (k * le) % 16 == 0 && (m * re) % 16 == 0 && aligned(left, 16) && aligned(right, 16);
+    if (left_dtype != right_dtype) {
+        if (left_dtype == SEGRED_BF16) return outer_split_dispatch<__bf16, float>(a, plan, stream);
+        if (left_dtype == SEGRED_F16) return outer_split_dispatch<_Float16, float>(a, plan, stream);
+        if (right_dtype == SEGRED_BF16) return outer_split_dispatch<float, __bf16>(a, plan, stream);
+        return outer_split_dispatch<float, _Float16>(a, plan, stream);
+    }
+    switch (left_dtype) {
     case SEGRED_BF16: return outer_dispatch<__bf16>(a, plan, direct, stream);
     case SEGRED_F16: return outer_dispatch<_Float16>(a, plan, direct, stream);
     default: return outer_dispatch<float>(a, plan, direct, stream);

@@ -93,6 +93,21 @@ __device__ __forceinline__ u32x4 load_unit(uint64_t addr, int n) {
     return v;
 }
 
+// The same of four neighbouring elements of type S as floats, for T = float.
+template <typename T, typename S>
+__device__ __forceinline__ u32x4 load_as(uint64_t addr, int n) {
+    if constexpr (__is_same(T, S)) {
+        return load_unit<T>(addr, n);
+    } else {
+        static_assert(sizeof(T) == 4 && sizeof(S) == 2, "16-bit elements as floats");
+        u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) v[j] = __float_as_uint((float)((__attribute__((address_space(1))) const S *)addr)[j]);
+        return v;
+    }
+}
+
 // ---------------------------------------------------------------- staging
 //
 // A stage object belongs to one thread and moves that thread's units of one
@@ -157,9 +172,11 @@ __device__ __forceinline__ int col_swizzle(int k) {
     return ((k >> 2) & 3) & kMask;
 }
 
-// Col form: kStep<T> rows of W elements.
-template <typename T, int W, int THREADS, bool DIRECT>
+// Col form: kStep<T> rows of W elements.  S: their type in memory, where that
+// is another (not DIRECT).
+template <typename T, int W, int THREADS, bool DIRECT, typename S = T>
 struct ColStage {
+    static_assert(!DIRECT || __is_same(T, S), "direct loads convert nothing");
     static constexpr int kWaves = THREADS / 64;
     static constexpr int kUnits = W / kUnit<T>;                         // per LDS row
     static constexpr int kGroups = kStep<T> * W * (int)sizeof(T) / 1024;  // wave loads of a step
@@ -186,7 +203,7 @@ struct ColStage {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             if constexpr (DIRECT) load_to_lds(left(i) > 0 ? src(i) : zeros, lds + group(i, wave) * 1024);
-            else v[i] = load_unit<T>(src(i), left(i));
+            else v[i] = load_as<T, S>(src(i), left(i));
         }
     }
     __device__ __forceinline__ void commit(lds_char *lds, int wave, int lane) {
@@ -406,25 +423,49 @@ __device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b, float &bad) {
     return s;
 }
 
+// A 16-bit operand beside a float one has fewer parts: a bf16 is its own h, a
+// float16 (11 bits) is h + m.
+template <typename S> constexpr int kPlanes = sizeof(S) == 4 ? 3 : __is_same(S, __bf16) ? 1 : 2;
+
+// h and m of eight 16-bit values (h alone for bf16); `bad` as in split_unit.
+template <typename S>
+__device__ __forceinline__ Split split_short(u32x4 a, float &bad) {
+    typedef __attribute__((ext_vector_type(8))) S S8;
+    const S8 x = __builtin_bit_cast(S8, a);
+    bf16x8 h, m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float f = (float)x[j], t = __uint_as_float(__float_as_uint(f) & 0xffff0000u), r = f - t;
+        h[j] = (__bf16)t;
+        m[j] = (__bf16)r;
+        bad = fmaf(r, 0.f, bad);
+    }
+    return {__is_same(S, __bf16) ? a : __builtin_bit_cast(u32x4, h), __builtin_bit_cast(u32x4, m), u32x4{0u, 0u, 0u, 0u}};
+}
+
 // One operand's step in registers: W rows (or columns) of 32 k, eight
-// neighbouring floats at a time.  COL: W neighbours of one k, else 32 k of one
-// row.  WHOLE: rows hold whole parts, so that each is there or not.
-template <int W, int THREADS, bool COL, bool WHOLE>
+// neighbouring values of type S at a time.  COL: W neighbours of one k, else 32
+// k of one row.  WHOLE: rows hold whole parts, so that each is there or not.
+template <int W, int THREADS, bool COL, bool WHOLE, typename S = float>
 struct SplitStage {
-    static constexpr int kParts = W * 4 / THREADS;  // of eight floats, per thread
+    static constexpr int kParts = W * 4 / THREADS;  // of eight values, per thread
     static constexpr int kPlane = W * 64;           // bytes
+    static constexpr int kLds = kPlanes<S> * kPlane;
     static_assert(kParts >= 1 && W * 4 % THREADS == 0, "whole parts");
-    u32x4 v[kParts][2];
+    u32x4 v[kParts][sizeof(S) / 2];
 
     // Row (k if COL) and first element inside it of part i.
     static __device__ __forceinline__ int row(int i, int tid) { return (i * THREADS + tid) / (COL ? W / 8 : 4); }
     static __device__ __forceinline__ int at(int i, int tid) { return (i * THREADS + tid) % (COL ? W / 8 : 4) * 8; }
-    // src(i): address of part i; left(i): floats of its row from there on.
+    // src(i): address of part i; left(i): values of its row from there on.
     template <bool EIGHT = WHOLE, typename F, typename G>
     __device__ __forceinline__ void issue(F src, G left) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            if constexpr (EIGHT) {
+            if constexpr (sizeof(S) == 2) {
+                if constexpr (EIGHT) v[i][0] = load_whole<S>(left(i) > 0 ? src(i) : (uint64_t)zero_unit());
+                else v[i][0] = load_unit<S>(src(i), left(i));
+            } else if constexpr (EIGHT) {
                 const uint64_t q = left(i) > 0 ? src(i) : (uint64_t)zero_unit();
                 v[i][0] = load_whole<float>(q);
                 v[i][1] = load_whole<float>(q + 16);
@@ -441,11 +482,13 @@ struct SplitStage {
             int off;
             if constexpr (COL) off = r * W * 2 + (((c >> 4) ^ col_swizzle<__bf16, W>(r)) << 5) + (c & 8) * 2;
             else off = r * 64 + (((c >> 3) ^ ((r >> 2) & 3)) << 4);
-            const Split s = split_unit(v[i][0], v[i][1], bad);
+            Split s;
+            if constexpr (sizeof(S) == 4) s = split_unit(v[i][0], v[i][1], bad);
+            else s = split_short<S>(v[i][0], bad);
             typedef __attribute__((address_space(3))) u32x4 lds_unit;
             *reinterpret_cast<lds_unit *>(lds + off) = s.h;
-            *reinterpret_cast<lds_unit *>(lds + kPlane + off) = s.m;
-            *reinterpret_cast<lds_unit *>(lds + 2 * kPlane + off) = s.l;
+            if constexpr (kPlanes<S> > 1) *reinterpret_cast<lds_unit *>(lds + kPlane + off) = s.m;
+            if constexpr (kPlanes<S> > 2) *reinterpret_cast<lds_unit *>(lds + 2 * kPlane + off) = s.l;
         }
     }
 };
@@ -457,23 +500,25 @@ __device__ __forceinline__ u32x4 split_frag(const lds_char *plane, int r0, int l
     return *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(plane + off);
 }
 
-// One step of a wave's MT x NT neighbouring blocks, the small terms first.
-template <int MT, int NT, bool A_COL, int AW, bool B_COL, int BW>
+// One step of a wave's MT x NT neighbouring blocks, the small terms first.  PA
+// and PB: parts of either operand.
+template <int MT, int NT, bool A_COL, int AW, bool B_COL, int BW, int PA = 3, int PB = 3>
 __device__ __forceinline__ void split_step(f32x4 (&acc)[MT][NT], const lds_char *la, const lds_char *lb, int m0, int n0,
                                            int lane) {
-    u32x4 a[3][MT];
+    u32x4 a[PA][MT];
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
+    for (int p = 0; p < PA; ++p)
 #pragma unroll
         for (int i = 0; i < MT; ++i) a[p][i] = split_frag<A_COL, AW>(la + p * AW * 64, m0 + 16 * i, lane);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        u32x4 b[3];
+        u32x4 b[PB];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) b[p] = split_frag<B_COL, BW>(lb + p * BW * 64, n0 + 16 * j, lane);
+        for (int p = 0; p < PB; ++p) b[p] = split_frag<B_COL, BW>(lb + p * BW * 64, n0 + 16 * j, lane);
 #pragma unroll
         for (int q = 0; q < 6; ++q) {
             constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
+            if (kA[q] >= PA || kB[q] >= PB) continue;
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[i][j] = mma<__bf16>(b[kB[q]], a[kA[q]][i], acc[i][j]);
         }
