@@ -324,11 +324,12 @@ def _calls(s):
     args = (s["weights"], s["offsets"], s["which"], s["down"], s["up"])
     if kind == "adapter":
         return sr.adapter(s["values"], *args, scale=s["scale"])
-    out, low = sr.adapter(s["values"], *args, scale=s["scale"], want_low=True)
-    grad, grad_low = sr.adapter(s["grad"], *args, scale=s["scale"], transpose=True, want_low=True)
+    # low-rank rows in float32, so that the factors' gradients are rounded once
+    out, low = sr.adapter(s["values"], *args, scale=s["scale"], want_low=torch.float32)
+    grad, grad_low = sr.adapter(s["grad"], *args, scale=s["scale"], transpose=True, want_low=torch.float32)
     order, _, bounds = sr.group(s["row_which"], case["adapters"])
-    grad_up = sr.outer(s["grad"], low, bounds, left_rows=order, right_rows=order)
-    grad_down = sr.outer(grad_low, s["values"], bounds, left_rows=order, right_rows=order)
+    grad_up = sr.outer(s["grad"], low, bounds, left_rows=order, right_rows=order, out_dtype=s["up"].dtype)
+    grad_down = sr.outer(grad_low, s["values"], bounds, left_rows=order, right_rows=order, out_dtype=s["down"].dtype)
     return out, grad, grad_down, grad_up
 
 
