@@ -473,7 +473,7 @@ __global__ __launch_bounds__(64 * WM * WN) void adapter_main(AdapterArgs a) {
     Tile::run(a, p.row0, p.rows, p.n0, met, s_ids, s_list, (lds_char *)lds_mem, wave, lane);
 }
 
-// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// The same for float, in bf16 parts; a tile with a sum that is not finite is
 // computed again with float products.
 constexpr int kSplitThreads = 256;
 template <int BN, bool B_COL, bool WHOLE>
@@ -517,7 +517,6 @@ __global__ __launch_bounds__(kSplitThreads, 3) void adapter_main_split(AdapterAr
     }
     const int base = (K + kSplitK - 1) / kSplitK, blocks = (int)a.blocks;
     f32x4 acc[MT][NT] = {};
-    float bad = 0.f;
     const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
     split_steps(
         base + met * blocks,
@@ -551,11 +550,11 @@ __global__ __launch_bounds__(kSplitThreads, 3) void adapter_main_split(AdapterAr
                     [&](int i) { return p.n0 + SB::row(i, tid) < a.M ? R - rank - SB::at(i, tid) : 0; });
         },
         [&] {
-            sa.commit(lds, tid, bad);
-            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+            sa.commit(lds, tid);
+            sb.commit(lds + 3 * SA::kPlane, tid);
         },
         [&] { split_step<MT, NT, false, BM, B_COL, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
-    if (__syncthreads_or(bad != 0.f)) {
+    if (__syncthreads_or(any_not_finite(acc))) {
         for (int c = 0; c < BN && p.n0 + c < a.M; c += 64) {
             __syncthreads();
             Plain::run(a, p.row0, p.rows, p.n0 + c, met, s_ids, s_list, lds, wave, lane);
@@ -708,13 +707,6 @@ int adapter_few_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     if (b_col) timed_launch_ggl(true, (adapter_main_few<T, MT, NW, STAGES, true>), grid, dim3(64 * NW), 0, st, a);
     else timed_launch_ggl(true, (adapter_main_few<T, MT, NW, STAGES, false>), grid, dim3(64 * NW), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
-}
-
-// NaN where a value of c is infinite or NaN, else z.
-__device__ __forceinline__ float not_finite(f32x4 c, float z) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) z = fmaf(c[j], 0.f, z);
-    return z;
 }
 
 // The infinities and NaN of a stored tile again, element by element, so that

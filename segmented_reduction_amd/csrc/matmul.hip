@@ -170,7 +170,7 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_matmul(MatmulArgs a) {
     if (p.rows > 0) Tile::run(a, p, (lds_char *)lds_mem, wave, lane);
 }
 
-// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// The same for float, in bf16 parts; a tile with a sum that is not finite is
 // computed again with float products.  (Three workgroups a CU: 8,192 rows in 8
 // segments, 1,024 x 1,024, take 122 us against 137 with the two that the
 // registers of transposed weights would allow otherwise.)
@@ -211,7 +211,6 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_matmul_split(MatmulArgs 
         }
     }
     f32x4 acc[MT][NT] = {};
-    float bad = 0.f;
     const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
     split_steps(
         (K + kSplitK - 1) / kSplitK,
@@ -225,11 +224,11 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_matmul_split(MatmulArgs 
                 sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * 4; }, [&](int i) { return bleft[i] - k0; });
         },
         [&] {
-            sa.commit(lds, tid, bad);
-            sb.commit(lds + 3 * SA::kPlane, tid, bad);
+            sa.commit(lds, tid);
+            sb.commit(lds + 3 * SA::kPlane, tid);
         },
         [&] { split_step<MT, NT, false, BM, B_COL, BN>(acc, lds, lds + 3 * SA::kPlane, m_w, n_w, lane); });
-    if (__syncthreads_or(bad != 0.f)) {
+    if (__syncthreads_or(any_not_finite(acc))) {
         for (int r = 0; r < p.rows; r += 64)
             for (int c = 0; c < BN && p.n0 + c < a.M; c += 64) {
                 const MatmulPlace q{p.s, p.row0 + r, p.n0 + c, min(64, p.rows - r)};

@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * WM * WN) void seg_outer(OuterArgs a) {
     if (at.work) Tile::run(a, at, (lds_char *)lds_mem, wave, lane);
 }
 
-// The same for float, in bf16 parts; a tile that met an infinity or a NaN is
+// The same for float, in bf16 parts; a tile with a sum that is not finite is
 // computed again with float products.
 // (Three workgroups a CU: 300,000 rows in 5 segments, 64 x 96 each, take 57 us
 // against 76 with the two that the registers would allow otherwise.)
@@ -292,7 +292,6 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
         right.ask(t * kSplitK, rows_of(t), rrow);
     };
     f32x4 acc[MT][NT] = {};
-    float bad = 0.f;
     const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
     ask(0);
     split_steps(
@@ -309,11 +308,11 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
             ask(t + 1);
         },
         [&] {
-            sa.commit(lds, tid, bad);
-            sb.commit(lds + SA::kLds, tid, bad);
+            sa.commit(lds, tid);
+            sb.commit(lds + SA::kLds, tid);
         },
         [&] { split_step<MT, NT, true, BM, true, BN, kPlanes<L>, kPlanes<Q>>(acc, lds, lds + SA::kLds, m_w, n_w, lane); });
-    if (__syncthreads_or(bad != 0.f)) {
+    if (__syncthreads_or(any_not_finite(acc))) {
         OuterPlace q = at;
         for (int r = 0; r < BM && at.m0 + r < a.K; r += 64)
             for (int c = 0; c < BN && at.n0 + c < a.M; c += 64) {

@@ -390,9 +390,13 @@ inline bool tile_grid(int64_t total, dim3 &grid) {
 // with what is left out (m l', l m', l l') below 2^-22 |x y|, about the
 // rounding of a product to float.  Six products at 16 times the rate.  bf16 has
 // float's exponents, but the matrix cores take parts below 2^-126 for zero, so
-// that values below 2^-102 lose bits (less than 2^-125 each).  An infinity has no such parts: whoever splits one
-// (or a NaN) notes it, and the tile is computed again with float products, so
-// that infinities and NaN come out as float arithmetic gives them.
+// that values below 2^-102 lose bits (less than 2^-125 each).
+//
+// An infinity has no such parts (h is infinite, m and l are NaN), and of a
+// product that leaves float's range l h' may be an infinity of the wrong sign
+// beside that of h h', since l has either sign.  Either way the sum is not
+// finite: a tile with such a sum is computed again with float products, so that
+// infinities and NaN come out as float arithmetic gives them.
 //
 // A step is 32 k.  It passes through registers, is split on its way into LDS
 // and lies there as three planes in the forms of the 16-bit types (row form
@@ -402,8 +406,8 @@ constexpr int kSplitK = 32;
 struct Split {
     u32x4 h, m, l;
 };
-// Splits eight floats; `bad` becomes NaN where one is infinite or NaN.
-__device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b, float &bad) {
+// Splits eight floats.
+__device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b) {
     typedef __attribute__((ext_vector_type(2))) float f32x2;
     typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
     Split s;
@@ -417,8 +421,6 @@ __device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b, float &bad) {
         s.h[j] = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
         s.m[j] = m;
         s.l[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{q0, q1}), bf16x2));
-        bad = fmaf(q0, 0.f, bad);
-        bad = fmaf(q1, 0.f, bad);
     }
     return s;
 }
@@ -427,20 +429,39 @@ __device__ __forceinline__ Split split_unit(u32x4 a, u32x4 b, float &bad) {
 // float16 (11 bits) is h + m.
 template <typename S> constexpr int kPlanes = sizeof(S) == 4 ? 3 : __is_same(S, __bf16) ? 1 : 2;
 
-// h and m of eight 16-bit values (h alone for bf16); `bad` as in split_unit.
+// h and m of eight 16-bit values (h alone for bf16).
 template <typename S>
-__device__ __forceinline__ Split split_short(u32x4 a, float &bad) {
-    typedef __attribute__((ext_vector_type(8))) S S8;
-    const S8 x = __builtin_bit_cast(S8, a);
-    bf16x8 h, m;
+__device__ __forceinline__ Split split_short(u32x4 a) {
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    if constexpr (__is_same(S, __bf16)) {
+        return {a, none, none};
+    } else {
+        const f16x8 x = __builtin_bit_cast(f16x8, a);
+        bf16x8 h, m;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float f = (float)x[j], t = __uint_as_float(__float_as_uint(f) & 0xffff0000u), r = f - t;
-        h[j] = (__bf16)t;
-        m[j] = (__bf16)r;
-        bad = fmaf(r, 0.f, bad);
+        for (int j = 0; j < 8; ++j) {
+            const float f = (float)x[j], t = __uint_as_float(__float_as_uint(f) & 0xffff0000u);
+            h[j] = (__bf16)t;
+            m[j] = (__bf16)(f - t);
+        }
+        return {__builtin_bit_cast(u32x4, h), __builtin_bit_cast(u32x4, m), none};
     }
-    return {__is_same(S, __bf16) ? a : __builtin_bit_cast(u32x4, h), __builtin_bit_cast(u32x4, m), u32x4{0u, 0u, 0u, 0u}};
+}
+
+// NaN where a value of c is infinite or NaN, else z.
+__device__ __forceinline__ float not_finite(f32x4 c, float z) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z = fmaf(c[j], 0.f, z);
+    return z;
+}
+template <int MT, int NT>
+__device__ __forceinline__ bool any_not_finite(const f32x4 (&acc)[MT][NT]) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) z = not_finite(acc[i][j], z);
+    return z != 0.f;
 }
 
 // One operand's step in registers: W rows (or columns) of 32 k, eight
@@ -475,7 +496,7 @@ struct SplitStage {
             }
         }
     }
-    __device__ __forceinline__ void commit(lds_char *lds, int tid, float &bad) const {
+    __device__ __forceinline__ void commit(lds_char *lds, int tid) const {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int r = row(i, tid), c = at(i, tid);
@@ -483,8 +504,8 @@ struct SplitStage {
             if constexpr (COL) off = r * W * 2 + (((c >> 4) ^ col_swizzle<__bf16, W>(r)) << 5) + (c & 8) * 2;
             else off = r * 64 + (((c >> 3) ^ ((r >> 2) & 3)) << 4);
             Split s;
-            if constexpr (sizeof(S) == 4) s = split_unit(v[i][0], v[i][1], bad);
-            else s = split_short<S>(v[i][0], bad);
+            if constexpr (sizeof(S) == 4) s = split_unit(v[i][0], v[i][1]);
+            else s = split_short<S>(v[i][0]);
             typedef __attribute__((address_space(3))) u32x4 lds_unit;
             *reinterpret_cast<lds_unit *>(lds + off) = s.h;
             if constexpr (kPlanes<S> > 1) *reinterpret_cast<lds_unit *>(lds + kPlane + off) = s.m;
