@@ -31,6 +31,7 @@ struct AdapterArgs {
     int64_t S, N, K, M, L, R;
     int64_t R2;           // ranks between rows of `second`: R, or more where it is a copy
     const char *copy_from;  // the caller's second factor, where `second` is a copy of it
+    int copy_rows;          // rows of it per workgroup
     int64_t slots, mtiles, ntiles, blocks;  // blocks: ceil(R / 32)
     char *u;              // [N, blocks * 128 bytes]
     int32_t *ids;         // [N] adapter of each row, -1: none
@@ -44,17 +45,19 @@ constexpr int kRankBlock = 32;
 
 // Rows of the second factor that do not hold whole 16-byte units are copied,
 // with zeros behind them, for the adapters that some segment has: by the
-// workgroups of its first segment, kCopyRows rows each.
-constexpr int kCopyRows = 512;
+// workgroups of its first segment, kCopyRows rows each, or as many as have at
+// most kCopyPart elements (at least one row, of up to 2^24): indexes inside a
+// workgroup's part have 32 bits.
+constexpr int64_t kCopyRows = 512, kCopyPart = int64_t(1) << 24;
 template <typename T>
 __device__ __forceinline__ void copy_second(const AdapterArgs &a, int64_t wg, int threads) {
-    const int64_t per = (a.M + kCopyRows - 1) / kCopyRows, s = wg / per, m0 = (wg - s * per) * kCopyRows;
+    const int64_t per = (a.M + a.copy_rows - 1) / a.copy_rows, s = wg / per, m0 = (wg - s * per) * a.copy_rows;
     const int64_t adapter = a.which[s];
     if (adapter < 0 || adapter >= a.L) return;
     const int lane = threadIdx.x & 63;
     for (int64_t q = 0; q < s; q += 64)
         if (ballot(q + lane < s && a.which[q + lane] == adapter) != 0) return;
-    const int R = (int)a.R, R2 = (int)a.R2, rows = (int)min((int64_t)kCopyRows, a.M - m0);
+    const int R = (int)a.R, R2 = (int)a.R2, rows = (int)min((int64_t)a.copy_rows, a.M - m0);
     const T *from = reinterpret_cast<const T *>(a.copy_from) + (adapter * a.M + m0) * R;
     T *to = reinterpret_cast<T *>(const_cast<char *>(a.second)) + (adapter * a.M + m0) * R2;
     for (int i = threadIdx.x; i < rows * R2; i += threads) {
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t launch = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (launch >= a.slots * a.blocks) {
-        if (a.copy_from && launch < a.slots * a.blocks + a.S * ((a.M + kCopyRows - 1) / kCopyRows))
+        if (a.copy_from && launch < a.slots * a.blocks + a.S * ((a.M + a.copy_rows - 1) / a.copy_rows))
             copy_second<T>(a, launch - a.slots * a.blocks, 64 * NW);
         return;
     }
@@ -360,8 +363,8 @@ struct AdapterTile {
         const int base = (K + kStep<T> - 1) / kStep<T>, blocks = (int)a.blocks;
         const int steps = base + met * blocks;
         auto issue = [&](int t, lds_char *buf) {
-            if (t < base || t >= steps) {  // past the last step: zeros
-                const int k0 = t * kStep<T>;
+            if (t < base || t >= steps) {  // past the last step: zeros, as past the contraction
+                const int k0 = min(t, base) * kStep<T>;
                 sa.issue(buf, wave, k0);
                 if constexpr (B_COL) {
                     const uint64_t step = (uint64_t)k0 * a.M * sizeof(T);
@@ -966,7 +969,7 @@ int adapter_low_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     constexpr int NW = DIRECT ? 4 : 8, STAGES = DIRECT ? 3 : 2;
     a.slots = tight_slots(a.N, a.S, __builtin_ctz(16 * MT));
     dim3 grid;
-    const int64_t copies = a.copy_from ? a.S * ((a.M + kCopyRows - 1) / kCopyRows) : 0;
+    const int64_t copies = a.copy_from ? a.S * ((a.M + a.copy_rows - 1) / a.copy_rows) : 0;
     if (!tile_grid(a.slots * a.blocks + copies, grid)) return SEGRED_ERR_UNSUPPORTED;
     if (b_col) timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, true, DIRECT>), grid, dim3(64 * NW), 0, st, a);
     else timed_launch_ggl(false, (adapter_low<T, MT, NW, STAGES, false, DIRECT>), grid, dim3(64 * NW), 0, st, a);
@@ -1104,6 +1107,7 @@ extern "C" int segred_adapter_mixed(const void *values, int32_t dtype, int64_t k
         a.copy_from = a.second;
         a.second = a.u + space.low;
         a.R2 = space.ranks;
+        a.copy_rows = (int)std::max<int64_t>(1, std::min(kCopyRows, kCopyPart / a.R2));
     }
     a.low = static_cast<char *>(low);
     a.low_f32 = low_dtype == SEGRED_F32;
