@@ -413,7 +413,8 @@ int segred_galloping_search(const void *values, int32_t dtype, int64_t value_cou
  * returns; NULL where that is 0), which is free again once the call's work
  * has run.  So they may be captured in a HIP graph, and graphs or streams
  * with workspaces of their own may run at once.  No atomics: results are the
- * same bit for bit from run to run.
+ * same bit for bit from run to run, where segred_combine_grad's rows are named
+ * once as it asks.
  *
  * segred_matmul -- the matrix product of each segment's rows with weights of
  * its own: out[r] = values[v(r)] W[s] for the rows r of segment s.
@@ -541,13 +542,31 @@ int segred_combine(const void *values, int32_t dtype, int64_t m, int64_t rows, c
  *   grad          [tokens, m] of type `dtype`.
  *   grad_values   [rows, m]; rows that no entry names are left as they were.
  *                 Each row may be named once only (as segred_group's positions
- *                 do); it is not checked.
+ *                 do); it is not checked, and of several entries that name a row
+ *                 any one may be what remains there.
  *   grad_weights  float32 [tokens, fanout]; 0 for entries that take no part.
  *   the others    as segred_combine, and the errors.
  */
 int segred_combine_grad(const void *grad, const void *values, int32_t dtype, int64_t m, int64_t rows,
                         const int64_t *position, const float *weights, int64_t tokens, int64_t fanout,
                         void *grad_values, float *grad_weights, hipStream_t stream);
+
+/*
+ * segred_combine_grad_repeated -- the same where a row may be named more than
+ * once: grad_values[p] = sum over the entries (t, j) with position[t, j] = p, in
+ * their order, of weights[t, j] grad[t], held in float32 and rounded once; zeros
+ * for a row that no entry names.  The entries are sorted by row first.
+ *
+ *   workspace  segred_combine_grad_repeated_workspace(rows, tokens, fanout) bytes.
+ *
+ * Errors: as segred_combine_grad, also for a workspace that is missing or too
+ * small; SEGRED_ERR_UNSUPPORTED for more than 2^31 - 2 rows or 2^31 - 1 entries.
+ */
+int segred_combine_grad_repeated(const void *grad, const void *values, int32_t dtype, int64_t m, int64_t rows,
+                                 const int64_t *position, const float *weights, int64_t tokens, int64_t fanout,
+                                 void *grad_values, float *grad_weights, void *workspace, int64_t workspace_bytes,
+                                 hipStream_t stream);
+int64_t segred_combine_grad_repeated_workspace(int64_t rows, int64_t tokens, int64_t fanout);
 
 /*
  * segred_adapter -- a projection that all rows share with a low-rank adapter

@@ -104,6 +104,10 @@ def library(path: str | None = None):
             lib.segred_combine.restype = ctypes.c_int
             lib.segred_combine_grad.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp]
             lib.segred_combine_grad.restype = ctypes.c_int
+            lib.segred_combine_grad_repeated.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp, i64, vp]
+            lib.segred_combine_grad_repeated.restype = ctypes.c_int
+            lib.segred_combine_grad_repeated_workspace.argtypes = [i64, i64, i64]
+            lib.segred_combine_grad_repeated_workspace.restype = i64
             lib.segred_adapter.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, i32, vp, vp,
                                            vp, i64, vp]
             lib.segred_adapter.restype = ctypes.c_int
@@ -616,12 +620,14 @@ def combine(values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
 
 
 def combine_grad(grad: torch.Tensor, values: torch.Tensor, position: torch.Tensor, weights: torch.Tensor, *,
-                 out: torch.Tensor | None = None):
+                 repeated: bool = False, out: torch.Tensor | None = None):
     """The gradient of ``combine`` (segred_combine_grad) from ``grad`` [T, M].
 
     Returns (grad_values [N, M], grad_weights float32 [T, k]).  Each row may be
-    named once only; rows that ``position`` does not name are left as they were
-    (uninitialised when ``out`` is not given)."""
+    named once only, as ``group``'s positions do, which is not checked; rows that
+    ``position`` does not name are left as they were (uninitialised when ``out``
+    is not given).  With ``repeated`` rows may be named any number of times: the
+    entries are sorted by row first, and a row that none names gets zeros."""
     dev, code = _check_combine(values, position, weights)
     _beside(dev, "grad", grad)
     (n, m), (t, k) = values.shape, position.shape
@@ -634,8 +640,16 @@ def combine_grad(grad: torch.Tensor, values: torch.Tensor, position: torch.Tenso
         if out.shape != values.shape or out.dtype != values.dtype:
             raise ValueError("out must have the shape and dtype of values")
     grad_weights = torch.empty_like(weights)
-    _launch((_lib or library()).segred_combine_grad, "segred_combine_grad", dev, grad.data_ptr(), values.data_ptr(),
-            code, m, n, position.data_ptr(), weights.data_ptr(), t, k, out.data_ptr(), grad_weights.data_ptr())
+    lib = _lib or library()
+    args = (grad.data_ptr(), values.data_ptr(), code, m, n, position.data_ptr(), weights.data_ptr(), t, k,
+            out.data_ptr(), grad_weights.data_ptr())
+    if repeated:
+        need = lib.segred_combine_grad_repeated_workspace(n, t, k)
+        work = torch.empty(need, dtype=torch.uint8, device=values.device) if need else None
+        _launch(lib.segred_combine_grad_repeated, "segred_combine_grad_repeated", dev, *args,
+                work.data_ptr() if need else None, need)
+    else:
+        _launch(lib.segred_combine_grad, "segred_combine_grad", dev, *args)
     return out, grad_weights
 
 

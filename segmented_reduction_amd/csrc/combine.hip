@@ -17,6 +17,7 @@ struct CombineArgs {
     char *out;                // [tokens, M], or the gradient of values [rows, M]
     float *grad_weights;      // [tokens, fanout]
     int64_t blocks;           // blocks of kJoin entries of a token (gradient call)
+    const int64_t *order, *offsets;  // entries by the row they name (gradient call, rows named more than once)
 };
 
 constexpr int kCombineThreads = 256;
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grads(CombineArgs a) 
                 dot[j] = fmaf((float)g.v[e], (float)y[j].v[e], dot[j]);
                 o.v[e] = (T)(w[j] * (float)g.v[e]);
             }
-            o.store(a.out + (p[j] * a.M + c) * (int64_t)sizeof(T));
+            if (!a.offsets) o.store(a.out + (p[j] * a.M + c) * (int64_t)sizeof(T));
         }
     }
 #pragma unroll
@@ -115,6 +116,39 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grads(CombineArgs a) 
         const float d = wave_sum(dot[j]);
         if (lane == 0 && j0 + j < a.fanout) a.grad_weights[t * a.fanout + j0 + j] = p[j] >= 0 ? d : 0.f;
     }
+}
+
+// Rows that several entries may name: one unit of one row per thread, which
+// adds the entries' gradients in their order, so that no two threads write a
+// row.  The entries come sorted by row, kJoin of them are under way at a time.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kCombineThreads) void combine_row_grads(CombineArgs a) {
+    using U = Unit<T, VEC>;
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kCombineThreads + threadIdx.x;
+    if (i >= a.rows * a.units) return;
+    const int64_t p = i / a.units, c = (i - p * a.units) * U::kN, end = a.offsets[p + 1];
+    float acc[U::kN] = {};
+    for (int64_t q0 = a.offsets[p]; q0 < end; q0 += kJoin) {
+        int64_t e[kJoin];
+        U g[kJoin];
+        float w[kJoin];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) e[j] = a.order[min(q0 + j, end - 1)];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            w[j] = a.weights[e[j]];
+            g[j].load(a.grad + (e[j] / a.fanout * a.M + c) * (int64_t)sizeof(T));
+        }
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+#pragma unroll
+            for (int n = 0; n < U::kN; ++n)
+                if (q0 + j < end) acc[n] = fmaf(w[j], (float)g[j].v[n], acc[n]);
+    }
+    U o;
+#pragma unroll
+    for (int n = 0; n < U::kN; ++n) o.v[n] = (T)acc[n];
+    o.store(a.out + (p * a.M + c) * (int64_t)sizeof(T));
 }
 
 template <typename T>
@@ -129,6 +163,11 @@ int combine_launch(CombineArgs a, bool grads, bool vec, hipStream_t st) {
     else if (grads) timed_launch_ggl(true, (combine_grads<T, false>), grid, dim3(kCombineThreads), 0, st, a);
     else if (vec) timed_launch_ggl(true, (combine_rows<T, true>), grid, dim3(kCombineThreads), 0, st, a);
     else timed_launch_ggl(true, (combine_rows<T, false>), grid, dim3(kCombineThreads), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
+    if (!a.offsets) return SEGRED_OK;
+    if (!tile_grid((a.rows * a.units + kCombineThreads - 1) / kCombineThreads, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (vec) timed_launch_ggl(true, (combine_row_grads<T, true>), grid, dim3(kCombineThreads), 0, st, a);
+    else timed_launch_ggl(true, (combine_row_grads<T, false>), grid, dim3(kCombineThreads), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
@@ -154,6 +193,19 @@ int combine_check(const void *values, int32_t dtype, int64_t m, int64_t rows, co
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (too_large(rows, m, 4) || too_large(tokens, m, 4) || too_large(tokens, fanout, 8)) return SEGRED_ERR_INVALID_ARGUMENT;
     return SEGRED_OK;
+}
+
+// The entries sorted by row, and what sorts them.
+struct CombineSpace {
+    size_t entries, offsets, group;  // bytes of each part; entries: of one array
+};
+CombineSpace combine_space(int64_t entries, int64_t rows) {
+    auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
+    return {up((size_t)entries * 8), up(((size_t)rows + 1) * 8), (size_t)segred_group_workspace(entries, rows)};
+}
+// Sizes that segred_group takes (the counts are not negative).
+bool combine_sortable(int64_t rows, int64_t tokens, int64_t fanout) {
+    return rows < INT32_MAX && !too_large(tokens, fanout, 8) && tokens * fanout <= INT32_MAX;
 }
 
 }  // namespace segred
@@ -197,5 +249,55 @@ extern "C" int segred_combine_grad(const void *grad, const void *values, int32_t
     a.M = m;
     a.out = static_cast<char *>(grad_values);
     a.grad_weights = grad_weights;
+    return combine_call(a, dtype, true, stream);
+}
+
+extern "C" int64_t segred_combine_grad_repeated_workspace(int64_t rows, int64_t tokens, int64_t fanout) {
+    if (rows < 1 || tokens < 1 || fanout < 1 || !combine_sortable(rows, tokens, fanout)) return 0;
+    const CombineSpace s = combine_space(tokens * fanout, rows);
+    return (int64_t)(2 * s.entries + s.offsets + s.group);
+}
+
+extern "C" int segred_combine_grad_repeated(const void *grad, const void *values, int32_t dtype, int64_t m, int64_t rows,
+                                            const int64_t *position, const float *weights, int64_t tokens,
+                                            int64_t fanout, void *grad_values, float *grad_weights, void *workspace,
+                                            int64_t workspace_bytes, hipStream_t stream) {
+    int rc = combine_check(values, dtype, m, rows, position, weights, tokens, fanout, grad_values);
+    if (rc != SEGRED_OK) return rc;
+    if (!aligned(grad, float_size(dtype)) || !aligned(grad_weights, 4) || !aligned(workspace, 16))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!combine_sortable(rows, tokens, fanout)) return SEGRED_ERR_UNSUPPORTED;
+    const bool some = tokens > 0 && fanout > 0;
+    if ((some && (!grad || !grad_weights)) || (rows > 0 && !grad_values)) return SEGRED_ERR_INVALID_ARGUMENT;
+    const int64_t need = segred_combine_grad_repeated_workspace(rows, tokens, fanout);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SEGRED_ERR_INVALID_ARGUMENT;
+    CombineArgs a{};
+    a.values = static_cast<const char *>(values);
+    a.grad = static_cast<const char *>(grad);
+    a.position = position;
+    a.weights = weights;
+    a.rows = rows;
+    a.tokens = tokens;
+    a.fanout = fanout;
+    a.M = m;
+    a.out = static_cast<char *>(grad_values);
+    a.grad_weights = grad_weights;
+    if (!some) {  // the sum over no entries: segred_combine of `rows` tokens without an entry
+        if (rows == 0) return SEGRED_OK;
+        a.tokens = rows;
+        a.fanout = 0;
+        return combine_call(a, dtype, false, stream);
+    }
+    if (rows > 0) {
+        const CombineSpace s = combine_space(tokens * fanout, rows);
+        char *w = static_cast<char *>(workspace);
+        int64_t *order = reinterpret_cast<int64_t *>(w), *place = reinterpret_cast<int64_t *>(w + s.entries);
+        int64_t *offsets = reinterpret_cast<int64_t *>(w + 2 * s.entries);
+        rc = segred_group(position, tokens * fanout, 1, rows, order, place, offsets, w + 2 * s.entries + s.offsets,
+                          (int64_t)s.group, stream);
+        if (rc != SEGRED_OK) return rc;
+        a.order = order;
+        a.offsets = offsets;
+    }
     return combine_call(a, dtype, true, stream);
 }

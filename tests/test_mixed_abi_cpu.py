@@ -36,3 +36,27 @@ def _adapter(**kw):
 ])
 def test_adapter_argument_checks(args, expect):
     assert _lib().segred_adapter_mixed(*args, None) == expect
+
+
+def _repeated(**kw):
+    return _args(dict(grad=FAKE, values=FAKE, dtype=3, m=64, rows=10, position=FAKE, weights=FAKE, tokens=5, fanout=2,
+                      grad_values=FAKE, grad_weights=FAKE, work=FAKE, bytes=2 ** 30), kw)
+
+
+@pytest.mark.parametrize("args,expect", [
+    (_repeated(dtype=5), 1), (_repeated(dtype=1), 2), (_repeated(m=0), 1), (_repeated(rows=-1), 1),
+    (_repeated(tokens=-1), 1), (_repeated(fanout=-1), 1), (_repeated(grad=None), 1), (_repeated(values=None), 1),
+    (_repeated(position=None), 1), (_repeated(weights=None), 1), (_repeated(grad_values=None), 1),
+    (_repeated(grad_weights=None), 1), (_repeated(grad=FAKE + 1), 1), (_repeated(grad_weights=FAKE + 2), 1),
+    (_repeated(work=None), 1), (_repeated(bytes=100), 1), (_repeated(work=FAKE + 8), 1),
+    (_repeated(rows=2 ** 31 - 1), 2), (_repeated(tokens=2 ** 30, fanout=2), 2), (_repeated(rows=0, tokens=0), 0),
+])
+def test_repeated_rows_argument_checks(args, expect):
+    assert _lib().segred_combine_grad_repeated(*args, None) == expect
+
+
+def test_repeated_rows_workspace():
+    lib = _lib()
+    assert lib.segred_combine_grad_repeated_workspace(0, 5, 2) == 0
+    assert lib.segred_combine_grad_repeated_workspace(2 ** 31, 5, 2) == 0
+    assert lib.segred_combine_grad_repeated_workspace(100, 5, 2) >= 2 * 80 + 101 * 8
