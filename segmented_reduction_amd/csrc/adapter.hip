@@ -712,36 +712,6 @@ int adapter_few_launch(AdapterArgs a, bool b_col, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
-// The infinities and NaN of a stored tile again, element by element, so that
-// only what the row's own adapter makes of it remains.
-template <typename T, bool B_COL, int BN, int THREADS>
-__device__ __forceinline__ void own_specials(const AdapterArgs &a, int64_t row0, int rows, int64_t n0, const int *s_ids) {
-#pragma unroll 1
-    for (int i = threadIdx.x; i < rows * (BN / 4); i += THREADS) {
-        const int r = i / (BN / 4);
-        const int64_t row = row0 + r, n = n0 + i % (BN / 4) * 4;
-        T *out = reinterpret_cast<T *>(a.out) + row * a.M + n;
-        bool any = false;
-        for (int j = 0; j < 4 && n + j < a.M; ++j) any = any || !((float)out[j] * 0.f == 0.f);
-        if (!any) continue;
-        const f32x4 q = adapter_quad<T, B_COL>(a, row, s_ids[r], n);
-#pragma unroll 1
-        for (int j = 0; j < 4 && n + j < a.M; ++j) {
-            if ((float)out[j] * 0.f == 0.f) continue;
-            float sum = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
-            if (sum == sum) {
-                const T *x = reinterpret_cast<const T *>(a.values) + row * a.K;
-                const T *w = reinterpret_cast<const T *>(a.weights) + (B_COL ? n + j : (n + j) * a.K);
-                float main = 0.f;
-#pragma unroll 1
-                for (int64_t k = 0; k < a.K; ++k) main = fmaf((float)x[k], (float)w[B_COL ? k * a.M : k], main);
-                sum += main;
-            }
-            out[j] = (T)sum;
-        }
-    }
-}
-
 // Many rows: AH * 128 rows x 256 columns per workgroup, in phases (16-bit
 // types, whole units).
 template <typename T, int AH, bool B_COL>
@@ -886,9 +856,11 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     if (extra > 0) {
         phase_steps<T, AH, B_COL>(acc, lds, extra, wave, lane, fetch_u, fetch_second, products);
         // Where rows differ in their adapter, an infinity or a NaN of one has
-        // reached the rows of others.  (Parts of their own as in
-        // adapter_products do not fit the registers; looking for these values
-        // in every step took 5% of a call.)
+        // reached the rows of others, and the tile is computed again in those of
+        // 64 x 128, which keep parts of their own.  (Such parts do not fit the
+        // registers here; looking for these values in every step took 5% of a
+        // call.)  6,000 rows of 12 requests beside 4,096 x 2,048, rank 64: 130 us,
+        // and 380 where one of eight adapters is NaN.
         bool mixed = met > 1;
         for (int r = lane; r < rows; r += 64) mixed = mixed || s_ids[r] < 0;
         float bad = 0.f;
@@ -918,8 +890,15 @@ __global__ __launch_bounds__(kPhaseThreads) void adapter_main_many(AdapterArgs a
     __syncthreads();
     tile_out<T, BM, BN, kPhaseThreads>(lds, reinterpret_cast<T *>(a.out) + row0 * a.M, rows, n0, a.M, a.vec != 0);
     if (*s_count < 0) {
-        __syncthreads();
-        own_specials<T, B_COL, BN, kPhaseThreads>(a, row0, rows, n0, s_ids);
+        using Again = AdapterTile<T, 64, 128, 2, 4, 3, B_COL, true>;
+        static_assert(Again::kThreads == kPhaseThreads && Again::kLds <= kPhaseLds, "the same workgroup and LDS");
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 64)
+#pragma unroll 1
+            for (int c = 0; c < BN && n0 + c < a.M; c += 128) {
+                __syncthreads();
+                Again::run(a, row0 + r, min(64, rows - r), n0 + c, met, s_ids + r, s_list, lds, wave, lane);
+            }
     }
 }
 
