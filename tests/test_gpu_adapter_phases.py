@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests import ragged_util as ru
+from tests.test_gpu_adapter import _check
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,22 @@ def cuts(rows, segments, seed):
 
 # (rows, k, m): 44 * 3 tiles of 128 rows in either direction; 17 * 8; and 48 * 8 forwards, where 256 rows save a round
 SIZES = [(5600, 648, 640), (2100, 1800, 2048), (6100, 264, 2048)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("rows,k,m", SIZES)
+@pytest.mark.parametrize("r", [33, 40])
+def test_large_tiles(kind, transpose, rows, k, m, r):
+    """Requests that end inside tiles, some without an adapter, ranks of more than one step, the low-rank rows too."""
+    _check(kind, cuts(rows, 15, rows), k, m, r, transpose, count=4, which=torch.arange(15) % 6 - 1, seed=r)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_one_adapter_for_all_and_none(kind, transpose):
+    _check(kind, [5700], 648, 640, 16, transpose, which=torch.tensor([2]))
+    _check(kind, [2000, 3700], 648, 640, 16, transpose, which=torch.tensor([-1, 7]))
 
 
 def specials(kind, transpose, rows, k, m, r, seed):
