@@ -170,7 +170,9 @@ __global__ __launch_bounds__(64 * NW) void adapter_low(AdapterArgs a) {
             bf16x4 hi, lo;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                hi[j] = (__bf16)sum[j];
+                // a float above the largest bf16 would round to an infinity
+                constexpr float kMost = 0x1.fep127f;
+                hi[j] = (__bf16)(sum[j] * 0.f == 0.f ? fminf(fmaxf(sum[j], -kMost), kMost) : sum[j]);
                 const float rest = sum[j] - (float)hi[j];  // NaN beside an infinity
                 lo[j] = (__bf16)(rest == rest ? rest : 0.f);
             }
