@@ -462,7 +462,7 @@ int segred_matmul(const void *values, int32_t dtype, int64_t k, const int64_t *r
  *                 weights [k, m]; swap left and right for [m, k].)
  *   workspace     segred_outer_workspace(k, m, num_segments, num_rows) bytes:
  *                 few long segments are cut into pieces whose sums are added
- *                 in row order by a second kernel.
+ *                 in a fixed order by a second kernel.
  *
  * Errors: as segred_matmul, and SEGRED_ERR_INVALID_ARGUMENT for another
  * out_dtype or a workspace that is missing or too small.
@@ -597,7 +597,8 @@ int64_t segred_combine_grad_repeated_workspace(int64_t rows, int64_t tokens, int
  * The low-rank rows enter the second product in float32, or as the sum of two
  * bf16 (2^-17 relative) for the 16-bit types.
  * An infinity or a NaN of a row reaches that row alone, one of an adapter its
- * rows alone.  (In the 16-bit types the adapter's part of such a row may be a
+ * rows alone (tiles that mix the two are computed again, which takes such a call
+ * to two or three times its time).  (In the 16-bit types the adapter's part of such a row may be a
  * NaN where the formula gives an infinity.)
  *
  * Errors: as segred_matmul; also SEGRED_ERR_INVALID_ARGUMENT for rank < 1,

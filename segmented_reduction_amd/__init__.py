@@ -23,6 +23,10 @@ Operators over ragged groups of rows (float32, bfloat16, float16):
     dh, dprob = combine_grad(dy, h, position, prob)
     dw = outer(x, dh, offsets, left_rows=order)        # the gradient of the weights
     y = adapter(x, weights, offsets, which, down, up)  # shared projection + low-rank adapter per request
+
+No call records a gradient: a result does not require one whatever its inputs
+do, and a model that is trained through these operators calls the gradients'
+operators itself, as above (torch.autograd.Function is the place).
 """
 from __future__ import annotations
 

@@ -966,13 +966,32 @@ int adapter_dispatch(const AdapterArgs &a, bool b_col, bool low_direct, bool mai
     // for two tiles and enough of them.  bfloat16 beside 4,096 x 256, times of
     // 16 and of 64: 45 us and 48 for 6,000 rows of rank 16; of rank 64, 41 and
     // 43 for 2,048 rows, 48 and 45 for 4,096, 55 and 49 for 6,000.  (Tiles of 16
-    // rows by 4 waves, of which a CU holds two; with 8 waves the latter take 60.)
+    // rows by 4 waves, of which a CU holds two; with 8 waves the latter take 60,
+    // and calls of 1 to 128 rows the same within 0.8 us.)
     const bool tall = sizeof(T) == 2 && a.blocks > 1 && (a.N / 64 + a.S / 2) * a.blocks >= kAdapterTall;
     int rc;
     if (!low_direct) rc = adapter_low_launch<T, 1, false>(a, b_col, st);
     else if (tall) rc = adapter_low_launch<T, sizeof(T) == 2 ? 4 : 1, true>(a, b_col, st);
     else rc = adapter_low_launch<T, 1, true>(a, b_col, st);
     if (rc != SEGRED_OK) return rc;
+    // Up to 128 rows waves split the contraction, in blocks of 16 to 64 rows by as
+    // many waves as there is LDS for.  Times in us, every row an adapter of 32, of
+    // blocks x waves x stages against tiles of 64 x 64:
+    //
+    //   rows                                16     32     48     64    128    129
+    //   bfloat16, 4,096 x 4,096, rank 16
+    //     1x4x4, 1x8x4                17.2/16.9  19/22
+    //     2x4x4, 2x8x3                18.3/17.4 18.4/17.9  27/25  27/25
+    //     3x4x4, 3x8x2                19.6/18.4 19.8/19.2 20.1/19.8  30/27  40/38  40/37
+    //     4x4x3, 4x8x2                20.8/18.8 21.2/19.6 21.1/20.3 20.6/21.1 30.8/30.9 42/39
+    //     64 x 64                       44.9   55.7   55.7   55.9   56.2   56.5
+    //   the same, transposed
+    //     4x4x3, 4x8x2                30.6/28.9 30.1/29.4 31.3/30.7 33.7/31.9 54/50  69/65
+    //     64 x 64                       49.5   61.4   61.0   61.1   61.4   61.5
+    //   float, 2,048 x 2,048, rank 16
+    //     1x4x4, 1x8x4                21.3/19.5 21.4/19.8
+    //     4x4x3, 4x8x2                29.1/27.7 29.0/27.5 29.0/27.8 28.5/27.8 29.7/28.6 46/43
+    //     64 x 64                       78.4   95.4   95.9   95.5   94.8   95.2
     if (main_direct && a.N <= kAdapterFew) {
         if (a.N <= 16) return adapter_few_launch<T, 1, 8, 4>(a, b_col, st);
         if (a.N <= 32) return adapter_few_launch<T, 2, 8, 3>(a, b_col, st);

@@ -362,13 +362,17 @@ __global__ __launch_bounds__(kJoinThreads) void outer_join(OuterArgs a) {
     }
 }
 
-// Tile and rows of a slot.  Where the segments' tiles of 128 x 128 give every
-// CU one, a slot is a whole segment; else the tiles are smaller and the
-// segments are cut into slots of at least kSlotRows rows, as many as the
-// device holds workgroups at a time (3 of 64 x 128 or 4 of 64 x 64 a CU).
+// Tile and rows of a slot.  Where the segments' tiles of 128 x 128 would give
+// every CU one, or there is a segment for every CU, a slot is a whole segment
+// (in tiles of that size for 16-bit types, of 64 x 128 in bf16 parts).  Else the
+// tiles are 64 x 64, or 64 x 128 where the left side has no more than 64 columns
+// and the right side more (the mirrored case, 96 x 64, reads its right side
+// twice: there is no tile of 128 x 64), and the segments are cut into slots of at
+// least kSlotRows rows, as many as the device holds workgroups at a time (3 of
+// 64 x 128 or 4 of 64 x 64 a CU).
 struct OuterPlan {
     bool small;  // 64 x 64, or
-    bool wide;   // 64 x 128, where that holds the whole sum
+    bool wide;   // 64 x 128
     int64_t step;
 };
 constexpr int64_t kCus = 256, kSlotRows = 256;
