@@ -710,7 +710,7 @@ def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, 
         _beside(dev, "out", out)
         if out.shape != (n, give) or out.dtype != values.dtype:
             raise ValueError("out must be [N, outputs] of the dtype of values")
-    low_dtype = values.dtype if want_low is True or not want_low else want_low
+    low_dtype = want_low if isinstance(want_low, torch.dtype) else values.dtype
     if low_dtype not in (values.dtype, torch.float32):
         raise TypeError("want_low must be float32 or the dtype of values")
     low = torch.empty((n, r), dtype=low_dtype, device=device) if want_low else None

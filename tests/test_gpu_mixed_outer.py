@@ -160,6 +160,7 @@ def test_low_rank_rows_of_a_16_bit_call_as_asked():
         same, wide = sr().adapter(*args, want_low=torch.float32)
         named = sr().adapter(*args, want_low=t)[1]
         assert low.dtype == t and torch.equal(out, same) and torch.equal(low, wide.to(t)) and torch.equal(low, named)
+        assert torch.equal(sr().adapter(*args, want_low=1)[1], low) and torch.equal(sr().adapter(*args, want_low=0), out)
         assert not wide[40:70].any() and not low[40:70].any()
 
 
