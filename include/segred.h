@@ -31,6 +31,11 @@ enum segred_dtype { SEGRED_U32 = 0, SEGRED_I32 = 1, SEGRED_F32 = 2, SEGRED_BF16 
 /* Reductions.  MEAN is float32 only. */
 enum segred_op { SEGRED_SUM = 0, SEGRED_MIN = 1, SEGRED_MAX = 2, SEGRED_MEAN = 3 };
 
+/* Activations of segred_gated: x / (1 + exp(-x)); x Phi(x), Phi the normal
+ * distribution; x / (1 + exp(-2 y)) with y = sqrt(2 / pi) (x + 0.044715 x^3),
+ * i.e. the tanh form of the one before; max(x, 0). */
+enum segred_activation { SEGRED_SILU = 0, SEGRED_GELU = 1, SEGRED_GELU_TANH = 2, SEGRED_RELU = 3 };
+
 /* Return codes. */
 enum segred_status {
     SEGRED_OK = 0,
@@ -624,6 +629,140 @@ int segred_adapter_mixed(const void *values, int32_t dtype, int64_t k, const voi
                          const void *down, const void *up, const float *scale, int64_t adapters, int64_t rank,
                          int32_t transpose, void *out, void *low, int32_t low_dtype, void *workspace,
                          int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * segred_gated -- the gated pair of projections of each segment's rows: with
+ * g = x G[s]^T and u = x U[s]^T, out = act(g) u.
+ *
+ *   values, rows, value_rows, offsets, num_rows  as segred_matmul.
+ *   weights     [num_segments, 2 m, k] of type `dtype`: the m rows of G[s], then
+ *               those of U[s].
+ *   activation  one of segred_activation.
+ *   out         [num_rows, m]; rows of no segment are left as they were.
+ *
+ * g and u are sums in float32 and not rounded before their product is.
+ * Errors: as segred_matmul; also SEGRED_ERR_INVALID_ARGUMENT for an unknown
+ * activation and SEGRED_ERR_UNSUPPORTED for m above 2^23.
+ */
+int segred_gated(const void *values, int32_t dtype, int64_t k, const int64_t *rows, int64_t value_rows,
+                 const void *weights, int64_t m, int32_t activation, const int64_t *offsets, int64_t num_segments,
+                 int64_t num_rows, void *out, hipStream_t stream);
+
+/*
+ * segred_gated_grad -- the gradient of segred_gated's projections (g, u) from
+ * that of its output: (grad u act'(g), grad act(g)).  g and u are formed again,
+ * so nothing need be kept from the forward call.  The gradient of the (gathered)
+ * rows is segred_matmul of this result with `weights` (transpose = 0) and that of
+ * `weights` segred_outer of it and `values`.
+ *
+ *   grad  [num_rows, m] of type `dtype`; rows of no segment are not read.
+ *   out   [num_rows, 2 m]: the gradient of g, then that of u; rows of no segment
+ *         are left as they were.
+ *   the others and the errors as segred_gated.
+ */
+int segred_gated_grad(const void *grad, const void *values, int32_t dtype, int64_t k, const int64_t *rows,
+                      int64_t value_rows, const void *weights, int64_t m, int32_t activation,
+                      const int64_t *offsets, int64_t num_segments, int64_t num_rows, void *out, hipStream_t stream);
+
+/*
+ * segred_norm -- layer norm of each row: with m its mean and v the mean of
+ * (x - m)^2, out = (x - m) / sqrt(v + eps) * weight + bias.  With center = 0 m is
+ * 0 (the norm by the root mean square).
+ *
+ *   values        [rows, k] of type `dtype`.
+ *   weight, bias  [k] of type `weight_dtype` (`dtype` or SEGRED_F32), or NULL: ones
+ *                 and zeros.
+ *   eps           finite, >= 0.  (With 0 a constant row gives NaN, 0 / 0.)
+ *   out           [rows, k]; may be `values` itself.
+ *
+ * Errors: SEGRED_ERR_INVALID_ARGUMENT for an unknown dtype, another weight_dtype,
+ * k < 1, rows < 0, an eps that is negative, infinite or NaN, a NULL pointer that
+ * is needed, misalignment (an element), sizes past INT64_MAX bytes.
+ * SEGRED_ERR_UNSUPPORTED for integer types or k above 2^24.  SEGRED_ERR_HIP if a
+ * launch fails.
+ */
+int segred_norm(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weight, const void *bias,
+                int32_t weight_dtype, float eps, int32_t center, void *out, hipStream_t stream);
+
+/*
+ * segred_norm_grad -- the gradients of segred_norm from that of its output:
+ * of the rows, and, added up over the rows in a fixed order, of weight and bias.
+ * The rows' statistics are found again from `values`.
+ *
+ *   grad         [rows, k] of type `dtype`.
+ *   grad_values  [rows, k] of type `dtype`.
+ *   grad_weight, grad_bias  [k] of type `weight_dtype`, or NULL: not asked for.
+ *                Written also for rows = 0 (zeros).
+ *   workspace    segred_norm_grad_workspace(k, rows) bytes where either is asked for.
+ *   the others and the errors as segred_norm, also
+ *   SEGRED_ERR_INVALID_ARGUMENT for a workspace that is missing or too small.
+ */
+int segred_norm_grad(const void *grad, const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weight,
+                     int32_t weight_dtype, float eps, int32_t center, void *grad_values, void *grad_weight,
+                     void *grad_bias, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t segred_norm_grad_workspace(int64_t k, int64_t rows);
+
+/*
+ * segred_cross_entropy -- the softmax cross entropy of each row against the
+ * weights of a vocabulary, without its logits ever being kept: with
+ * z_v = scale <x, W_v>, targets v_j of probability t_j and s = sum of the t_j,
+ * loss = s lse - sum of t_j z_(v_j), lse = log sum over v of exp z_v.  (One target
+ * of probability 1: the usual loss.  A teacher's most likely entries with their
+ * probabilities: the distillation loss up to the teacher's own entropy.)
+ *
+ *   values   [rows, k] of type `dtype`.
+ *   weights  W [vocab, k] of type `dtype`.
+ *   target   int64 [rows, picks].  An entry outside [0, vocab) takes no part; a row
+ *            without any has loss 0 and no gradient, whatever its values are.
+ *            One named twice in a row counts twice.
+ *   probs    float32 [rows, picks], or NULL: 1 each.  Need not add up to 1.
+ *   scale    finite, > 0.
+ *   loss, lse  float32 [rows].
+ *   picked   float32 [rows, picks]: the targets' logits z, 0 for entries that take
+ *            no part; the gradient call reads them and lse.
+ *   workspace  segred_cross_entropy_workspace(dtype, k, rows, vocab) bytes (8 for
+ *            every 64 logits).
+ *
+ * Logits are sums in float32 and are not rounded.  A row with an infinite
+ * positive logit, or a NaN, has NaN.
+ *
+ * Errors: SEGRED_ERR_INVALID_ARGUMENT for an unknown dtype, k, vocab or picks < 1,
+ * rows < 0, a scale that is not positive and finite, a NULL pointer that is
+ * needed, misalignment (an element, 8 bytes for target, 16 for the workspace), a
+ * workspace that is missing or too small.  SEGRED_ERR_UNSUPPORTED for integer
+ * types, k above 2^24, vocab above 2^30, rows above 2^31 or picks above 2^20.
+ * SEGRED_ERR_HIP if a launch fails.
+ */
+int segred_cross_entropy(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights,
+                         int64_t vocab, const int64_t *target, const float *probs, int64_t picks, float scale,
+                         float *loss, float *lse, float *picked, void *workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+int64_t segred_cross_entropy_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab);
+
+/*
+ * segred_cross_entropy_grad -- the gradients of segred_cross_entropy's loss, by
+ * pieces of the vocabulary: the logits of a piece are formed again, their gradient
+ * dz = grad scale (s exp(z - lse) - t) is rounded to `dtype` once, and its products
+ * with the weights and the rows are added up in float32.  In float16 dz is scaled
+ * by a power of two that all rows share, so that small probabilities are not
+ * lost.
+ *
+ *   grad          float32 [rows], the gradient of the loss.
+ *   lse, picked   of segred_cross_entropy for the same arguments.
+ *   grad_values   [rows, k] of type `dtype`, or NULL: not asked for.
+ *   grad_weights  [vocab, k] of type grad_weights_dtype (`dtype` or SEGRED_F32), or
+ *                 NULL: not asked for.  Every element is written.
+ *   workspace     segred_cross_entropy_grad_workspace(dtype, k, rows, vocab) bytes:
+ *                 a piece of dz (256 MiB, or 4,096 entries where these take more)
+ *                 and the sums of grad_values in float32.
+ *   the others and the errors as segred_cross_entropy.
+ */
+int segred_cross_entropy_grad(const float *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
+                              const void *weights, int64_t vocab, const int64_t *target, const float *probs,
+                              int64_t picks, float scale, const float *lse, const float *picked, void *grad_values,
+                              void *grad_weights, int32_t grad_weights_dtype, void *workspace, int64_t workspace_bytes,
+                              hipStream_t stream);
+int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab);
 
 /* Static, host-side description of a status code (never NULL). */
 const char *segred_status_string(int status);

@@ -23,6 +23,15 @@ Operators over ragged groups of rows (float32, bfloat16, float16):
     dh, dprob = combine_grad(dy, h, position, prob)
     dw = outer(x, dh, offsets, left_rows=order)        # the gradient of the weights
     y = adapter(x, weights, offsets, which, down, up)  # shared projection + low-rank adapter per request
+    h = gated(x, weights, offsets, rows=order)         # act(x gate^T) * (x up^T) per group
+    dpair = gated_grad(dh, x, weights, offsets, rows=order)   # of both projections; then matmul and outer
+
+Around them in a training step:
+
+    y = norm(x, weight, bias)                          # layer norm of rows, or by the root mean square
+    dx, dweight, dbias = norm_grad(dy, x, weight, want_bias=True)
+    loss, lse, picked = cross_entropy(x, vocabulary, target)  # the logits are never kept
+    dx, dvocabulary = cross_entropy_grad(dloss, x, vocabulary, target, lse, picked)
 
 No call records a gradient: a result does not require one whatever its inputs
 do, and a model that is trained through these operators calls the gradients'
@@ -42,6 +51,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libsegred.so")
 SUM, MIN, MAX, MEAN = 0, 1, 2, 3
 OPS = {"sum": SUM, "min": MIN, "max": MAX, "mean": MEAN}
 DTYPES = {torch.uint32: 0, torch.int32: 1, torch.float32: 2}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 FLOATS = {torch.float32: 2, torch.bfloat16: 3, torch.float16: 4}  # the products and combine calls
 STATUS = {0: "SEGRED_OK", 1: "SEGRED_ERR_INVALID_ARGUMENT", 2: "SEGRED_ERR_UNSUPPORTED",
           3: "SEGRED_ERR_OUT_OF_MEMORY", 4: "SEGRED_ERR_HIP", 5: "SEGRED_ERR_SCRATCH_LIMIT"}
@@ -120,6 +130,26 @@ def library(path: str | None = None):
             lib.segred_adapter_mixed.restype = ctypes.c_int
             lib.segred_adapter_workspace.argtypes = [i32, i64, i64, i64, i64]
             lib.segred_adapter_workspace.restype = i64
+            f32 = ctypes.c_float
+            lib.segred_gated.argtypes = [vp, i32, i64, vp, i64, vp, i64, i32, vp, i64, i64, vp, vp]
+            lib.segred_gated.restype = ctypes.c_int
+            lib.segred_gated_grad.argtypes = [vp, vp, i32, i64, vp, i64, vp, i64, i32, vp, i64, i64, vp, vp]
+            lib.segred_gated_grad.restype = ctypes.c_int
+            lib.segred_norm.argtypes = [vp, i32, i64, i64, vp, vp, i32, f32, i32, vp, vp]
+            lib.segred_norm.restype = ctypes.c_int
+            lib.segred_norm_grad.argtypes = [vp, vp, i32, i64, i64, vp, i32, f32, i32, vp, vp, vp, vp, i64, vp]
+            lib.segred_norm_grad.restype = ctypes.c_int
+            lib.segred_norm_grad_workspace.argtypes = [i64, i64]
+            lib.segred_norm_grad_workspace.restype = i64
+            lib.segred_cross_entropy.argtypes = [vp, i32, i64, i64, vp, i64, vp, vp, i64, f32, vp, vp, vp, vp, i64, vp]
+            lib.segred_cross_entropy.restype = ctypes.c_int
+            lib.segred_cross_entropy_workspace.argtypes = [i32, i64, i64, i64]
+            lib.segred_cross_entropy_workspace.restype = i64
+            lib.segred_cross_entropy_grad.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, i64, f32, vp, vp, vp, vp,
+                                                      i32, vp, i64, vp]
+            lib.segred_cross_entropy_grad.restype = ctypes.c_int
+            lib.segred_cross_entropy_grad_workspace.argtypes = [i32, i64, i64, i64]
+            lib.segred_cross_entropy_grad_workspace.restype = i64
             lib.segred_status_string.argtypes = [ctypes.c_int]
             lib.segred_status_string.restype = ctypes.c_char_p
             lib.segred_set_shares.argtypes = [i64]
@@ -722,6 +752,241 @@ def adapter(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, 
             scale.data_ptr() if scale is not None else None, count, r, 1 if transpose else 0, out.data_ptr(),
             low.data_ptr() if want_low else None, FLOATS[low_dtype], work.data_ptr() if need else None, need)
     return (out, low) if want_low else out
+
+
+def _check_gated(values, weights, offsets, activation, rows):
+    """(GPU index, dtype code, activation code, S, N, K, M) of the tensors that both gated calls take."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    dev, code = _floats("values", values)
+    if weights.dtype != values.dtype:
+        raise TypeError("weights must have the dtype of values")
+    _beside(dev, "weights", weights)
+    _rows(dev, "offsets", offsets)
+    n, k = values.shape
+    s = offsets.shape[0] - 1
+    if rows is not None:
+        _rows(dev, "rows", rows)
+        n = rows.shape[0]
+    if s < 0 or weights.dim() != 3 or weights.shape[0] != s or weights.shape[1] % 2 or weights.shape[2] != k:
+        raise ValueError("weights must be [S, 2 * M, K] with S + 1 offsets and the features of values")
+    return dev, code, act, s, n, k, weights.shape[1] // 2
+
+
+def gated(values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *, activation: str = "silu",
+          rows: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated pair of projections of each segment's rows (segred_gated):
+    ``out[r] = act(values[r] @ gate[s].T) * (values[r] @ up[s].T)`` for the rows r
+    of segment s, ``gate[s], up[s] = weights[s, :M], weights[s, M:]``.
+
+    values      [N, K] float32 / bfloat16 / float16 on a GPU, contiguous.
+    weights     [S, 2 * M, K] of the same type.
+    offsets     int64 [S + 1] on the same GPU.
+    activation  "silu", "gelu" (by the normal distribution), "gelu_tanh" or "relu".
+    rows        optional int64 [R]: row r is then made from ``values[rows[r]]``, as
+                in ``matmul``.
+    Returns out [N or R, M]; rows of no segment are left as they were
+    (uninitialised when ``out`` is not given).
+    """
+    dev, code, act, s, n, k, m = _check_gated(values, weights, offsets, activation, rows)
+    if out is None:
+        out = torch.empty((n, m), dtype=values.dtype, device=values.device)
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (n, m) or out.dtype != values.dtype:
+            raise ValueError("out must be [rows, M] of the dtype of values")
+    _launch((_lib or library()).segred_gated, "segred_gated", dev, values.data_ptr(), code, k,
+            rows.data_ptr() if rows is not None else None, values.shape[0], weights.data_ptr(), m, act,
+            offsets.data_ptr(), s, n, out.data_ptr())
+    return out
+
+
+def gated_grad(grad: torch.Tensor, values: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, *,
+               activation: str = "silu", rows: torch.Tensor | None = None,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``gated``'s two projections from that of its output,
+    ``grad`` [N or R, M] (segred_gated_grad): [N or R, 2 * M], the gate's, then the
+    other's.  Both projections are formed again from ``values`` and ``weights``.
+
+    ``matmul(pair, weights, offsets)`` is then the gradient of the (gathered)
+    rows, ``outer(pair, values, offsets, right_rows=rows)`` that of the weights.
+    Rows of no segment are left as they were.
+    """
+    dev, code, act, s, n, k, m = _check_gated(values, weights, offsets, activation, rows)
+    _beside(dev, "grad", grad)
+    if grad.shape != (n, m) or grad.dtype != values.dtype:
+        raise ValueError("grad must be [rows, M] of the dtype of values")
+    if out is None:
+        out = torch.empty((n, 2 * m), dtype=values.dtype, device=values.device)
+    else:
+        _beside(dev, "out", out)
+        if out.shape != (n, 2 * m) or out.dtype != values.dtype:
+            raise ValueError("out must be [rows, 2 * M] of the dtype of values")
+    _launch((_lib or library()).segred_gated_grad, "segred_gated_grad", dev, grad.data_ptr(), values.data_ptr(), code, k,
+            rows.data_ptr() if rows is not None else None, values.shape[0], weights.data_ptr(), m, act,
+            offsets.data_ptr(), s, n, out.data_ptr())
+    return out
+
+
+def _check_norm(values, weight, bias):
+    """(GPU index, dtype code, type of the parameters) of the tensors that both norm calls take."""
+    dev, code = _floats("values", values)
+    kind = values.dtype if weight is None and bias is None else (weight if weight is not None else bias).dtype
+    if kind not in (values.dtype, torch.float32):
+        raise TypeError("weight and bias must be float32 or have the dtype of values")
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is None:
+            continue
+        _beside(dev, name, p)
+        if p.dtype != kind:
+            raise TypeError("weight and bias must have one dtype")
+        if p.shape != (values.shape[1],):
+            raise ValueError(f"{name} must have one entry per feature of values")
+    return dev, code, kind
+
+
+def norm(values: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+         eps: float = 1e-5, center: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Layer norm of each row (segred_norm): ``(x - mean) / sqrt(mean((x - mean)**2)
+    + eps) * weight + bias``; without ``center`` the mean is taken as 0 (the norm by
+    the root mean square).
+
+    values  [N, K] float32 / bfloat16 / float16 on a GPU, contiguous.
+    weight, bias  optional [K], both float32 or both of the values' type.
+    Returns out [N, K] of the values' type; ``out`` may be ``values`` itself.
+    """
+    dev, code, kind = _check_norm(values, weight, bias)
+    n, k = values.shape
+    if out is None:
+        out = torch.empty_like(values)
+    else:
+        _beside(dev, "out", out)
+        if out.shape != values.shape or out.dtype != values.dtype:
+            raise ValueError("out must have the shape and dtype of values")
+    _launch((_lib or library()).segred_norm, "segred_norm", dev, values.data_ptr(), code, k, n,
+            weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None,
+            FLOATS[kind], eps, 1 if center else 0, out.data_ptr())
+    return out
+
+
+def norm_grad(grad: torch.Tensor, values: torch.Tensor, weight: torch.Tensor | None = None, *, eps: float = 1e-5,
+              center: bool = True, want_weight: bool | None = None, want_bias: bool = False,
+              dtype: torch.dtype | None = None, out: torch.Tensor | None = None):
+    """The gradients of ``norm`` from that of its output, ``grad`` [N, K]
+    (segred_norm_grad); the rows' statistics are found again.
+
+    want_weight, want_bias  which parameters' gradients to form (the weight's by
+            default where there is one): sums over the rows in a fixed order.
+    dtype   their type where there is no ``weight`` to go by: float32 or the values'.
+    Returns (grad_values [N, K], grad_weight [K] or None, grad_bias [K] or None).
+    """
+    dev, code, kind = _check_norm(values, weight, None)
+    if dtype is not None:
+        if dtype not in (values.dtype, torch.float32) or (weight is not None and dtype != weight.dtype):
+            raise TypeError("dtype must be the weight's, or without one float32 or the dtype of values")
+        kind = dtype
+    _beside(dev, "grad", grad)
+    if grad.shape != values.shape or grad.dtype != values.dtype:
+        raise ValueError("grad must have the shape and dtype of values")
+    n, k = values.shape
+    if out is None:
+        out = torch.empty_like(values)
+    else:
+        _beside(dev, "out", out)
+        if out.shape != values.shape or out.dtype != values.dtype:
+            raise ValueError("out must have the shape and dtype of values")
+    if want_weight is None:
+        want_weight = weight is not None
+    grad_weight = torch.empty(k, dtype=kind, device=values.device) if want_weight else None
+    grad_bias = torch.empty(k, dtype=kind, device=values.device) if want_bias else None
+    lib = _lib or library()
+    need = lib.segred_norm_grad_workspace(k, n) if want_weight or want_bias else 0
+    work = torch.empty(need, dtype=torch.uint8, device=values.device) if need else None
+    _launch(lib.segred_norm_grad, "segred_norm_grad", dev, grad.data_ptr(), values.data_ptr(), code, k, n,
+            weight.data_ptr() if weight is not None else None, FLOATS[kind], eps, 1 if center else 0, out.data_ptr(),
+            grad_weight.data_ptr() if want_weight else None, grad_bias.data_ptr() if want_bias else None,
+            work.data_ptr() if need else None, need)
+    return out, grad_weight, grad_bias
+
+
+def _check_entropy(values, weights, target, probs):
+    """(GPU index, dtype code, targets per row) of the tensors that both cross entropy calls take."""
+    dev, code = _floats("values", values)
+    if weights.dtype != values.dtype:
+        raise TypeError("weights must have the dtype of values")
+    _beside(dev, "weights", weights)
+    if weights.dim() != 2 or weights.shape[1] != values.shape[1] or weights.shape[0] < 1:
+        raise ValueError("weights must be [V, K] with the features of values")
+    if target.get_device() != dev or target.dtype != torch.int64 or not target.is_contiguous():
+        raise ValueError("target must be a contiguous int64 tensor on the GPU of the other inputs")
+    if target.dim() not in (1, 2) or target.shape[0] != values.shape[0] or (target.dim() == 2 and target.shape[1] < 1):
+        raise ValueError("target must be [N] or [N, k] with a row per row of values")
+    if probs is not None:
+        _beside(dev, "probs", probs)
+        if probs.dtype != torch.float32 or probs.shape != target.shape:
+            raise ValueError("probs must be float32 of the shape of target")
+    return dev, code, target.shape[1] if target.dim() == 2 else 1
+
+
+def cross_entropy(values: torch.Tensor, weights: torch.Tensor, target: torch.Tensor, *,
+                  probs: torch.Tensor | None = None, scale: float = 1.0):
+    """The softmax cross entropy of each row against a vocabulary's weights, whose
+    logits ``scale * values @ weights.T`` are never kept (segred_cross_entropy).
+
+    values   [N, K] float32 / bfloat16 / float16 on a GPU, contiguous.
+    weights  [V, K] of the same type.
+    target   int64 [N], or [N, k]: the entries that a teacher holds most likely,
+             with their ``probs`` float32 [N, k] (1 each if not given).  Entries
+             outside [0, V) take no part; a row without any has loss 0.
+    Returns (loss [N], lse [N], picked, shaped as target), all float32: the
+    logarithms of the sums of exponentials and the targets' logits are what
+    ``cross_entropy_grad`` goes on from.
+    """
+    dev, code, picks = _check_entropy(values, weights, target, probs)
+    (n, k), v, device = values.shape, weights.shape[0], values.device
+    loss = torch.empty(n, dtype=torch.float32, device=device)
+    lse = torch.empty(n, dtype=torch.float32, device=device)
+    picked = torch.empty(target.shape, dtype=torch.float32, device=device)
+    lib = _lib or library()
+    need = lib.segred_cross_entropy_workspace(code, k, n, v)
+    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _launch(lib.segred_cross_entropy, "segred_cross_entropy", dev, values.data_ptr(), code, k, n, weights.data_ptr(), v,
+            target.data_ptr(), probs.data_ptr() if probs is not None else None, picks, scale, loss.data_ptr(),
+            lse.data_ptr(), picked.data_ptr(), work.data_ptr() if need else None, need)
+    return loss, lse, picked
+
+
+def cross_entropy_grad(grad: torch.Tensor, values: torch.Tensor, weights: torch.Tensor, target: torch.Tensor,
+                       lse: torch.Tensor, picked: torch.Tensor, *, probs: torch.Tensor | None = None,
+                       scale: float = 1.0, want_values: bool = True, want_weights: bool = True,
+                       weights_dtype: torch.dtype | None = None):
+    """The gradients of ``cross_entropy``'s loss from ``grad`` float32 [N]
+    (segred_cross_entropy_grad), by pieces of the vocabulary.
+
+    lse, picked    what ``cross_entropy`` returned for the same arguments.
+    weights_dtype  type of the weights' gradient: theirs (default) or float32.
+    Returns (grad_values [N, K] or None, grad_weights [V, K] or None).
+    """
+    dev, code, picks = _check_entropy(values, weights, target, probs)
+    (n, k), v, device = values.shape, weights.shape[0], values.device
+    for name, t, shape in (("grad", grad, (n,)), ("lse", lse, (n,)), ("picked", picked, target.shape)):
+        _beside(dev, name, t)
+        if t.dtype != torch.float32 or t.shape != shape:
+            raise ValueError(f"{name} must be float32 {list(shape)}")
+    kind = weights_dtype or weights.dtype
+    if kind not in (weights.dtype, torch.float32):
+        raise TypeError("weights_dtype must be float32 or the dtype of weights")
+    grad_values = torch.empty_like(values) if want_values else None
+    grad_weights = torch.empty((v, k), dtype=kind, device=device) if want_weights else None
+    lib = _lib or library()
+    need = lib.segred_cross_entropy_grad_workspace(code, k, n, v)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
+    _launch(lib.segred_cross_entropy_grad, "segred_cross_entropy_grad", dev, grad.data_ptr(), values.data_ptr(), code, k, n,
+            weights.data_ptr(), v, target.data_ptr(), probs.data_ptr() if probs is not None else None, picks, scale,
+            lse.data_ptr(), picked.data_ptr(), grad_values.data_ptr() if want_values else None,
+            grad_weights.data_ptr() if want_weights else None, FLOATS[kind], work.data_ptr(), need)
+    return grad_values, grad_weights
 
 
 def set_shares(shares: int):

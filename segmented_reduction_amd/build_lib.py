@@ -21,7 +21,8 @@ LIB_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 LIB = os.path.join(LIB_DIR, "libsegred.so")
 SOURCES = ["api.hip", "reduce.hip", "rle.hip", "scatter.hip", "segscan.hip", "galloping.hip", "probe.hip",
-           "matmul.hip", "outer.hip", "group.hip", "combine.hip", "adapter.hip"]
+           "matmul.hip", "outer.hip", "group.hip", "combine.hip", "adapter.hip", "norm.hip",
+           "gated.hip", "loss.hip"]
 ARCH = os.environ.get("SEGRED_OFFLOAD_ARCH", "gfx950")
 
 

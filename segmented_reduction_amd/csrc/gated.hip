@@ -1,0 +1,427 @@
+// gated.hip -- the gated pair of projections of each segment's rows and its
+// gradient: with g = x G[s]^T and u = x U[s]^T, G[s] and U[s] the first and the
+// last m rows of weights[s],
+//   out  = act(g) u
+//   grad = (d u act'(g), d act(g)) from d, the gradient of out: the gradient of the
+//          pair (g, u), [., 2 m], whose products with the weights and the rows are
+//          segred_matmul's and segred_outer's.
+// One kernel forms both projections side by side: of a tile's columns one half are
+// rows of G and the other the same rows of U, so that a lane holds g and u of the
+// same outputs and neither goes to memory.  The gradient forms them again: kept in
+// float32 they would take 16 bytes an output to write and read, against 4 k
+// operations to form them again, about equal at k = 1,024.
+#include <algorithm>
+
+#include "internal.hpp"
+#include "rowtile.hpp"
+
+namespace segred {
+
+struct GatedArgs {
+    const char *values;
+    const int64_t *rows;  // row of `values` behind each row, or null
+    int64_t value_rows;
+    const char *weights;  // [S, 2 M, K]
+    const int64_t *offsets;
+    int64_t S, N, K, M;
+    int64_t slots, ntiles;
+    const char *grad;  // [N, M], the gradient call's
+    void *out;         // [N, M], or [N, 2 M]
+    int vec;           // halves of rows of `out` (and of `grad`) hold whole 16-byte units on 16-byte boundaries
+    float c1, c2;      // act(x) = x / (1 + exp(-x (c1 + c2 x^2))) where it is neither of the others
+    int relu;
+};
+
+// An activation and its slope.  ERF: x Phi(x).
+struct Bend {
+    float value, slope;
+};
+template <bool ERF>
+__device__ __forceinline__ Bend bend(float x, const GatedArgs &a) {
+    if constexpr (ERF) {
+        const float phi = 0.5f * erfcf(x * -0.70710678118654752f);
+        return {x * phi, fmaf(x * 0.39894228040143268f, __expf(-0.5f * x * x), phi)};
+    } else {
+        if (a.relu) return {x < 0.f ? 0.f : x, x <= 0.f ? 0.f : 1.f};
+        const float q = fminf(x * x, 1e6f);  // beyond that s is 0 or 1 already
+        const float p = x * fmaf(a.c2, q, a.c1);
+        const float e = __expf(-p), s = __builtin_amdgcn_rcpf(1.f + e);
+        const float rest = p > 0.f ? e * s : 1.f - s;  // 1 - s
+        return {x * s, fmaf(x * s * rest, fmaf(3.f * a.c2, q, a.c1), s)};
+    }
+}
+template <bool ERF>
+__device__ __forceinline__ f32x4 gated_value(f32x4 g, f32x4 u, const GatedArgs &a) {
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = bend<ERF>(g[e], a).value * u[e];
+    return y;
+}
+template <bool ERF>
+__device__ __forceinline__ void gated_slope(f32x4 &g, f32x4 &u, f32x4 d, const GatedArgs &a) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const Bend b = bend<ERF>(g[e], a);
+        g[e] = d[e] * u[e] * b.slope;
+        u[e] = d[e] * b.value;
+    }
+}
+
+// A tile of one segment: rows row0 .. row0 + rows - 1, outputs from n0.
+struct GatedPlace {
+    int64_t s, row0, n0;
+    int rows;  // 0: nothing to do
+};
+// BM rows x BN outputs.
+template <int BM, int BN>
+__device__ __forceinline__ GatedPlace gated_place(const GatedArgs &a, int lane) {
+    constexpr int kLg = __builtin_ctz(BM);
+    GatedPlace p{0, 0, 0, 0};
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return p;
+    const TilePlace at = tile_place(id, a.slots, a.ntiles);
+    p.s = tight_segment(a.offsets, a.S, kLg, at.m, lane);
+    p.n0 = at.n * BN;
+    p.row0 = a.offsets[p.s] + ((at.m - tight_key(a.offsets, p.s, kLg)) << kLg);
+    const int64_t end = min(a.offsets[p.s + 1], a.N);
+    if (p.row0 < end && p.row0 >= 0) p.rows = (int)min((int64_t)BM, end - p.row0);
+    return p;
+}
+template <typename T>
+__device__ __forceinline__ const char *gated_row(const GatedArgs &a, const GatedPlace &p, int r) {
+    if (r >= p.rows) return nullptr;
+    int64_t v = p.row0 + r;
+    if (a.rows) v = a.rows[v];
+    return v >= 0 && v < a.value_rows ? a.values + v * a.K * (int64_t)sizeof(T) : nullptr;
+}
+// Row of the weights for output n of the tile's segment, half 0 (G) or 1 (U).
+template <typename T>
+__device__ __forceinline__ const char *gated_weight(const GatedArgs &a, const GatedPlace &p, int64_t n, int half) {
+    n += p.n0;
+    return n < a.M ? a.weights + ((2 * p.s + half) * a.M + n) * a.K * (int64_t)sizeof(T) : nullptr;
+}
+// The same for tile column c where blocks of 16 of G and U take turns.
+template <typename T>
+__device__ __forceinline__ const char *gated_pair(const GatedArgs &a, const GatedPlace &p, int c) {
+    return gated_weight<T>(a, p, (c >> 5) * 16 + (c & 15), (c >> 4) & 1);
+}
+
+// Four elements of the output's gradient.
+template <typename T>
+__device__ __forceinline__ f32x4 load_quad(const T *row, int64_t n, int64_t width, bool vec) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+        if (n < width) {
+            typedef __attribute__((ext_vector_type(4))) T T4;
+            const T4 q = *reinterpret_cast<const T4 *>(row + n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = (float)q[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < width) c[j] = (float)row[n + j];
+    }
+    return c;
+}
+
+// Quads of 16-bit results pass through LDS so that whole stretches are moved; a
+// tile of the output's gradient enters the same way, and each quad of it is
+// replaced by the result's.  quad(f) calls f(row, column, g, u) for each of a
+// lane's; BM x BN outputs.
+template <typename T, int BM, int BN, int THREADS, bool GRAD, bool ERF, typename Q>
+__device__ __forceinline__ void gated_store(const GatedArgs &a, const GatedPlace &p, lds_char *lds, Q quad) {
+    T *out = reinterpret_cast<T *>(a.out);
+    const bool vec = a.vec != 0;
+    if constexpr (sizeof(T) == 4) {
+        quad([&](int r, int c, f32x4 g, f32x4 u) {
+            if (r >= p.rows) return;
+            const int64_t n = p.n0 + c, row = p.row0 + r;
+            if constexpr (GRAD) {
+                gated_slope<ERF>(g, u, load_quad<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M, vec), a);
+                store_quad<T>(out + row * 2 * a.M, n, a.M, g, vec);
+                store_quad<T>(out + row * 2 * a.M + a.M, n, a.M, u, vec);
+            } else {
+                store_quad<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a), vec);
+            }
+        });
+    } else if constexpr (GRAD) {
+        lds_char *second = lds + BM * BN * 2;
+        tile_in<T, BM, BN, THREADS>(lds, reinterpret_cast<const T *>(a.grad) + p.row0 * a.M, p.rows, p.n0, a.M, vec);
+        __syncthreads();
+        quad([&](int r, int c, f32x4 g, f32x4 u) {
+            gated_slope<ERF>(g, u, tile_get<T, BN>(lds, r, c), a);
+            tile_put<T, BN>(lds, r, c, g);
+            tile_put<T, BN>(second, r, c, u);
+        });
+        __syncthreads();
+        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * 2 * a.M, p.rows, p.n0, a.M, 2 * a.M, vec);
+        tile_write<T, BM, BN, THREADS>(second, out + p.row0 * 2 * a.M + a.M, p.rows, p.n0, a.M, 2 * a.M, vec);
+    } else {
+        quad([&](int r, int c, f32x4 g, f32x4 u) { tile_put<T, BN>(lds, r, c, gated_value<ERF>(g, u, a)); });
+        __syncthreads();
+        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * a.M, p.rows, p.n0, a.M, a.M, vec);
+    }
+}
+
+// BM rows x BN / 2 outputs per workgroup.
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool GRAD, bool ERF>
+struct GatedTile {
+    using Tile = RowTile<T, BM, BN, WM, WN, STAGES, DIRECT>;
+    static constexpr int kOut = GRAD ? 2 : 1;
+    static constexpr int kLds = std::max(Tile::kLds, sizeof(T) == 2 ? kOut * BM * BN : 0);
+
+    static __device__ __forceinline__ void run(const GatedArgs &a, const GatedPlace &p, lds_char *lds, int wave, int lane) {
+        f32x4 acc[Tile::MT][Tile::NT] = {};
+        Tile::run(acc, (int)a.K, lds, wave, lane, [&](int r) { return gated_row<T>(a, p, r); },
+                  [&](int c) { return gated_pair<T>(a, p, c); });
+        gated_store<T, BM, BN / 2, Tile::kThreads, GRAD, ERF>(a, p, lds, [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < Tile::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Tile::NT; j += 2)
+                    f(Tile::m0(wave) + 16 * i + (lane & 15), Tile::n0(wave) / 2 + 8 * j + (lane >> 4) * 4, acc[i][j],
+                      acc[i][j + 1]);
+        });
+    }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool GRAD, bool ERF>
+__global__ __launch_bounds__(64 * WM * WN) void seg_gated(GatedArgs a) {
+    using Tile = GatedTile<T, BM, BN, WM, WN, STAGES, DIRECT, GRAD, ERF>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const GatedPlace p = gated_place<BM, BN / 2>(a, lane);
+    if (p.rows > 0) Tile::run(a, p, (lds_char *)lds_mem, wave, lane);
+}
+
+// The same for float, in bf16 parts; a tile with a sum that is not finite is
+// computed again with float products.
+template <int BM, int BN, bool WHOLE, bool GRAD, bool ERF>
+__global__ __launch_bounds__(kRowSplitThreads, 3) void seg_gated_split(GatedArgs a) {
+    using Tile = SplitTile<BM, BN, WHOLE>;
+    using Plain = GatedTile<float, 64, 64, 2, 2, 2, false, GRAD, ERF>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds > Plain::kLds ? Tile::kLds : Plain::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const GatedPlace p = gated_place<BM, BN / 2>(a, lane);
+    if (p.rows == 0) return;
+    f32x4 acc[Tile::MT][Tile::NT] = {};
+    if (!Tile::run(acc, (int)a.K, lds, threadIdx.x, [&](int r) { return gated_row<float>(a, p, r); },
+                   [&](int c) { return gated_pair<float>(a, p, c); })) {
+        for (int r = 0; r < p.rows; r += 64)
+            for (int c = 0; c < BN / 2 && p.n0 + c < a.M; c += 32) {
+                const GatedPlace q{p.s, p.row0 + r, p.n0 + c, min(64, p.rows - r)};
+                __syncthreads();
+                Plain::run(a, q, lds, wave, lane);
+            }
+        return;
+    }
+    gated_store<float, BM, BN / 2, kRowSplitThreads, GRAD, ERF>(a, p, lds, [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < Tile::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Tile::NT; j += 2)
+                f(Tile::m0(wave) + 16 * i + (lane & 15), Tile::n0(wave) / 2 + 8 * j + (lane >> 4) * 4, acc[i][j],
+                  acc[i][j + 1]);
+    });
+}
+
+// Many rows per segment: AH * 128 rows x 128 outputs per workgroup, in phases.
+// The halves of the tile's columns are G's rows and U's.
+template <typename T, int AH, bool GRAD, bool ERF>
+__global__ __launch_bounds__(kPhaseThreads) void seg_gated_many(GatedArgs a) {
+    using Tile = PhaseTile<T, AH>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const GatedPlace p = gated_place<AH * kHalf, kHalf>(a, lane);
+    if (p.rows == 0) return;
+    f32x4 acc[2][2][4][2] = {};
+    Tile::run(acc, p.rows, (int)a.K, lds, wave, lane, [&](int r) { return gated_row<T>(a, p, r); },
+              [&](int c) { return gated_weight<T>(a, p, c & (kHalf - 1), c >> 7); });
+    gated_store<T, AH * kHalf, kHalf, kPhaseThreads, GRAD, ERF>(a, p, lds, [&](auto f) {
+#pragma unroll
+        for (int h = 0; h < AH; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    f(phase_row(h, i, wave) + (lane & 15), phase_col(0, j, wave) + (lane >> 4) * 4, acc[h][0][i][j],
+                      acc[h][1][i][j]);
+    });
+}
+
+// Few rows per segment: 16 rows x 8 NT outputs per workgroup, the contraction
+// split over its waves.
+template <typename T, int NT, int NW, int STAGES, bool GRAD, bool ERF>
+__global__ __launch_bounds__(64 * NW) void seg_gated_few(GatedArgs a) {
+    using Tile = FewTile<T, NT, NW, STAGES>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.slots * a.ntiles);
+    if (id >= a.slots * a.ntiles) return;
+    GatedPlace p;
+    const int64_t slot = id / a.ntiles;
+    p.n0 = (id - slot * a.ntiles) * (8 * NT);
+    p.s = tight_segment(a.offsets, a.S, 4, slot, lane);
+    p.row0 = a.offsets[p.s] + ((slot - tight_key(a.offsets, p.s, 4)) << 4);
+    const int64_t end = min(a.offsets[p.s + 1], a.N);
+    if (p.row0 >= end || p.row0 < 0) return;
+    p.rows = (int)min((int64_t)16, end - p.row0);
+    Tile::run((int)a.K, lds, wave, lane, [&](int r) { return gated_row<T>(a, p, r); },
+              [&](int c) { return gated_pair<T>(a, p, c); });
+    T *out = reinterpret_cast<T *>(a.out);
+    const int r = lane & 15;
+    const int64_t row = p.row0 + r;
+    for (int j = wave; j < NT / 2; j += NW) {
+        f32x4 g = Tile::sum(lds, 2 * j, lane), u = Tile::sum(lds, 2 * j + 1, lane);
+        if (r >= p.rows) continue;
+        const int64_t n = p.n0 + 16 * j + (lane >> 4) * 4;
+        const bool vec = a.vec != 0;
+        if constexpr (GRAD) {
+            gated_slope<ERF>(g, u, load_quad<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M, vec), a);
+            store_quad<T>(out + row * 2 * a.M, n, a.M, g, vec);
+            store_quad<T>(out + row * 2 * a.M + a.M, n, a.M, u, vec);
+        } else {
+            store_quad<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a), vec);
+        }
+    }
+}
+
+// Slots of BM rows and tiles of `outputs`.
+bool gated_grid(GatedArgs &a, int lg, int64_t outputs, dim3 &grid) {
+    a.slots = tight_slots(a.N, a.S, lg);
+    a.ntiles = (a.M + outputs - 1) / outputs;
+    return a.slots <= INT64_MAX / a.ntiles && tile_grid(a.slots * a.ntiles, grid);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool GRAD, bool ERF>
+int gated_launch(GatedArgs a, hipStream_t st) {
+    dim3 grid;
+    if (!gated_grid(a, __builtin_ctz(BM), BN / 2, grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(true, (seg_gated<T, BM, BN, WM, WN, STAGES, DIRECT, GRAD, ERF>), grid, dim3(64 * WM * WN), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+template <int BM, int BN, bool GRAD, bool ERF>
+int gated_split_launch(GatedArgs a, hipStream_t st) {
+    dim3 grid;
+    if (!gated_grid(a, __builtin_ctz(BM), BN / 2, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (a.K % 8 == 0) timed_launch_ggl(true, (seg_gated_split<BM, BN, true, GRAD, ERF>), grid, dim3(kRowSplitThreads), 0, st, a);
+    else timed_launch_ggl(true, (seg_gated_split<BM, BN, false, GRAD, ERF>), grid, dim3(kRowSplitThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+template <typename T, int AH, bool GRAD, bool ERF>
+int gated_many_launch(GatedArgs a, hipStream_t st) {
+    dim3 grid;
+    if (!gated_grid(a, AH == 2 ? 8 : 7, kHalf, grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(true, (seg_gated_many<T, AH, GRAD, ERF>), grid, dim3(kPhaseThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+template <typename T, int NT, int NW, int STAGES, bool GRAD, bool ERF>
+int gated_few_launch(GatedArgs a, hipStream_t st) {
+    dim3 grid;
+    if (!gated_grid(a, 4, 8 * NT, grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(true, (seg_gated_few<T, NT, NW, STAGES, GRAD, ERF>), grid, dim3(64 * NW), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+// The kernel for a call: the rule of segred_matmul with 2 m outputs.
+constexpr int64_t kFewRows = 8, kManyRows = 64, kManyTiles = 1536, kFewTiles = 512;
+constexpr int64_t kSplitRows = 24, kSplitTiles = 224;
+template <typename T, bool GRAD, bool ERF>
+int gated_dispatch(const GatedArgs &a, bool direct, hipStream_t st) {
+    const int64_t mean = a.N / a.S, wide = 2 * a.M;
+    const int64_t tiles = (a.N / 64 + a.S / 2) * ((wide + 127) / 128);
+    if constexpr (sizeof(T) == 4) {
+        if (direct && mean <= kFewRows) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
+        if (direct && (mean <= kSplitRows || tiles < kSplitTiles))
+            return gated_launch<T, 32, 128, 1, 4, 3, true, GRAD, ERF>(a, st);
+        if (mean <= kSplitRows) return gated_launch<T, 16, 128, 1, 4, 2, false, GRAD, ERF>(a, st);
+        return gated_split_launch<64, 128, GRAD, ERF>(a, st);
+    } else {
+        if (!direct && mean <= 2 * kFewRows) return gated_launch<T, 16, 128, 1, 4, 2, false, GRAD, ERF>(a, st);
+        if (!direct) return gated_launch<T, 64, 128, 2, 2, 2, false, GRAD, ERF>(a, st);
+        const bool few_tiles = (a.N / 64 + a.S / 2) * ((wide + 63) / 64) <= kFewTiles;  // of 64 x 64
+        if (mean <= (few_tiles ? 2 * kFewRows : kFewRows)) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
+        if (a.K >= 256 && wide > 128 && tiles >= kManyTiles && mean >= kManyRows) {
+            const int64_t nt = (wide + 255) / 256;
+            const int64_t one = ((a.N / 128 + a.S / 2) * nt + 255) / 256, two = ((a.N / 256 + a.S / 2) * nt + 255) / 256;
+            if (4 * one < 7 * two) return gated_many_launch<T, 1, GRAD, ERF>(a, st);
+            return gated_many_launch<T, 2, GRAD, ERF>(a, st);
+        }
+        if (few_tiles) return gated_launch<T, 64, 64, 2, 2, 3, true, GRAD, ERF>(a, st);
+        return gated_launch<T, 64, 128, 2, 2, 2, true, GRAD, ERF>(a, st);
+    }
+}
+
+template <bool GRAD, bool ERF>
+int gated_typed(const GatedArgs &a, int32_t dtype, bool direct, hipStream_t st) {
+    switch (dtype) {
+    case SEGRED_BF16: return gated_dispatch<__bf16, GRAD, ERF>(a, direct, st);
+    case SEGRED_F16: return gated_dispatch<_Float16, GRAD, ERF>(a, direct, st);
+    default: return gated_dispatch<float, GRAD, ERF>(a, direct, st);
+    }
+}
+
+int gated_call(bool is_grad, const void *grad, const void *values, int32_t dtype, int64_t k, const int64_t *rows,
+               int64_t value_rows, const void *weights, int64_t m, int32_t activation, const int64_t *offsets,
+               int64_t num_segments, int64_t num_rows, void *out, hipStream_t stream) {
+    const int64_t e = float_size(dtype);
+    if (dtype < SEGRED_U32 || dtype > SEGRED_F16) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (activation < SEGRED_SILU || activation > SEGRED_RELU) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (k < 1 || m < 1 || value_rows < 0 || num_segments < 0 || num_rows < 0) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!rows && value_rows < num_rows) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments > 0 && num_rows > 0 &&
+        ((value_rows > 0 && !values) || !weights || !offsets || !out || (is_grad && !grad)))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (e == 0 || k > kMaxWidth || m > kMaxWidth / 2) return SEGRED_ERR_UNSUPPORTED;
+    if (!aligned(values, e) || !aligned(weights, e) || !aligned(out, e) || !aligned(grad, e) || !aligned(offsets, 8) ||
+        !aligned(rows, 8))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (too_large(value_rows, k, 4) || too_large(num_rows, m, 8) || too_large(num_segments, k * m, 8))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (num_segments == 0 || num_rows == 0) return SEGRED_OK;
+
+    GatedArgs a{};
+    a.values = static_cast<const char *>(values);
+    a.rows = rows;
+    a.value_rows = value_rows;
+    a.weights = static_cast<const char *>(weights);
+    a.offsets = offsets;
+    a.S = num_segments;
+    a.N = num_rows;
+    a.K = k;
+    a.M = m;
+    a.grad = static_cast<const char *>(grad);
+    a.out = out;
+    a.vec = ((m * e) % 16 == 0 && aligned(out, 16) && aligned(grad, 16)) ? 1 : 0;
+    // 0.5 (1 + tanh y) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (x + 0.044715 x^3)
+    a.c1 = activation == SEGRED_GELU_TANH ? 1.5957691216057308f : 1.f;
+    a.c2 = activation == SEGRED_GELU_TANH ? 0.071354816272600248f : 0.f;
+    a.relu = activation == SEGRED_RELU;
+    const bool direct = (k * e) % 16 == 0 && aligned(values, 16) && aligned(weights, 16);
+    if (activation == SEGRED_GELU)
+        return is_grad ? gated_typed<true, true>(a, dtype, direct, stream) : gated_typed<false, true>(a, dtype, direct, stream);
+    return is_grad ? gated_typed<true, false>(a, dtype, direct, stream) : gated_typed<false, false>(a, dtype, direct, stream);
+}
+
+}  // namespace segred
+
+using namespace segred;
+
+extern "C" int segred_gated(const void *values, int32_t dtype, int64_t k, const int64_t *rows, int64_t value_rows,
+                            const void *weights, int64_t m, int32_t activation, const int64_t *offsets,
+                            int64_t num_segments, int64_t num_rows, void *out, hipStream_t stream) {
+    return gated_call(false, nullptr, values, dtype, k, rows, value_rows, weights, m, activation, offsets, num_segments,
+                      num_rows, out, stream);
+}
+
+extern "C" int segred_gated_grad(const void *grad, const void *values, int32_t dtype, int64_t k, const int64_t *rows,
+                                 int64_t value_rows, const void *weights, int64_t m, int32_t activation,
+                                 const int64_t *offsets, int64_t num_segments, int64_t num_rows, void *out,
+                                 hipStream_t stream) {
+    return gated_call(true, grad, values, dtype, k, rows, value_rows, weights, m, activation, offsets, num_segments,
+                      num_rows, out, stream);
+}

@@ -1,0 +1,936 @@
+// loss.hip -- the softmax cross entropy of rows against a vocabulary's weights,
+// and its gradient, by pieces of the vocabulary: the logits are never kept.
+//
+// With z_v = scale <x, W_v>, targets v_j of probability t_j and s = sum t_j,
+//   loss = s lse - sum_j t_j z_(v_j), lse = log sum_v exp z_v
+//   dz_v = g scale (s exp(z_v - lse) - sum of the t_j with v_j = v)
+//   dx = sum_v dz_v W_v, dW_v = sum over rows of dz_v x.
+// Forward: tiles of x W^T leave one pair (largest, sum of exponentials) per row
+// and tile; a second kernel joins a row's pairs and forms its targets' logits.
+// Back, for each piece of the vocabulary: the tiles again, whose epilogue makes
+// dz of them (rounded to the inputs' type, once), then the two products of dz.
+// dx is added up in float32 over the pieces and rounded at the end.
+// Exponentials are powers of two: z scale log2(e) minus the base in one fma.
+#include <algorithm>
+#include <cmath>
+
+#include "internal.hpp"
+#include "outer.hpp"
+#include "rowtile.hpp"
+
+namespace segred {
+
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+struct LossArgs {
+    const char *values, *weights;
+    const int64_t *target;  // [N, picks]
+    const float *probs;     // [N, picks], or null: 1
+    int64_t N, V, K, picks;
+    float scale, bend;  // bend = scale log2(e)
+    int64_t v0, vc;     // the piece of the vocabulary
+    int64_t mtiles, ntiles;
+    // forward
+    float2 *partial;  // [N, parts] of (base, sum of 2^(z bend - base))
+    int64_t parts;
+    float *loss, *lse, *picked;  // picked: [N, picks], also the gradient call's
+    // back
+    const float *grad;
+    float *share, *hit;  // [N]: grad scale s and grad scale, by `factor`
+    float *bound;        // [N]: what |dz| of a row is at most
+    int64_t *live;       // [N]: the row, or -1 where it has no target
+    float *factor;       // what dz is multiplied by before it is rounded, and 1 / factor
+    char *slope;         // [N, ld]: dz of the piece
+    int64_t ld;
+    float *sums;  // [parts_k, N, K]: dx so far
+    int64_t cuts;
+    int first;  // the first piece
+    void *grad_values;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Over the four rows of 16 lanes.
+template <typename F>
+__device__ __forceinline__ float quarters_fold(float v, F f) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// A tile: rows row0 .. row0 + rows - 1, columns of the piece from n0.
+struct LossPlace {
+    int64_t row0, n0, tile;  // tile: of the columns
+    int rows;
+};
+template <int BM, int BN>
+__device__ __forceinline__ LossPlace loss_place(const LossArgs &a) {
+    const int64_t id = xcd_tile(a.mtiles * a.ntiles);
+    if (id >= a.mtiles * a.ntiles) return {0, 0, 0, 0};
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    return {at.m * BM, at.n * BN, at.n, (int)min((int64_t)BM, a.N - at.m * BM)};
+}
+template <typename T>
+__device__ __forceinline__ const char *loss_row(const LossArgs &a, const LossPlace &p, int r) {
+    return r < p.rows ? a.values + (p.row0 + r) * a.K * (int64_t)sizeof(T) : nullptr;
+}
+template <typename T>
+__device__ __forceinline__ const char *loss_word(const LossArgs &a, const LossPlace &p, int c) {
+    return p.n0 + c < a.vc ? a.weights + (a.v0 + p.n0 + c) * a.K * (int64_t)sizeof(T) : nullptr;
+}
+
+// The pair of each row of a tile: RI x CJ quads per lane, get(i, j) at row(i)
+// and column col(j); WN waves (this one is `wn`) share a row.  `part` is the
+// place of the pair among the row's.
+template <int RI, int CJ, int WN, int BM, int BN, typename G, typename R, typename C>
+__device__ __forceinline__ void loss_pairs(const LossArgs &a, const LossPlace &p, int64_t part, lds_char *lds, int wn,
+                                           int lane, G get, R row, C col) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2;
+    typedef __attribute__((address_space(3))) f32x2 lds_pair;
+    lds_pair *s = reinterpret_cast<lds_pair *>(lds);
+    const bool cut = p.n0 + BN > a.vc;
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+            f32x4 &z = get(i, j);
+            if (cut)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (p.n0 + col(j) + e >= a.vc) z[e] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, z[e]);
+        }
+        m = quarters_fold(m, [](float x, float y) { return fmaxf(x, y); }) * a.bend;
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+            const f32x4 &z = get(i, j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += exp2_fast(fmaf(z[e], a.bend, -base));
+        }
+        sum = quarters_fold(sum, [](float x, float y) { return x + y; });
+        if (lane < 16) s[wn * BM + row(i)] = f32x2{m, sum};
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < p.rows; r += blockDim.x) {
+        f32x2 v = s[r];
+#pragma unroll
+        for (int w = 1; w < WN; ++w) {
+            const f32x2 o = s[w * BM + r];
+            const float m = fmaxf(v[0], o[0]), base = m == -INFINITY ? 0.f : m;
+            v = f32x2{m, v[1] * exp2_fast(v[0] - base) + o[1] * exp2_fast(o[0] - base)};
+        }
+        a.partial[(p.row0 + r) * a.parts + part] = make_float2(v[0], v[1]);
+    }
+}
+
+// dz of a row's logits, without its targets.
+struct LossRow {
+    float share, base;
+    bool live;
+};
+__device__ __forceinline__ LossRow loss_row_of(const LossArgs &a, int64_t row) {
+    return {a.share[row], a.lse[row] * kLog2e, a.live[row] >= 0};
+}
+__device__ __forceinline__ f32x4 loss_slopes(const LossArgs &a, const LossRow &o, f32x4 z, int64_t n) {
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        y[e] = o.live && n + e < a.vc ? o.share * exp2_fast(fmaf(z[e], a.bend, -o.base)) : 0.f;
+    return y;
+}
+// Calls put(r, c, dz) for the targets of the tile's rows in its columns, from
+// the logits that the forward call kept; a target named twice gets both shares.
+template <int BN, typename P>
+__device__ __forceinline__ void loss_targets(const LossArgs &a, const LossPlace &p, P put) {
+    const int picks = (int)a.picks;
+    const int64_t begin = a.v0 + p.n0;
+    const int64_t left = min((int64_t)BN, a.vc - p.n0), all = (int64_t)p.rows * picks;
+    const int64_t *target = a.target + p.row0 * picks;
+    for (int64_t i = threadIdx.x; i < all; i += blockDim.x) {
+        const int64_t t = target[i] - begin;
+        if (t < 0 || t >= left) continue;
+        const int64_t r = i / picks, row = p.row0 + r;
+        float sum = 0.f;
+        for (int j = 0; j < picks; ++j)
+            if (target[r * picks + j] - begin == t) sum += a.probs ? a.probs[row * picks + j] : 1.f;
+        const float e = exp2_fast(fmaf(a.picked[row * picks + i - r * picks], kLog2e, -a.lse[row] * kLog2e));
+        put((int)r, (int)t, fmaf(a.share[row], e, -a.hit[row] * sum));
+    }
+}
+
+// Leaves dz of a tile in the piece.
+template <typename T, int RI, int CJ, int BM, int BN, int THREADS, typename G, typename R, typename C>
+__device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p, lds_char *lds, int lane, G get, R row,
+                                           C col) {
+    T *out = reinterpret_cast<T *>(a.slope) + p.row0 * a.ld;
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+        const int r = row(i);
+        const LossRow o = r < p.rows ? loss_row_of(a, p.row0 + r) : LossRow{0.f, 0.f, false};
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+            const f32x4 y = loss_slopes(a, o, get(i, j), p.n0 + col(j));
+            if constexpr (sizeof(T) == 2) tile_put<T, BN>(lds, r, col(j), y);
+            else if (r < p.rows) store_quad<T>(out + r * a.ld, p.n0 + col(j), a.ld, y, true);
+        }
+    }
+    if constexpr (sizeof(T) == 2) {
+        __syncthreads();
+        loss_targets<BN>(a, p, [&](int r, int c, float y) {
+            *reinterpret_cast<__attribute__((address_space(3))) T *>(lds + tile_unit<T, BN>(r, c >> 3) + (c & 7) * 2) = (T)y;
+        });
+        __syncthreads();
+        tile_write<T, BM, BN, THREADS>(lds, out, p.rows, p.n0, a.ld, a.ld, true);
+    } else {
+        // the stores of other waves to the same places must have gone before
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        loss_targets<BN>(a, p, [&](int r, int c, float y) { out[r * a.ld + p.n0 + c] = (T)y; });
+    }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool SLOPE>
+struct LossTile {
+    using Tile = RowTile<T, BM, BN, WM, WN, STAGES, DIRECT>;
+    static constexpr int kLds = std::max(Tile::kLds, sizeof(T) == 2 && SLOPE ? BM * BN * 2 : WN * BM * 8);
+    static __device__ __forceinline__ void run(const LossArgs &a, const LossPlace &p, int64_t part, lds_char *lds,
+                                               int wave, int lane) {
+        f32x4 acc[Tile::MT][Tile::NT] = {};
+        Tile::run(acc, (int)a.K, lds, wave, lane, [&](int r) { return loss_row<T>(a, p, r); },
+                  [&](int c) { return loss_word<T>(a, p, c); });
+        auto get = [&](int i, int j) -> f32x4 & { return acc[i][j]; };
+        auto row = [&](int i) { return Tile::m0(wave) + 16 * i + (lane & 15); };
+        auto col = [&](int j) { return Tile::n0(wave) + 16 * j + (lane >> 4) * 4; };
+        if constexpr (SLOPE) loss_slope<T, Tile::MT, Tile::NT, BM, BN, Tile::kThreads>(a, p, lds, lane, get, row, col);
+        else loss_pairs<Tile::MT, Tile::NT, WN, BM, BN>(a, p, part, lds, wave % WN, lane, get, row, col);
+    }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool SLOPE>
+__global__ __launch_bounds__(64 * WM * WN) void loss_tiles(LossArgs a) {
+    using Tile = LossTile<T, BM, BN, WM, WN, STAGES, DIRECT, SLOPE>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossPlace p = loss_place<BM, BN>(a);
+    if (p.rows > 0) Tile::run(a, p, p.tile, (lds_char *)lds_mem, wave, lane);
+}
+
+// Float in bf16 parts, 64 x 128; a tile with a sum that is not finite is computed
+// again with float products, 64 columns at a time: a pair covers 64 columns, and
+// where there is one for 128 the second is empty.
+template <bool WHOLE, bool SLOPE>
+__global__ __launch_bounds__(kRowSplitThreads, 3) void loss_split(LossArgs a) {
+    using Tile = SplitTile<64, 128, WHOLE>;
+    using Plain = LossTile<float, 64, 64, 2, 2, 2, false, SLOPE>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds > Plain::kLds ? Tile::kLds : Plain::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossPlace p = loss_place<64, 128>(a);
+    if (p.rows <= 0) return;
+    f32x4 acc[Tile::MT][Tile::NT] = {};
+    if (!Tile::run(acc, (int)a.K, lds, threadIdx.x, [&](int r) { return loss_row<float>(a, p, r); },
+                   [&](int c) { return loss_word<float>(a, p, c); })) {
+        for (int c = 0; c < 128; c += 64) {
+            const LossPlace q{p.row0, p.n0 + c, 0, p.rows};
+            __syncthreads();
+            if (q.n0 < a.vc) Plain::run(a, q, q.n0 >> 6, lds, wave, lane);
+            else if (!SLOPE)
+                for (int r = threadIdx.x; r < p.rows; r += kRowSplitThreads)
+                    a.partial[(p.row0 + r) * a.parts + (q.n0 >> 6)] = make_float2(-INFINITY, 0.f);
+        }
+        return;
+    }
+    auto get = [&](int i, int j) -> f32x4 & { return acc[i][j]; };
+    auto row = [&](int i) { return Tile::m0(wave) + 16 * i + (lane & 15); };
+    auto col = [&](int j) { return Tile::n0(wave) + 16 * j + (lane >> 4) * 4; };
+    if constexpr (SLOPE) {
+        loss_slope<float, Tile::MT, Tile::NT, 64, 128, kRowSplitThreads>(a, p, lds, lane, get, row, col);
+    } else {
+        loss_pairs<Tile::MT, Tile::NT, 2, 64, 128>(a, p, p.n0 >> 6, lds, wave % 2, lane, get, row, col);
+        for (int r = threadIdx.x; r < p.rows; r += kRowSplitThreads)
+            a.partial[(p.row0 + r) * a.parts + (p.n0 >> 6) + 1] = make_float2(-INFINITY, 0.f);
+    }
+}
+
+// Many rows, 16-bit types: AH * 128 rows x 256 columns in phases.
+template <typename T, int AH, bool SLOPE>
+__global__ __launch_bounds__(kPhaseThreads) void loss_many(LossArgs a) {
+    using Tile = PhaseTile<T, AH>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossPlace p = loss_place<AH * kHalf, 2 * kHalf>(a);
+    if (p.rows <= 0) return;
+    f32x4 acc[2][2][4][2] = {};
+    Tile::run(acc, p.rows, (int)a.K, lds, wave, lane, [&](int r) { return loss_row<T>(a, p, r); },
+              [&](int c) { return loss_word<T>(a, p, c); });
+    auto get = [&](int i, int j) -> f32x4 & { return acc[i >> 2][j >> 1][i & 3][j & 1]; };
+    auto row = [&](int i) { return phase_row(i >> 2, i & 3, wave) + (lane & 15); };
+    auto col = [&](int j) { return phase_col(j >> 1, j & 1, wave) + (lane >> 4) * 4; };
+    if constexpr (SLOPE) loss_slope<T, 4 * AH, 4, AH * kHalf, 2 * kHalf, kPhaseThreads>(a, p, lds, lane, get, row, col);
+    else loss_pairs<4 * AH, 4, 4, AH * kHalf, 2 * kHalf>(a, p, p.tile, lds, wave & 3, lane, get, row, col);
+}
+
+// Up to 16 rows: 64 columns per workgroup, the contraction split over its waves.
+template <typename T, int NT, int NW, int STAGES, bool SLOPE>
+__global__ __launch_bounds__(64 * NW) void loss_few(LossArgs a) {
+    using Tile = FewTile<T, NT, NW, STAGES>;
+    static_assert(NT == NW, "a wave per block of columns");
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossPlace p = loss_place<16, 16 * NT>(a);
+    if (p.rows <= 0) return;
+    Tile::run((int)a.K, lds, wave, lane, [&](int r) { return loss_row<T>(a, p, r); },
+              [&](int c) { return loss_word<T>(a, p, c); });
+    f32x4 z = Tile::sum(lds, wave, lane);
+    const int r = lane & 15, c = 16 * wave + (lane >> 4) * 4;
+    if constexpr (SLOPE) {
+        T *out = reinterpret_cast<T *>(a.slope) + p.row0 * a.ld;
+        if (r < p.rows) store_quad<T>(out + r * a.ld, p.n0 + c, a.ld, loss_slopes(a, loss_row_of(a, p.row0 + r), z, p.n0 + c), true);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        loss_targets<16 * NT>(a, p, [&](int i, int j, float y) { out[i * a.ld + p.n0 + j] = (T)y; });
+    } else {
+        auto get = [&](int, int) -> f32x4 & { return z; };
+        auto row = [&](int) { return r; };
+        auto col = [&](int) { return c; };
+        loss_pairs<1, 1, NW, 16, 16 * NT>(a, p, p.tile, lds + NW * NT * 1024, wave, lane, get, row, col);
+    }
+}
+
+// Joins a row's pairs and forms its targets' logits; WAVES waves per row.
+template <typename T>
+__device__ __forceinline__ float loss_dot(const char *x, const char *w, int K, int lane) {
+    float sum = 0.f;
+    for (int c = lane * kUnit<T>; c < K; c += 64 * kUnit<T>) {
+        const u32x4 p = load_unit<T>((uint64_t)(x + (int64_t)c * sizeof(T)), K - c);
+        const u32x4 q = load_unit<T>((uint64_t)(w + (int64_t)c * sizeof(T)), K - c);
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; ++e) {
+            if constexpr (sizeof(T) == 4) sum = fmaf(__uint_as_float(p[e]), __uint_as_float(q[e]), sum);
+            else if constexpr (__is_same(T, __bf16))
+                sum = fmaf((float)__builtin_bit_cast(bf16x8, p)[e], (float)__builtin_bit_cast(bf16x8, q)[e], sum);
+            else sum = fmaf((float)__builtin_bit_cast(f16x8, p)[e], (float)__builtin_bit_cast(f16x8, q)[e], sum);
+        }
+    }
+    return lanes_sum<64>(sum);
+}
+template <typename T, int WAVES>
+__global__ __launch_bounds__(256) void loss_join(LossArgs a) {
+    __shared__ float s_at[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (4 / WAVES) + wave / WAVES;
+    const int part = wave % WAVES;
+    if (row >= a.N) return;
+    const int64_t *target = a.target + row * a.picks;
+    const char *x = a.values + row * a.K * (int64_t)sizeof(T);
+    float share = 0.f, at = 0.f;
+    for (int64_t j = 0; j < a.picks; ++j) {
+        const int64_t t = target[j];
+        const bool there = t >= 0 && t < a.V;
+        const float prob = there ? (a.probs ? a.probs[row * a.picks + j] : 1.f) : 0.f;
+        share += prob;
+        if (j % WAVES != part) continue;
+        float z = 0.f;
+        if (there) z = a.scale * loss_dot<T>(x, a.weights + t * a.K * (int64_t)sizeof(T), (int)a.K, lane);
+        if (there) at = fmaf(prob, z, at);
+        if (lane == 0) a.picked[row * a.picks + j] = z;
+    }
+    if constexpr (WAVES > 1) {
+        if (lane == 0) s_at[wave] = at;
+        __syncthreads();
+        if (part > 0) return;
+        at = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) at += s_at[w];
+    }
+    const float2 *pair = a.partial + row * a.parts;
+    float m = -INFINITY, sum = 0.f;
+    for (int64_t i = lane; i < a.parts; i += 64) m = fmaxf(m, pair[i].x);
+    m = lanes_fold<64>(m, [](float p, float q) { return fmaxf(p, q); });
+    const float base = m == -INFINITY ? 0.f : m;
+    for (int64_t i = lane; i < a.parts; i += 64) sum = fmaf(pair[i].y, exp2_fast(pair[i].x - base), sum);
+    sum = lanes_sum<64>(sum);
+    if (lane == 0) {
+        const float lse = kLn2 * (m + __log2f(sum));
+        a.lse[row] = lse;
+        // a row without a target has no loss, whatever its logits are
+        bool live = false;
+        for (int64_t j = 0; j < a.picks; ++j) live = live || (target[j] >= 0 && target[j] < a.V);
+        a.loss[row] = live ? fmaf(share, lse, -at) : 0.f;
+    }
+}
+
+// What the gradient's tiles need of each row.
+__global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a) {
+    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (row >= a.N) return;
+    float share = 0.f, size = 0.f;
+    bool live = false;
+    for (int64_t j = 0; j < a.picks; ++j) {
+        const int64_t t = a.target[row * a.picks + j];
+        if (t < 0 || t >= a.V) continue;
+        const float p = a.probs ? a.probs[row * a.picks + j] : 1.f;
+        share += p;
+        size += fabsf(p);
+        live = true;
+    }
+    const float g = a.grad[row] * a.scale, bound = fabsf(g) * size;
+    a.share[row] = live ? g * share : 0.f;
+    a.hit[row] = g;
+    a.bound[row] = bound < INFINITY ? bound : 0.f;
+    a.live[row] = live ? row : -1;
+}
+
+// float16 holds 2^-24 to 2^16, so dz is brought near 2^13 by a power of two that
+// all rows share (|dz| is at most twice its bound, so below 2^15), and the products take it out again:
+// of the row with the largest bound, probabilities from 2^-37 on are kept, those
+// from 2^-27 on with all bits.
+__global__ __launch_bounds__(1024) void loss_factor(LossArgs a) {
+    __shared__ float s[16];
+    float m = 0.f;
+    for (int64_t i = threadIdx.x; i < a.N; i += 1024) m = fmaxf(m, a.bound[i]);
+    m = lanes_fold<64>(m, [](float p, float q) { return fmaxf(p, q); });
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) m = fmaxf(m, s[w]);
+    const int up = m > 0.f ? min(max(13 - ilogbf(m), -100), 100) : 0;
+    const float f = ldexpf(1.f, up);
+    for (int64_t i = threadIdx.x; i < a.N; i += 1024) {
+        a.share[i] *= f;
+        a.hit[i] *= f;
+    }
+    if (threadIdx.x == 0) {
+        a.factor[0] = f;
+        a.factor[1] = ldexpf(1.f, -up);
+    }
+}
+
+// dx += dz W of a piece: rows of dz in row form, rows of W across the
+// contraction.  `cuts` workgroups share a tile's contraction, each with sums of its
+// own.
+struct LossBack {
+    int64_t row0, n0, cut;
+    int rows;
+};
+template <int BM, int BN>
+__device__ __forceinline__ LossBack loss_back_place(const LossArgs &a) {
+    const int64_t tiles = a.mtiles * a.ntiles, id = xcd_tile(tiles * a.cuts);
+    if (id >= tiles * a.cuts) return {0, 0, 0, 0};
+    const int64_t cut = id / tiles;
+    const TilePlace at = tile_place(id - cut * tiles, a.mtiles, a.ntiles);
+    return {at.m * BM, at.n * BN, cut, (int)min((int64_t)BM, a.N - at.m * BM)};
+}
+__device__ __forceinline__ void loss_add(const LossArgs &a, const LossBack &p, int r, int64_t n, f32x4 c) {
+    if (r >= p.rows) return;
+    float *to = a.sums + ((p.cut * a.N + p.row0 + r) * a.K) + n;
+    if (a.K % 4 == 0) {
+        if (n < a.K) {
+            f32x4 *q = reinterpret_cast<f32x4 *>(to);
+            *q = a.first ? c : *q + c;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.K) to[e] = a.first ? c[e] : to[e] + c[e];
+    }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+struct LossBackTile {
+    static constexpr int kThreads = 64 * WM * WN, kStages = DIRECT ? 3 : 2;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    using AStage = RowStage<T, BM, kThreads, DIRECT>;
+    using BStage = ColStage<T, BN, kThreads, DIRECT>;
+    static constexpr int kStageBytes = AStage::kBytes + BStage::kBytes, kLds = kStages * kStageBytes;
+
+    static __device__ __forceinline__ void run(const LossArgs &a, const LossBack &p, int t0, int t1, lds_char *lds,
+                                               int wave, int lane) {
+        constexpr int kLoads = AStage::kLoads + BStage::kLoads;
+        AStage sa;
+        BStage sb;
+        sa.init(wave, lane, (int)a.ld, [&](int r) -> const char * {
+            return r < p.rows ? a.slope + (p.row0 + r) * a.ld * (int64_t)sizeof(T) : nullptr;
+        });
+        uint64_t wp[BStage::kLoads];
+        int left[BStage::kLoads];
+#pragma unroll
+        for (int i = 0; i < BStage::kLoads; ++i) {
+            const int64_t n = p.n0 + BStage::col(i, wave, lane);
+            wp[i] = (uint64_t)(a.weights + ((a.v0 + BStage::row(i, wave, lane)) * a.K + n) * (int64_t)sizeof(T));
+            left[i] = (int)(a.K - n);
+        }
+        auto issue = [&](int t, lds_char *buf) {
+            const int k0 = t * kStep<T>;
+            const uint64_t step = (uint64_t)k0 * a.K * sizeof(T);
+            sa.issue(buf, wave, k0);
+            sb.issue(
+                buf + AStage::kBytes, wave, [&](int i) { return wp[i] + step; },
+                [&](int i) { return k0 + BStage::row(i, wave, lane) < a.vc ? left[i] : 0; });
+        };
+        f32x4 acc[MT][NT] = {};
+        const int m_w = wave / WN * (MT * 16), n_w = wave % WN * (NT * 16);
+        auto products = [&](const lds_char *buf) {
+            step_products<T, MT, NT, false, BM, true, BN>(acc, buf, buf + AStage::kBytes, m_w, n_w, lane);
+        };
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int t = 0; t < kStages - 1; ++t) issue(t0 + t, lds + t * kStageBytes);
+            int cur = 0, fill = kStages - 1;
+            for (int t = t0; t < t1; ++t) {
+                wait_and_meet<(kStages - 2) * kLoads>();
+                issue(t + kStages - 1, lds + fill * kStageBytes);
+                products(lds + cur * kStageBytes);
+                cur = cur + 1 == kStages ? 0 : cur + 1;
+                fill = fill + 1 == kStages ? 0 : fill + 1;
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+            issue(t0, lds);
+            sa.commit(lds, wave, lane);
+            sb.commit(lds + AStage::kBytes, wave, lane);
+            for (int t = t0; t < t1; ++t) {
+                lds_char *next = lds + ((t + 1 - t0) & 1) * kStageBytes;
+                __syncthreads();
+                if (t + 1 < t1) issue(t + 1, next);
+                products(lds + ((t - t0) & 1) * kStageBytes);
+                if (t + 1 < t1) {
+                    sa.commit(next, wave, lane);
+                    sb.commit(next + AStage::kBytes, wave, lane);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                loss_add(a, p, m_w + 16 * i + (lane & 15), p.n0 + n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+    }
+};
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void loss_back(LossArgs a) {
+    using Tile = LossBackTile<T, BM, BN, WM, WN, DIRECT>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossBack p = loss_back_place<BM, BN>(a);
+    if (p.rows <= 0) return;
+    const int64_t steps = (a.vc + kStep<T> - 1) / kStep<T>;
+    Tile::run(a, p, (int)(p.cut * steps / a.cuts), (int)((p.cut + 1) * steps / a.cuts), (lds_char *)lds_mem, wave, lane);
+}
+
+// Float in bf16 parts, as above where a sum is not finite.
+template <bool WHOLE>
+__global__ __launch_bounds__(kRowSplitThreads, 3) void loss_back_split(LossArgs a) {
+    constexpr int BM = 64, BN = 128, MT = 2, NT = 4;
+    using Plain = LossBackTile<float, 64, 64, 2, 2, false>;
+    using SA = SplitStage<BM, kRowSplitThreads, false, true>;  // rows of dz hold whole parts
+    using SB = SplitStage<BN, kRowSplitThreads, true, WHOLE>;
+    constexpr int kLds = SA::kLds + SB::kLds;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kLds > Plain::kLds ? kLds : Plain::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const LossBack p = loss_back_place<BM, BN>(a);
+    if (p.rows <= 0) return;
+    const int64_t steps = (a.vc + kSplitK - 1) / kSplitK;
+    const int64_t t0 = p.cut * steps / a.cuts, t1 = (p.cut + 1) * steps / a.cuts;
+    SA sa;
+    SB sb;
+    uint64_t ap[SA::kParts], bp[SB::kParts];
+    int aleft[SA::kParts], bleft[SB::kParts];
+#pragma unroll
+    for (int i = 0; i < SA::kParts; ++i) {
+        const int r = SA::row(i, tid);
+        ap[i] = (uint64_t)(a.slope + ((p.row0 + r) * a.ld + SA::at(i, tid)) * 4);
+        aleft[i] = r < p.rows ? (int)a.ld - SA::at(i, tid) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < SB::kParts; ++i) {
+        const int64_t n = p.n0 + SB::at(i, tid);
+        bp[i] = (uint64_t)(a.weights + ((a.v0 + SB::row(i, tid)) * a.K + n) * 4);
+        bleft[i] = (int)(a.K - n);
+    }
+    f32x4 acc[MT][NT] = {};
+    const int m_w = wave / 2 * (BM / 2), n_w = wave % 2 * (BN / 2);
+    split_steps(
+        t1 - t0,
+        [&](int64_t t) {
+            const int64_t k0 = (t0 + t) * kSplitK;
+            sa.issue([&](int i) { return ap[i] + (uint64_t)k0 * 4; }, [&](int i) { return aleft[i] - (int)k0; });
+            sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * a.K * 4; },
+                     [&](int i) { return k0 + SB::row(i, tid) < a.vc ? bleft[i] : 0; });
+        },
+        [&] {
+            sa.commit(lds, tid);
+            sb.commit(lds + SA::kLds, tid);
+        },
+        [&] { split_step<MT, NT, false, BM, true, BN>(acc, lds, lds + SA::kLds, m_w, n_w, lane); });
+    if (__syncthreads_or(any_not_finite(acc))) {
+        // in steps of the same length
+        static_assert(kStep<float> == kSplitK, "cuts agree");
+        for (int c = 0; c < BN && p.n0 + c < a.K; c += 64) {
+            const LossBack q{p.row0, p.n0 + c, p.cut, p.rows};
+            __syncthreads();
+            Plain::run(a, q, (int)t0, (int)t1, lds, wave, lane);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            loss_add(a, p, m_w + 16 * i + (lane & 15), p.n0 + n_w + 16 * j + (lane >> 4) * 4, acc[i][j]);
+}
+
+// 128 rows x 256 columns in phases, 16-bit types.
+template <typename T>
+__global__ __launch_bounds__(kPhaseThreads) void loss_back_many(LossArgs a) {
+    using AStage = RowStage<T, kHalf, kPhaseThreads, true>;
+    using BStage = ColStage<T, kHalf, kPhaseThreads, true>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossBack p = loss_back_place<kHalf, 2 * kHalf>(a);
+    if (p.rows <= 0) return;
+    const int64_t steps = (a.vc + kStep<T> - 1) / kStep<T>;
+    const int t0 = (int)(p.cut * steps / a.cuts), t1 = (int)((p.cut + 1) * steps / a.cuts);
+    AStage sa;
+    sa.init(wave, lane, (int)a.ld, [&](int r) -> const char * {
+        return r < p.rows ? a.slope + (p.row0 + r) * a.ld * (int64_t)sizeof(T) : nullptr;
+    });
+    BStage sb;
+    uint64_t wp[2][BStage::kLoads];
+    int left[2][BStage::kLoads];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < BStage::kLoads; ++i) {
+            const int64_t n = p.n0 + h * kHalf + BStage::col(i, wave, lane);
+            wp[h][i] = (uint64_t)(a.weights + ((a.v0 + BStage::row(i, wave, lane)) * a.K + n) * (int64_t)sizeof(T));
+            left[h][i] = (int)(a.K - n);
+        }
+    f32x4 acc[2][2][4][2] = {};
+    auto fetch_a = [&](int, int t, lds_char *place) { sa.issue(place, wave, (t0 + t) * kStep<T>); };
+    auto fetch_b = [&](int h, int t, lds_char *place) {
+        const int k0 = (t0 + t) * kStep<T>;
+        const uint64_t step = (uint64_t)k0 * a.K * sizeof(T);
+        sb.issue(
+            place, wave, [&](int i) { return wp[h][i] + step; },
+            [&](int i) { return k0 + BStage::row(i, wave, lane) < a.vc ? left[h][i] : 0; });
+    };
+    auto products = [](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+    phase_steps<T, 1, true>(acc, lds, t1 - t0, wave, lane, fetch_a, fetch_b, products);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                loss_add(a, p, phase_row(0, i, wave) + (lane & 15), p.n0 + phase_col(q, j, wave) + (lane >> 4) * 4,
+                         acc[0][q][i][j]);
+}
+
+// Adds the cuts' sums in order and rounds once.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_back_join(LossArgs a) {
+    const int64_t i = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4, all = a.N * a.K;
+    if (i >= all) return;
+    const float f = a.factor ? a.factor[1] : 1.f;
+    if (i + 4 <= all) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        typedef f32x4 __attribute__((aligned(4))) quad4;
+        for (int64_t c = 0; c < a.cuts; ++c) s += *reinterpret_cast<const quad4 *>(a.sums + c * all + i);
+        T *to = static_cast<T *>(a.grad_values) + i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = (T)(s[e] * f);
+    } else {
+        for (int64_t j = i; j < all; ++j) {
+            float s = 0.f;
+            for (int64_t c = 0; c < a.cuts; ++c) s += a.sums[c * all + j];
+            static_cast<T *>(a.grad_values)[j] = (T)(s * f);
+        }
+    }
+}
+
+// --------------------------------------------------------------------- host
+
+constexpr int64_t kLossFewRows = 16;
+// Kernels of the tiles: columns that a pair covers.
+enum LossKind { kLossFew, kLossSmall, kLossOne, kLossTwo, kLossSplit, kLossAny };
+LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) {
+    if (dtype == SEGRED_F32) return direct && n <= 8 ? kLossFew : kLossSplit;
+    if (!direct) return kLossAny;
+    if (n <= kLossFewRows) return kLossFew;
+    if (k < 256 || ((n + 127) / 128) * ((v + 255) / 256) < 128) return kLossSmall;
+    return n > 128 ? kLossTwo : kLossOne;
+}
+int64_t loss_columns(LossKind kind) {
+    return kind == kLossOne || kind == kLossTwo ? 256 : kind == kLossSmall || kind == kLossAny ? 128 : 64;
+}
+
+template <typename T, bool SLOPE>
+int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
+    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne ? 128 : kind == kLossFew ? 16 : 64;
+    const int64_t bn = kind == kLossSplit ? 128 : loss_columns(kind);
+    a.mtiles = (a.N + bm - 1) / bm;
+    a.ntiles = (a.vc + bn - 1) / bn;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if constexpr (sizeof(T) == 4) {
+        if (kind == kLossFew) timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a);
+        else if (a.K % 8 == 0) timed_launch_ggl(true, (loss_split<true, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
+        else timed_launch_ggl(true, (loss_split<false, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
+    } else {
+        switch (kind) {
+        case kLossFew: timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a); break;
+        case kLossSmall:
+            timed_launch_ggl(true, (loss_tiles<T, 64, 128, 2, 2, 2, true, SLOPE>), grid, dim3(256), 0, st, a);
+            break;
+        case kLossOne: timed_launch_ggl(true, (loss_many<T, 1, SLOPE>), grid, dim3(kPhaseThreads), 0, st, a); break;
+        case kLossTwo: timed_launch_ggl(true, (loss_many<T, 2, SLOPE>), grid, dim3(kPhaseThreads), 0, st, a); break;
+        default: timed_launch_ggl(true, (loss_tiles<T, 64, 128, 2, 2, 2, false, SLOPE>), grid, dim3(256), 0, st, a); break;
+        }
+    }
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+int64_t loss_parts(LossKind kind, int64_t v) {
+    const int64_t c = loss_columns(kind);
+    // in pairs of 64 columns of 128
+    return kind == kLossSplit ? (v + 127) / 128 * 2 : (v + c - 1) / c;
+}
+
+// What both calls ask of the arguments that they share.
+int loss_check(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights, int64_t vocab,
+               const int64_t *target, const float *probs, int64_t picks, float scale, const void *workspace) {
+    const int64_t e = float_size(dtype);
+    if (dtype < SEGRED_U32 || dtype > SEGRED_F16 || k < 1 || rows < 0 || vocab < 1 || picks < 1)
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!(scale > 0.f) || std::isinf(scale)) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!weights || (rows > 0 && (!values || !target))) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (e == 0 || k > kMaxWidth || vocab > (int64_t(1) << 30) || picks > (int64_t(1) << 20) || rows > (int64_t(1) << 31))
+        return SEGRED_ERR_UNSUPPORTED;
+    if (!aligned(values, e) || !aligned(weights, e) || !aligned(target, 8) || !aligned(probs, 4) || !aligned(workspace, 16))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    return SEGRED_OK;
+}
+
+bool loss_direct(const void *values, const void *weights, int32_t dtype, int64_t k) {
+    return (k * float_size(dtype)) % 16 == 0 && aligned(values, 16) && aligned(weights, 16);
+}
+
+LossArgs loss_args(const void *values, int64_t k, int64_t rows, const void *weights, int64_t vocab,
+                   const int64_t *target, const float *probs, int64_t picks, float scale) {
+    LossArgs a{};
+    a.values = static_cast<const char *>(values);
+    a.weights = static_cast<const char *>(weights);
+    a.target = target;
+    a.probs = probs;
+    a.N = rows;
+    a.V = a.vc = vocab;
+    a.K = k;
+    a.picks = picks;
+    a.scale = scale;
+    a.bend = scale * kLog2e;
+    return a;
+}
+
+template <typename T>
+int loss_forward(const LossArgs &a, LossKind kind, hipStream_t st) {
+    const int rc = loss_tiles_launch<T, false>(a, kind, st);
+    if (rc != SEGRED_OK) return rc;
+    dim3 grid;
+    if (!tile_grid(a.picks > 1 ? a.N : (a.N + 3) / 4, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (a.picks > 1) timed_launch_ggl(false, (loss_join<T, 4>), grid, dim3(256), 0, st, a);
+    else timed_launch_ggl(false, (loss_join<T, 1>), grid, dim3(256), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+// The gradient's pieces and its working memory.
+struct LossPlan {
+    int64_t piece, cuts;  // columns of a piece; workgroups that share a tile of dx
+    bool many;            // dx in tiles of 128 x 256
+    int64_t slope, sums, share, hit, bound, live, offsets, factor, outer, bytes;  // places
+};
+constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096;
+LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v) {
+    const int64_t e = float_size(dtype);
+    LossPlan p{};
+    p.piece = std::min(v, std::max(kPieceLeast, kPieceBytes / (std::max<int64_t>(n, 1) * e) / 256 * 256));
+    // pieces of about the same size
+    const int64_t pieces = (v + p.piece - 1) / p.piece;
+    p.piece = std::min(v, ((v + pieces - 1) / pieces + 255) / 256 * 256);
+    p.many = e == 2 && n > 64 && k > 128;
+    const int64_t tiles = p.many ? ((n + 127) / 128) * ((k + 255) / 256)
+                                 : (n <= 16 && e == 2 ? 1 : (n + 63) / 64) * ((k + 127) / 128);
+    const int64_t room = p.many ? 256 : 512, steps = (p.piece + 63) / 64;
+    p.cuts = std::max<int64_t>(1, std::min({room / std::max<int64_t>(tiles, 1), steps / 8, (int64_t)64}));
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    p.slope = take(n * ((p.piece + 7) / 8 * 8) * e);
+    p.sums = take(p.cuts * n * k * 4);
+    p.share = take(n * 4);
+    p.hit = take(n * 4);
+    p.bound = take(n * 4);
+    p.live = take(n * 8);
+    p.offsets = take(16);
+    p.factor = take(8);
+    // the last piece is no wider than the others, but may be cut otherwise
+    const int64_t last = v - (pieces - 1) * p.piece;
+    p.outer = take(std::max(segred_outer_workspace(p.piece, k, 1, n), last > 0 ? segred_outer_workspace(last, k, 1, n) : 0));
+    p.bytes = at;
+    return p;
+}
+
+__global__ void loss_bounds(int64_t *offsets, int64_t n) {
+    offsets[0] = 0;
+    offsets[1] = n;
+}
+
+template <typename T>
+int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int32_t dtype, void *grad_weights,
+                  int32_t grad_weights_dtype, char *work, hipStream_t st) {
+    const int64_t e = sizeof(T), ge = float_size(grad_weights_dtype);
+    int64_t *offsets = reinterpret_cast<int64_t *>(work + p.offsets);
+    if (grad_weights) timed_launch_ggl(false, loss_bounds, dim3(1), dim3(1), 0, st, offsets, a.N);
+    if (a.N > 0) {
+        timed_launch_ggl(false, loss_rows_prepare, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, st, a);
+        if (__is_same(T, _Float16)) timed_launch_ggl(false, loss_factor, dim3(1), dim3(1024), 0, st, a);
+    }
+    if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
+    for (a.v0 = 0; a.v0 < a.V; a.v0 += p.piece) {
+        a.vc = std::min(p.piece, a.V - a.v0);
+        a.ld = (a.vc + 7) / 8 * 8;
+        a.first = a.v0 == 0;
+        if (a.N > 0) {
+            const int rc = loss_tiles_launch<T, true>(a, kind, st);
+            if (rc != SEGRED_OK) return rc;
+        }
+        if (a.grad_values && a.N > 0) {
+            LossArgs b = a;
+            const int64_t bm = p.many ? 128 : a.N <= 16 && e == 2 ? 16 : 64, bn = p.many && direct ? 256 : 128;
+            b.mtiles = (a.N + bm - 1) / bm;
+            b.ntiles = (a.K + bn - 1) / bn;
+            dim3 grid;
+            if (!tile_grid(b.mtiles * b.ntiles * b.cuts, grid)) return SEGRED_ERR_UNSUPPORTED;
+            if constexpr (sizeof(T) == 4) {
+                if (a.K % 8 == 0) timed_launch_ggl(true, (loss_back_split<true>), grid, dim3(kRowSplitThreads), 0, st, b);
+                else timed_launch_ggl(true, (loss_back_split<false>), grid, dim3(kRowSplitThreads), 0, st, b);
+            } else if (p.many && direct) {
+                timed_launch_ggl(true, (loss_back_many<T>), grid, dim3(kPhaseThreads), 0, st, b);
+            } else if (p.many) {
+                timed_launch_ggl(true, (loss_back<T, 128, 128, 2, 2, false>), grid, dim3(256), 0, st, b);
+            } else if (bm == 16) {
+                if (direct) timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, true>), grid, dim3(256), 0, st, b);
+                else timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, false>), grid, dim3(256), 0, st, b);
+            } else {
+                if (direct) timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, true>), grid, dim3(256), 0, st, b);
+                else timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, false>), grid, dim3(256), 0, st, b);
+            }
+            if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
+        }
+        if (grad_weights) {
+            const int rc = outer_scaled(a.slope, a.ld, a.vc, a.values, a.live, a.N, a.K, dtype, offsets,
+                                        static_cast<char *>(grad_weights) + a.v0 * a.K * ge, grad_weights_dtype,
+                                        a.factor ? a.factor + 1 : nullptr, work + p.outer, st);
+            if (rc != SEGRED_OK) return rc;
+        }
+    }
+    if (a.grad_values && a.N > 0) {
+        dim3 grid;
+        if (!tile_grid((a.N * a.K + 1023) / 1024, grid)) return SEGRED_ERR_UNSUPPORTED;
+        timed_launch_ggl(false, (loss_back_join<T>), grid, dim3(256), 0, st, a);
+    }
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+}  // namespace segred
+
+using namespace segred;
+
+extern "C" int64_t segred_cross_entropy_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab) {
+    if (float_size(dtype) == 0 || k < 1 || rows < 1 || vocab < 1 || too_large(rows, vocab, 8)) return 0;
+    // the smallest pairs, whatever kernel the pointers' alignment chooses
+    return rows * ((vocab + 127) / 128 * 2) * 8;
+}
+
+extern "C" int segred_cross_entropy(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights,
+                                    int64_t vocab, const int64_t *target, const float *probs, int64_t picks,
+                                    float scale, float *loss, float *lse, float *picked, void *workspace,
+                                    int64_t workspace_bytes, hipStream_t stream) {
+    const int rc = loss_check(values, dtype, k, rows, weights, vocab, target, probs, picks, scale, workspace);
+    if (rc != SEGRED_OK) return rc;
+    if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(picked, 4)) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return SEGRED_OK;
+    if (!loss || !lse || !picked || !workspace ||
+        workspace_bytes < segred_cross_entropy_workspace(dtype, k, rows, vocab))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    LossArgs a = loss_args(values, k, rows, weights, vocab, target, probs, picks, scale);
+    const LossKind kind = loss_kind(dtype, rows, k, vocab, loss_direct(values, weights, dtype, k));
+    a.partial = static_cast<float2 *>(workspace);
+    a.parts = loss_parts(kind, vocab);
+    a.loss = loss;
+    a.lse = lse;
+    a.picked = picked;
+    switch (dtype) {
+    case SEGRED_BF16: return loss_forward<__bf16>(a, kind, stream);
+    case SEGRED_F16: return loss_forward<_Float16>(a, kind, stream);
+    default: return loss_forward<float>(a, kind, stream);
+    }
+}
+
+extern "C" int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab) {
+    if (float_size(dtype) == 0 || k < 1 || k > kMaxWidth || rows < 0 || vocab < 1 || vocab > (int64_t(1) << 30) ||
+        rows > (int64_t(1) << 31))
+        return 0;
+    return loss_plan(dtype, k, rows, vocab).bytes;
+}
+
+extern "C" int segred_cross_entropy_grad(const float *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
+                                         const void *weights, int64_t vocab, const int64_t *target,
+                                         const float *probs, int64_t picks, float scale, const float *lse,
+                                         const float *picked, void *grad_values, void *grad_weights,
+                                         int32_t grad_weights_dtype, void *workspace, int64_t workspace_bytes,
+                                         hipStream_t stream) {
+    const int rc = loss_check(values, dtype, k, rows, weights, vocab, target, probs, picks, scale, workspace);
+    if (rc != SEGRED_OK) return rc;
+    const int64_t e = float_size(dtype);
+    if (grad_weights_dtype != dtype && grad_weights_dtype != SEGRED_F32) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && (!grad || !lse || !picked)) return SEGRED_ERR_INVALID_ARGUMENT;
+    if (!aligned(grad, 4) || !aligned(lse, 4) || !aligned(picked, 4) || !aligned(grad_values, e) ||
+        !aligned(grad_weights, float_size(grad_weights_dtype)))
+        return SEGRED_ERR_INVALID_ARGUMENT;
+    const LossPlan p = loss_plan(dtype, k, rows, vocab);
+    if (!workspace || workspace_bytes < p.bytes) return SEGRED_ERR_INVALID_ARGUMENT;
+    LossArgs a = loss_args(values, k, rows, weights, vocab, target, probs, picks, scale);
+    char *work = static_cast<char *>(workspace);
+    a.grad = grad;
+    a.lse = const_cast<float *>(lse);
+    a.picked = const_cast<float *>(picked);
+    a.grad_values = grad_values;
+    a.slope = work + p.slope;
+    a.sums = reinterpret_cast<float *>(work + p.sums);
+    a.share = reinterpret_cast<float *>(work + p.share);
+    a.hit = reinterpret_cast<float *>(work + p.hit);
+    a.bound = reinterpret_cast<float *>(work + p.bound);
+    a.live = reinterpret_cast<int64_t *>(work + p.live);
+    a.factor = dtype == SEGRED_F16 && rows > 0 ? reinterpret_cast<float *>(work + p.factor) : nullptr;
+    a.cuts = p.cuts;
+    const bool direct = loss_direct(values, weights, dtype, k);
+    const LossKind kind = loss_kind(dtype, rows, k, p.piece, direct);
+    switch (dtype) {
+    case SEGRED_BF16: return loss_backward<__bf16>(a, p, kind, direct, dtype, grad_weights, grad_weights_dtype, work, stream);
+    case SEGRED_F16: return loss_backward<_Float16>(a, p, kind, direct, dtype, grad_weights, grad_weights_dtype, work, stream);
+    default: return loss_backward<float>(a, p, kind, direct, dtype, grad_weights, grad_weights_dtype, work, stream);
+    }
+}

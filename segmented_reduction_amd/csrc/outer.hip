@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "internal.hpp"
+#include "outer.hpp"
 #include "tile.hpp"
 
 namespace segred {
@@ -22,6 +23,8 @@ struct OuterArgs {
     void *out;      // T or float [S, K, M]
     float *partial;  // [slots, K, M], when a segment may have more than one slot
     int out_f32, vec;
+    int64_t width;       // elements from one row of `left` to the next, K or more
+    const float *scale;  // what the sums are multiplied by, or null
 };
 
 // What a workgroup computes: a tile of one slot's sum.
@@ -98,6 +101,7 @@ int64_t outer_tiles(const OuterArgs &a) {
 // Four sums of row r from column n: a partial one of the slot, or the result.
 template <typename T>
 __device__ __forceinline__ void outer_store(const OuterArgs &a, int64_t s, int64_t slot, int64_t r, int64_t n, f32x4 c) {
+    if (a.scale && !a.partial) c *= *a.scale;
     if (a.partial)
         store_quad<float>(a.partial + (slot * a.K + r) * a.M, n, a.M, c, a.vec != 0);
     else if (a.out_f32)
@@ -188,7 +192,7 @@ struct OuterTile {
     // O: the type of a result that is not float.
     template <typename O = T>
     static __device__ __forceinline__ void run(const OuterArgs &a, const OuterPlace &at, lds_char *lds, int wave, int lane) {
-        const int64_t m0 = at.m0, n0 = at.n0, lb = a.K * (int64_t)sizeof(L), rb = a.M * (int64_t)sizeof(Q);
+        const int64_t m0 = at.m0, n0 = at.n0, lb = a.width * (int64_t)sizeof(L), rb = a.M * (int64_t)sizeof(Q);
         SA sa;
         SB sb;
         OuterSide<SA::kLoads> left;
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(kSplitThreads, 3) void seg_outer_split(OuterArgs a)
     auto rrow = [&](int i) { return SB::row(i, tid); };
     auto lcol = [&](int i) { return (int)(a.K - at.m0) - SA::at(i, tid); };
     auto rcol = [&](int i) { return (int)(a.M - at.n0) - SB::at(i, tid); };
-    left.init(at, a.left_rows, a.left_count, a.left, a.K * (int64_t)sizeof(L), kSplitK, lrow,
+    left.init(at, a.left_rows, a.left_count, a.left, a.width * (int64_t)sizeof(L), kSplitK, lrow,
               [&](int i) { return (at.m0 + SA::at(i, tid)) * (int64_t)sizeof(L); });
     right.init(at, a.right_rows, a.right_count, a.right, a.M * (int64_t)sizeof(Q), kSplitK, rrow,
                [&](int i) { return (at.n0 + SB::at(i, tid)) * (int64_t)sizeof(Q); });
@@ -356,6 +360,7 @@ __global__ __launch_bounds__(kJoinThreads) void outer_join(OuterArgs a) {
 #pragma unroll
         for (int q = 1; q < PARTS; ++q) sum += s_part[q][cell];
     }
+    if (a.scale) sum *= *a.scale;
     if (i < a.S * cells) {
         if (a.out_f32) static_cast<float *>(a.out)[i] = sum;
         else static_cast<T *>(a.out)[i] = (T)sum;
@@ -422,7 +427,7 @@ int outer_split_launch(OuterArgs a, hipStream_t st) {
     a.ntiles = (a.M + BN - 1) / BN;
     dim3 grid;
     if (!tile_grid(outer_tiles(a), grid)) return SEGRED_ERR_UNSUPPORTED;
-    if (a.K % 8 == 0 && a.M % 8 == 0)
+    if (a.width % 8 == 0 && a.M % 8 == 0)
         timed_launch_ggl(true, (seg_outer_split<BM, BN, true, L, Q>), grid, dim3(kSplitThreads), 0, st, a);
     else
         timed_launch_ggl(true, (seg_outer_split<BM, BN, false, L, Q>), grid, dim3(kSplitThreads), 0, st, a);
@@ -443,6 +448,37 @@ int outer_dispatch(const OuterArgs &a, const OuterPlan &p, bool direct, hipStrea
         if (p.wide) return outer_launch<T, 64, 128, 2, 2>(a, direct, st);
         if (p.small) return outer_launch<T, 64, 64, 2, 2>(a, direct, st);
         return outer_launch<T, 128, 128, 2, 2>(a, direct, st);
+    }
+}
+
+int outer_scaled(const void *left, int64_t width, int64_t vc, const void *right, const int64_t *right_rows, int64_t n,
+                 int64_t m, int32_t dtype, const int64_t *offsets, void *out, int32_t out_dtype, const float *scale,
+                 void *workspace, hipStream_t stream) {
+    const int64_t e = float_size(dtype), oe = float_size(out_dtype);
+    OuterArgs a{};
+    a.left = static_cast<const char *>(left);
+    a.right = static_cast<const char *>(right);
+    a.right_rows = right_rows;
+    a.left_count = a.right_count = n;
+    a.offsets = offsets;
+    a.S = 1;
+    a.N = n;
+    a.K = vc;
+    a.width = width;
+    a.M = m;
+    const OuterPlan plan = outer_plan(vc, m, 1, n);
+    a.step = plan.step;
+    a.slots = n / a.step + 1;
+    a.out = out;
+    a.out_f32 = out_dtype == SEGRED_F32;
+    a.partial = plan.step == kWhole ? nullptr : static_cast<float *>(workspace);
+    a.scale = scale;
+    a.vec = (m % 4 == 0 && aligned(out, 4 * oe)) ? 1 : 0;
+    const bool direct = (width * e) % 16 == 0 && (m * e) % 16 == 0 && aligned(left, 16) && aligned(right, 16);
+    switch (dtype) {
+    case SEGRED_BF16: return outer_dispatch<__bf16>(a, plan, direct, stream);
+    case SEGRED_F16: return outer_dispatch<_Float16>(a, plan, direct, stream);
+    default: return outer_dispatch<float>(a, plan, direct, stream);
     }
 }
 
@@ -501,7 +537,7 @@ extern "C" int segred_outer_mixed(const void *left, int32_t left_dtype, const in
     a.offsets = offsets;
     a.S = num_segments;
     a.N = num_rows;
-    a.K = k;
+    a.K = a.width = k;
     a.M = m;
     const OuterPlan plan = outer_plan(k, m, num_segments, num_rows);
     a.step = plan.step;

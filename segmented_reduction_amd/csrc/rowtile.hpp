@@ -1,0 +1,253 @@
+// rowtile.hpp -- tiles of x W^T whose sums stay in registers for an epilogue of
+// the caller's: gated projections and the softmax cross entropy.
+//
+// Both operands run along the contraction in memory (row form, tile.hpp).  The
+// caller names their rows: arow(r) and brow(c) give the start of tile row r's
+// and tile column c's operand row, or null for a row of zeros.
+#pragma once
+
+#include "internal.hpp"
+#include "tile.hpp"
+
+namespace segred {
+
+// A BM x BN tile of WM x WN waves: acc[i][j] are the wave's neighbouring 16 x 16
+// blocks.  Afterwards all LDS has been read and written.
+template <typename T, int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
+struct RowTile {
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    using AStage = RowStage<T, BM, kThreads, DIRECT>;
+    using BStage = RowStage<T, BN, kThreads, DIRECT>;
+    static constexpr int kStageBytes = AStage::kBytes + BStage::kBytes;
+    static constexpr int kLds = STAGES * kStageBytes;
+    static_assert(DIRECT || STAGES == 2, "units that pass through registers use two buffers");
+    // Row and column of block (0, 0) of a wave.
+    static __device__ __forceinline__ int m0(int wave) { return wave / WN * (MT * 16); }
+    static __device__ __forceinline__ int n0(int wave) { return wave % WN * (NT * 16); }
+
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void run(f32x4 (&acc)[MT][NT], int K, lds_char *lds, int wave, int lane, FA arow,
+                                               FB brow) {
+        constexpr int kLoads = AStage::kLoads + BStage::kLoads;
+        AStage sa;
+        BStage sb;
+        sa.init(wave, lane, K, arow);
+        sb.init(wave, lane, K, brow);
+        auto issue = [&](int t, lds_char *buf) {
+            sa.issue(buf, wave, t * kStep<T>);
+            sb.issue(buf + AStage::kBytes, wave, t * kStep<T>);
+        };
+        auto commit = [&](lds_char *buf) {
+            sa.commit(buf, wave, lane);
+            sb.commit(buf + AStage::kBytes, wave, lane);
+        };
+        auto products = [&](const lds_char *buf) {
+            step_products<T, MT, NT, false, BM, false, BN>(acc, buf, buf + AStage::kBytes, m0(wave), n0(wave), lane);
+        };
+        const int steps = (K + kStep<T> - 1) / kStep<T>;
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int t = 0; t < STAGES - 1; ++t) issue(t, lds + t * kStageBytes);
+            int cur = 0, fill = STAGES - 1;
+            for (int t = 0; t < steps; ++t) {
+                wait_and_meet<(STAGES - 2) * kLoads>();
+                issue(t + STAGES - 1, lds + fill * kStageBytes);
+                products(lds + cur * kStageBytes);
+                cur = cur + 1 == STAGES ? 0 : cur + 1;
+                fill = fill + 1 == STAGES ? 0 : fill + 1;
+            }
+            // the last loads write zeros into LDS; they must land before it is given away
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+            issue(0, lds);
+            commit(lds);
+            for (int t = 0; t < steps; ++t) {
+                __syncthreads();
+                if (t + 1 < steps) issue(t + 1, lds);
+                products(lds + (t & 1) * kStageBytes);
+                if (t + 1 < steps) commit(lds + ((t + 1) & 1) * kStageBytes);
+            }
+        }
+        __syncthreads();
+    }
+};
+
+// AH * 128 rows x 256 columns in phases, 16-bit types, rows of whole 16-byte
+// units.  acc[a][b] are the quadrants; brow's column c of half h is h * 128 + c.
+// A tile of at most 128 rows walks the steps of one half only.
+template <typename T, int AH>
+struct PhaseTile {
+    using Stage = RowStage<T, kHalf, kPhaseThreads, true>;
+
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void run(f32x4 (&acc)[2][2][4][2], int rows, int K, lds_char *lds, int wave,
+                                               int lane, FA arow, FB brow) {
+        Stage sa[AH], sb[2];
+#pragma unroll
+        for (int h = 0; h < AH; ++h) sa[h].init(wave, lane, K, [&](int r) { return arow(h * kHalf + r); });
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sb[h].init(wave, lane, K, [&](int c) { return brow(h * kHalf + c); });
+        auto fetch_a = [&](int h, int t, lds_char *place) { sa[h].issue(place, wave, t * kStep<T>); };
+        auto fetch_b = [&](int h, int t, lds_char *place) { sb[h].issue(place, wave, t * kStep<T>); };
+        auto products = [](f32x4 (&c)[4][2], const u32x4 (&x)[2][4], const u32x4 (&y)[2][2]) { quadrant<T>(c, x, y); };
+        const int steps = (K + kStep<T> - 1) / kStep<T>;
+        if (AH == 2 && rows > kHalf)
+            phase_steps<T, AH, false>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products);
+        else
+            phase_steps<T, 1, false>(acc, lds, steps, wave, lane, fetch_a, fetch_b, products);
+        __syncthreads();
+    }
+};
+
+// Float in three bf16 parts, BM x BN by four waves, 2 by 2.  False where a sum is
+// not finite: then the caller has the tile computed again by RowTile<float, ...>.
+constexpr int kRowSplitThreads = 256;
+template <int BM, int BN, bool WHOLE>
+struct SplitTile {
+    using Stage = SplitStage<BM, kRowSplitThreads, false, WHOLE>;
+    using BStage = SplitStage<BN, kRowSplitThreads, false, WHOLE>;
+    static constexpr int MT = BM / 32, NT = BN / 32;
+    static constexpr int kLds = Stage::kLds + BStage::kLds;
+    static __device__ __forceinline__ int m0(int wave) { return wave / 2 * (BM / 2); }
+    static __device__ __forceinline__ int n0(int wave) { return wave % 2 * (BN / 2); }
+
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ bool run(f32x4 (&acc)[MT][NT], int K, lds_char *lds, int tid, FA arow, FB brow) {
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        Stage sa;
+        BStage sb;
+        uint64_t ap[Stage::kParts], bp[BStage::kParts];
+        int aleft[Stage::kParts], bleft[BStage::kParts];
+#pragma unroll
+        for (int i = 0; i < Stage::kParts; ++i) {
+            const char *q = arow(Stage::row(i, tid));
+            ap[i] = (uint64_t)(q + Stage::at(i, tid) * 4);
+            aleft[i] = q ? K - Stage::at(i, tid) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < BStage::kParts; ++i) {
+            const char *q = brow(BStage::row(i, tid));
+            bp[i] = (uint64_t)(q + BStage::at(i, tid) * 4);
+            bleft[i] = q ? K - BStage::at(i, tid) : 0;
+        }
+        split_steps(
+            (K + kSplitK - 1) / kSplitK,
+            [&](int64_t t) {
+                const int k0 = (int)t * kSplitK;
+                sa.issue([&](int i) { return ap[i] + (uint64_t)k0 * 4; }, [&](int i) { return aleft[i] - k0; });
+                sb.issue([&](int i) { return bp[i] + (uint64_t)k0 * 4; }, [&](int i) { return bleft[i] - k0; });
+            },
+            [&] {
+                sa.commit(lds, tid);
+                sb.commit(lds + Stage::kLds, tid);
+            },
+            [&] { split_step<MT, NT, false, BM, false, BN>(acc, lds, lds + Stage::kLds, m0(wave), n0(wave), lane); });
+        return !__syncthreads_or(any_not_finite(acc));
+    }
+};
+
+// 16 rows x 16 NT columns, the contraction split over NW waves, rows of whole
+// units.  Each quad of four columns of all NT blocks belongs to one thread
+// afterwards: out(block j, row, column in the block, sum), j uniform in a wave.
+template <typename T, int NT, int NW, int STAGES>
+struct FewTile {
+    using AStage = RowStage<T, 16, 64, true>;
+    using BStage = RowStage<T, 16 * NT, 64, true>;
+    static constexpr int kThreads = 64 * NW;
+    static constexpr int kStageBytes = AStage::kBytes + BStage::kBytes;
+    static constexpr int kLds = NW * STAGES * kStageBytes;
+
+    // Leaves the waves' sums in LDS, each NT KiB: quad `lane` of block j of wave w
+    // at (w * NT + j) * 1024 + lane * 16.
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void run(int K, lds_char *lds, int wave, int lane, FA arow, FB brow) {
+        AStage sa;
+        BStage sb;
+        sa.init(0, lane, K, arow);
+        sb.init(0, lane, K, brow);
+        f32x4 acc[1][NT] = {};
+        const int steps = (K + kStep<T> - 1) / kStep<T>;
+        wave_steps<STAGES, true, AStage::kLoads + BStage::kLoads, kStageBytes>(
+            lds + wave * STAGES * kStageBytes, wave * steps / NW, (wave + 1) * steps / NW,
+            [&](int t, bool live, lds_char *buf) {
+                const int k0 = live ? t * kStep<T> : K;
+                sa.issue(buf, 0, k0);
+                sb.issue(buf + AStage::kBytes, 0, k0);
+            },
+            [](lds_char *) {},
+            [&](int, const lds_char *buf) {
+                step_products<T, 1, NT, false, 16, false, 16 * NT>(acc, buf, buf + AStage::kBytes, 0, 0, lane);
+            },
+            [] {});
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<__attribute__((address_space(3))) f32x4 *>(lds + (wave * NT + j) * 1024 + lane * 16) =
+                acc[0][j];
+        __syncthreads();
+    }
+    // The sum of quad `lane` of block j, added in wave order.
+    static __device__ __forceinline__ f32x4 sum(const lds_char *lds, int j, int lane) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            s += *reinterpret_cast<const __attribute__((address_space(3))) f32x4 *>(lds + (w * NT + j) * 1024 + lane * 16);
+        return s;
+    }
+};
+
+// ---------------------------------------------------------- tiles and memory
+
+// A tile of 16-bit elements, first `rows` rows and the columns below `limit`,
+// from rows of `width` elements into the places of tile_put; zeros elsewhere.
+template <typename T, int BM, int BN, int THREADS>
+__device__ __forceinline__ void tile_in(lds_char *lds, const T *from, int rows, int64_t n0, int64_t width, bool vec) {
+    constexpr int kUnits = BN / 8;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < BM * kUnits; i += THREADS) {
+        const int r = i / kUnits, u = i % kUnits;
+        const int64_t n = n0 + u * 8;
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (r < rows && n < width) {
+            const T *p = from + r * width + n;
+            if (vec) v = *reinterpret_cast<const u32x4 *>(p);
+            else v = load_unit<T>((uint64_t)p, (int)min(width - n, (int64_t)8));
+        }
+        *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BN>(r, u)) = v;
+    }
+}
+template <typename T, int BN>
+__device__ __forceinline__ f32x4 tile_get(const lds_char *lds, int r, int c) {
+    typedef __attribute__((ext_vector_type(4))) T T4;
+    const T4 q = *reinterpret_cast<const __attribute__((address_space(3))) T4 *>(lds + tile_unit<T, BN>(r, c >> 3) + (c & 4) * 2);
+    return f32x4{(float)q[0], (float)q[1], (float)q[2], (float)q[3]};
+}
+// Writes the first `rows` rows of the tile to out, whose rows are `stride`
+// elements apart, the columns below `limit`.
+template <typename T, int BM, int BN, int THREADS>
+__device__ __forceinline__ void tile_write(const lds_char *lds, T *out, int rows, int64_t n0, int64_t limit,
+                                           int64_t stride, bool vec) {
+    constexpr int kUnits = BN / 8;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < BM * kUnits; i += THREADS) {
+        const int r = i / kUnits, u = i % kUnits;
+        const int64_t n = n0 + u * 8;
+        if (r >= rows || n >= limit) continue;
+        union {
+            u32x4 v;
+            T e[8];
+        } x;
+        x.v = *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BN>(r, u));
+        T *to = out + r * stride + n;
+        if (vec) {
+            *reinterpret_cast<u32x4 *>(to) = x.v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < limit) to[e] = x.e[e];
+        }
+    }
+}
+
+}  // namespace segred

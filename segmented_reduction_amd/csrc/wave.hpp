@@ -96,6 +96,32 @@ __device__ __forceinline__ void seg_scan_wave(T &x, bool &f, T id, Comb comb) {
 #undef SEGRED_SCAN_STEP
 }
 
+// The sum (or the largest) over each L neighbouring lanes (8, 16, 32 or 64, at a
+// multiple of L), in all of them and in the same order every time: exchanges
+// inside a row of 16 lanes by DPP, between rows by the swaps of gfx950.
+enum : int { kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140 };
+template <int L, typename F>
+__device__ __forceinline__ float lanes_fold(float v, F f) {
+    static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes that share a value");
+    v = f(v, dpp_move<kDppXor1>(v, v));
+    v = f(v, dpp_move<kDppXor2>(v, v));
+    v = f(v, dpp_move<kDppHalfMirror>(v, v));
+    if constexpr (L >= 16) v = f(v, dpp_move<kDppMirror>(v, v));
+    if constexpr (L >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    }
+    if constexpr (L >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return lanes_fold<L>(v, [](float a, float b) { return a + b; });
+}
+
 // Make LDS writes of this wave visible to the other lanes of the same wave.
 __device__ __forceinline__ void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
