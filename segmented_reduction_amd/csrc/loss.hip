@@ -144,21 +144,27 @@ __device__ __forceinline__ f32x4 loss_slopes(const LossArgs &a, const LossRow &o
 }
 // Calls put(r, c, dz) for the targets of the tile's rows in its columns, from
 // the logits that the forward call kept; a target named twice gets both shares.
-template <int BN, typename P>
+template <int BM, int BN, int THREADS, typename P>
 __device__ __forceinline__ void loss_targets(const LossArgs &a, const LossPlace &p, P put) {
-    const int picks = (int)a.picks;
-    const int64_t begin = a.v0 + p.n0;
-    const int64_t left = min((int64_t)BN, a.vc - p.n0), all = (int64_t)p.rows * picks;
-    const int64_t *target = a.target + p.row0 * picks;
-    for (int64_t i = threadIdx.x; i < all; i += blockDim.x) {
-        const int64_t t = target[i] - begin;
-        if (t < 0 || t >= left) continue;
-        const int64_t r = i / picks, row = p.row0 + r;
-        float sum = 0.f;
-        for (int j = 0; j < picks; ++j)
-            if (target[r * picks + j] - begin == t) sum += a.probs ? a.probs[row * picks + j] : 1.f;
-        const float e = exp2_fast(fmaf(a.picked[row * picks + i - r * picks], kLog2e, -a.lse[row] * kLog2e));
-        put((int)r, (int)t, fmaf(a.share[row], e, -a.hit[row] * sum));
+    constexpr int kEach = THREADS / BM, kBatch = 8;  // threads of a row, targets that a thread looks at at a time
+    const int picks = (int)a.picks, r = threadIdx.x / kEach;
+    if (r >= p.rows) return;
+    const int64_t begin = a.v0 + p.n0, row = p.row0 + r;
+    const uint64_t left = min((int64_t)BN, a.vc - p.n0);
+    const int64_t *target = a.target + row * picks;
+    for (int j0 = threadIdx.x % kEach; j0 < picks; j0 += kBatch * kEach) {
+        int64_t t[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) t[b] = j0 + b * kEach < picks ? target[j0 + b * kEach] - begin : -1;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if ((uint64_t)t[b] >= left) continue;
+            float sum = 0.f;
+            for (int j = 0; j < picks; ++j)
+                if (target[j] - begin == t[b]) sum += a.probs ? a.probs[row * picks + j] : 1.f;
+            const float e = exp2_fast(fmaf(a.picked[row * picks + j0 + b * kEach], kLog2e, -a.lse[row] * kLog2e));
+            put(r, (int)t[b], fmaf(a.share[row], e, -a.hit[row] * sum));
+        }
     }
 }
 
@@ -180,7 +186,7 @@ __device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p
     }
     if constexpr (sizeof(T) == 2) {
         __syncthreads();
-        loss_targets<BN>(a, p, [&](int r, int c, float y) {
+        loss_targets<BM, BN, THREADS>(a, p, [&](int r, int c, float y) {
             *reinterpret_cast<__attribute__((address_space(3))) T *>(lds + tile_unit<T, BN>(r, c >> 3) + (c & 7) * 2) = (T)y;
         });
         __syncthreads();
@@ -189,7 +195,7 @@ __device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p
         // the stores of other waves to the same places must have gone before
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        loss_targets<BN>(a, p, [&](int r, int c, float y) { out[r * a.ld + p.n0 + c] = (T)y; });
+        loss_targets<BM, BN, THREADS>(a, p, [&](int r, int c, float y) { out[r * a.ld + p.n0 + c] = (T)y; });
     }
 }
 
@@ -294,7 +300,7 @@ __global__ __launch_bounds__(64 * NW) void loss_few(LossArgs a) {
         if (r < p.rows) store_quad<T>(out + r * a.ld, p.n0 + c, a.ld, loss_slopes(a, loss_row_of(a, p.row0 + r), z, p.n0 + c), true);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        loss_targets<16 * NT>(a, p, [&](int i, int j, float y) { out[i * a.ld + p.n0 + j] = (T)y; });
+        loss_targets<16, 16 * NT, 64 * NW>(a, p, [&](int i, int j, float y) { out[i * a.ld + p.n0 + j] = (T)y; });
     } else {
         auto get = [&](int, int) -> f32x4 & { return z; };
         auto row = [&](int) { return r; };
@@ -303,83 +309,136 @@ __global__ __launch_bounds__(64 * NW) void loss_few(LossArgs a) {
     }
 }
 
-// Joins a row's pairs and forms its targets' logits; WAVES waves per row.
+// Joins a row's pairs and forms its targets' logits, kDots at a time; WAVES waves
+// per row.
+constexpr int kDots = 4;
 template <typename T>
-__device__ __forceinline__ float loss_dot(const char *x, const char *w, int K, int lane) {
-    float sum = 0.f;
+__device__ __forceinline__ void loss_dots(float (&sum)[kDots], const char *x, const char *const (&w)[kDots], int K, int lane) {
+#pragma unroll
+    for (int d = 0; d < kDots; ++d) sum[d] = 0.f;
+#pragma unroll 2
     for (int c = lane * kUnit<T>; c < K; c += 64 * kUnit<T>) {
         const u32x4 p = load_unit<T>((uint64_t)(x + (int64_t)c * sizeof(T)), K - c);
-        const u32x4 q = load_unit<T>((uint64_t)(w + (int64_t)c * sizeof(T)), K - c);
+        u32x4 q[kDots];
 #pragma unroll
-        for (int e = 0; e < kUnit<T>; ++e) {
-            if constexpr (sizeof(T) == 4) sum = fmaf(__uint_as_float(p[e]), __uint_as_float(q[e]), sum);
-            else if constexpr (__is_same(T, __bf16))
-                sum = fmaf((float)__builtin_bit_cast(bf16x8, p)[e], (float)__builtin_bit_cast(bf16x8, q)[e], sum);
-            else sum = fmaf((float)__builtin_bit_cast(f16x8, p)[e], (float)__builtin_bit_cast(f16x8, q)[e], sum);
-        }
+        for (int d = 0; d < kDots; ++d) q[d] = load_unit<T>((uint64_t)(w[d] + (int64_t)c * sizeof(T)), w[d] ? K - c : 0);
+#pragma unroll
+        for (int d = 0; d < kDots; ++d)
+#pragma unroll
+            for (int e = 0; e < kUnit<T>; ++e) sum[d] = fmaf(element<T>(p, e), element<T>(q[d], e), sum[d]);
     }
-    return lanes_sum<64>(sum);
+#pragma unroll
+    for (int d = 0; d < kDots; ++d) sum[d] = lanes_sum<64>(sum[d]);
 }
 template <typename T, int WAVES>
 __global__ __launch_bounds__(256) void loss_join(LossArgs a) {
-    __shared__ float s_at[4];
+    __shared__ float s_part[4][5];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (4 / WAVES) + wave / WAVES;
     const int part = wave % WAVES;
     if (row >= a.N) return;
+    // the pairs
+    const float2 *pair = a.partial + row * a.parts;
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int64_t i = part * 64 + lane; i < a.parts; i += 64 * WAVES) m = fmaxf(m, pair[i].x);
+    m = lanes_fold<64>(m, [](float p, float q) { return fmaxf(p, q); });
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int64_t i = part * 64 + lane; i < a.parts; i += 64 * WAVES) sum = fmaf(pair[i].y, exp2_fast(pair[i].x - base), sum);
+    sum = lanes_sum<64>(sum);
+    // the targets
     const int64_t *target = a.target + row * a.picks;
     const char *x = a.values + row * a.K * (int64_t)sizeof(T);
     float share = 0.f, at = 0.f;
-    for (int64_t j = 0; j < a.picks; ++j) {
-        const int64_t t = target[j];
-        const bool there = t >= 0 && t < a.V;
-        const float prob = there ? (a.probs ? a.probs[row * a.picks + j] : 1.f) : 0.f;
-        share += prob;
-        if (j % WAVES != part) continue;
-        float z = 0.f;
-        if (there) z = a.scale * loss_dot<T>(x, a.weights + t * a.K * (int64_t)sizeof(T), (int)a.K, lane);
-        if (there) at = fmaf(prob, z, at);
-        if (lane == 0) a.picked[row * a.picks + j] = z;
+    bool live = false;
+    for (int64_t j0 = part; j0 < a.picks; j0 += kDots * WAVES) {
+        const char *w[kDots];
+        float prob[kDots], z[kDots];
+#pragma unroll
+        for (int d = 0; d < kDots; ++d) {
+            const int64_t j = j0 + d * WAVES, t = j < a.picks ? target[j] : -1;
+            const bool there = t >= 0 && t < a.V;
+            w[d] = there ? a.weights + t * a.K * (int64_t)sizeof(T) : nullptr;
+            prob[d] = !there ? 0.f : a.probs ? a.probs[row * a.picks + j] : 1.f;
+            live = live || there;
+        }
+        if (a.picks == 1) {
+            const char *one[kDots] = {w[0], nullptr, nullptr, nullptr};
+            loss_dots<T>(z, x, one, (int)a.K, lane);
+        } else {
+            loss_dots<T>(z, x, w, (int)a.K, lane);
+        }
+#pragma unroll
+        for (int d = 0; d < kDots; ++d) {
+            const int64_t j = j0 + d * WAVES;
+            const float y = w[d] ? a.scale * z[d] : 0.f;
+            share += prob[d];
+            if (w[d]) at = fmaf(prob[d], y, at);
+            if (lane == 0 && j < a.picks) a.picked[row * a.picks + j] = y;
+        }
     }
     if constexpr (WAVES > 1) {
-        if (lane == 0) s_at[wave] = at;
+        // the waves of the row in order
+        if (lane == 0) {
+            s_part[wave][0] = m;
+            s_part[wave][1] = sum;
+            s_part[wave][2] = share;
+            s_part[wave][3] = at;
+            s_part[wave][4] = live ? 1.f : 0.f;
+        }
         __syncthreads();
         if (part > 0) return;
-        at = 0.f;
+        float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) at += s_at[w];
+        for (int q = 0; q < WAVES; ++q) top = fmaxf(top, s_part[wave + q][0]);
+        const float low = top == -INFINITY ? 0.f : top;
+        m = top;
+        sum = share = at = 0.f;
+        live = false;
+#pragma unroll
+        for (int q = 0; q < WAVES; ++q) {
+            const float *o = s_part[wave + q];
+            sum = fmaf(o[1], exp2_fast(o[0] - low), sum);
+            share += o[2];
+            at += o[3];
+            live = live || o[4] != 0.f;
+        }
     }
-    const float2 *pair = a.partial + row * a.parts;
-    float m = -INFINITY, sum = 0.f;
-    for (int64_t i = lane; i < a.parts; i += 64) m = fmaxf(m, pair[i].x);
-    m = lanes_fold<64>(m, [](float p, float q) { return fmaxf(p, q); });
-    const float base = m == -INFINITY ? 0.f : m;
-    for (int64_t i = lane; i < a.parts; i += 64) sum = fmaf(pair[i].y, exp2_fast(pair[i].x - base), sum);
-    sum = lanes_sum<64>(sum);
     if (lane == 0) {
         const float lse = kLn2 * (m + __log2f(sum));
         a.lse[row] = lse;
         // a row without a target has no loss, whatever its logits are
-        bool live = false;
-        for (int64_t j = 0; j < a.picks; ++j) live = live || (target[j] >= 0 && target[j] < a.V);
         a.loss[row] = live ? fmaf(share, lse, -at) : 0.f;
     }
 }
 
-// What the gradient's tiles need of each row.
-__global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (row >= a.N) return;
-    float share = 0.f, size = 0.f;
-    bool live = false;
-    for (int64_t j = 0; j < a.picks; ++j) {
+// What the gradient's tiles need of each row, LANES lanes a row, and the one
+// segment of the weights' sums.
+template <int LANES>
+__global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *offsets) {
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
+    if (row == 0) {
+        offsets[0] = 0;
+        offsets[1] = a.N;
+    }
+    if (row >= a.N) return;  // whole groups of LANES
+    float share = 0.f, size = 0.f, any = 0.f;
+    for (int64_t j = threadIdx.x % LANES; j < a.picks; j += LANES) {
         const int64_t t = a.target[row * a.picks + j];
         if (t < 0 || t >= a.V) continue;
         const float p = a.probs ? a.probs[row * a.picks + j] : 1.f;
         share += p;
         size += fabsf(p);
-        live = true;
+        any = 1.f;
     }
+    if constexpr (LANES > 1) {
+        share = lanes_sum<LANES>(share);
+        size = lanes_sum<LANES>(size);
+        any = lanes_sum<LANES>(any);
+    }
+    if (threadIdx.x % LANES > 0) return;
+    const bool live = any > 0.f;
     const float g = a.grad[row] * a.scale, bound = fabsf(g) * size;
     a.share[row] = live ? g * share : 0.f;
     a.hit[row] = g;
@@ -746,8 +805,9 @@ int loss_forward(const LossArgs &a, LossKind kind, hipStream_t st) {
     const int rc = loss_tiles_launch<T, false>(a, kind, st);
     if (rc != SEGRED_OK) return rc;
     dim3 grid;
-    if (!tile_grid(a.picks > 1 ? a.N : (a.N + 3) / 4, grid)) return SEGRED_ERR_UNSUPPORTED;
-    if (a.picks > 1) timed_launch_ggl(false, (loss_join<T, 4>), grid, dim3(256), 0, st, a);
+    const bool shared = a.picks > 1 || a.N <= 1024;  // four waves a row
+    if (!tile_grid(shared ? a.N : (a.N + 3) / 4, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (shared) timed_launch_ggl(false, (loss_join<T, 4>), grid, dim3(256), 0, st, a);
     else timed_launch_ggl(false, (loss_join<T, 1>), grid, dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
@@ -802,9 +862,13 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
                   int32_t grad_weights_dtype, char *work, hipStream_t st) {
     const int64_t e = sizeof(T), ge = float_size(grad_weights_dtype);
     int64_t *offsets = reinterpret_cast<int64_t *>(work + p.offsets);
-    if (grad_weights) timed_launch_ggl(false, loss_bounds, dim3(1), dim3(1), 0, st, offsets, a.N);
-    if (a.N > 0) {
-        timed_launch_ggl(false, loss_rows_prepare, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, st, a);
+    if (a.N == 0) {
+        timed_launch_ggl(false, loss_bounds, dim3(1), dim3(1), 0, st, offsets, a.N);
+    } else {
+        if (a.picks > 1)
+            timed_launch_ggl(false, (loss_rows_prepare<16>), dim3((unsigned)((a.N + 15) / 16)), dim3(256), 0, st, a, offsets);
+        else
+            timed_launch_ggl(false, (loss_rows_prepare<1>), dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, st, a, offsets);
         if (__is_same(T, _Float16)) timed_launch_ggl(false, loss_factor, dim3(1), dim3(1024), 0, st, a);
     }
     if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;

@@ -31,13 +31,6 @@ struct NormArgs {
     int64_t blocks;
 };
 
-template <typename T>
-__device__ __forceinline__ float element(u32x4 v, int e) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(v[e]);
-    else if constexpr (__is_same(T, __bf16)) return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
-    else return (float)__builtin_bit_cast(f16x8, v)[e];
-}
-
 // Column of unit u of a row's lane `l` of L.
 template <typename T, int L>
 __device__ __forceinline__ int norm_col(int u, int l) { return (u * L + l) * kUnit<T>; }
@@ -63,9 +56,44 @@ __device__ __forceinline__ void store_unit(char *to, const float (&c)[kUnit<T>],
     }
 }
 
+// Unit u of a row that begins at `row` (0: no row), zeros behind its end.  WHOLE:
+// rows hold whole units, so that each is there or not.
+template <typename T, int L, bool WHOLE>
+__device__ __forceinline__ u32x4 norm_load(uint64_t row, int u, int l, int K) {
+    const int c = norm_col<T, L>(u, l);
+    const uint64_t at = row + (uint64_t)c * sizeof(T);
+    if constexpr (WHOLE) return load_whole<T>(row != 0 && c < K ? at : (uint64_t)zero_unit());
+    else return load_unit<T>(at, row != 0 ? K - c : 0);
+}
+template <typename T, int L, bool WHOLE>
+__device__ __forceinline__ void norm_store(uint64_t row, int u, int l, int K, const float (&y)[kUnit<T>]) {
+    const int c = norm_col<T, L>(u, l);
+    if (c < K) store_unit<T>((char *)(row + (uint64_t)c * sizeof(T)), y, WHOLE ? kUnit<T> : K - c);
+}
+
 template <typename T>
 __device__ __forceinline__ float param(const void *p, int f32, int c) {
     return f32 ? static_cast<const float *>(p)[c] : (float)static_cast<const T *>(p)[c];
+}
+// Those of a unit's columns, `left` of which exist; the others, and all without
+// a parameter, are `none`.
+template <typename T>
+__device__ __forceinline__ void param_unit(float (&to)[kUnit<T>], const void *p, int f32, int c, int left, float none) {
+    constexpr int N = kUnit<T>;
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = none;
+    } else if (f32 || sizeof(T) == 4) {
+        u32x4 v[N / 4];
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) v[q] = load_unit<float>((uint64_t)p + (uint64_t)c * 4 + q * 16, left - 4 * q);
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = __uint_as_float(v[e / 4][e % 4]);
+    } else {
+        const u32x4 v = load_unit<T>((uint64_t)p + (uint64_t)c * sizeof(T), left);
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = element<T>(v, e);
+    }
 }
 template <typename T>
 __device__ __forceinline__ void put_param(void *p, int f32, int64_t c, float v) {
@@ -77,10 +105,10 @@ __device__ __forceinline__ void put_param(void *p, int f32, int64_t c, float v) 
 // meet in LDS, two places in turn, so that one barrier a row is enough.
 template <int L, int Q>
 struct RowJoin {
-    static constexpr int kWaves = L / 64;
-    float (*s)[kWaves > 1 ? kWaves : 1][Q];  // [2][waves][Q]
+    static constexpr int kWaves = (L > 256 ? L : 256) / 64, kRowWaves = L > 64 ? L / 64 : 1;
+    float (*s)[kWaves][Q];  // [2][waves][Q]
     int turn = 0;
-    // all(w, q): value q of wave w, valid until the call after the next.
+    // The values of the row's waves, there until the call after the next.
     __device__ __forceinline__ const float (*meet(const float (&v)[Q], int wave, int lane))[Q] {
         float (*p)[Q] = s[turn];
         turn ^= 1;
@@ -88,97 +116,121 @@ struct RowJoin {
 #pragma unroll
             for (int q = 0; q < Q; ++q) p[wave][q] = v[q];
         __syncthreads();
-        return p;
+        return p + wave / kRowWaves * kRowWaves;
     }
 };
+
+// Elements of a row that wave `part` of its L lanes holds.
+template <typename T, int L, int U>
+__device__ __forceinline__ int norm_part(int part, int K) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) n += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, part * 64)));
+    return n;
+}
 
 // L lanes hold a row, E elements each.  A workgroup walks rows with its weight
 // and bias in registers; the next row is on its way while one is worked on.
 template <int L> constexpr int kNormThreads = L > 256 ? L : 256;
 
-template <typename T, int L, int E>
-__global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
-    constexpr int kThreads = kNormThreads<L>, kRows = kThreads / L, U = E / kUnit<T>, W = L > 64 ? L / 64 : 1;
-    constexpr int LW = L > 64 ? 64 : L;  // lanes of a row in one wave
-    __shared__ float s_join[2][W][2];
-    const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, K = a.K;
-    RowJoin<L, 2> join{s_join};
-    const int64_t row_bytes = (int64_t)K * sizeof(T), stride = (int64_t)gridDim.x * kRows;
-    const float per = 1.f / (float)K;
-    float w[E], b[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int c = norm_col<T, L>(i / kUnit<T>, l) + i % kUnit<T>;
-        w[i] = c < K && a.weight ? param<T>(a.weight, a.weight_f32, c) : 1.f;
-        b[i] = c < K && a.bias ? param<T>(a.bias, a.weight_f32, c) : 0.f;
+// What a lane of these kernels goes through: rows `first`, `first` + stride, ..., one
+// per L lanes, as addresses; a row past the last has address 0.
+template <int L>
+struct NormWalk {
+    int64_t row, step;
+    uint64_t row_bytes;
+    __device__ __forceinline__ NormWalk(int64_t rows_each, int K, int element) {
+        int at = threadIdx.x / L;
+        if constexpr (L >= 64) at = __builtin_amdgcn_readfirstlane(at);
+        row = (int64_t)blockIdx.x * rows_each + at;
+        step = (int64_t)gridDim.x * rows_each;
+        row_bytes = (uint64_t)K * element;
     }
-    // elements of this wave's part of a row
-    int mine = 0;
-    if constexpr (W > 1)
-        for (int u = 0; u < U; ++u) mine += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, wave * 64)));
+    __device__ __forceinline__ uint64_t of(const void *base, int64_t r, int64_t rows) const {
+        return r < rows ? (uint64_t)base + (uint64_t)r * row_bytes : 0;
+    }
+};
 
-    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+template <typename T, int L, int E, bool WHOLE>
+__global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
+    constexpr int kRows = kNormThreads<L> / L, N = kUnit<T>, U = E / N, W = L > 64 ? L / 64 : 1;
+    constexpr int LW = L > 64 ? 64 : L;  // lanes of a row in one wave
+    __shared__ float s_join[2][kNormThreads<L> / 64][2];
+    const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = a.K;
+    const int part = wave % W;
+    RowJoin<L, 2> join{s_join};
+    const float per = 1.f / (float)K;
+    float w[U][N], b[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = norm_col<T, L>(u, l);
+        param_unit<T>(w[u], a.weight, a.weight_f32, c, K - c, 1.f);
+        param_unit<T>(b[u], a.bias, a.weight_f32, c, K - c, 0.f);
+    }
+    const float own = 1.f / (float)max(norm_part<T, L, U>(part, K), 1);
+
+    NormWalk<L> at(kRows, K, sizeof(T));
     u32x4 next[U];
     auto fetch = [&](int64_t r) {
+        const uint64_t from = at.of(a.values, r, a.N);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = norm_col<T, L>(u, l);
-            next[u] = load_unit<T>((uint64_t)(a.values + r * row_bytes) + c * sizeof(T), r < a.N ? K - c : 0);
-        }
+        for (int u = 0; u < U; ++u) next[u] = norm_load<T, L, WHOLE>(from, u, l, K);
     };
-    fetch(row);
-    for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.N; first += stride, row += stride) {
-        float x[E];
-        float sum = 0.f;
+    fetch(at.row);
+    for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.N; first += at.step, at.row += at.step) {
+        float x[U][N], sum = 0.f, mean = 0.f, m2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = element<T>(next[i / kUnit<T>], i % kUnit<T>);
-        fetch(row + stride);
-        float mean = 0.f, m2 = 0.f;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[u][e] = element<T>(next[u], e);
+        fetch(at.row + at.step);
         if (a.center) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) sum += x[i];
-            sum = lanes_sum<LW>(sum);
-            mean = W > 1 ? (mine > 0 ? sum / (float)mine : 0.f) : sum * per;
-        }
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = norm_col<T, L>(i / kUnit<T>, l) + i % kUnit<T>;
-            const float d = c < K ? x[i] - mean : 0.f;
-            m2 = fmaf(d, d, m2);
+                for (int e = 0; e < N; ++e) sum += x[u][e];
+            sum = lanes_sum<LW>(sum);
+            mean = sum * (W > 1 ? own : per);
+        }
+        const float shift = mean;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int left = K - norm_col<T, L>(u, l);
+            const float m = left > 0 ? mean : 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                x[u][e] -= WHOLE || e < left ? m : 0.f;
+                m2 = fmaf(x[u][e], x[u][e], m2);
+            }
         }
         m2 = lanes_sum<LW>(m2);
         if constexpr (W > 1) {
             // the parts' means and squares around them, joined
             const float v[2] = {sum, m2};
             const auto p = join.meet(v, wave, lane);
-            m2 = 0.f;
+            m2 = mean = 0.f;
             if (a.center) {
-                mean = 0.f;
 #pragma unroll
                 for (int q = 0; q < W; ++q) mean += p[q][0];
                 mean *= per;
             }
 #pragma unroll
             for (int q = 0; q < W; ++q) {
-                int n = 0;
-#pragma unroll
-                for (int u = 0; u < U; ++u) n += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, q * 64)));
-                const float d = a.center && n > 0 ? p[q][0] / (float)n - mean : 0.f;
-                m2 += fmaf((float)n * d, d, p[q][1]);
+                const float n = (float)norm_part<T, L, U>(q, K);
+                const float d = a.center && n > 0.f ? p[q][0] / n - mean : 0.f;
+                m2 += fmaf(n * d, d, p[q][1]);
             }
         }
         const float r = 1.f / sqrtf(fmaf(m2, per, a.eps));
-        if (row < a.N)
+        const float rest = (shift - mean) * r;  // the part's mean was taken off before
+        const uint64_t to = at.of(a.out, at.row, a.N);
+        if (to != 0)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = norm_col<T, L>(u, l);
-                float y[kUnit<T>];
+                float y[N];
 #pragma unroll
-                for (int e = 0; e < kUnit<T>; ++e) {
-                    const int i = u * kUnit<T> + e;
-                    y[e] = fmaf((x[i] - mean) * r, w[i], b[i]);
-                }
-                if (c < K) store_unit<T>(a.out + row * row_bytes + c * (int64_t)sizeof(T), y, K - c);
+                for (int e = 0; e < N; ++e) y[e] = fmaf(W > 1 ? fmaf(x[u][e], r, rest) : x[u][e] * r, w[u][e], b[u][e]);
+                norm_store<T, L, WHOLE>(to, u, l, K, y);
             }
     }
 }
@@ -187,62 +239,66 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
 // columns in registers; at the end its parts go to `partial`.  One exchange a
 // row between waves: besides the mean and the squares, sum gw and the sum of
 // gw (x - mean of this wave's part), which is corrected for the row's mean.
-template <typename T, int L, int E>
-__global__ __launch_bounds__(kNormThreads<L>) void norm_grad_rows(NormArgs a) {
-    constexpr int kThreads = kNormThreads<L>, kRows = kThreads / L, U = E / kUnit<T>, W = L > 64 ? L / 64 : 1;
+template <typename T, int L, int E, bool WHOLE>
+__global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __is_same(T, __bf16) ? 4 : 1) void norm_grad_rows(NormArgs a) {
+    constexpr int kThreads = kNormThreads<L>, kRows = kThreads / L, N = kUnit<T>, U = E / N, W = L > 64 ? L / 64 : 1;
     constexpr int LW = L > 64 ? 64 : L;
-    __shared__ float s_join[2][W][4];
-    __shared__ float s_sums[kRows > 1 ? 2 * LW * E : 1];
-    const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, K = a.K;
+    __shared__ float s_join[2][kThreads / 64][4];
+    __shared__ float s_sums[kRows > 1 ? 2 * L * E : 1];
+    const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = a.K;
+    const int part = wave % W;
     RowJoin<L, 4> join{s_join};
-    const int64_t row_bytes = (int64_t)K * sizeof(T), stride = (int64_t)gridDim.x * kRows;
     const float per = 1.f / (float)K;
-    float w[E], dw[E], db[E];
+    float w[U][N], dw[U][N], db[U][N];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int c = norm_col<T, L>(i / kUnit<T>, l) + i % kUnit<T>;
-        w[i] = c < K ? (a.weight ? param<T>(a.weight, a.weight_f32, c) : 1.f) : 0.f;
-        dw[i] = db[i] = 0.f;
+    for (int u = 0; u < U; ++u) {
+        const int c = norm_col<T, L>(u, l);
+        param_unit<T>(w[u], a.weight, a.weight_f32, c, K - c, 1.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[u][e] = db[u][e] = 0.f;
     }
-    int mine = 0;
-    if constexpr (W > 1)
-        for (int u = 0; u < U; ++u) mine += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, wave * 64)));
+    const float own = 1.f / (float)max(norm_part<T, L, U>(part, K), 1);
 
-    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    NormWalk<L> at(kRows, K, sizeof(T));
     u32x4 next_x[U], next_g[U];
     auto fetch = [&](int64_t r) {
+        const uint64_t from_x = at.of(a.values, r, a.N), from_g = at.of(a.grad, r, a.N);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = norm_col<T, L>(u, l), n = r < a.N ? K - c : 0;
-            const uint64_t at = (uint64_t)(r * row_bytes) + c * sizeof(T);
-            next_x[u] = load_unit<T>((uint64_t)a.values + at, n);
-            next_g[u] = load_unit<T>((uint64_t)a.grad + at, n);
+            next_x[u] = norm_load<T, L, WHOLE>(from_x, u, l, K);
+            next_g[u] = norm_load<T, L, WHOLE>(from_g, u, l, K);
         }
     };
-    fetch(row);
-    for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.N; first += stride, row += stride) {
+    fetch(at.row);
+    for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.N; first += at.step, at.row += at.step) {
         u32x4 x[U], g[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             x[u] = next_x[u];
             g[u] = next_g[u];
         }
-        fetch(row + stride);
+        fetch(at.row + at.step);
         float sum = 0.f, mean = 0.f, m2 = 0.f, c1 = 0.f, c2 = 0.f;
         if (a.center) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) sum += element<T>(x[i / kUnit<T>], i % kUnit<T>);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) sum += element<T>(x[u], e);
             sum = lanes_sum<LW>(sum);
-            mean = W > 1 ? (mine > 0 ? sum / (float)mine : 0.f) : sum * per;
+            mean = sum * (W > 1 ? own : per);
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = norm_col<T, L>(i / kUnit<T>, l) + i % kUnit<T>;
-            const float d = c < K ? element<T>(x[i / kUnit<T>], i % kUnit<T>) - mean : 0.f;
-            const float gw = element<T>(g[i / kUnit<T>], i % kUnit<T>) * w[i];
-            m2 = fmaf(d, d, m2);
-            c1 += gw;
-            c2 = fmaf(gw, d, c2);
+        for (int u = 0; u < U; ++u) {
+            const int left = K - norm_col<T, L>(u, l);
+            const float m = left > 0 ? mean : 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = element<T>(x[u], e) - (WHOLE || e < left ? m : 0.f);
+                const float gw = element<T>(g[u], e) * w[u][e];
+                m2 = fmaf(d, d, m2);
+                c1 += gw;
+                c2 = fmaf(gw, d, c2);
+            }
         }
         m2 = lanes_sum<LW>(m2);
         c1 = lanes_sum<LW>(c1);
@@ -250,42 +306,38 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_grad_rows(NormArgs a) {
         if constexpr (W > 1) {
             const float v[4] = {sum, m2, c1, c2};
             const auto p = join.meet(v, wave, lane);
-            m2 = c1 = c2 = 0.f;
+            m2 = c1 = c2 = mean = 0.f;
             if (a.center) {
-                mean = 0.f;
 #pragma unroll
                 for (int q = 0; q < W; ++q) mean += p[q][0];
                 mean *= per;
             }
 #pragma unroll
             for (int q = 0; q < W; ++q) {
-                int n = 0;
-#pragma unroll
-                for (int u = 0; u < U; ++u) n += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, q * 64)));
-                const float d = a.center && n > 0 ? p[q][0] / (float)n - mean : 0.f;
-                m2 += fmaf((float)n * d, d, p[q][1]);
+                const float n = (float)norm_part<T, L, U>(q, K);
+                const float d = a.center && n > 0.f ? p[q][0] / n - mean : 0.f;
+                m2 += fmaf(n * d, d, p[q][1]);
                 c1 += p[q][2];
                 c2 += fmaf(p[q][2], d, p[q][3]);
             }
         }
         const float r = 1.f / sqrtf(fmaf(m2, per, a.eps));
-        const float along = c2 * r * per;  // mean(gw u)
-        const float level = a.center ? c1 * per : 0.f;
+        const float along = c2 * r * per * r;               // mean(gw u) r
+        const float level = a.center ? c1 * per * r : 0.f;  // mean(gw) r
+        const uint64_t to = at.of(a.out, at.row, a.N);
+        if (to != 0)  // past the last row g is 0, but r may be infinite
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = norm_col<T, L>(u, l);
-            float y[kUnit<T>];
+            for (int u = 0; u < U; ++u) {
+                float y[N];
 #pragma unroll
-            for (int e = 0; e < kUnit<T>; ++e) {
-                const int i = u * kUnit<T> + e;
-                const float unit = (element<T>(x[u], e) - mean) * r, ge = element<T>(g[u], e);
-                y[e] = r * (fmaf(ge, w[i], -level) - unit * along);
-                // a row past the last has g = 0, but r of it may be infinite
-                if (row < a.N) dw[i] = fmaf(ge, unit, dw[i]);
-                db[i] += ge;
+                for (int e = 0; e < N; ++e) {
+                    const float unit = (element<T>(x[u], e) - mean) * r, ge = element<T>(g[u], e);
+                    y[e] = fmaf(ge * r, w[u][e], -fmaf(unit, along, level));
+                    dw[u][e] = fmaf(ge, unit, dw[u][e]);
+                    db[u][e] += ge;
+                }
+                norm_store<T, L, WHOLE>(to, u, l, K, y);
             }
-            if (row < a.N && c < K) store_unit<T>(a.out + row * row_bytes + c * (int64_t)sizeof(T), y, K - c);
-        }
     }
     if (!a.partial) return;
 
@@ -294,35 +346,35 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_grad_rows(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < E; ++i)
             for (int s = 32; s >= LW; s >>= 1) {
-                dw[i] += lane_get(dw[i], lane ^ s);
-                db[i] += lane_get(db[i], lane ^ s);
+                dw[i / N][i % N] += lane_get(dw[i / N][i % N], lane ^ s);
+                db[i / N][i % N] += lane_get(db[i / N][i % N], lane ^ s);
             }
     }
     if constexpr (kRows > 1) {
-        for (int v = 0; v < kThreads / 64; ++v) {
-            if (wave == v && lane < LW)
+        for (int v = 0; v < kThreads / 64 / W; ++v) {
+            if (wave / W == v && lane < LW)
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    float *p = s_sums + i * LW + lane, *q = p + LW * E;
-                    *p = v ? *p + dw[i] : dw[i];
-                    *q = v ? *q + db[i] : db[i];
+                    float *p = s_sums + i * L + l, *q = p + L * E;
+                    *p = v ? *p + dw[i / N][i % N] : dw[i / N][i % N];
+                    *q = v ? *q + db[i / N][i % N] : db[i / N][i % N];
                 }
             __syncthreads();
         }
-        if (wave > 0 || lane >= LW) return;
+        if (wave >= W || lane >= LW) return;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            dw[i] = s_sums[i * LW + lane];
-            db[i] = s_sums[(E + i) * LW + lane];
+            dw[i / N][i % N] = s_sums[i * L + l];
+            db[i / N][i % N] = s_sums[(E + i) * L + l];
         }
     }
     float *to = a.partial + (int64_t)blockIdx.x * 2 * K;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        const int c = norm_col<T, L>(i / kUnit<T>, l) + i % kUnit<T>;
+        const int c = norm_col<T, L>(i / N, l) + i % N;
         if (c < K) {
-            to[c] = dw[i];
-            to[K + c] = db[i];
+            to[c] = dw[i / N][i % N];
+            to[K + c] = db[i / N][i % N];
         }
     }
 }
@@ -396,7 +448,7 @@ __global__ __launch_bounds__(kNormJoinCols *kNormJoinParts) void norm_join(NormA
     const int64_t c = (int64_t)blockIdx.x * kNormJoinCols + col, width = 2 * (int64_t)a.K;
     float sum = 0.f;
     if (c < width)
-#pragma unroll 4
+#pragma unroll 16
         for (int64_t p = part; p < a.blocks; p += kNormJoinParts) sum += a.partial[p * width + c];
     s_part[part][col] = sum;
     __syncthreads();
@@ -410,46 +462,68 @@ __global__ __launch_bounds__(kNormJoinCols *kNormJoinParts) void norm_join(NormA
     }
 }
 
-// Lanes and elements per lane of a row.
+// Lanes and elements per lane of a row.  Few waves per row, so that fewer wait for
+// each other, as long as the gradient's sums fit the registers.  33.5M bfloat16
+// elements, forward / gradient in us (a copy of them takes 26):
+//
+//   k       512       1024      2048      4096      8192      16384
+//           25 / 45   24 / 42   26 / 46   26 / 56   28 / 60   29 / 64   as below
+//                     30 / 64   24 / 49                                 128 lanes (8, 16 each)
+//                               29 / 65   43 / 83   30 / 77             twice the lanes, half the elements
+//
+// and of 16.8M float32 with k = 2,048 the gradient 43 by 128 lanes, 47 by 64.
 struct NormShape {
     int lanes, elements;  // lanes 0: too long for registers
 };
-NormShape norm_shape(int64_t k) {
+NormShape norm_shape(int64_t k, bool grad, bool wide) {
     if (k <= 128) return {16, 8};
     if (k <= 512) return {64, 8};
     if (k <= 1024) return {64, 16};
-    if (k <= 2048) return {64, 32};
+    if (k <= 2048) return grad && !wide ? NormShape{64, 32} : NormShape{128, 16};
     if (k <= 4096) return {256, 16};
     if (k <= 8192) return {256, 32};
     if (k <= 16384) return {512, 32};
     return {0, 0};
 }
 
-// Workgroups of a call: by rows alone, so that sums do not depend on the device.
-constexpr int64_t kNormBlocks = 2048, kNormGradBlocks = 512;
-int64_t norm_blocks(int64_t k, int64_t rows, int64_t most) {
-    const NormShape s = norm_shape(k);
+// Workgroups of a call, by its sizes alone, so that sums do not depend on the
+// device: as many as it holds at a time (more read the parameters more often: k =
+// 4,096 in 1,024 workgroups 24 us, in 4,096 27), and for the gradient fewer where
+// their parts are long (k = 8,192 in 256 60 us, in 512 63; k = 512 in 512 50, in
+// 768 46).
+int64_t norm_blocks(const NormShape &s, int64_t rows, bool grad) {
+    const int64_t row = (int64_t)s.lanes * s.elements;
+    int64_t most = s.lanes == 0 ? 512 : s.lanes <= 128 ? 2048 : s.lanes == 256 ? 1024 : 512;
+    if (grad) most = s.lanes == 0 || row > 4096 ? 256 : row <= 512 ? 768 : 512;
     const int64_t each = s.lanes > 0 && s.lanes < 256 ? 256 / s.lanes : 1;
     return std::min(most, (rows + each - 1) / each);
 }
 
+template <typename T, bool GRAD, int L, int E, bool WHOLE>
+void norm_start_as(const NormArgs &a, hipStream_t st) {
+    if constexpr (GRAD)
+        timed_launch_ggl(true, (norm_grad_rows<T, L, E, WHOLE>), dim3((unsigned)a.blocks), dim3(kNormThreads<L>), 0, st, a);
+    else
+        timed_launch_ggl(true, (norm_rows<T, L, E, WHOLE>), dim3((unsigned)a.blocks), dim3(kNormThreads<L>), 0, st, a);
+}
 template <typename T, bool GRAD, int L, int E>
 void norm_start(const NormArgs &a, hipStream_t st) {
-    if constexpr (GRAD)
-        timed_launch_ggl(true, (norm_grad_rows<T, L, E>), dim3((unsigned)a.blocks), dim3(kNormThreads<L>), 0, st, a);
-    else
-        timed_launch_ggl(true, (norm_rows<T, L, E>), dim3((unsigned)a.blocks), dim3(kNormThreads<L>), 0, st, a);
+    if (a.K % kUnit<T> == 0) norm_start_as<T, GRAD, L, E, true>(a, st);
+    else norm_start_as<T, GRAD, L, E, false>(a, st);
 }
 
 template <typename T, bool GRAD>
-int norm_dispatch(const NormArgs &a, hipStream_t st) {
+int norm_dispatch(NormArgs a, hipStream_t st) {
     if (a.N > 0) {
-        const NormShape s = norm_shape(a.K);
+        const NormShape s = norm_shape(a.K, GRAD, sizeof(T) == 4);
+        const int row = s.lanes * s.elements;
+        constexpr bool kMiddle = GRAD && sizeof(T) == 2;
+        a.blocks = norm_blocks(s, a.N, GRAD);
         if (s.lanes == 0) timed_launch_ggl(true, (norm_long<T, GRAD>), dim3((unsigned)a.blocks), dim3(kLongThreads), 0, st, a);
         else if (s.lanes == 16) norm_start<T, GRAD, 16, 8>(a, st);
         else if (s.lanes == 64 && s.elements == 8) norm_start<T, GRAD, 64, 8>(a, st);
         else if (s.lanes == 64 && s.elements == 16) norm_start<T, GRAD, 64, 16>(a, st);
-        else if (s.lanes == 64) norm_start<T, GRAD, 64, 32>(a, st);
+        else if (row == 2048) norm_start<T, GRAD, kMiddle ? 64 : 128, kMiddle ? 32 : 16>(a, st);
         else if (s.lanes == 256 && s.elements == 16) norm_start<T, GRAD, 256, 16>(a, st);
         else if (s.lanes == 256) norm_start<T, GRAD, 256, 32>(a, st);
         else norm_start<T, GRAD, 512, 32>(a, st);
@@ -505,13 +579,14 @@ extern "C" int segred_norm(const void *values, int32_t dtype, int64_t k, int64_t
     a.center = center != 0;
     a.eps = eps;
     a.out = static_cast<char *>(out);
-    a.blocks = norm_blocks(k, rows, kNormBlocks);
     return norm_typed<false>(a, dtype, stream);
 }
 
 extern "C" int64_t segred_norm_grad_workspace(int64_t k, int64_t rows) {
     if (k < 1 || rows < 1 || k > kMaxWidth) return 0;
-    return norm_blocks(k, rows, kNormGradBlocks) * 2 * k * 4;
+    const int64_t blocks = std::max(norm_blocks(norm_shape(k, true, false), rows, true),
+                                    norm_blocks(norm_shape(k, true, true), rows, true));
+    return blocks * 2 * k * 4;
 }
 
 extern "C" int segred_norm_grad(const void *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
@@ -540,6 +615,5 @@ extern "C" int segred_norm_grad(const void *grad, const void *values, int32_t dt
     a.grad_weight = grad_weight;
     a.grad_bias = grad_bias;
     a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
-    a.blocks = norm_blocks(k, rows, kNormGradBlocks);
     return norm_typed<true>(a, dtype, stream);
 }

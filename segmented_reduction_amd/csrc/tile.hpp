@@ -93,6 +93,14 @@ __device__ __forceinline__ u32x4 load_unit(uint64_t addr, int n) {
     return v;
 }
 
+// Element e of a 16-byte unit.
+template <typename T>
+__device__ __forceinline__ float element(u32x4 v, int e) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(v[e]);
+    else if constexpr (__is_same(T, __bf16)) return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
+    else return (float)__builtin_bit_cast(f16x8, v)[e];
+}
+
 // The same of four neighbouring elements of type S as floats, for T = float.
 template <typename T, typename S>
 __device__ __forceinline__ u32x4 load_as(uint64_t addr, int n) {

@@ -100,13 +100,17 @@ __device__ __forceinline__ void seg_scan_wave(T &x, bool &f, T id, Comb comb) {
 // multiple of L), in all of them and in the same order every time: exchanges
 // inside a row of 16 lanes by DPP, between rows by the swaps of gfx950.
 enum : int { kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140 };
+template <int CTRL>
+__device__ __forceinline__ float dpp_take(float v) {  // every lane has a source; becomes part of the instruction that uses it
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
 template <int L, typename F>
 __device__ __forceinline__ float lanes_fold(float v, F f) {
     static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes that share a value");
-    v = f(v, dpp_move<kDppXor1>(v, v));
-    v = f(v, dpp_move<kDppXor2>(v, v));
-    v = f(v, dpp_move<kDppHalfMirror>(v, v));
-    if constexpr (L >= 16) v = f(v, dpp_move<kDppMirror>(v, v));
+    v = f(v, dpp_take<kDppXor1>(v));
+    v = f(v, dpp_take<kDppXor2>(v));
+    v = f(v, dpp_take<kDppHalfMirror>(v));
+    if constexpr (L >= 16) v = f(v, dpp_take<kDppMirror>(v));
     if constexpr (L >= 32) {
         const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
         v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
