@@ -730,7 +730,7 @@ int64_t segred_norm_grad_workspace(int64_t k, int64_t rows);
  * rows < 0, a scale that is not positive and finite, a NULL pointer that is
  * needed, misalignment (an element, 8 bytes for target, 16 for the workspace), a
  * workspace that is missing or too small.  SEGRED_ERR_UNSUPPORTED for integer
- * types, k above 2^24, vocab above 2^30, rows above 2^31 or picks above 2^20.
+ * types, k above 2^24, vocab above 2^30, rows above 2^31 or picks above 4,096.
  * SEGRED_ERR_HIP if a launch fails.
  */
 int segred_cross_entropy(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights,
@@ -752,9 +752,11 @@ int64_t segred_cross_entropy_workspace(int32_t dtype, int64_t k, int64_t rows, i
  *   grad_values   [rows, k] of type `dtype`, or NULL: not asked for.
  *   grad_weights  [vocab, k] of type grad_weights_dtype (`dtype` or SEGRED_F32), or
  *                 NULL: not asked for.  Every element is written.
- *   workspace     segred_cross_entropy_grad_workspace(dtype, k, rows, vocab) bytes:
- *                 a piece of dz (256 MiB, or 4,096 entries where these take more)
- *                 and the sums of grad_values in float32.
+ *   workspace     segred_cross_entropy_grad_workspace(dtype, k, rows, vocab,
+ *                 picks) bytes: a piece of dz (256 MiB, or 4,096 entries where these
+ *                 take more), for many rows of 16 bits once more turned, with the
+ *                 values and a piece of the weights, and the sums of grad_values in
+ *                 float32.
  *   the others and the errors as segred_cross_entropy.
  */
 int segred_cross_entropy_grad(const float *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
@@ -762,7 +764,7 @@ int segred_cross_entropy_grad(const float *grad, const void *values, int32_t dty
                               int64_t picks, float scale, const float *lse, const float *picked, void *grad_values,
                               void *grad_weights, int32_t grad_weights_dtype, void *workspace, int64_t workspace_bytes,
                               hipStream_t stream);
-int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab);
+int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab, int64_t picks);
 
 /* Static, host-side description of a status code (never NULL). */
 const char *segred_status_string(int status);

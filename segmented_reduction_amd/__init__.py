@@ -148,7 +148,7 @@ def library(path: str | None = None):
             lib.segred_cross_entropy_grad.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, i64, f32, vp, vp, vp, vp,
                                                       i32, vp, i64, vp]
             lib.segred_cross_entropy_grad.restype = ctypes.c_int
-            lib.segred_cross_entropy_grad_workspace.argtypes = [i32, i64, i64, i64]
+            lib.segred_cross_entropy_grad_workspace.argtypes = [i32, i64, i64, i64, i64]
             lib.segred_cross_entropy_grad_workspace.restype = i64
             lib.segred_status_string.argtypes = [ctypes.c_int]
             lib.segred_status_string.restype = ctypes.c_char_p
@@ -980,7 +980,7 @@ def cross_entropy_grad(grad: torch.Tensor, values: torch.Tensor, weights: torch.
     grad_values = torch.empty_like(values) if want_values else None
     grad_weights = torch.empty((v, k), dtype=kind, device=device) if want_weights else None
     lib = _lib or library()
-    need = lib.segred_cross_entropy_grad_workspace(code, k, n, v)
+    need = lib.segred_cross_entropy_grad_workspace(code, k, n, v, picks)
     work = torch.empty(need, dtype=torch.uint8, device=device)
     _launch(lib.segred_cross_entropy_grad, "segred_cross_entropy_grad", dev, grad.data_ptr(), values.data_ptr(), code, k, n,
             weights.data_ptr(), v, target.data_ptr(), probs.data_ptr() if probs is not None else None, picks, scale,

@@ -36,12 +36,15 @@ struct LossArgs {
     float *loss, *lse, *picked;  // picked: [N, picks], also the gradient call's
     // back
     const float *grad;
-    float *share, *hit;  // [N]: grad scale s and grad scale, by `factor`
+    float *share, *hit;  // [N]: grad scale s (by `factor`) and grad scale
     float *bound;        // [N]: what |dz| of a row is at most
     int64_t *live;       // [N]: the row, or -1 where it has no target
     float *factor;       // what dz is multiplied by before it is rounded, and 1 / factor
     char *slope;         // [N, ld]: dz of the piece
-    int64_t ld;
+    char *turned;        // [vc, ldn]: the same turned, or null
+    int64_t ld, ldn;
+    float *hits;         // [N, picks]: dz of the targets, before `factor`
+    const char *rows_turned, *words_turned;  // [K, ldn] of the values, [K, ld] of the piece's weights
     float *sums;  // [parts_k, N, K]: dx so far
     int64_t cuts;
     int first;  // the first piece
@@ -142,8 +145,7 @@ __device__ __forceinline__ f32x4 loss_slopes(const LossArgs &a, const LossRow &o
         y[e] = o.live && n + e < a.vc ? o.share * exp2_fast(fmaf(z[e], a.bend, -o.base)) : 0.f;
     return y;
 }
-// Calls put(r, c, dz) for the targets of the tile's rows in its columns, from
-// the logits that the forward call kept; a target named twice gets both shares.
+// Calls put(r, c, dz) for the targets of the tile's rows in its columns.
 template <int BM, int BN, int THREADS, typename P>
 __device__ __forceinline__ void loss_targets(const LossArgs &a, const LossPlace &p, P put) {
     constexpr int kEach = THREADS / BM, kBatch = 8;  // threads of a row, targets that a thread looks at at a time
@@ -152,6 +154,7 @@ __device__ __forceinline__ void loss_targets(const LossArgs &a, const LossPlace 
     const int64_t begin = a.v0 + p.n0, row = p.row0 + r;
     const uint64_t left = min((int64_t)BN, a.vc - p.n0);
     const int64_t *target = a.target + row * picks;
+    const float f = a.factor ? a.factor[0] : 1.f;
     for (int j0 = threadIdx.x % kEach; j0 < picks; j0 += kBatch * kEach) {
         int64_t t[kBatch];
 #pragma unroll
@@ -159,17 +162,13 @@ __device__ __forceinline__ void loss_targets(const LossArgs &a, const LossPlace 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if ((uint64_t)t[b] >= left) continue;
-            float sum = 0.f;
-            for (int j = 0; j < picks; ++j)
-                if (target[j] - begin == t[b]) sum += a.probs ? a.probs[row * picks + j] : 1.f;
-            const float e = exp2_fast(fmaf(a.picked[row * picks + j0 + b * kEach], kLog2e, -a.lse[row] * kLog2e));
-            put(r, (int)t[b], fmaf(a.share[row], e, -a.hit[row] * sum));
+            put(r, (int)t[b], f * a.hits[row * picks + j0 + b * kEach]);
         }
     }
 }
 
-// Leaves dz of a tile in the piece.
-template <typename T, int RI, int CJ, int BM, int BN, int THREADS, typename G, typename R, typename C>
+// Leaves dz of a tile in the piece, and turned (TURN).
+template <typename T, int RI, int CJ, int BM, int BN, int THREADS, bool TURN, typename G, typename R, typename C>
 __device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p, lds_char *lds, int lane, G get, R row,
                                            C col) {
     T *out = reinterpret_cast<T *>(a.slope) + p.row0 * a.ld;
@@ -191,6 +190,12 @@ __device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p
         });
         __syncthreads();
         tile_write<T, BM, BN, THREADS>(lds, out, p.rows, p.n0, a.ld, a.ld, true);
+        if constexpr (TURN)
+            if (a.turned) {
+                tile_turn<T, BM, BN, THREADS>(lds, threadIdx.x >> 6, lane);
+                tile_write<T, BN, BM, THREADS>(lds, reinterpret_cast<T *>(a.turned) + p.n0 * a.ldn,
+                                               (int)min((int64_t)BN, a.vc - p.n0), p.row0, a.ldn, a.ldn, true);
+            }
     } else {
         // the stores of other waves to the same places must have gone before
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -211,7 +216,7 @@ struct LossTile {
         auto get = [&](int i, int j) -> f32x4 & { return acc[i][j]; };
         auto row = [&](int i) { return Tile::m0(wave) + 16 * i + (lane & 15); };
         auto col = [&](int j) { return Tile::n0(wave) + 16 * j + (lane >> 4) * 4; };
-        if constexpr (SLOPE) loss_slope<T, Tile::MT, Tile::NT, BM, BN, Tile::kThreads>(a, p, lds, lane, get, row, col);
+        if constexpr (SLOPE) loss_slope<T, Tile::MT, Tile::NT, BM, BN, Tile::kThreads, false>(a, p, lds, lane, get, row, col);
         else loss_pairs<Tile::MT, Tile::NT, WN, BM, BN>(a, p, part, lds, wave % WN, lane, get, row, col);
     }
 };
@@ -254,7 +259,7 @@ __global__ __launch_bounds__(kRowSplitThreads, 3) void loss_split(LossArgs a) {
     auto row = [&](int i) { return Tile::m0(wave) + 16 * i + (lane & 15); };
     auto col = [&](int j) { return Tile::n0(wave) + 16 * j + (lane >> 4) * 4; };
     if constexpr (SLOPE) {
-        loss_slope<float, Tile::MT, Tile::NT, 64, 128, kRowSplitThreads>(a, p, lds, lane, get, row, col);
+        loss_slope<float, Tile::MT, Tile::NT, 64, 128, kRowSplitThreads, false>(a, p, lds, lane, get, row, col);
     } else {
         loss_pairs<Tile::MT, Tile::NT, 2, 64, 128>(a, p, p.n0 >> 6, lds, wave % 2, lane, get, row, col);
         for (int r = threadIdx.x; r < p.rows; r += kRowSplitThreads)
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_many(LossArgs a) {
     auto get = [&](int i, int j) -> f32x4 & { return acc[i >> 2][j >> 1][i & 3][j & 1]; };
     auto row = [&](int i) { return phase_row(i >> 2, i & 3, wave) + (lane & 15); };
     auto col = [&](int j) { return phase_col(j >> 1, j & 1, wave) + (lane >> 4) * 4; };
-    if constexpr (SLOPE) loss_slope<T, 4 * AH, 4, AH * kHalf, 2 * kHalf, kPhaseThreads>(a, p, lds, lane, get, row, col);
+    if constexpr (SLOPE) loss_slope<T, 4 * AH, 4, AH * kHalf, 2 * kHalf, kPhaseThreads, true>(a, p, lds, lane, get, row, col);
     else loss_pairs<4 * AH, 4, 4, AH * kHalf, 2 * kHalf>(a, p, p.tile, lds, wave & 3, lane, get, row, col);
 }
 
@@ -413,6 +418,12 @@ __global__ __launch_bounds__(256) void loss_join(LossArgs a) {
     }
 }
 
+// dz of a row's target `i` that has probability p in all.
+__device__ __forceinline__ float loss_hit(const LossArgs &a, int64_t row, int64_t i, float p) {
+    const float e = exp2_fast(fmaf(a.picked[i], kLog2e, -a.lse[row] * kLog2e));
+    return fmaf(a.share[row], e, -a.hit[row] * p);
+}
+
 // What the gradient's tiles need of each row, LANES lanes a row, and the one
 // segment of the weights' sums.
 template <int LANES>
@@ -444,6 +455,23 @@ __global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *of
     a.hit[row] = g;
     a.bound[row] = bound < INFINITY ? bound : 0.f;
     a.live[row] = live ? row : -1;
+    if constexpr (LANES == 1) a.hits[row] = live ? loss_hit(a, row, row, share) : 0.f;
+}
+// dz of the targets of rows that have several, from the logits that the forward
+// call kept; a target named twice in a row gets both shares.
+__global__ __launch_bounds__(256) void loss_hits(LossArgs a) {
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.N * a.picks) return;
+    const int64_t row = i / a.picks, t = a.target[i];
+    const int64_t *target = a.target + row * a.picks;
+    float sum = 0.f;
+    if (t >= 0 && t < a.V) {
+#pragma unroll 8
+        for (int64_t j = 0; j < a.picks; ++j)
+            sum += target[j] == t ? (a.probs ? a.probs[row * a.picks + j] : 1.f) : 0.f;
+        sum = loss_hit(a, row, i, sum);
+    }
+    a.hits[i] = sum;
 }
 
 // float16 holds 2^-24 to 2^16, so dz is brought near 2^13 by a power of two that
@@ -462,10 +490,7 @@ __global__ __launch_bounds__(1024) void loss_factor(LossArgs a) {
     for (int w = 0; w < 16; ++w) m = fmaxf(m, s[w]);
     const int up = m > 0.f ? min(max(13 - ilogbf(m), -100), 100) : 0;
     const float f = ldexpf(1.f, up);
-    for (int64_t i = threadIdx.x; i < a.N; i += 1024) {
-        a.share[i] *= f;
-        a.hit[i] *= f;
-    }
+    for (int64_t i = threadIdx.x; i < a.N; i += 1024) a.share[i] *= f;
     if (threadIdx.x == 0) {
         a.factor[0] = f;
         a.factor[1] = ldexpf(1.f, -up);
@@ -695,6 +720,101 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_back_many(LossArgs a) {
                          acc[0][q][i][j]);
 }
 
+// The same from the piece's weights turned: both operands run along the
+// contraction, AH * 128 x 256.
+template <typename T, int AH>
+__global__ __launch_bounds__(kPhaseThreads) void loss_back_turned(LossArgs a) {
+    using Tile = PhaseTile<T, AH>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LossBack p = loss_back_place<AH * kHalf, 2 * kHalf>(a);
+    if (p.rows <= 0) return;
+    const int64_t steps = (a.vc + kStep<T> - 1) / kStep<T>, k0 = p.cut * steps / a.cuts * kStep<T>;
+    const int64_t k1 = min((p.cut + 1) * steps / a.cuts * kStep<T>, a.ld);
+    f32x4 acc[2][2][4][2] = {};
+    Tile::run(
+        acc, p.rows, (int)(k1 - k0), lds, wave, lane,
+        [&](int r) -> const char * {
+            return r < p.rows ? a.slope + ((p.row0 + r) * a.ld + k0) * (int64_t)sizeof(T) : nullptr;
+        },
+        [&](int c) -> const char * {
+            return p.n0 + c < a.K ? a.words_turned + ((p.n0 + c) * a.ld + k0) * (int64_t)sizeof(T) : nullptr;
+        });
+#pragma unroll
+    for (int h = 0; h < AH; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    loss_add(a, p, phase_row(h, i, wave) + (lane & 15), p.n0 + phase_col(q, j, wave) + (lane >> 4) * 4,
+                             acc[h][q][i][j]);
+}
+
+// dW of a piece from dz and the values, both turned: 256 entries x 256 columns.
+template <typename T>
+__global__ __launch_bounds__(kPhaseThreads) void loss_words_turned(LossArgs a, char *out, int f32) {
+    using Tile = PhaseTile<T, 2>;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.mtiles * a.ntiles);
+    if (id >= a.mtiles * a.ntiles) return;
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    const int64_t m0 = at.m * 256, n0 = at.n * 256;
+    const int rows = (int)min((int64_t)256, a.vc - m0);
+    f32x4 acc[2][2][4][2] = {};
+    Tile::run(
+        acc, rows, (int)a.ldn, lds, wave, lane,
+        [&](int r) -> const char * { return r < rows ? a.turned + (m0 + r) * a.ldn * (int64_t)sizeof(T) : nullptr; },
+        [&](int c) -> const char * {
+            return n0 + c < a.K ? a.rows_turned + (n0 + c) * a.ldn * (int64_t)sizeof(T) : nullptr;
+        });
+    const float f = a.factor ? a.factor[1] : 1.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = phase_row(h, i, wave) + (lane & 15), c = phase_col(q, j, wave) + (lane >> 4) * 4;
+                    const f32x4 y = acc[h][q][i][j] * f;
+                    if (!f32) tile_put<T, 256>(lds, r, c, y);
+                    else if (r < rows) store_quad<float>(reinterpret_cast<float *>(out) + (m0 + r) * a.K, n0 + c, a.K, y, true);
+                }
+    if (f32) return;
+    __syncthreads();
+    tile_write<T, 256, 256, kPhaseThreads>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K, true);
+}
+
+// out[c][r] = in[r][c] for `rows` rows of `cols` (whole units), `ld` and `old`
+// elements apart; rows that `live` leaves out and the columns up to `old` are zeros.
+constexpr int kTurnRows = 128, kTurnCols = 64;
+template <typename T>
+__global__ __launch_bounds__(256) void loss_turn(const T *in, int64_t rows, int64_t cols, int64_t ld, const int64_t *live,
+                                                 T *out, int64_t old) {
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kTurnRows * kTurnCols * 2];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, high = (old + kTurnRows - 1) / kTurnRows;
+    const int64_t r0 = id % high * kTurnRows, c0 = id / high * kTurnCols;
+    if (c0 >= cols) return;
+#pragma unroll
+    for (int i = threadIdx.x; i < kTurnRows * kTurnCols / 8; i += 256) {
+        const int r = i / (kTurnCols / 8), u = i % (kTurnCols / 8);
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (r0 + r < rows && c0 + u * 8 < cols && (!live || live[r0 + r] >= 0))
+            v = *reinterpret_cast<const u32x4 *>(in + (r0 + r) * ld + c0 + u * 8);
+        *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, kTurnCols>(r, u)) = v;
+    }
+    __syncthreads();
+    tile_turn<T, kTurnRows, kTurnCols, 256>(lds, threadIdx.x >> 6, threadIdx.x & 63);
+    tile_write<T, kTurnCols, kTurnRows, 256>(lds, out + c0 * old, (int)min((int64_t)kTurnCols, cols - c0), r0, old, old, true);
+}
+
 // Adds the cuts' sums in order and rounds once.
 template <typename T>
 __global__ __launch_bounds__(256) void loss_back_join(LossArgs a) {
@@ -719,7 +839,7 @@ __global__ __launch_bounds__(256) void loss_back_join(LossArgs a) {
 
 // --------------------------------------------------------------------- host
 
-constexpr int64_t kLossFewRows = 16;
+constexpr int64_t kLossFewRows = 16, kLossRows = int64_t(1) << 31, kLossVocab = 1 << 30, kLossPicks = 4096;
 // Kernels of the tiles: columns that a pair covers.
 enum LossKind { kLossFew, kLossSmall, kLossOne, kLossTwo, kLossSplit, kLossAny };
 LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) {
@@ -773,7 +893,7 @@ int loss_check(const void *values, int32_t dtype, int64_t k, int64_t rows, const
         return SEGRED_ERR_INVALID_ARGUMENT;
     if (!(scale > 0.f) || std::isinf(scale)) return SEGRED_ERR_INVALID_ARGUMENT;
     if (!weights || (rows > 0 && (!values || !target))) return SEGRED_ERR_INVALID_ARGUMENT;
-    if (e == 0 || k > kMaxWidth || vocab > (int64_t(1) << 30) || picks > (int64_t(1) << 20) || rows > (int64_t(1) << 31))
+    if (e == 0 || k > kMaxWidth || vocab > kLossVocab || picks > kLossPicks || rows > kLossRows)
         return SEGRED_ERR_UNSUPPORTED;
     if (!aligned(values, e) || !aligned(weights, e) || !aligned(target, 8) || !aligned(probs, 4) || !aligned(workspace, 16))
         return SEGRED_ERR_INVALID_ARGUMENT;
@@ -813,13 +933,20 @@ int loss_forward(const LossArgs &a, LossKind kind, hipStream_t st) {
 }
 
 // The gradient's pieces and its working memory.
+//
+// Products whose operands both run along the contraction are the fastest (bfloat16,
+// 4,096 rows, 2,048 columns, 32,768 entries: 410 us against 580 and 673 with one or
+// both across it), so operands are turned where that is less than it saves: dz
+// as the tiles write it, the values once, the weights a piece at a time.
 struct LossPlan {
     int64_t piece, cuts;  // columns of a piece; workgroups that share a tile of dx
     bool many;            // dx in tiles of 128 x 256
-    int64_t slope, sums, share, hit, bound, live, offsets, factor, outer, bytes;  // places
+    bool turn_rows, turn_words;  // dW from dz and the values turned; dx from the weights turned
+    // places in the working memory
+    int64_t slope, turned, rows_turned, words_turned, sums, share, hit, bound, live, hits, offsets, factor, outer, bytes;
 };
 constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096;
-LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v) {
+LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v, int64_t picks) {
     const int64_t e = float_size(dtype);
     LossPlan p{};
     p.piece = std::min(v, std::max(kPieceLeast, kPieceBytes / (std::max<int64_t>(n, 1) * e) / 256 * 256));
@@ -827,8 +954,12 @@ LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v) {
     const int64_t pieces = (v + p.piece - 1) / p.piece;
     p.piece = std::min(v, ((v + pieces - 1) / pieces + 255) / 256 * 256);
     p.many = e == 2 && n > 64 && k > 128;
-    const int64_t tiles = p.many ? ((n + 127) / 128) * ((k + 255) / 256)
-                                 : (n <= 16 && e == 2 ? 1 : (n + 63) / 64) * ((k + 127) / 128);
+    const bool whole = e == 2 && k % 8 == 0 && loss_kind(dtype, n, k, p.piece, true) == kLossTwo;
+    p.turn_rows = whole && n >= 512 && k >= 512;
+    p.turn_words = whole && n >= 2048;
+    const int64_t tiles = p.turn_words ? ((n + 255) / 256) * ((k + 255) / 256)
+                          : p.many     ? ((n + 127) / 128) * ((k + 255) / 256)
+                                       : (n <= 16 && e == 2 ? 1 : (n + 63) / 64) * ((k + 127) / 128);
     const int64_t room = p.many ? 256 : 512, steps = (p.piece + 63) / 64;
     p.cuts = std::max<int64_t>(1, std::min({room / std::max<int64_t>(tiles, 1), steps / 8, (int64_t)64}));
     int64_t at = 0;
@@ -837,12 +968,17 @@ LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    p.slope = take(n * ((p.piece + 7) / 8 * 8) * e);
+    const int64_t ld = (p.piece + 7) / 8 * 8, ldn = (n + 7) / 8 * 8;
+    p.slope = take(n * ld * e);
+    p.turned = take(p.turn_rows ? p.piece * ldn * e : 0);
+    p.rows_turned = take(p.turn_rows ? k * ldn * e : 0);
+    p.words_turned = take(p.turn_words ? k * ld * e : 0);
     p.sums = take(p.cuts * n * k * 4);
     p.share = take(n * 4);
     p.hit = take(n * 4);
     p.bound = take(n * 4);
     p.live = take(n * 8);
+    p.hits = take(n * picks * 4);
     p.offsets = take(16);
     p.factor = take(8);
     // the last piece is no wider than the others, but may be cut otherwise
@@ -858,58 +994,99 @@ __global__ void loss_bounds(int64_t *offsets, int64_t n) {
 }
 
 template <typename T>
+int loss_turn_launch(const void *in, int64_t rows, int64_t cols, int64_t ld, const int64_t *live, void *out, int64_t old,
+                     hipStream_t st) {
+    dim3 grid;
+    if (!tile_grid((old + kTurnRows - 1) / kTurnRows * ((cols + kTurnCols - 1) / kTurnCols), grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(false, (loss_turn<T>), grid, dim3(256), 0, st, static_cast<const T *>(in), rows, cols, ld, live,
+                     static_cast<T *>(out), old);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+// dx += dz W of a piece.
+template <typename T>
+int loss_back_launch(LossArgs a, const LossPlan &p, bool direct, hipStream_t st) {
+    const int64_t e = sizeof(T);
+    const bool turned = p.turn_words && direct;
+    const int64_t bm = turned ? 256 : p.many ? 128 : a.N <= 16 && e == 2 ? 16 : 64, bn = p.many && direct ? 256 : 128;
+    a.mtiles = (a.N + bm - 1) / bm;
+    a.ntiles = (a.K + bn - 1) / bn;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles * a.cuts, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if constexpr (sizeof(T) == 4) {
+        if (a.K % 8 == 0) timed_launch_ggl(true, (loss_back_split<true>), grid, dim3(kRowSplitThreads), 0, st, a);
+        else timed_launch_ggl(true, (loss_back_split<false>), grid, dim3(kRowSplitThreads), 0, st, a);
+    } else if (turned) {
+        const int rc = loss_turn_launch<T>(a.weights + a.v0 * a.K * e, a.vc, a.K, a.K, nullptr,
+                                           const_cast<char *>(a.words_turned), a.ld, st);
+        if (rc != SEGRED_OK) return rc;
+        timed_launch_ggl(true, (loss_back_turned<T, 2>), grid, dim3(kPhaseThreads), 0, st, a);
+    } else if (p.many && direct) {
+        timed_launch_ggl(true, (loss_back_many<T>), grid, dim3(kPhaseThreads), 0, st, a);
+    } else if (p.many) {
+        timed_launch_ggl(true, (loss_back<T, 128, 128, 2, 2, false>), grid, dim3(256), 0, st, a);
+    } else if (bm == 16) {
+        if (direct) timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, true>), grid, dim3(256), 0, st, a);
+        else timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, false>), grid, dim3(256), 0, st, a);
+    } else {
+        if (direct) timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, true>), grid, dim3(256), 0, st, a);
+        else timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, false>), grid, dim3(256), 0, st, a);
+    }
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+template <typename T>
 int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int32_t dtype, void *grad_weights,
                   int32_t grad_weights_dtype, char *work, hipStream_t st) {
-    const int64_t e = sizeof(T), ge = float_size(grad_weights_dtype);
+    const int64_t ge = float_size(grad_weights_dtype);
     int64_t *offsets = reinterpret_cast<int64_t *>(work + p.offsets);
+    const bool turn_rows = p.turn_rows && direct && grad_weights &&
+                           aligned(grad_weights, 16);  // whole units of dW's rows, too
+    a.ldn = (a.N + 7) / 8 * 8;
+    a.turned = turn_rows ? work + p.turned : nullptr;
+    a.rows_turned = work + p.rows_turned;
+    a.words_turned = work + p.words_turned;
     if (a.N == 0) {
         timed_launch_ggl(false, loss_bounds, dim3(1), dim3(1), 0, st, offsets, a.N);
     } else {
-        if (a.picks > 1)
+        dim3 grid;
+        if (a.picks > 1) {
+            if (!tile_grid((a.N * a.picks + 255) / 256, grid)) return SEGRED_ERR_UNSUPPORTED;
             timed_launch_ggl(false, (loss_rows_prepare<16>), dim3((unsigned)((a.N + 15) / 16)), dim3(256), 0, st, a, offsets);
-        else
+            timed_launch_ggl(false, loss_hits, grid, dim3(256), 0, st, a);
+        } else {
             timed_launch_ggl(false, (loss_rows_prepare<1>), dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, st, a, offsets);
+        }
         if (__is_same(T, _Float16)) timed_launch_ggl(false, loss_factor, dim3(1), dim3(1024), 0, st, a);
     }
     if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
-    for (a.v0 = 0; a.v0 < a.V; a.v0 += p.piece) {
+    int rc = SEGRED_OK;
+    if constexpr (sizeof(T) == 2)
+        if (turn_rows) rc = loss_turn_launch<T>(a.values, a.N, a.K, a.K, a.live, work + p.rows_turned, a.ldn, st);
+    for (a.v0 = 0; a.v0 < a.V && rc == SEGRED_OK; a.v0 += p.piece) {
         a.vc = std::min(p.piece, a.V - a.v0);
         a.ld = (a.vc + 7) / 8 * 8;
         a.first = a.v0 == 0;
-        if (a.N > 0) {
-            const int rc = loss_tiles_launch<T, true>(a, kind, st);
-            if (rc != SEGRED_OK) return rc;
-        }
-        if (a.grad_values && a.N > 0) {
-            LossArgs b = a;
-            const int64_t bm = p.many ? 128 : a.N <= 16 && e == 2 ? 16 : 64, bn = p.many && direct ? 256 : 128;
-            b.mtiles = (a.N + bm - 1) / bm;
-            b.ntiles = (a.K + bn - 1) / bn;
-            dim3 grid;
-            if (!tile_grid(b.mtiles * b.ntiles * b.cuts, grid)) return SEGRED_ERR_UNSUPPORTED;
-            if constexpr (sizeof(T) == 4) {
-                if (a.K % 8 == 0) timed_launch_ggl(true, (loss_back_split<true>), grid, dim3(kRowSplitThreads), 0, st, b);
-                else timed_launch_ggl(true, (loss_back_split<false>), grid, dim3(kRowSplitThreads), 0, st, b);
-            } else if (p.many && direct) {
-                timed_launch_ggl(true, (loss_back_many<T>), grid, dim3(kPhaseThreads), 0, st, b);
-            } else if (p.many) {
-                timed_launch_ggl(true, (loss_back<T, 128, 128, 2, 2, false>), grid, dim3(256), 0, st, b);
-            } else if (bm == 16) {
-                if (direct) timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, true>), grid, dim3(256), 0, st, b);
-                else timed_launch_ggl(true, (loss_back<T, 16, 128, 1, 4, false>), grid, dim3(256), 0, st, b);
-            } else {
-                if (direct) timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, true>), grid, dim3(256), 0, st, b);
-                else timed_launch_ggl(true, (loss_back<T, 64, 128, 2, 2, false>), grid, dim3(256), 0, st, b);
+        if (a.N > 0) rc = loss_tiles_launch<T, true>(a, kind, st);
+        if (rc == SEGRED_OK && a.grad_values && a.N > 0) rc = loss_back_launch<T>(a, p, direct, st);
+        if (rc != SEGRED_OK || !grad_weights) continue;
+        char *to = static_cast<char *>(grad_weights) + a.v0 * a.K * ge;
+        if constexpr (sizeof(T) == 2) {
+            if (turn_rows) {
+                LossArgs b = a;
+                b.mtiles = (a.vc + 255) / 256;
+                b.ntiles = (a.K + 255) / 256;
+                dim3 grid;
+                if (!tile_grid(b.mtiles * b.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+                timed_launch_ggl(true, (loss_words_turned<T>), grid, dim3(kPhaseThreads), 0, st, b, to, ge == 4 ? 1 : 0);
+                rc = hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+                continue;
             }
-            if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
         }
-        if (grad_weights) {
-            const int rc = outer_scaled(a.slope, a.ld, a.vc, a.values, a.live, a.N, a.K, dtype, offsets,
-                                        static_cast<char *>(grad_weights) + a.v0 * a.K * ge, grad_weights_dtype,
-                                        a.factor ? a.factor + 1 : nullptr, work + p.outer, st);
-            if (rc != SEGRED_OK) return rc;
-        }
+        rc = outer_scaled(a.slope, a.ld, a.vc, a.values, a.live, a.N, a.K, dtype, offsets, to, grad_weights_dtype,
+                          a.factor ? a.factor + 1 : nullptr, work + p.outer, st);
     }
+    if (rc != SEGRED_OK) return rc;
     if (a.grad_values && a.N > 0) {
         dim3 grid;
         if (!tile_grid((a.N * a.K + 1023) / 1024, grid)) return SEGRED_ERR_UNSUPPORTED;
@@ -953,11 +1130,12 @@ extern "C" int segred_cross_entropy(const void *values, int32_t dtype, int64_t k
     }
 }
 
-extern "C" int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab) {
-    if (float_size(dtype) == 0 || k < 1 || k > kMaxWidth || rows < 0 || vocab < 1 || vocab > (int64_t(1) << 30) ||
-        rows > (int64_t(1) << 31))
+extern "C" int64_t segred_cross_entropy_grad_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab,
+                                                       int64_t picks) {
+    if (float_size(dtype) == 0 || k < 1 || k > kMaxWidth || rows < 0 || rows > kLossRows || vocab < 1 ||
+        vocab > kLossVocab || picks < 1 || picks > kLossPicks)
         return 0;
-    return loss_plan(dtype, k, rows, vocab).bytes;
+    return loss_plan(dtype, k, rows, vocab, picks).bytes;
 }
 
 extern "C" int segred_cross_entropy_grad(const float *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
@@ -974,7 +1152,7 @@ extern "C" int segred_cross_entropy_grad(const float *grad, const void *values, 
     if (!aligned(grad, 4) || !aligned(lse, 4) || !aligned(picked, 4) || !aligned(grad_values, e) ||
         !aligned(grad_weights, float_size(grad_weights_dtype)))
         return SEGRED_ERR_INVALID_ARGUMENT;
-    const LossPlan p = loss_plan(dtype, k, rows, vocab);
+    const LossPlan p = loss_plan(dtype, k, rows, vocab, picks);
     if (!workspace || workspace_bytes < p.bytes) return SEGRED_ERR_INVALID_ARGUMENT;
     LossArgs a = loss_args(values, k, rows, weights, vocab, target, probs, picks, scale);
     char *work = static_cast<char *>(workspace);
@@ -988,6 +1166,7 @@ extern "C" int segred_cross_entropy_grad(const float *grad, const void *values, 
     a.hit = reinterpret_cast<float *>(work + p.hit);
     a.bound = reinterpret_cast<float *>(work + p.bound);
     a.live = reinterpret_cast<int64_t *>(work + p.live);
+    a.hits = reinterpret_cast<float *>(work + p.hits);
     a.factor = dtype == SEGRED_F16 && rows > 0 ? reinterpret_cast<float *>(work + p.factor) : nullptr;
     a.cuts = p.cuts;
     const bool direct = loss_direct(values, weights, dtype, k);

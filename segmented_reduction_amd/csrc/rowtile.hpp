@@ -250,4 +250,35 @@ __device__ __forceinline__ void tile_write(const lds_char *lds, T *out, int rows
     }
 }
 
+// Turns a tile of 16-bit elements in LDS: BM rows of BN in the places of
+// tile_put become BN rows of BM.  Every thread holds its share in registers
+// between two barriers; 16 lanes read 4 x 16 elements transposed at a time.
+template <typename T, int BM, int BN, int THREADS>
+__device__ __forceinline__ void tile_turn(lds_char *lds, int wave, int lane) {
+    constexpr int kUnits = BM / 8 * BN / THREADS;  // of 8 elements, per thread
+    static_assert(kUnits >= 1 && BM / 8 * BN % THREADS == 0 && BN % 16 == 0, "whole units");
+    const int group = wave * 4 + (lane >> 4), l = lane & 15;
+    union {
+        s16x4 h[2];
+        u32x4 v;
+    } x[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int at = i * (THREADS / 16) + group, ru = at % (BM / 8), cb = at / (BM / 8);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = ru * 8 + h * 4 + (l >> 2), c = cb * 16 + (l & 3) * 4;
+            x[i].h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(lds + tile_unit<T, BN>(r, c >> 3) + (c & 4) * 2));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int at = i * (THREADS / 16) + group, ru = at % (BM / 8), cb = at / (BM / 8);
+        *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BM>(cb * 16 + l, ru)) = x[i].v;
+    }
+    __syncthreads();
+}
+
 }  // namespace segred

@@ -91,7 +91,7 @@ def _loss_grad(**kw):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(dtype=5), 1), (dict(dtype=1), 2), (dict(k=0), 1), (dict(rows=-1), 1), (dict(vocab=0), 1), (dict(picks=0), 1),
-    (dict(k=2 ** 24 + 1), 2), (dict(vocab=2 ** 30 + 1), 2), (dict(rows=2 ** 31 + 1), 2), (dict(picks=2 ** 20 + 1), 2),
+    (dict(k=2 ** 24 + 1), 2), (dict(vocab=2 ** 30 + 1), 2), (dict(rows=2 ** 31 + 1), 2), (dict(picks=4097), 2),
     (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=NAN), 1), (dict(scale=INF), 1), (dict(values=None), 1),
     (dict(weights=None), 1), (dict(target=None), 1), (dict(values=FAKE + 1), 1), (dict(weights=FAKE + 1), 1),
     (dict(target=FAKE + 4), 1), (dict(probs=FAKE + 2), 1), (dict(lse=None), 1), (dict(picked=None), 1), (dict(lse=FAKE + 2), 1),
@@ -122,8 +122,8 @@ def test_workspaces():
     assert lib.segred_cross_entropy_workspace(3, 64, 0, 10) == 0 and lib.segred_cross_entropy_workspace(0, 64, 1, 10) == 0
     assert lib.segred_cross_entropy_workspace(3, 64, 100, 6400) == 100 * 100 * 8
     for dtype, k, n, v in ((3, 2048, 4096, 65536), (2, 2048, 4096, 65536), (4, 64, 1, 2 ** 30), (3, 4096, 2 ** 20, 2 ** 17)):
-        need, e = lib.segred_cross_entropy_grad_workspace(dtype, k, n, v), 4 if dtype == 2 else 2
+        need, e = lib.segred_cross_entropy_grad_workspace(dtype, k, n, v, 3), 4 if dtype == 2 else 2
         piece = min(v, max(2 ** 28 // (n * e), 4096) + 8)
         # a piece, the rows' sums (up to 64 of them where there are few), and what the weights' sums need
-        assert need <= n * piece * e + 64 * min(n, 4096) * k * 4 + n * k * 4 + n * 64 + 2 ** 28
-    assert lib.segred_cross_entropy_grad_workspace(0, 64, 10, 10) == 0
+        assert need <= 2 * (n + 8) * piece * e + (n + piece) * k * e + 64 * min(n, 4096) * k * 4 + n * k * 4 + n * 64 + 2 ** 28
+    assert lib.segred_cross_entropy_grad_workspace(0, 64, 10, 10, 1) == 0

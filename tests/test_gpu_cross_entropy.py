@@ -53,7 +53,8 @@ def test_shapes(t, n, k, v):
 
 KERNELS = [("bf16", 100, 256, 33000), ("f16", 300, 256, 16500), ("bf16", 257, 512, 20001), ("f16", 8, 512, 30011),
            ("bf16", 300, 257, 5003), ("f32", 300, 128, 5003), ("f32", 5, 128, 9001), ("f32", 100, 65, 2001),
-           ("bf16", 513, 64, 9000), ("f16", 30, 1024, 3000)]
+           ("bf16", 513, 64, 9000), ("f16", 30, 1024, 3000),
+           ("bf16", 2100, 520, 5003), ("f16", 701, 512, 9001), ("bf16", 2051, 264, 8200), ("f16", 2304, 1024, 4100)]
 
 
 @pytest.mark.parametrize("t,n,k,v", KERNELS)
@@ -63,7 +64,7 @@ def test_kernels(t, n, k, v):
 
 
 @pytest.mark.parametrize("t,n,k,v", [("bf16", 16500, 64, 9001), ("f16", 16500, 72, 8193), ("f32", 8200, 40, 9000),
-                                     ("bf16", 16400, 65, 8300)])
+                                     ("bf16", 16400, 65, 8300), ("bf16", 16389, 512, 8300)])
 def test_pieces(t, n, k, v):
     """More than one piece of the vocabulary (256 MiB hold less)."""
     _check(*_case(t, n, k, v), f"cross entropy {t} {n}x{k} vocab {v} in pieces")
@@ -99,6 +100,18 @@ def test_rows_without_a_target(t, n):
     loss, lse, picked = sr.cross_entropy(dirty, w, nothing)
     dx, dw = sr.cross_entropy_grad(grad, dirty, w, nothing, lse, picked)
     assert (loss == 0).all() and (dx == 0).all() and (dw == 0).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_rows_without_a_target_among_many(t):
+    x, w, target, _, grad = _case(t, 2100, 512, 4100, none=0.0)
+    none = torch.arange(2100, device="cuda") % 3 == 1
+    target = torch.where(none, -100, target)
+    clean = _check(torch.where(none[:, None], 0, x), w, target, None, grad, f"cross entropy {t} 2100 rows, a third padding")
+    x[none] = float("nan")
+    loss, lse, picked = sr.cross_entropy(x, w, target)
+    dx, dw = sr.cross_entropy_grad(grad, x, w, target, lse, picked)
+    assert torch.equal(loss, clean[0]) and torch.equal(dx, clean[3]) and torch.equal(dw, clean[4])
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
