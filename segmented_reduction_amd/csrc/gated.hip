@@ -11,6 +11,7 @@
 // float32 they would take 16 bytes an output to write and read, against 4 k
 // operations to form them again, about equal at k = 1,024.
 #include <algorithm>
+#include <cmath>
 
 #include "internal.hpp"
 #include "rowtile.hpp"
@@ -27,20 +28,27 @@ struct GatedArgs {
     int64_t slots, ntiles;
     const char *grad;  // [N, M], the gradient call's
     void *out;         // [N, M], or [N, 2 M]
-    int vec;           // halves of rows of `out` (and of `grad`) hold whole 16-byte units on 16-byte boundaries
     float c1, c2;      // act(x) = x / (1 + exp(-x (c1 + c2 x^2))) where it is neither of the others
     int relu;
 };
 
-// An activation and its slope.  ERF: x Phi(x).
+// An activation and its slope.  ERF: x Phi(x), Phi of the normal distribution by
+// Abramowitz and Stegun 7.1.26 (erf to 1.5e-7, so Phi to 2^-23.6), whose factor
+// exp(-x^2 / 2) the slope needs as well: with the C library's erfc the epilogue took
+// a quarter of the time of a float call of 40,000 rows, 96 x 130.
 struct Bend {
     float value, slope;
 };
 template <bool ERF>
 __device__ __forceinline__ Bend bend(float x, const GatedArgs &a) {
     if constexpr (ERF) {
-        const float phi = 0.5f * erfcf(x * -0.70710678118654752f);
-        return {x * phi, fmaf(x * 0.39894228040143268f, __expf(-0.5f * x * x), phi)};
+        const float z = fabsf(x), e = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f);
+        const float t = __builtin_amdgcn_rcpf(fmaf(0.23164188899668f, z, 1.f));  // 0.3275911 / sqrt(2)
+        // halves of the formula's coefficients
+        const float q = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f), 0.127414796f);
+        const float tail = q * t * e;  // Phi(-|x|)
+        const float phi = x > 0.f ? 1.f - tail : tail;
+        return {x * phi, fmaf(x * 0.39894228040143268f, e, phi)};
     } else {
         if (a.relu) return {x < 0.f ? 0.f : x, x <= 0.f ? 0.f : 1.f};
         const float q = fminf(x * x, 1e6f);  // beyond that s is 0 or 1 already
@@ -106,25 +114,6 @@ __device__ __forceinline__ const char *gated_pair(const GatedArgs &a, const Gate
     return gated_weight<T>(a, p, (c >> 5) * 16 + (c & 15), (c >> 4) & 1);
 }
 
-// Four elements of the output's gradient.
-template <typename T>
-__device__ __forceinline__ f32x4 load_quad(const T *row, int64_t n, int64_t width, bool vec) {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-        if (n < width) {
-            typedef __attribute__((ext_vector_type(4))) T T4;
-            const T4 q = *reinterpret_cast<const T4 *>(row + n);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = (float)q[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n + j < width) c[j] = (float)row[n + j];
-    }
-    return c;
-}
-
 // Quads of 16-bit results pass through LDS so that whole stretches are moved; a
 // tile of the output's gradient enters the same way, and each quad of it is
 // replaced by the result's.  quad(f) calls f(row, column, g, u) for each of a
@@ -132,22 +121,21 @@ __device__ __forceinline__ f32x4 load_quad(const T *row, int64_t n, int64_t widt
 template <typename T, int BM, int BN, int THREADS, bool GRAD, bool ERF, typename Q>
 __device__ __forceinline__ void gated_store(const GatedArgs &a, const GatedPlace &p, lds_char *lds, Q quad) {
     T *out = reinterpret_cast<T *>(a.out);
-    const bool vec = a.vec != 0;
     if constexpr (sizeof(T) == 4) {
         quad([&](int r, int c, f32x4 g, f32x4 u) {
             if (r >= p.rows) return;
             const int64_t n = p.n0 + c, row = p.row0 + r;
             if constexpr (GRAD) {
-                gated_slope<ERF>(g, u, load_quad<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M, vec), a);
-                store_quad<T>(out + row * 2 * a.M, n, a.M, g, vec);
-                store_quad<T>(out + row * 2 * a.M + a.M, n, a.M, u, vec);
+                gated_slope<ERF>(g, u, load_four<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M), a);
+                store_four<T>(out + row * 2 * a.M, n, a.M, g);
+                store_four<T>(out + row * 2 * a.M + a.M, n, a.M, u);
             } else {
-                store_quad<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a), vec);
+                store_four<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a));
             }
         });
     } else if constexpr (GRAD) {
         lds_char *second = lds + BM * BN * 2;
-        tile_in<T, BM, BN, THREADS>(lds, reinterpret_cast<const T *>(a.grad) + p.row0 * a.M, p.rows, p.n0, a.M, vec);
+        tile_in<T, BM, BN, THREADS>(lds, reinterpret_cast<const T *>(a.grad) + p.row0 * a.M, p.rows, p.n0, a.M);
         __syncthreads();
         quad([&](int r, int c, f32x4 g, f32x4 u) {
             gated_slope<ERF>(g, u, tile_get<T, BN>(lds, r, c), a);
@@ -155,12 +143,12 @@ __device__ __forceinline__ void gated_store(const GatedArgs &a, const GatedPlace
             tile_put<T, BN>(second, r, c, u);
         });
         __syncthreads();
-        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * 2 * a.M, p.rows, p.n0, a.M, 2 * a.M, vec);
-        tile_write<T, BM, BN, THREADS>(second, out + p.row0 * 2 * a.M + a.M, p.rows, p.n0, a.M, 2 * a.M, vec);
+        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * 2 * a.M, p.rows, p.n0, a.M, 2 * a.M);
+        tile_write<T, BM, BN, THREADS>(second, out + p.row0 * 2 * a.M + a.M, p.rows, p.n0, a.M, 2 * a.M);
     } else {
         quad([&](int r, int c, f32x4 g, f32x4 u) { tile_put<T, BN>(lds, r, c, gated_value<ERF>(g, u, a)); });
         __syncthreads();
-        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * a.M, p.rows, p.n0, a.M, a.M, vec);
+        tile_write<T, BM, BN, THREADS>(lds, out + p.row0 * a.M, p.rows, p.n0, a.M, a.M);
     }
 }
 
@@ -279,13 +267,12 @@ __global__ __launch_bounds__(64 * NW) void seg_gated_few(GatedArgs a) {
         f32x4 g = Tile::sum(lds, 2 * j, lane), u = Tile::sum(lds, 2 * j + 1, lane);
         if (r >= p.rows) continue;
         const int64_t n = p.n0 + 16 * j + (lane >> 4) * 4;
-        const bool vec = a.vec != 0;
-        if constexpr (GRAD) {
-            gated_slope<ERF>(g, u, load_quad<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M, vec), a);
-            store_quad<T>(out + row * 2 * a.M, n, a.M, g, vec);
-            store_quad<T>(out + row * 2 * a.M + a.M, n, a.M, u, vec);
+            if constexpr (GRAD) {
+            gated_slope<ERF>(g, u, load_four<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M), a);
+            store_four<T>(out + row * 2 * a.M, n, a.M, g);
+            store_four<T>(out + row * 2 * a.M + a.M, n, a.M, u);
         } else {
-            store_quad<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a), vec);
+            store_four<T>(out + row * a.M, n, a.M, gated_value<ERF>(g, u, a));
         }
     }
 }
@@ -327,14 +314,63 @@ int gated_few_launch(GatedArgs a, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
-// The kernel for a call: the rule of segred_matmul with 2 m outputs.
-constexpr int64_t kFewRows = 8, kManyRows = 64, kManyTiles = 1536, kFewTiles = 512;
-constexpr int64_t kSplitRows = 24, kSplitTiles = 224;
+// The kernel for a 16-bit call whose rows are whole units.  Measured times in us
+// (bfloat16, mean rows per segment given, uneven, weights from HBM; forward, the
+// gradient adds about the same to all):
+//
+//   segments, k, m      64, 2048, 1024               8, 1024, 2560   8, 512, 2560   1, 4096, 4096
+//   mean rows           1    8   64  128  512         256   2048     1024   2048    128   1024  4096
+//   256 x 128          75  159  154  164  337          59    196       84    127     58     89   222
+//   128 x 128          70  151  141  169  376          42    228       82    148     56     65   262
+//   128 x 64           77  152  146  190  406          44    217       68    128     52     72   274
+//   64 x 32            70  115  172  223  578          60    310       96    195     25    120   435
+//   32 x 64            62  120  174  237  674          69    389      129    247     27    161   532
+//   few                77  115  406  767 2883         297   2267      646   1299     77    566  2258
+//
+// Each kernel's time is its rounds over the CUs, each an overhead (loads until the
+// first product, the epilogue) and a part that grows with k; small tiles have less
+// of the one and more of the other.  The rule takes the least of what these
+// constants, fitted to such times, give.
+struct GatedKind {
+    int rows, outputs, each;  // of a tile; tiles that a CU holds
+    double fixed, grad, alone, full;  // us of a round, more for the gradient, per 1,024 of k: one tile, `each` tiles
+};
+constexpr GatedKind kGatedKinds[] = {{256, 128, 1, 13, 11, 24.8, 24.8},
+                                     {128, 128, 1, 6, 4.7, 15.7, 15.7},
+                                     {128, 64, 2, 2.5, 4.3, 12, 18.3},
+                                     {64, 32, 3, 2.9, 2, 5, 9}};
+double gated_time(const GatedKind &g, const GatedArgs &a, bool grad) {
+    const double k = (double)a.K / 1024, fixed = g.fixed + (grad ? g.grad : 0), whole = fixed + k * g.full;
+    const int64_t columns = (a.M + g.outputs - 1) / g.outputs;
+    // half a tile more per segment for its end
+    const double tiles = (double)columns * (a.S == 1 ? (double)((a.N + g.rows - 1) / g.rows)
+                                                     : (double)a.N / g.rows + 0.5 * a.S);
+    auto part = [&](int n) {  // a round of n tiles a CU
+        return fixed + k * (g.each > 1 ? g.alone + (g.full - g.alone) * (n - 1) / (g.each - 1) : g.full);
+    };
+    const double load = tiles / 256, x = load / g.each;
+    if (x <= 0.92) return part((int)std::ceil(load));
+    if (a.S == 1) {
+        const int64_t n = (int64_t)std::ceil(load);
+        return n / g.each * whole + (n % g.each ? part((int)(n % g.each)) : 0);
+    }
+    // uneven segments: the last round is seldom full, a round that just fits does not always
+    return whole * (x <= 1 ? 1.35 : x < 2 ? 2 : x + 0.4);
+}
+int gated_kind(const GatedArgs &a, bool grad) {
+    int best = 0;
+    for (int i = 1; i < 4; ++i)
+        if (gated_time(kGatedKinds[i], a, grad) < gated_time(kGatedKinds[best], a, grad)) best = i;
+    return best;
+}
+
+// Float: segred_matmul's rule with 2 m outputs.
+constexpr int64_t kFewRows = 8, kFewGroups = 192, kSplitRows = 24, kSplitTiles = 224;
 template <typename T, bool GRAD, bool ERF>
 int gated_dispatch(const GatedArgs &a, bool direct, hipStream_t st) {
-    const int64_t mean = a.N / a.S, wide = 2 * a.M;
-    const int64_t tiles = (a.N / 64 + a.S / 2) * ((wide + 127) / 128);
+    const int64_t mean = a.N / a.S;
     if constexpr (sizeof(T) == 4) {
+        const int64_t tiles = (a.N / 64 + a.S / 2) * ((2 * a.M + 127) / 128);
         if (direct && mean <= kFewRows) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
         if (direct && (mean <= kSplitRows || tiles < kSplitTiles))
             return gated_launch<T, 32, 128, 1, 4, 3, true, GRAD, ERF>(a, st);
@@ -343,16 +379,16 @@ int gated_dispatch(const GatedArgs &a, bool direct, hipStream_t st) {
     } else {
         if (!direct && mean <= 2 * kFewRows) return gated_launch<T, 16, 128, 1, 4, 2, false, GRAD, ERF>(a, st);
         if (!direct) return gated_launch<T, 64, 128, 2, 2, 2, false, GRAD, ERF>(a, st);
-        const bool few_tiles = (a.N / 64 + a.S / 2) * ((wide + 63) / 64) <= kFewTiles;  // of 64 x 64
-        if (mean <= (few_tiles ? 2 * kFewRows : kFewRows)) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
-        if (a.K >= 256 && wide > 128 && tiles >= kManyTiles && mean >= kManyRows) {
-            const int64_t nt = (wide + 255) / 256;
-            const int64_t one = ((a.N / 128 + a.S / 2) * nt + 255) / 256, two = ((a.N / 256 + a.S / 2) * nt + 255) / 256;
-            if (4 * one < 7 * two) return gated_many_launch<T, 1, GRAD, ERF>(a, st);
-            return gated_many_launch<T, 2, GRAD, ERF>(a, st);
+        // waves that split the contraction where there are few workgroups (one
+        // segment of 16 rows, 4,096 x 4,096: 15 us against 23 of 64 x 32)
+        if (mean <= 2 * kFewRows && a.S * ((a.M + 31) / 32) <= kFewGroups) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
+        if (mean <= 2) return gated_launch<T, 32, 128, 1, 4, 3, true, GRAD, ERF>(a, st);
+        switch (gated_kind(a, GRAD)) {
+        case 0: return gated_many_launch<T, 2, GRAD, ERF>(a, st);
+        case 1: return gated_many_launch<T, 1, GRAD, ERF>(a, st);
+        case 2: return gated_launch<T, 128, 128, 2, 4, 2, true, GRAD, ERF>(a, st);
+        default: return gated_launch<T, 64, 64, 2, 2, 3, true, GRAD, ERF>(a, st);
         }
-        if (few_tiles) return gated_launch<T, 64, 64, 2, 2, 3, true, GRAD, ERF>(a, st);
-        return gated_launch<T, 64, 128, 2, 2, 2, true, GRAD, ERF>(a, st);
     }
 }
 
@@ -396,7 +432,6 @@ int gated_call(bool is_grad, const void *grad, const void *values, int32_t dtype
     a.M = m;
     a.grad = static_cast<const char *>(grad);
     a.out = out;
-    a.vec = ((m * e) % 16 == 0 && aligned(out, 16) && aligned(grad, 16)) ? 1 : 0;
     // 0.5 (1 + tanh y) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (x + 0.044715 x^3)
     a.c1 = activation == SEGRED_GELU_TANH ? 1.5957691216057308f : 1.f;
     a.c2 = activation == SEGRED_GELU_TANH ? 0.071354816272600248f : 0.f;

@@ -189,12 +189,12 @@ __device__ __forceinline__ void loss_slope(const LossArgs &a, const LossPlace &p
             *reinterpret_cast<__attribute__((address_space(3))) T *>(lds + tile_unit<T, BN>(r, c >> 3) + (c & 7) * 2) = (T)y;
         });
         __syncthreads();
-        tile_write<T, BM, BN, THREADS>(lds, out, p.rows, p.n0, a.ld, a.ld, true);
+        tile_write<T, BM, BN, THREADS>(lds, out, p.rows, p.n0, a.ld, a.ld);
         if constexpr (TURN)
             if (a.turned) {
                 tile_turn<T, BM, BN, THREADS>(lds, threadIdx.x >> 6, lane);
                 tile_write<T, BN, BM, THREADS>(lds, reinterpret_cast<T *>(a.turned) + p.n0 * a.ldn,
-                                               (int)min((int64_t)BN, a.vc - p.n0), p.row0, a.ldn, a.ldn, true);
+                                               (int)min((int64_t)BN, a.vc - p.n0), p.row0, a.ldn, a.ldn);
             }
     } else {
         // the stores of other waves to the same places must have gone before
@@ -514,17 +514,8 @@ __device__ __forceinline__ LossBack loss_back_place(const LossArgs &a) {
 }
 __device__ __forceinline__ void loss_add(const LossArgs &a, const LossBack &p, int r, int64_t n, f32x4 c) {
     if (r >= p.rows) return;
-    float *to = a.sums + ((p.cut * a.N + p.row0 + r) * a.K) + n;
-    if (a.K % 4 == 0) {
-        if (n < a.K) {
-            f32x4 *q = reinterpret_cast<f32x4 *>(to);
-            *q = a.first ? c : *q + c;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.K) to[e] = a.first ? c[e] : to[e] + c[e];
-    }
+    float *row = a.sums + (p.cut * a.N + p.row0 + r) * a.K;
+    store_four<float>(row, n, a.K, a.first ? c : load_four<float>(row, n, a.K) + c);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
@@ -788,7 +779,7 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_words_turned(LossArgs a, c
                 }
     if (f32) return;
     __syncthreads();
-    tile_write<T, 256, 256, kPhaseThreads>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K, true);
+    tile_write<T, 256, 256, kPhaseThreads>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K);
 }
 
 // out[c][r] = in[r][c] for `rows` rows of `cols` (whole units), `ld` and `old`
@@ -812,7 +803,7 @@ __global__ __launch_bounds__(256) void loss_turn(const T *in, int64_t rows, int6
     }
     __syncthreads();
     tile_turn<T, kTurnRows, kTurnCols, 256>(lds, threadIdx.x >> 6, threadIdx.x & 63);
-    tile_write<T, kTurnCols, kTurnRows, 256>(lds, out + c0 * old, (int)min((int64_t)kTurnCols, cols - c0), r0, old, old, true);
+    tile_write<T, kTurnCols, kTurnRows, 256>(lds, out + c0 * old, (int)min((int64_t)kTurnCols, cols - c0), r0, old, old);
 }
 
 // Adds the cuts' sums in order and rounds once.

@@ -199,21 +199,51 @@ struct FewTile {
 
 // ---------------------------------------------------------- tiles and memory
 
+// Four neighbouring elements from column n of a row of `width`, at any element
+// boundary (one access; elements behind the row's end are left alone).
+template <typename T> struct QuadOf;
+template <> struct QuadOf<float> { typedef f32x4 __attribute__((aligned(4))) any; typedef f32x4 type; };
+template <> struct QuadOf<__bf16> { typedef bf16x4 __attribute__((aligned(2))) any; typedef bf16x4 type; };
+template <> struct QuadOf<_Float16> { typedef f16x4 __attribute__((aligned(2))) any; typedef f16x4 type; };
+template <typename T>
+__device__ __forceinline__ f32x4 load_four(const T *row, int64_t n, int64_t width) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+    if (n + 4 <= width) {
+        const typename QuadOf<T>::type q = *(__attribute__((address_space(1))) const typename QuadOf<T>::any *)(row + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = (float)q[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (n + j < width) c[j] = (float)row[n + j];
+    }
+    return c;
+}
+template <typename T>
+__device__ __forceinline__ void store_four(T *row, int64_t n, int64_t width, f32x4 c) {
+    if (n + 4 <= width) {
+        typename QuadOf<T>::type q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = (T)c[j];
+        *(__attribute__((address_space(1))) typename QuadOf<T>::any *)(row + n) = q;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (n + j < width) row[n + j] = (T)c[j];
+    }
+}
+
 // A tile of 16-bit elements, first `rows` rows and the columns below `limit`,
 // from rows of `width` elements into the places of tile_put; zeros elsewhere.
 template <typename T, int BM, int BN, int THREADS>
-__device__ __forceinline__ void tile_in(lds_char *lds, const T *from, int rows, int64_t n0, int64_t width, bool vec) {
+__device__ __forceinline__ void tile_in(lds_char *lds, const T *from, int rows, int64_t n0, int64_t width) {
     constexpr int kUnits = BN / 8;
 #pragma unroll 4
     for (int i = threadIdx.x; i < BM * kUnits; i += THREADS) {
         const int r = i / kUnits, u = i % kUnits;
         const int64_t n = n0 + u * 8;
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (r < rows && n < width) {
-            const T *p = from + r * width + n;
-            if (vec) v = *reinterpret_cast<const u32x4 *>(p);
-            else v = load_unit<T>((uint64_t)p, (int)min(width - n, (int64_t)8));
-        }
+        if (r < rows && n < width) v = load_unit<T>((uint64_t)(from + r * width + n), (int)min(width - n, (int64_t)8));
         *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BN>(r, u)) = v;
     }
 }
@@ -227,7 +257,8 @@ __device__ __forceinline__ f32x4 tile_get(const lds_char *lds, int r, int c) {
 // elements apart, the columns below `limit`.
 template <typename T, int BM, int BN, int THREADS>
 __device__ __forceinline__ void tile_write(const lds_char *lds, T *out, int rows, int64_t n0, int64_t limit,
-                                           int64_t stride, bool vec) {
+                                           int64_t stride) {
+    typedef u32x4 __attribute__((aligned(2))) unit2;
     constexpr int kUnits = BN / 8;
 #pragma unroll 4
     for (int i = threadIdx.x; i < BM * kUnits; i += THREADS) {
@@ -240,8 +271,8 @@ __device__ __forceinline__ void tile_write(const lds_char *lds, T *out, int rows
         } x;
         x.v = *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BN>(r, u));
         T *to = out + r * stride + n;
-        if (vec) {
-            *reinterpret_cast<u32x4 *>(to) = x.v;
+        if (n + 8 <= limit) {
+            *(__attribute__((address_space(1))) unit2 *)to = x.v;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
