@@ -11,7 +11,6 @@
 // float32 they would take 16 bytes an output to write and read, against 4 k
 // operations to form them again, about equal at k = 1,024.
 #include <algorithm>
-#include <cmath>
 
 #include "internal.hpp"
 #include "rowtile.hpp"
@@ -327,40 +326,18 @@ int gated_few_launch(GatedArgs a, hipStream_t st) {
 //   32 x 64            62  120  174  237  674          69    389      129    247     27    161   532
 //   few                77  115  406  767 2883         297   2267      646   1299     77    566  2258
 //
-// Each kernel's time is its rounds over the CUs, each an overhead (loads until the
-// first product, the epilogue) and a part that grows with k; small tiles have less
-// of the one and more of the other.  The rule takes the least of what these
-// constants, fitted to such times, give.
-struct GatedKind {
-    int rows, outputs, each;  // of a tile; tiles that a CU holds
-    double fixed, grad, alone, full;  // us of a round, more for the gradient, per 1,024 of k: one tile, `each` tiles
-};
-constexpr GatedKind kGatedKinds[] = {{256, 128, 1, 13, 11, 24.8, 24.8},
-                                     {128, 128, 1, 6, 4.7, 15.7, 15.7},
-                                     {128, 64, 2, 2.5, 4.3, 12, 18.3},
-                                     {64, 32, 3, 2.9, 2, 5, 9}};
-double gated_time(const GatedKind &g, const GatedArgs &a, bool grad) {
-    const double k = (double)a.K / 1024, fixed = g.fixed + (grad ? g.grad : 0), whole = fixed + k * g.full;
-    const int64_t columns = (a.M + g.outputs - 1) / g.outputs;
-    // half a tile more per segment for its end
-    const double tiles = (double)columns * (a.S == 1 ? (double)((a.N + g.rows - 1) / g.rows)
-                                                     : (double)a.N / g.rows + 0.5 * a.S);
-    auto part = [&](int n) {  // a round of n tiles a CU
-        return fixed + k * (g.each > 1 ? g.alone + (g.full - g.alone) * (n - 1) / (g.each - 1) : g.full);
-    };
-    const double load = tiles / 256, x = load / g.each;
-    if (x <= 0.92) return part((int)std::ceil(load));
-    if (a.S == 1) {
-        const int64_t n = (int64_t)std::ceil(load);
-        return n / g.each * whole + (n % g.each ? part((int)(n % g.each)) : 0);
-    }
-    // uneven segments: the last round is seldom full, a round that just fits does not always
-    return whole * (x <= 1 ? 1.35 : x < 2 ? 2 : x + 0.4);
-}
+// The rule is the least of tile_time().
 int gated_kind(const GatedArgs &a, bool grad) {
+    constexpr double kMore[] = {11, 4.7, 4.3, 2};  // us more of a round for the gradient
+    auto time = [&](int i) {
+        const TileCost &g = kTileCosts[i];
+        // half a tile more per segment for its end
+        const double slots = a.S == 1 ? (double)((a.N + g.rows - 1) / g.rows) : (double)a.N / g.rows + 0.5 * a.S;
+        return tile_time(g, grad ? kMore[i] : 0, a.K, slots * ((2 * a.M + g.columns - 1) / g.columns), a.S == 1);
+    };
     int best = 0;
     for (int i = 1; i < 4; ++i)
-        if (gated_time(kGatedKinds[i], a, grad) < gated_time(kGatedKinds[best], a, grad)) best = i;
+        if (time(i) < time(best)) best = i;
     return best;
 }
 

@@ -831,22 +831,43 @@ __global__ __launch_bounds__(256) void loss_back_join(LossArgs a) {
 // --------------------------------------------------------------------- host
 
 constexpr int64_t kLossFewRows = 16, kLossRows = int64_t(1) << 31, kLossVocab = 1 << 30, kLossPicks = 4096;
-// Kernels of the tiles: columns that a pair covers.
-enum LossKind { kLossFew, kLossSmall, kLossOne, kLossTwo, kLossSplit, kLossAny };
+// Kernels of the tiles.  Times in us of the forward call (bfloat16, the joining
+// kernel's 6 to 10 among them):
+//
+//   rows, k, vocabulary       16   64  128  256  512 1024  4096     4096   2048    8192
+//                             2048, 32,000                       1024, 5,000  512, 32,000
+//   few                       33   69  121  229  445  783
+//   64 x 64                   34   35   48   74  125  232   796       79    127     466
+//   128 x 128                 42   42   43   50   82  143   538       56     84     311
+//   128 x 256                 40   41   43   43   80  143   529       65     95     349
+//   256 x 256                 42   43   45   54   64  114   432       66     75     279
+//
+// Up to 16 rows waves split the contraction, else the rule is the least of
+// tile_time(), less 3 us a round for the largest tiles (rows are not gathered and
+// need no search).
+enum LossKind { kLossFew, kLossSmall, kLossMiddle, kLossOne, kLossTwo, kLossSplit, kLossAny };
 LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) {
     if (dtype == SEGRED_F32) return direct && n <= 8 ? kLossFew : kLossSplit;
     if (!direct) return kLossAny;
     if (n <= kLossFewRows) return kLossFew;
-    if (k < 256 || ((n + 127) / 128) * ((v + 255) / 256) < 128) return kLossSmall;
-    return n > 128 ? kLossTwo : kLossOne;
+    constexpr LossKind kKinds[] = {kLossTwo, kLossOne, kLossMiddle, kLossSmall};
+    auto time = [&](int i) {
+        const TileCost &g = kTileCosts[i];
+        return tile_time(g, i == 0 ? -3 : 0, k, (double)((n + g.rows - 1) / g.rows) * ((v + g.columns - 1) / g.columns), true);
+    };
+    int best = 0;
+    for (int i = 1; i < 4; ++i)
+        if (time(i) < time(best)) best = i;
+    return kKinds[best];
 }
+// Columns that a pair covers.
 int64_t loss_columns(LossKind kind) {
-    return kind == kLossOne || kind == kLossTwo ? 256 : kind == kLossSmall || kind == kLossAny ? 128 : 64;
+    return kind == kLossOne || kind == kLossTwo ? 256 : kind == kLossMiddle || kind == kLossAny ? 128 : 64;
 }
 
 template <typename T, bool SLOPE>
 int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
-    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne ? 128 : kind == kLossFew ? 16 : 64;
+    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne || kind == kLossMiddle ? 128 : kind == kLossFew ? 16 : 64;
     const int64_t bn = kind == kLossSplit ? 128 : loss_columns(kind);
     a.mtiles = (a.N + bm - 1) / bm;
     a.ntiles = (a.vc + bn - 1) / bn;
@@ -860,7 +881,10 @@ int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
         switch (kind) {
         case kLossFew: timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a); break;
         case kLossSmall:
-            timed_launch_ggl(true, (loss_tiles<T, 64, 128, 2, 2, 2, true, SLOPE>), grid, dim3(256), 0, st, a);
+            timed_launch_ggl(true, (loss_tiles<T, 64, 64, 2, 2, 3, true, SLOPE>), grid, dim3(256), 0, st, a);
+            break;
+        case kLossMiddle:
+            timed_launch_ggl(true, (loss_tiles<T, 128, 128, 2, 4, 2, true, SLOPE>), grid, dim3(512), 0, st, a);
             break;
         case kLossOne: timed_launch_ggl(true, (loss_many<T, 1, SLOPE>), grid, dim3(kPhaseThreads), 0, st, a); break;
         case kLossTwo: timed_launch_ggl(true, (loss_many<T, 2, SLOPE>), grid, dim3(kPhaseThreads), 0, st, a); break;

@@ -6,6 +6,8 @@
 // and tile column c's operand row, or null for a row of zeros.
 #pragma once
 
+#include <cmath>
+
 #include "internal.hpp"
 #include "tile.hpp"
 
@@ -310,6 +312,37 @@ __device__ __forceinline__ void tile_turn(lds_char *lds, int wave, int lane) {
         *reinterpret_cast<__attribute__((address_space(3))) u32x4 *>(lds + tile_unit<T, BM>(cb * 16 + l, ru)) = x[i].v;
     }
     __syncthreads();
+}
+
+// ---------------------------------------------------------- which tile to take
+//
+// A kernel's time is its rounds over the CUs, each an overhead (loads until the
+// first product, the epilogue) and a part that grows with k; small tiles have less
+// of the one and more of the other.  The constants are fitted to measured times
+// (gated.hip and loss.hip have tables of these).
+struct TileCost {
+    int rows, columns, each;    // of a tile (columns: rows of the weights); tiles that a CU holds
+    double fixed, alone, full;  // us of a round; per 1,024 of k: with one tile on the CU, with `each`
+};
+constexpr TileCost kTileCosts[] = {{256, 256, 1, 13, 24.8, 24.8},
+                                   {128, 256, 1, 6, 15.7, 15.7},
+                                   {128, 128, 2, 2.5, 12, 18.3},
+                                   {64, 64, 3, 2.9, 5, 9}};
+// us of `tiles` tiles, where a round takes `more` us more; EXACT: so many there are
+// for certain (uneven segments: the last round is seldom full, and tiles that just
+// fit one round do not always).
+inline double tile_time(const TileCost &g, double more, int64_t k, double tiles, bool exact) {
+    const double kk = (double)k / 1024, fixed = g.fixed + more, whole = fixed + kk * g.full;
+    auto part = [&](int n) {  // a round of n tiles a CU
+        return fixed + kk * (g.each > 1 ? g.alone + (g.full - g.alone) * (n - 1) / (g.each - 1) : g.full);
+    };
+    const double load = tiles / 256, x = load / g.each;
+    if (x <= 0.92) return part((int)std::ceil(load));
+    if (exact) {
+        const int64_t n = (int64_t)std::ceil(load);
+        return (double)(n / g.each) * whole + (n % g.each ? part((int)(n % g.each)) : 0);
+    }
+    return whole * (x <= 1 ? 1.35 : x < 2 ? 2 : x + 0.4);
 }
 
 }  // namespace segred
