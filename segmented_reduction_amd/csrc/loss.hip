@@ -216,7 +216,7 @@ struct LossTile {
         auto get = [&](int i, int j) -> f32x4 & { return acc[i][j]; };
         auto row = [&](int i) { return Tile::m0(wave) + 16 * i + (lane & 15); };
         auto col = [&](int j) { return Tile::n0(wave) + 16 * j + (lane >> 4) * 4; };
-        if constexpr (SLOPE) loss_slope<T, Tile::MT, Tile::NT, BM, BN, Tile::kThreads, false>(a, p, lds, lane, get, row, col);
+        if constexpr (SLOPE) loss_slope<T, Tile::MT, Tile::NT, BM, BN, Tile::kThreads, DIRECT>(a, p, lds, lane, get, row, col);
         else loss_pairs<Tile::MT, Tile::NT, WN, BM, BN>(a, p, part, lds, wave % WN, lane, get, row, col);
     }
 };
@@ -744,9 +744,51 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_back_turned(LossArgs a) {
                              acc[h][q][i][j]);
 }
 
-// dW of a piece from dz and the values, both turned: 256 entries x 256 columns.
+// dW of a piece from dz and the values, both turned.  BM: 256 (in phases) or less.
+template <typename T, int BM, int BN, int THREADS, typename F>
+__device__ __forceinline__ void loss_words_store(const LossArgs &a, char *out, int f32, int64_t m0, int64_t n0, int rows,
+                                                 lds_char *lds, F quads) {
+    const float f = a.factor ? a.factor[1] : 1.f;
+    if (f32) {
+        float *to = reinterpret_cast<float *>(out) + m0 * a.K;
+        quads([&](int r, int c, f32x4 y) {
+            if (r < rows) store_four<float>(to + r * a.K, n0 + c, a.K, y * f);
+        });
+    } else {
+        quads([&](int r, int c, f32x4 y) { tile_put<T, BN>(lds, r, c, y * f); });
+        __syncthreads();
+        tile_write<T, BM, BN, THREADS>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K);
+    }
+}
+template <typename T, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN) void loss_words(LossArgs a, char *out, int f32) {
+    using Tile = RowTile<T, BM, BN, WM, WN, STAGES, true>;
+    static_assert(BM * BN * 2 <= Tile::kLds, "the results fit");
+    __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
+    lds_char *lds = (lds_char *)lds_mem;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_tile(a.mtiles * a.ntiles);
+    if (id >= a.mtiles * a.ntiles) return;
+    const TilePlace at = tile_place(id, a.mtiles, a.ntiles);
+    const int64_t m0 = at.m * BM, n0 = at.n * BN;
+    const int rows = (int)min((int64_t)BM, a.vc - m0);
+    f32x4 acc[Tile::MT][Tile::NT] = {};
+    Tile::run(
+        acc, (int)a.ldn, lds, wave, lane,
+        [&](int r) -> const char * { return r < rows ? a.turned + (m0 + r) * a.ldn * (int64_t)sizeof(T) : nullptr; },
+        [&](int c) -> const char * {
+            return n0 + c < a.K ? a.rows_turned + (n0 + c) * a.ldn * (int64_t)sizeof(T) : nullptr;
+        });
+    loss_words_store<T, BM, BN, Tile::kThreads>(a, out, f32, m0, n0, rows, lds, [&](auto put) {
+#pragma unroll
+        for (int i = 0; i < Tile::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Tile::NT; ++j)
+                put(Tile::m0(wave) + 16 * i + (lane & 15), Tile::n0(wave) + 16 * j + (lane >> 4) * 4, acc[i][j]);
+    });
+}
 template <typename T>
-__global__ __launch_bounds__(kPhaseThreads) void loss_words_turned(LossArgs a, char *out, int f32) {
+__global__ __launch_bounds__(kPhaseThreads) void loss_words_many(LossArgs a, char *out, int f32) {
     using Tile = PhaseTile<T, 2>;
     __shared__ __attribute__((aligned(1024))) char lds_mem[kPhaseLds];
     lds_char *lds = (lds_char *)lds_mem;
@@ -763,23 +805,17 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_words_turned(LossArgs a, c
         [&](int c) -> const char * {
             return n0 + c < a.K ? a.rows_turned + (n0 + c) * a.ldn * (int64_t)sizeof(T) : nullptr;
         });
-    const float f = a.factor ? a.factor[1] : 1.f;
+    loss_words_store<T, 256, 256, kPhaseThreads>(a, out, f32, m0, n0, rows, lds, [&](auto put) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = phase_row(h, i, wave) + (lane & 15), c = phase_col(q, j, wave) + (lane >> 4) * 4;
-                    const f32x4 y = acc[h][q][i][j] * f;
-                    if (!f32) tile_put<T, 256>(lds, r, c, y);
-                    else if (r < rows) store_quad<float>(reinterpret_cast<float *>(out) + (m0 + r) * a.K, n0 + c, a.K, y, true);
-                }
-    if (f32) return;
-    __syncthreads();
-    tile_write<T, 256, 256, kPhaseThreads>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K);
+                    for (int j = 0; j < 2; ++j)
+                        put(phase_row(h, i, wave) + (lane & 15), phase_col(q, j, wave) + (lane >> 4) * 4, acc[h][q][i][j]);
+    });
 }
 
 // out[c][r] = in[r][c] for `rows` rows of `cols` (whole units), `ld` and `old`
@@ -806,26 +842,30 @@ __global__ __launch_bounds__(256) void loss_turn(const T *in, int64_t rows, int6
     tile_write<T, kTurnCols, kTurnRows, 256>(lds, out + c0 * old, (int)min((int64_t)kTurnCols, cols - c0), r0, old, old);
 }
 
-// Adds the cuts' sums in order and rounds once.
-template <typename T>
-__global__ __launch_bounds__(256) void loss_back_join(LossArgs a) {
-    const int64_t i = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4, all = a.N * a.K;
-    if (i >= all) return;
-    const float f = a.factor ? a.factor[1] : 1.f;
-    if (i + 4 <= all) {
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
-        typedef f32x4 __attribute__((aligned(4))) quad4;
-        for (int64_t c = 0; c < a.cuts; ++c) s += *reinterpret_cast<const quad4 *>(a.sums + c * all + i);
-        T *to = static_cast<T *>(a.grad_values) + i;
+// Adds the cuts' sums and rounds once: PARTS threads share four elements, each
+// adds its part of the cuts in order, and these sums are added in order.  (8 rows of
+// 2,048 from 32 cuts: 4.8 us by four threads, 10.5 by one; 4,096 rows of 1,024 from 4
+// cuts 14 and 7.7.)
+constexpr int kBackJoin = 256, kBackParts = 4, kBackCuts = 16;
+template <typename T, int PARTS>
+__global__ __launch_bounds__(kBackJoin) void loss_back_join(LossArgs a) {
+    constexpr int kEach = kBackJoin / PARTS;
+    __shared__ f32x4 s_part[PARTS > 1 ? PARTS - 1 : 1][kEach];
+    const int part = threadIdx.x / kEach, at = threadIdx.x % kEach;
+    const int64_t i = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kEach + at) * 4, all = a.N * a.K;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    const int64_t c0 = part * a.cuts / PARTS, c1 = (part + 1) * a.cuts / PARTS;
+    if (i < all)
+#pragma unroll 8
+        for (int64_t c = c0; c < c1; ++c) s += load_four<float>(a.sums + c * all, i, all);
+    if constexpr (PARTS > 1) {
+        if (part > 0) s_part[part - 1][at] = s;
+        __syncthreads();
+        if (part > 0) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to[e] = (T)(s[e] * f);
-    } else {
-        for (int64_t j = i; j < all; ++j) {
-            float s = 0.f;
-            for (int64_t c = 0; c < a.cuts; ++c) s += a.sums[c * all + j];
-            static_cast<T *>(a.grad_values)[j] = (T)(s * f);
-        }
+        for (int q = 0; q < PARTS - 1; ++q) s += s_part[q][at];
     }
+    if (i < all) store_four<T>(static_cast<T *>(a.grad_values), i, all, s * (a.factor ? a.factor[1] : 1.f));
 }
 
 // --------------------------------------------------------------------- host
@@ -969,9 +1009,9 @@ LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v, int64_t picks
     const int64_t pieces = (v + p.piece - 1) / p.piece;
     p.piece = std::min(v, ((v + pieces - 1) / pieces + 255) / 256 * 256);
     p.many = e == 2 && n > 64 && k > 128;
-    const bool whole = e == 2 && k % 8 == 0 && loss_kind(dtype, n, k, p.piece, true) == kLossTwo;
-    p.turn_rows = whole && n >= 512 && k >= 512;
-    p.turn_words = whole && n >= 2048;
+    const bool whole = e == 2 && k % 8 == 0 && n > 0;
+    p.turn_rows = whole && (k >= 512 || (n <= 512 && k >= 128));
+    p.turn_words = whole && n >= 2048 && ((n + 255) / 256) * ((k + 255) / 256) >= 64;
     const int64_t tiles = p.turn_words ? ((n + 255) / 256) * ((k + 255) / 256)
                           : p.many     ? ((n + 127) / 128) * ((k + 255) / 256)
                                        : (n <= 16 && e == 2 ? 1 : (n + 63) / 64) * ((k + 127) / 128);
@@ -1050,13 +1090,38 @@ int loss_back_launch(LossArgs a, const LossPlan &p, bool direct, hipStream_t st)
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
+// dW of a piece; `later`: dz is still to be turned.
+template <typename T>
+int loss_words_launch(LossArgs a, bool later, char *to, int f32, hipStream_t st) {
+    if (later) {
+        const int rc = loss_turn_launch<T>(a.slope, a.N, a.vc, a.ld, nullptr, a.turned, a.ldn, st);
+        if (rc != SEGRED_OK) return rc;
+    }
+    // few rows are a short contraction: then the small tiles store while others load
+    int best = 0;
+    auto time = [&](int i) {
+        const TileCost &g = kTileCosts[i];
+        const int64_t tiles = ((a.vc + g.rows - 1) / g.rows) * ((a.K + g.columns - 1) / g.columns);
+        return tile_time(g, i == 0 ? -3 : 0, a.N, (double)tiles, true);
+    };
+    for (int i : {2, 3})
+        if (time(i) < time(best)) best = i;
+    a.mtiles = (a.vc + kTileCosts[best].rows - 1) / kTileCosts[best].rows;
+    a.ntiles = (a.K + kTileCosts[best].columns - 1) / kTileCosts[best].columns;
+    dim3 grid;
+    if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
+    if (best == 0) timed_launch_ggl(true, (loss_words_many<T>), grid, dim3(kPhaseThreads), 0, st, a, to, f32);
+    else if (best == 2) timed_launch_ggl(true, (loss_words<T, 128, 128, 2, 4, 2>), grid, dim3(512), 0, st, a, to, f32);
+    else timed_launch_ggl(true, (loss_words<T, 64, 64, 2, 2, 3>), grid, dim3(256), 0, st, a, to, f32);
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
 template <typename T>
 int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int32_t dtype, void *grad_weights,
                   int32_t grad_weights_dtype, char *work, hipStream_t st) {
     const int64_t ge = float_size(grad_weights_dtype);
     int64_t *offsets = reinterpret_cast<int64_t *>(work + p.offsets);
-    const bool turn_rows = p.turn_rows && direct && grad_weights &&
-                           aligned(grad_weights, 16);  // whole units of dW's rows, too
+    const bool turn_rows = p.turn_rows && direct && grad_weights;
     a.ldn = (a.N + 7) / 8 * 8;
     a.turned = turn_rows ? work + p.turned : nullptr;
     a.rows_turned = work + p.rows_turned;
@@ -1088,13 +1153,7 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
         char *to = static_cast<char *>(grad_weights) + a.v0 * a.K * ge;
         if constexpr (sizeof(T) == 2) {
             if (turn_rows) {
-                LossArgs b = a;
-                b.mtiles = (a.vc + 255) / 256;
-                b.ntiles = (a.K + 255) / 256;
-                dim3 grid;
-                if (!tile_grid(b.mtiles * b.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
-                timed_launch_ggl(true, (loss_words_turned<T>), grid, dim3(kPhaseThreads), 0, st, b, to, ge == 4 ? 1 : 0);
-                rc = hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+                rc = loss_words_launch<T>(a, kind == kLossFew, to, ge == 4 ? 1 : 0, st);
                 continue;
             }
         }
@@ -1104,8 +1163,11 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
     if (rc != SEGRED_OK) return rc;
     if (a.grad_values && a.N > 0) {
         dim3 grid;
-        if (!tile_grid((a.N * a.K + 1023) / 1024, grid)) return SEGRED_ERR_UNSUPPORTED;
-        timed_launch_ggl(false, (loss_back_join<T>), grid, dim3(256), 0, st, a);
+        const bool shared = p.cuts >= kBackCuts;
+        const int64_t each = 4 * kBackJoin / (shared ? kBackParts : 1);
+        if (!tile_grid((a.N * a.K + each - 1) / each, grid)) return SEGRED_ERR_UNSUPPORTED;
+        if (shared) timed_launch_ggl(false, (loss_back_join<T, kBackParts>), grid, dim3(kBackJoin), 0, st, a);
+        else timed_launch_ggl(false, (loss_back_join<T, 1>), grid, dim3(kBackJoin), 0, st, a);
     }
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
