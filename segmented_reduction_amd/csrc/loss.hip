@@ -887,7 +887,12 @@ constexpr int64_t kLossFewRows = 16, kLossRows = int64_t(1) << 31, kLossVocab = 
 // need no search).
 enum LossKind { kLossFew, kLossSmall, kLossMiddle, kLossOne, kLossTwo, kLossSplit, kLossAny };
 LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) {
-    if (dtype == SEGRED_F32) return direct && n <= 8 ? kLossFew : kLossSplit;
+    if (dtype == SEGRED_F32) {
+        // bf16 parts need tiles enough for every CU to be worth their splitting
+        if (!direct) return kLossSplit;
+        if (n <= kLossFewRows) return kLossFew;
+        return n <= 64 || ((n + 63) / 64) * ((v + 127) / 128) < 224 ? kLossSmall : kLossSplit;
+    }
     if (!direct) return kLossAny;
     if (n <= kLossFewRows) return kLossFew;
     constexpr LossKind kKinds[] = {kLossTwo, kLossOne, kLossMiddle, kLossSmall};
@@ -907,7 +912,7 @@ int64_t loss_columns(LossKind kind) {
 
 template <typename T, bool SLOPE>
 int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
-    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne || kind == kLossMiddle ? 128 : kind == kLossFew ? 16 : 64;
+    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne || kind == kLossMiddle ? 128 : kind == kLossFew ? 16 : sizeof(T) == 4 && kind == kLossSmall ? 32 : 64;
     const int64_t bn = kind == kLossSplit ? 128 : loss_columns(kind);
     a.mtiles = (a.N + bm - 1) / bm;
     a.ntiles = (a.vc + bn - 1) / bn;
@@ -915,6 +920,7 @@ int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
     if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
     if constexpr (sizeof(T) == 4) {
         if (kind == kLossFew) timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a);
+        else if (kind == kLossSmall) timed_launch_ggl(true, (loss_tiles<T, 32, 64, 1, 4, 4, true, SLOPE>), grid, dim3(256), 0, st, a);
         else if (a.K % 8 == 0) timed_launch_ggl(true, (loss_split<true, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
         else timed_launch_ggl(true, (loss_split<false, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
     } else {
