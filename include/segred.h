@@ -754,7 +754,7 @@ int64_t segred_cross_entropy_workspace(int32_t dtype, int64_t k, int64_t rows, i
  *                 NULL: not asked for.  Every element is written.
  *   workspace     segred_cross_entropy_grad_workspace(dtype, k, rows, vocab,
  *                 picks) bytes: a piece of dz (256 MiB, or 4,096 entries where these
- *                 take more), for many rows of 16 bits once more turned, with the
+ *                 take more), in the 16-bit types once more turned, with the
  *                 values and a piece of the weights, and the sums of grad_values in
  *                 float32.
  *   the others and the errors as segred_cross_entropy.

@@ -27,6 +27,7 @@ struct LossArgs {
     const int64_t *target;  // [N, picks]
     const float *probs;     // [N, picks], or null: 1
     int64_t N, V, K, picks;
+    int64_t KO;  // columns of the gradients: K, or fewer where the operands are copies of wider rows
     float scale, bend;  // bend = scale log2(e)
     int64_t v0, vc;     // the piece of the vocabulary
     int64_t mtiles, ntiles;
@@ -514,8 +515,8 @@ __device__ __forceinline__ LossBack loss_back_place(const LossArgs &a) {
 }
 __device__ __forceinline__ void loss_add(const LossArgs &a, const LossBack &p, int r, int64_t n, f32x4 c) {
     if (r >= p.rows) return;
-    float *row = a.sums + (p.cut * a.N + p.row0 + r) * a.K;
-    store_four<float>(row, n, a.K, a.first ? c : load_four<float>(row, n, a.K) + c);
+    float *row = a.sums + (p.cut * a.N + p.row0 + r) * a.KO;
+    store_four<float>(row, n, a.KO, a.first ? c : load_four<float>(row, n, a.KO) + c);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
@@ -750,14 +751,14 @@ __device__ __forceinline__ void loss_words_store(const LossArgs &a, char *out, i
                                                  lds_char *lds, F quads) {
     const float f = a.factor ? a.factor[1] : 1.f;
     if (f32) {
-        float *to = reinterpret_cast<float *>(out) + m0 * a.K;
+        float *to = reinterpret_cast<float *>(out) + m0 * a.KO;
         quads([&](int r, int c, f32x4 y) {
-            if (r < rows) store_four<float>(to + r * a.K, n0 + c, a.K, y * f);
+            if (r < rows) store_four<float>(to + r * a.KO, n0 + c, a.KO, y * f);
         });
     } else {
         quads([&](int r, int c, f32x4 y) { tile_put<T, BN>(lds, r, c, y * f); });
         __syncthreads();
-        tile_write<T, BM, BN, THREADS>(lds, reinterpret_cast<T *>(out) + m0 * a.K, rows, n0, a.K, a.K);
+        tile_write<T, BM, BN, THREADS>(lds, reinterpret_cast<T *>(out) + m0 * a.KO, rows, n0, a.KO, a.KO);
     }
 }
 template <typename T, int BM, int BN, int WM, int WN, int STAGES>
@@ -842,6 +843,16 @@ __global__ __launch_bounds__(256) void loss_turn(const T *in, int64_t rows, int6
     tile_write<T, kTurnCols, kTurnRows, 256>(lds, out + c0 * old, (int)min((int64_t)kTurnCols, cols - c0), r0, old, old);
 }
 
+// Copies `rows` rows of `cols` 16-bit elements, of any width and place, to rows of
+// whole 16-byte units, zeros behind their end.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_pad(const T *in, int64_t rows, int64_t cols, u32x4 *out) {
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, units = (cols + 7) / 8;
+    if (i >= rows * units) return;
+    const int64_t r = i / units, u = i - r * units;
+    out[i] = load_unit<T>((uint64_t)(in + r * cols + u * 8), (int)min(cols - u * 8, (int64_t)8));
+}
+
 // Adds the cuts' sums and rounds once: PARTS threads share four elements, each
 // adds its part of the cuts in order, and these sums are added in order.  (8 rows of
 // 2,048 from 32 cuts: 4.8 us by four threads, 10.5 by one; 4,096 rows of 1,024 from 4
@@ -852,7 +863,7 @@ __global__ __launch_bounds__(kBackJoin) void loss_back_join(LossArgs a) {
     constexpr int kEach = kBackJoin / PARTS;
     __shared__ f32x4 s_part[PARTS > 1 ? PARTS - 1 : 1][kEach];
     const int part = threadIdx.x / kEach, at = threadIdx.x % kEach;
-    const int64_t i = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kEach + at) * 4, all = a.N * a.K;
+    const int64_t i = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kEach + at) * 4, all = a.N * a.KO;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     const int64_t c0 = part * a.cuts / PARTS, c1 = (part + 1) * a.cuts / PARTS;
     if (i < all)
@@ -974,16 +985,67 @@ LossArgs loss_args(const void *values, int64_t k, int64_t rows, const void *weig
     a.probs = probs;
     a.N = rows;
     a.V = a.vc = vocab;
-    a.K = k;
+    a.K = a.KO = k;
     a.picks = picks;
     a.scale = scale;
     a.bend = scale * kLog2e;
     return a;
 }
 
+// 16-bit rows that are not whole 16-byte units are copied to rows that are, the
+// weights a piece at a time: read as they are, through registers, they made the
+// kernels several times slower (4,096 rows, 32,000 entries, bfloat16: k = 2,047 took
+// 1,156 us forward and 5,787 back, 2,048 472 and 1,445).  Few rows go as they are
+// in the forward call (1 row: 65 us against 33 and 65 for the copy).
+constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096, kPadRows = 256;
+bool loss_padded(int32_t dtype, int64_t k) { return dtype != SEGRED_F32 && k % 8 != 0; }
 template <typename T>
-int loss_forward(const LossArgs &a, LossKind kind, hipStream_t st) {
-    const int rc = loss_tiles_launch<T, false>(a, kind, st);
+int loss_pad_launch(const void *in, int64_t rows, int64_t cols, void *out, hipStream_t st) {
+    dim3 grid;
+    if (!tile_grid((rows * ((cols + 7) / 8) + 255) / 256, grid)) return SEGRED_ERR_UNSUPPORTED;
+    timed_launch_ggl(false, (loss_pad<T>), grid, dim3(256), 0, st, static_cast<const T *>(in), rows, cols,
+                     static_cast<u32x4 *>(out));
+    return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
+}
+
+// The forward call's working memory: the pairs, and the copies.
+struct LossRoom {
+    bool pad;
+    int64_t wide, piece;  // columns of a copy, rows of one of the weights
+    int64_t values, words, bytes;  // places
+};
+LossRoom loss_room(int32_t dtype, int64_t k, int64_t n, int64_t v) {
+    LossRoom r{};
+    r.pad = loss_padded(dtype, k) && n >= kPadRows;
+    r.wide = (k + 7) / 8 * 8;
+    r.piece = std::min(v, std::max(kPieceLeast, kPieceBytes / (r.wide * 2) / 256 * 256));
+    // the smallest pairs, whatever kernel is taken
+    const int64_t pairs = n * ((v + 127) / 128 * 2) * 8;
+    r.values = (pairs + 255) / 256 * 256;
+    r.words = r.values + n * r.wide * 2;
+    r.bytes = r.pad ? r.words + r.piece * r.wide * 2 : pairs;
+    return r;
+}
+
+template <typename T>
+int loss_forward(const LossArgs &a, LossKind kind, const LossRoom &room, hipStream_t st) {
+    int rc = SEGRED_OK;
+    char *work = reinterpret_cast<char *>(a.partial);
+    if (!room.pad) {
+        rc = loss_tiles_launch<T, false>(a, kind, st);
+    } else if constexpr (sizeof(T) == 2) {
+        rc = loss_pad_launch<T>(a.values, a.N, a.K, work + room.values, st);
+        LossArgs b = a;
+        b.values = work + room.values;
+        b.K = room.wide;
+        for (; b.v0 < a.V && rc == SEGRED_OK; b.v0 += room.piece) {
+            b.vc = std::min(room.piece, a.V - b.v0);
+            rc = loss_pad_launch<T>(a.weights + b.v0 * a.K * 2, b.vc, a.K, work + room.words, st);
+            b.weights = work + room.words - b.v0 * b.K * 2;
+            b.partial = a.partial + b.v0 / loss_columns(kind);
+            if (rc == SEGRED_OK) rc = loss_tiles_launch<T, false>(b, kind, st);
+        }
+    }
     if (rc != SEGRED_OK) return rc;
     dim3 grid;
     const bool shared = a.picks > 1 || a.N <= 1024;  // four waves a row
@@ -1001,22 +1063,26 @@ int loss_forward(const LossArgs &a, LossKind kind, hipStream_t st) {
 // as the tiles write it, the values once, the weights a piece at a time.
 struct LossPlan {
     int64_t piece, cuts;  // columns of a piece; workgroups that share a tile of dx
+    int64_t wide;         // columns of the copies
+    bool pad;             // the operands are copied to whole units
     bool many;            // dx in tiles of 128 x 256
     bool turn_rows, turn_words;  // dW from dz and the values turned; dx from the weights turned
     // places in the working memory
-    int64_t slope, turned, rows_turned, words_turned, sums, share, hit, bound, live, hits, offsets, factor, outer, bytes;
+    int64_t slope, turned, rows_turned, words_turned, values, words, sums, share, hit, bound, live, hits, offsets, factor, outer, bytes;
 };
-constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096;
-LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v, int64_t picks) {
+LossPlan loss_plan(int32_t dtype, int64_t columns, int64_t n, int64_t v, int64_t picks) {
     const int64_t e = float_size(dtype);
     LossPlan p{};
+    p.pad = loss_padded(dtype, columns);
+    const int64_t k = p.pad ? (columns + 7) / 8 * 8 : columns;
+    p.wide = k;
     p.piece = std::min(v, std::max(kPieceLeast, kPieceBytes / (std::max<int64_t>(n, 1) * e) / 256 * 256));
     // pieces of about the same size
     const int64_t pieces = (v + p.piece - 1) / p.piece;
     p.piece = std::min(v, ((v + pieces - 1) / pieces + 255) / 256 * 256);
     p.many = e == 2 && n > 64 && k > 128;
     const bool whole = e == 2 && k % 8 == 0 && n > 0;
-    p.turn_rows = whole && (k >= 512 || (n <= 512 && k >= 128));
+    p.turn_rows = whole && (p.pad || k >= 512 || (n <= 512 && k >= 128));
     p.turn_words = whole && n >= 2048 && ((n + 255) / 256) * ((k + 255) / 256) >= 64;
     const int64_t tiles = p.turn_words ? ((n + 255) / 256) * ((k + 255) / 256)
                           : p.many     ? ((n + 127) / 128) * ((k + 255) / 256)
@@ -1034,7 +1100,9 @@ LossPlan loss_plan(int32_t dtype, int64_t k, int64_t n, int64_t v, int64_t picks
     p.turned = take(p.turn_rows ? p.piece * ldn * e : 0);
     p.rows_turned = take(p.turn_rows ? k * ldn * e : 0);
     p.words_turned = take(p.turn_words ? k * ld * e : 0);
-    p.sums = take(p.cuts * n * k * 4);
+    p.values = take(p.pad ? n * k * e : 0);
+    p.words = take(p.pad ? p.piece * k * e : 0);
+    p.sums = take(p.cuts * n * columns * 4);
     p.share = take(n * 4);
     p.hit = take(n * 4);
     p.bound = take(n * 4);
@@ -1147,23 +1215,38 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
     }
     if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
     int rc = SEGRED_OK;
+    const char *const weights = a.weights;
+    if constexpr (sizeof(T) == 2) {
+        if (p.pad) {
+            if (a.N > 0) rc = loss_pad_launch<T>(a.values, a.N, a.K, work + p.values, st);
+            if (rc != SEGRED_OK) return rc;
+            a.values = work + p.values;
+            a.K = p.wide;
+        }
+    }
     if constexpr (sizeof(T) == 2)
         if (turn_rows) rc = loss_turn_launch<T>(a.values, a.N, a.K, a.K, a.live, work + p.rows_turned, a.ldn, st);
     for (a.v0 = 0; a.v0 < a.V && rc == SEGRED_OK; a.v0 += p.piece) {
         a.vc = std::min(p.piece, a.V - a.v0);
         a.ld = (a.vc + 7) / 8 * 8;
         a.first = a.v0 == 0;
+        if constexpr (sizeof(T) == 2)
+            if (p.pad && a.N > 0) {
+                rc = loss_pad_launch<T>(weights + a.v0 * a.KO * 2, a.vc, a.KO, work + p.words, st);
+                if (rc != SEGRED_OK) return rc;
+                a.weights = work + p.words - a.v0 * a.K * 2;
+            }
         if (a.N > 0) rc = loss_tiles_launch<T, true>(a, kind, st);
         if (rc == SEGRED_OK && a.grad_values && a.N > 0) rc = loss_back_launch<T>(a, p, direct, st);
         if (rc != SEGRED_OK || !grad_weights) continue;
-        char *to = static_cast<char *>(grad_weights) + a.v0 * a.K * ge;
+        char *to = static_cast<char *>(grad_weights) + a.v0 * a.KO * ge;
         if constexpr (sizeof(T) == 2) {
             if (turn_rows) {
                 rc = loss_words_launch<T>(a, kind == kLossFew, to, ge == 4 ? 1 : 0, st);
                 continue;
             }
         }
-        rc = outer_scaled(a.slope, a.ld, a.vc, a.values, a.live, a.N, a.K, dtype, offsets, to, grad_weights_dtype,
+        rc = outer_scaled(a.slope, a.ld, a.vc, a.values, a.live, a.N, a.KO, dtype, offsets, to, grad_weights_dtype,
                           a.factor ? a.factor + 1 : nullptr, work + p.outer, st);
     }
     if (rc != SEGRED_OK) return rc;
@@ -1171,7 +1254,7 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
         dim3 grid;
         const bool shared = p.cuts >= kBackCuts;
         const int64_t each = 4 * kBackJoin / (shared ? kBackParts : 1);
-        if (!tile_grid((a.N * a.K + each - 1) / each, grid)) return SEGRED_ERR_UNSUPPORTED;
+        if (!tile_grid((a.N * a.KO + each - 1) / each, grid)) return SEGRED_ERR_UNSUPPORTED;
         if (shared) timed_launch_ggl(false, (loss_back_join<T, kBackParts>), grid, dim3(kBackJoin), 0, st, a);
         else timed_launch_ggl(false, (loss_back_join<T, 1>), grid, dim3(kBackJoin), 0, st, a);
     }
@@ -1183,9 +1266,9 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
 using namespace segred;
 
 extern "C" int64_t segred_cross_entropy_workspace(int32_t dtype, int64_t k, int64_t rows, int64_t vocab) {
-    if (float_size(dtype) == 0 || k < 1 || rows < 1 || vocab < 1 || too_large(rows, vocab, 8)) return 0;
-    // the smallest pairs, whatever kernel the pointers' alignment chooses
-    return rows * ((vocab + 127) / 128 * 2) * 8;
+    if (float_size(dtype) == 0 || k < 1 || k > kMaxWidth || rows < 1 || rows > kLossRows || vocab < 1 || vocab > kLossVocab)
+        return 0;
+    return loss_room(dtype, k, rows, vocab).bytes;
 }
 
 extern "C" int segred_cross_entropy(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights,
@@ -1200,16 +1283,18 @@ extern "C" int segred_cross_entropy(const void *values, int32_t dtype, int64_t k
         workspace_bytes < segred_cross_entropy_workspace(dtype, k, rows, vocab))
         return SEGRED_ERR_INVALID_ARGUMENT;
     LossArgs a = loss_args(values, k, rows, weights, vocab, target, probs, picks, scale);
-    const LossKind kind = loss_kind(dtype, rows, k, vocab, loss_direct(values, weights, dtype, k));
+    const LossRoom room = loss_room(dtype, k, rows, vocab);
+    const LossKind kind = room.pad ? loss_kind(dtype, rows, room.wide, room.piece, true)
+                                   : loss_kind(dtype, rows, k, vocab, loss_direct(values, weights, dtype, k));
     a.partial = static_cast<float2 *>(workspace);
     a.parts = loss_parts(kind, vocab);
     a.loss = loss;
     a.lse = lse;
     a.picked = picked;
     switch (dtype) {
-    case SEGRED_BF16: return loss_forward<__bf16>(a, kind, stream);
-    case SEGRED_F16: return loss_forward<_Float16>(a, kind, stream);
-    default: return loss_forward<float>(a, kind, stream);
+    case SEGRED_BF16: return loss_forward<__bf16>(a, kind, room, stream);
+    case SEGRED_F16: return loss_forward<_Float16>(a, kind, room, stream);
+    default: return loss_forward<float>(a, kind, room, stream);
     }
 }
 
@@ -1252,8 +1337,8 @@ extern "C" int segred_cross_entropy_grad(const float *grad, const void *values, 
     a.hits = reinterpret_cast<float *>(work + p.hits);
     a.factor = dtype == SEGRED_F16 && rows > 0 ? reinterpret_cast<float *>(work + p.factor) : nullptr;
     a.cuts = p.cuts;
-    const bool direct = loss_direct(values, weights, dtype, k);
-    const LossKind kind = loss_kind(dtype, rows, k, p.piece, direct);
+    const bool direct = p.pad || loss_direct(values, weights, dtype, k);
+    const LossKind kind = loss_kind(dtype, rows, p.wide, p.piece, direct);
     switch (dtype) {
     case SEGRED_BF16: return loss_backward<__bf16>(a, p, kind, direct, dtype, grad_weights, grad_weights_dtype, work, stream);
     case SEGRED_F16: return loss_backward<_Float16>(a, p, kind, direct, dtype, grad_weights, grad_weights_dtype, work, stream);

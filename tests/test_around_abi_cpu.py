@@ -125,5 +125,5 @@ def test_workspaces():
         need, e = lib.segred_cross_entropy_grad_workspace(dtype, k, n, v, 3), 4 if dtype == 2 else 2
         piece = min(v, max(2 ** 28 // (n * e), 4096) + 8)
         # a piece, the rows' sums (up to 64 of them where there are few), and what the weights' sums need
-        assert need <= 2 * (n + 8) * piece * e + (n + piece) * k * e + 64 * min(n, 4096) * k * 4 + n * k * 4 + n * 64 + 2 ** 28
+        assert need <= 2 * (n + 8) * piece * e + 2 * (n + piece) * (k + 8) * e + 64 * min(n, 4096) * k * 4 + n * k * 4 + n * 64 + 2 ** 28
     assert lib.segred_cross_entropy_grad_workspace(0, 64, 10, 10, 1) == 0

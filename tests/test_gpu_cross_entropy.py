@@ -54,6 +54,7 @@ def test_shapes(t, n, k, v):
 KERNELS = [("bf16", 100, 256, 33000), ("f16", 300, 256, 16500), ("bf16", 257, 512, 20001), ("f16", 8, 512, 30011),
            ("bf16", 300, 257, 5003), ("f32", 300, 128, 5003), ("f32", 5, 128, 9001), ("f32", 100, 65, 2001),
            ("bf16", 513, 64, 9000), ("f16", 30, 1024, 3000),
+           ("bf16", 2100, 1030, 5003), ("f16", 300, 1030, 70001), ("bf16", 10, 131, 3001), ("f16", 2500, 2047, 4200),
            ("bf16", 5, 256, 3001), ("f16", 40, 520, 2001), ("bf16", 128, 128, 4099), ("f16", 300, 1032, 2051),
            ("bf16", 2100, 520, 5003), ("f16", 701, 512, 9001), ("bf16", 2051, 264, 8200), ("f16", 2304, 1024, 4100)]
 
@@ -65,7 +66,7 @@ def test_kernels(t, n, k, v):
 
 
 @pytest.mark.parametrize("t,n,k,v", [("bf16", 16500, 64, 9001), ("f16", 16500, 72, 8193), ("f32", 8200, 40, 9000),
-                                     ("bf16", 16400, 65, 8300), ("bf16", 16389, 512, 8300)])
+                                     ("bf16", 16400, 65, 8300), ("bf16", 16389, 512, 8300), ("f16", 16389, 513, 8300)])
 def test_pieces(t, n, k, v):
     """More than one piece of the vocabulary (256 MiB hold less)."""
     _check(*_case(t, n, k, v), f"cross entropy {t} {n}x{k} vocab {v} in pieces")
