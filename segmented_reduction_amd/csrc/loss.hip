@@ -489,7 +489,7 @@ __global__ __launch_bounds__(1024) void loss_factor(LossArgs a) {
     m = 0.f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) m = fmaxf(m, s[w]);
-    const int up = m > 0.f ? min(max(13 - ilogbf(m), -100), 100) : 0;
+    const int up = m > 0.f ? min(max(13 - ilogbf(m), -126), 126) : 0;
     const float f = ldexpf(1.f, up);
     for (int64_t i = threadIdx.x; i < a.N; i += 1024) a.share[i] *= f;
     if (threadIdx.x == 0) {

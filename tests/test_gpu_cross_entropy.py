@@ -154,6 +154,38 @@ def test_small_and_uneven_gradients_in_float16(n):
     _check(x, w, target, None, grad, "cross entropy f16, small gradients", weights_dtype=torch.float32)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -140, 2.0 ** -60, 2.0 ** 100, 2.0 ** 125])
+def test_gradients_of_any_size_in_float16(size):
+    """The common power of two brings them into float16's range; the weights' gradient leaves in float32."""
+    x, w, target, _, grad = _case("f16", 50, 64, 300, none=0.0)
+    # few and small values, so that their sums stay in float32's range
+    x, w = (x.float() * 2.0 ** -6).half(), (w.float() * 2.0 ** -4).half()
+    sign = grad.sign()
+    grad = (sign.cpu() * size).cuda()  # made on the host, which keeps the smallest numbers
+    _, lse, picked = sr.cross_entropy(x, w, target)
+    _, dw = sr.cross_entropy_grad(grad, x, w, target, lse, picked, weights_dtype=torch.float32)
+    one = sr.cross_entropy_grad(sign, x, w, target, lse, picked, weights_dtype=torch.float32)[1].cpu().double()
+    # the same but for the power of two: exact, down to float32's own smallest step and, where the
+    # power would pass 2^126, half of float16's, 2^-25 2^-126 for each slope
+    more = 2.0 ** -151 * float(x.abs().float().sum(0).max()) if size < 2.0 ** -113 else 0.0
+    assert ((dw.cpu().double() - one * size).abs() <= 2.0 ** -23 * one.abs() * size + 2.0 ** -149 + more).all()
+
+
+@pytest.mark.parametrize("t,n,picks", [("bf16", 9, 700), ("f32", 40, 130), ("f16", 300, 4096)])
+def test_many_targets(t, n, picks):
+    """Up to 4,096 a row, many of them named again and again."""
+    _check(*_case(t, n, 64, 900, picks), f"cross entropy {t}, {picks} targets a row")
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_one_target_of_any_probability(t):
+    x, w, target, _, grad = _case(t, 60, 64, 200)
+    probs = torch.linspace(-1, 3, 60, device="cuda")
+    one = _check(x, w, target, probs, grad, f"cross entropy {t}, one target of any probability")
+    two = _check(x, w, target[:, None].contiguous(), probs[:, None].contiguous(), grad, "the same in two dimensions")
+    assert two[2].shape == (60, 1) and all(torch.equal(a, b.view(a.shape)) for a, b in zip(one, two))
+
+
 def test_logits_of_minus_infinity():
     """An entry of the vocabulary that is impossible takes no part."""
     g = A.gen(2)

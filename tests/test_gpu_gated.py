@@ -132,6 +132,16 @@ def test_no_rows_and_no_segments():
     assert (out == 3).all()
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("k,m", [(64, 128), (13, 7)])
+def test_no_source_rows_at_all(t, k, m):
+    """Operands without a row, of which every row that is named is missing: act(0) * 0."""
+    none, w = torch.empty(0, k, dtype=A.TYPES[t], device="cuda"), torch.ones(2, 2 * m, k, dtype=A.TYPES[t], device="cuda")
+    rows, off = torch.tensor([0, -1, 5], device="cuda"), torch.tensor([0, 1, 3], device="cuda")
+    assert not sr.gated(none, w, off, rows=rows).any()
+    assert not sr.gated_grad(torch.ones(3, m, dtype=A.TYPES[t], device="cuda"), none, w, off, rows=rows).any()
+
+
 def test_refusals():
     x, w = torch.zeros(4, 16, device="cuda"), torch.zeros(2, 64, 16, device="cuda")
     off, d = torch.tensor([0, 2, 4], device="cuda"), torch.zeros(4, 32, device="cuda")
