@@ -9,7 +9,8 @@
 // Both directions move their rows once and are bound by memory: a row is held
 // in registers (up to 16,384 elements), the statistics are found there in two
 // passes (mean, then squares around it), and the gradient finds them again
-// instead of reading them.
+// instead of reading them.  (16,384 x 4,096 bfloat16 forward 50 us, 5.3 TB/s; 16,384 x
+// 2,048 forward 25 and gradient 38 + 5 for the join of the workgroups' sums, 5.3 TB/s.)
 #include <algorithm>
 #include <cmath>
 
