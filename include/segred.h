@@ -25,7 +25,8 @@ extern "C" {
 #endif
 
 /* Element types of `values` (4-byte packed scalars; the 2-byte types are
- * those of the matrix products and the combine calls only). */
+ * those of the matrix products, the combine calls, the norms and the cross
+ * entropy only). */
 enum segred_dtype { SEGRED_U32 = 0, SEGRED_I32 = 1, SEGRED_F32 = 2, SEGRED_BF16 = 3, SEGRED_F16 = 4 };
 
 /* Reductions.  MEAN is float32 only. */
@@ -409,8 +410,9 @@ int segred_galloping_search(const void *values, int32_t dtype, int64_t value_cou
 /*
  * Operators over ragged groups of rows: grouping rows by an index, products
  * of each group with weights of its own and their gradients, the weighted
- * join of the rows an entry was sent to, and a shared projection with a
- * low-rank adapter per segment.  Types are SEGRED_F32, SEGRED_BF16 and
+ * join of the rows an entry was sent to, a shared projection with a
+ * low-rank adapter per segment, gated projections, norms of rows, and the
+ * cross entropy against a vocabulary.  Types are SEGRED_F32, SEGRED_BF16 and
  * SEGRED_F16; sums are held in float32 and every output is rounded to its
  * type once.  None of these calls allocates memory or uses the library's own
  * scratch: where one needs working memory the caller passes `workspace`
@@ -730,7 +732,7 @@ int64_t segred_norm_grad_workspace(int64_t k, int64_t rows);
  * rows < 0, a scale that is not positive and finite, a NULL pointer that is
  * needed, misalignment (an element, 8 bytes for target, 16 for the workspace), a
  * workspace that is missing or too small.  SEGRED_ERR_UNSUPPORTED for integer
- * types, k above 2^24, vocab above 2^30, rows above 2^31 or picks above 4,096.
+ * types, k above 2^24, vocab above 2^30, rows above 2^27 or picks above 4,096.
  * SEGRED_ERR_HIP if a launch fails.
  */
 int segred_cross_entropy(const void *values, int32_t dtype, int64_t k, int64_t rows, const void *weights,

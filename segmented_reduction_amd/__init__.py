@@ -52,7 +52,7 @@ SUM, MIN, MAX, MEAN = 0, 1, 2, 3
 OPS = {"sum": SUM, "min": MIN, "max": MAX, "mean": MEAN}
 DTYPES = {torch.uint32: 0, torch.int32: 1, torch.float32: 2}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
-FLOATS = {torch.float32: 2, torch.bfloat16: 3, torch.float16: 4}  # the products and combine calls
+FLOATS = {torch.float32: 2, torch.bfloat16: 3, torch.float16: 4}  # the products, combine calls, norms and cross entropy
 STATUS = {0: "SEGRED_OK", 1: "SEGRED_ERR_INVALID_ARGUMENT", 2: "SEGRED_ERR_UNSUPPORTED",
           3: "SEGRED_ERR_OUT_OF_MEMORY", 4: "SEGRED_ERR_HIP", 5: "SEGRED_ERR_SCRATCH_LIMIT"}
 

@@ -270,7 +270,7 @@ __global__ __launch_bounds__(64 * NW) void seg_gated_few(GatedArgs a) {
         f32x4 g = Tile::sum(lds, 2 * j, lane), u = Tile::sum(lds, 2 * j + 1, lane);
         if (r >= p.rows) continue;
         const int64_t n = p.n0 + 16 * j + (lane >> 4) * 4;
-            if constexpr (GRAD) {
+        if constexpr (GRAD) {
             gated_slope<ERF>(g, u, load_four<T>(reinterpret_cast<const T *>(a.grad) + row * a.M, n, a.M), a);
             store_four<T>(out + row * 2 * a.M, n, a.M, g);
             store_four<T>(out + row * 2 * a.M + a.M, n, a.M, u);

@@ -889,7 +889,9 @@ __global__ __launch_bounds__(kBackJoin) void loss_back_join(LossArgs a) {
 
 // --------------------------------------------------------------------- host
 
-constexpr int64_t kLossFewRows = 16, kLossRows = int64_t(1) << 31, kLossVocab = 1 << 30, kLossPicks = 4096;
+// Rows up to 2^27: 16 lanes prepare one, and a launch has fewer than 2^32; the products
+// over them count in 32 bits.
+constexpr int64_t kLossFewRows = 16, kLossRows = 1 << 27, kLossVocab = 1 << 30, kLossPicks = 4096;
 // Kernels of the tiles.  Times in us of the forward call (bfloat16, the joining
 // kernel's 6 to 10 among them):
 //

@@ -91,7 +91,7 @@ def _loss_grad(**kw):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(dtype=5), 1), (dict(dtype=1), 2), (dict(k=0), 1), (dict(rows=-1), 1), (dict(vocab=0), 1), (dict(picks=0), 1),
-    (dict(k=2 ** 24 + 1), 2), (dict(vocab=2 ** 30 + 1), 2), (dict(rows=2 ** 31 + 1), 2), (dict(picks=4097), 2),
+    (dict(k=2 ** 24 + 1), 2), (dict(vocab=2 ** 30 + 1), 2), (dict(rows=2 ** 27 + 1), 2), (dict(picks=4097), 2),
     (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=NAN), 1), (dict(scale=INF), 1), (dict(values=None), 1),
     (dict(weights=None), 1), (dict(target=None), 1), (dict(values=FAKE + 1), 1), (dict(weights=FAKE + 1), 1),
     (dict(target=FAKE + 4), 1), (dict(probs=FAKE + 2), 1), (dict(lse=None), 1), (dict(picked=None), 1), (dict(lse=FAKE + 2), 1),
