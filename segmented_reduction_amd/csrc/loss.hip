@@ -431,18 +431,12 @@ __device__ __forceinline__ float loss_hit(const LossArgs &a, int64_t row, int64_
     return fmaf(a.share[row], e, -a.hit[row] * p);
 }
 
-// What the gradient's tiles need of each row, LANES lanes a row, and the one
-// segment of the weights' sums.
+// What the gradient's tiles need of row `row`, from the LANES lanes it has (lane
+// `l`): left in `share`, `hit`, `bound` and `live`.
 template <int LANES>
-__global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *offsets) {
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
-    if (row == 0) {
-        offsets[0] = 0;
-        offsets[1] = a.N;
-    }
-    if (row >= a.N) return;  // whole groups of LANES
+__device__ __forceinline__ void loss_row_prepare(const LossArgs &a, int64_t row, int l) {
     float share = 0.f, size = 0.f, any = 0.f;
-    for (int64_t j = threadIdx.x % LANES; j < a.picks; j += LANES) {
+    for (int64_t j = l; j < a.picks; j += LANES) {
         const int64_t t = a.target[row * a.picks + j];
         if (t < 0 || t >= a.V) continue;
         const float p = a.probs ? a.probs[row * a.picks + j] : 1.f;
@@ -455,7 +449,7 @@ __global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *of
         size = lanes_sum<LANES>(size);
         any = lanes_sum<LANES>(any);
     }
-    if (threadIdx.x % LANES > 0) return;
+    if (l > 0) return;
     const bool live = any > 0.f;
     const float g = a.grad[row] * a.scale, bound = fabsf(g) * size;
     a.share[row] = live ? g * share : 0.f;
@@ -464,11 +458,20 @@ __global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *of
     a.live[row] = live ? row : -1;
     if constexpr (LANES == 1) a.hits[row] = live ? loss_hit(a, row, row, share) : 0.f;
 }
-// dz of the targets of rows that have several, from the logits that the forward
-// call kept; a target named twice in a row gets both shares.
-__global__ __launch_bounds__(256) void loss_hits(LossArgs a) {
-    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-    if (i >= a.N * a.picks) return;
+// The one segment of the weights' sums.
+__device__ __forceinline__ void loss_bounds(int64_t *offsets, int64_t n) {
+    offsets[0] = 0;
+    offsets[1] = n;
+}
+template <int LANES>
+__global__ __launch_bounds__(256) void loss_rows_prepare(LossArgs a, int64_t *offsets) {
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
+    if (row == 0) loss_bounds(offsets, a.N);
+    if (row < a.N) loss_row_prepare<LANES>(a, row, threadIdx.x % LANES);  // whole groups of LANES
+}
+// dz of target i (of all rows) from the logits that the forward call kept; a target
+// named twice in a row gets both shares.
+__device__ __forceinline__ void loss_target_hit(const LossArgs &a, int64_t i) {
     const int64_t row = i / a.picks, t = a.target[i];
     const int64_t *target = a.target + row * a.picks;
     float sum = 0.f;
@@ -480,28 +483,54 @@ __global__ __launch_bounds__(256) void loss_hits(LossArgs a) {
     }
     a.hits[i] = sum;
 }
+__global__ __launch_bounds__(256) void loss_hits(LossArgs a) {
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (i < a.N * a.picks) loss_target_hit(a, i);
+}
 
 // float16 holds 2^-24 to 2^16, so dz is brought near 2^13 by a power of two that
 // all rows share (|dz| is at most twice its bound, so below 2^15), and the products take it out again:
 // of the row with the largest bound, probabilities from 2^-37 on are kept, those
-// from 2^-27 on with all bits.
-__global__ __launch_bounds__(1024) void loss_factor(LossArgs a) {
-    __shared__ float s[16];
+// from 2^-27 on with all bits.  By one workgroup.
+constexpr int kOnce = 1024;
+__device__ __forceinline__ void loss_scale(const LossArgs &a) {
+    __shared__ float s[kOnce / 64];
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < a.N; i += 1024) m = fmaxf(m, a.bound[i]);
+    for (int64_t i = threadIdx.x; i < a.N; i += kOnce) m = fmaxf(m, a.bound[i]);
     m = lanes_fold<64>(m, [](float p, float q) { return fmaxf(p, q); });
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
     __syncthreads();
     m = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) m = fmaxf(m, s[w]);
+    for (int w = 0; w < kOnce / 64; ++w) m = fmaxf(m, s[w]);
     const int up = m > 0.f ? min(max(13 - ilogbf(m), -126), 126) : 0;
     const float f = ldexpf(1.f, up);
-    for (int64_t i = threadIdx.x; i < a.N; i += 1024) a.share[i] *= f;
+    for (int64_t i = threadIdx.x; i < a.N; i += kOnce) a.share[i] *= f;
     if (threadIdx.x == 0) {
         a.factor[0] = f;
         a.factor[1] = ldexpf(1.f, -up);
     }
+}
+__global__ __launch_bounds__(kOnce) void loss_factor(LossArgs a) { loss_scale(a); }
+
+// All of these by one workgroup, for calls whose launches are what they take (15 rows
+// of 4 targets, 144 columns, 876 entries, float16: the call 22 us, 29 with kernels of their
+// own and dz turned; 5 rows of one 22.5 and 28; but 128 rows of 32 66 and 51, so rows of several
+// only where each thread has one).
+constexpr bool loss_once(int64_t n, int64_t picks) {
+    return picks == 1 ? n <= 4 * kOnce : n <= kOnce / 16 && n * picks <= kOnce;
+}
+__global__ __launch_bounds__(kOnce) void loss_prepare_once(LossArgs a, int64_t *offsets) {
+    if (threadIdx.x == 0) loss_bounds(offsets, a.N);
+    if (a.picks == 1) {
+        for (int64_t row = threadIdx.x; row < a.N; row += kOnce) loss_row_prepare<1>(a, row, 0);
+    } else {
+        for (int64_t row = threadIdx.x / 16; row < a.N; row += kOnce / 16) loss_row_prepare<16>(a, row, threadIdx.x % 16);
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < a.N * a.picks; i += kOnce) loss_target_hit(a, i);
+    }
+    __syncthreads();
+    if (a.factor) loss_scale(a);
 }
 
 // dx += dz W of a piece: rows of dz in row form, rows of W across the
@@ -1080,6 +1109,7 @@ struct LossPlan {
     // places in the working memory
     int64_t slope, turned, rows_turned, words_turned, values, words, sums, share, hit, bound, live, hits, offsets, factor, outer, bytes;
 };
+constexpr int64_t kTurnWords = 12 << 20;
 LossPlan loss_plan(int32_t dtype, int64_t columns, int64_t n, int64_t v, int64_t picks) {
     const int64_t e = float_size(dtype);
     LossPlan p{};
@@ -1092,7 +1122,10 @@ LossPlan loss_plan(int32_t dtype, int64_t columns, int64_t n, int64_t v, int64_t
     p.piece = std::min(v, ((v + pieces - 1) / pieces + 255) / 256 * 256);
     p.many = e == 2 && n > 64 && k > 128;
     const bool whole = e == 2 && k % 8 == 0 && n > 0;
-    p.turn_rows = whole && (p.pad || k >= 512 || (n <= 512 && k >= 128));
+    // (16 / 64 / 256 rows, 512 columns, 4,000 entries: the call 28 / 30 / 42 us with dz and
+    // values turned, 22 / 27 / 39 without; 8 x 1,024 x 32,000 65 and 70, 64 x 2,048 x 16,000 68
+    // and 75; 1,024 x 512 x 4,000 55 and 64)
+    p.turn_rows = whole && (p.pad || (n <= 256 ? k >= 128 && k * v >= kTurnWords : k >= 512 || (n <= 512 && k >= 128)));
     p.turn_words = whole && n >= 2048 && ((n + 255) / 256) * ((k + 255) / 256) >= 64;
     const int64_t tiles = p.turn_words ? ((n + 255) / 256) * ((k + 255) / 256)
                           : p.many     ? ((n + 127) / 128) * ((k + 255) / 256)
@@ -1125,11 +1158,6 @@ LossPlan loss_plan(int32_t dtype, int64_t columns, int64_t n, int64_t v, int64_t
     p.outer = take(std::max(segred_outer_workspace(p.piece, k, 1, n), last > 0 ? segred_outer_workspace(last, k, 1, n) : 0));
     p.bytes = at;
     return p;
-}
-
-__global__ void loss_bounds(int64_t *offsets, int64_t n) {
-    offsets[0] = 0;
-    offsets[1] = n;
 }
 
 template <typename T>
@@ -1216,18 +1244,19 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
     a.turned = turn_rows ? work + p.turned : nullptr;
     a.rows_turned = work + p.rows_turned;
     a.words_turned = work + p.words_turned;
-    if (a.N == 0) {
-        timed_launch_ggl(false, loss_bounds, dim3(1), dim3(1), 0, st, offsets, a.N);
+    const bool several = a.picks > 1;
+    if (loss_once(a.N, a.picks) && (several || a.factor || a.N == 0)) {
+        timed_launch_ggl(false, loss_prepare_once, dim3(1), dim3(kOnce), 0, st, a, offsets);
     } else {
-        dim3 grid;
-        if (a.picks > 1) {
+        if (several) {
+            dim3 grid;
             if (!tile_grid((a.N * a.picks + 255) / 256, grid)) return SEGRED_ERR_UNSUPPORTED;
             timed_launch_ggl(false, (loss_rows_prepare<16>), dim3((unsigned)((a.N + 15) / 16)), dim3(256), 0, st, a, offsets);
             timed_launch_ggl(false, loss_hits, grid, dim3(256), 0, st, a);
         } else {
             timed_launch_ggl(false, (loss_rows_prepare<1>), dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, st, a, offsets);
         }
-        if (__is_same(T, _Float16)) timed_launch_ggl(false, loss_factor, dim3(1), dim3(1024), 0, st, a);
+        if (a.factor) timed_launch_ggl(false, loss_factor, dim3(1), dim3(kOnce), 0, st, a);
     }
     if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
     int rc = SEGRED_OK;

@@ -28,7 +28,7 @@ struct NormArgs {
     float eps;
     char *out;       // or the gradient of the values
     void *grad_weight, *grad_bias;  // null: not asked for
-    float *partial;  // [blocks][2][K]
+    float *partial;  // [blocks][2][K]; null: one workgroup has the whole sums
     int64_t blocks;
 };
 
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
                 norm_store<T, L, WHOLE>(to, u, l, K, y);
             }
     }
-    if (!a.partial) return;
+    if (!a.grad_weight && !a.grad_bias) return;
 
     // The rows of a wave, then of the workgroup, in order.
     if constexpr (LW < 64) {
@@ -369,13 +369,17 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
             db[i / N][i % N] = s_sums[(E + i) * L + l];
         }
     }
-    float *to = a.partial + (int64_t)blockIdx.x * 2 * K;
+    float *to = a.partial ? a.partial + (int64_t)blockIdx.x * 2 * K : nullptr;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int c = norm_col<T, L>(i / N, l) + i % N;
-        if (c < K) {
+        if (c >= K) continue;
+        if (to) {
             to[c] = dw[i / N][i % N];
             to[K + c] = db[i / N][i % N];
+        } else {  // the only workgroup
+            if (a.grad_weight) put_param<T>(a.grad_weight, a.weight_f32, c, dw[i / N][i % N]);
+            if (a.grad_bias) put_param<T>(a.grad_bias, a.weight_f32, c, db[i / N][i % N]);
         }
     }
 }
@@ -491,13 +495,23 @@ NormShape norm_shape(int64_t k, bool grad, bool wide) {
 // device: as many as it holds at a time (more read the parameters more often: k =
 // 4,096 in 1,024 workgroups 24 us, in 4,096 27), and for the gradient fewer where
 // their parts are long (k = 8,192 in 256 60 us, in 512 63; k = 512 in 512 50, in
-// 768 46).
+// 768 46).  One workgroup takes the gradient of as many rows as it has in two rounds and
+// leaves the sums itself (8 rows of 512: 4.8 us, 10.2 with the host's side, against 5.9 and
+// 14.3 with the join; in four rounds 6.2 and 10.2, but rows of 8,192 16 and 14).
 int64_t norm_blocks(const NormShape &s, int64_t rows, bool grad) {
     const int64_t row = (int64_t)s.lanes * s.elements;
     int64_t most = s.lanes == 0 ? 512 : s.lanes <= 128 ? 2048 : s.lanes == 256 ? 1024 : 512;
     if (grad) most = s.lanes == 0 || row > 4096 ? 256 : row <= 512 ? 768 : 512;
     const int64_t each = s.lanes > 0 && s.lanes < 256 ? 256 / s.lanes : 1;
+    if (grad && s.lanes > 0 && rows <= 2 * each) return 1;
     return std::min(most, (rows + each - 1) / each);
+}
+
+// Bytes of the workgroups' sums.
+int64_t norm_room(int64_t k, int64_t rows, bool wide) {
+    const NormShape s = norm_shape(k, true, wide);
+    const int64_t blocks = norm_blocks(s, rows, true);
+    return blocks == 1 && s.lanes > 0 ? 0 : blocks * 2 * k * 4;
 }
 
 template <typename T, bool GRAD, int L, int E, bool WHOLE>
@@ -530,7 +544,7 @@ int norm_dispatch(NormArgs a, hipStream_t st) {
         else norm_start<T, GRAD, 512, 32>(a, st);
         if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
     }
-    if (GRAD && (a.grad_weight || a.grad_bias)) {
+    if (GRAD && (a.grad_weight || a.grad_bias) && (a.partial || a.N == 0)) {
         const int64_t wgs = (2 * (int64_t)a.K + kNormJoinCols - 1) / kNormJoinCols;
         timed_launch_ggl(false, (norm_join<T>), dim3((unsigned)wgs), dim3(kNormJoinCols * kNormJoinParts), 0, st, a);
         if (hipGetLastError() != hipSuccess) return SEGRED_ERR_HIP;
@@ -585,9 +599,7 @@ extern "C" int segred_norm(const void *values, int32_t dtype, int64_t k, int64_t
 
 extern "C" int64_t segred_norm_grad_workspace(int64_t k, int64_t rows) {
     if (k < 1 || rows < 1 || k > kMaxWidth) return 0;
-    const int64_t blocks = std::max(norm_blocks(norm_shape(k, true, false), rows, true),
-                                    norm_blocks(norm_shape(k, true, true), rows, true));
-    return blocks * 2 * k * 4;
+    return std::max(norm_room(k, rows, false), norm_room(k, rows, true));
 }
 
 extern "C" int segred_norm_grad(const void *grad, const void *values, int32_t dtype, int64_t k, int64_t rows,
@@ -615,6 +627,6 @@ extern "C" int segred_norm_grad(const void *grad, const void *values, int32_t dt
     a.out = static_cast<char *>(grad_values);
     a.grad_weight = grad_weight;
     a.grad_bias = grad_bias;
-    a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.partial = sums && rows > 0 && norm_room(k, rows, dtype == SEGRED_F32) > 0 ? static_cast<float *>(workspace) : nullptr;
     return norm_typed<true>(a, dtype, stream);
 }

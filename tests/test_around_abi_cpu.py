@@ -72,7 +72,7 @@ def test_norm_own_checks(kw, expect):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(grad=None), 1), (dict(grad=FAKE + 1), 1), (dict(dx=None), 1), (dict(dx=FAKE + 1), 1), (dict(dw=FAKE + 1), 1),
-    (dict(db=FAKE + 1), 1), (dict(work=None), 1), (dict(work=FAKE + 8), 1), (dict(bytes=100), 1),
+    (dict(db=FAKE + 1), 1), (dict(rows=100, work=None), 1), (dict(work=FAKE + 8), 1), (dict(rows=100, bytes=100), 1),
     (dict(rows=0, grad=None, values=None, dx=None, dw=None, db=None, work=None, bytes=0), 0),
 ])
 def test_norm_grad_own_checks(kw, expect):
@@ -117,7 +117,8 @@ def test_cross_entropy_grad_own_checks(kw, expect):
 def test_workspaces():
     lib = _lib()
     assert lib.segred_norm_grad_workspace(64, 0) == 0 and lib.segred_norm_grad_workspace(0, 5) == 0
-    assert lib.segred_norm_grad_workspace(4096, 1) == 2 * 4096 * 4
+    assert lib.segred_norm_grad_workspace(4096, 2) == 0  # one workgroup has the sums
+    assert lib.segred_norm_grad_workspace(4096, 3) == 3 * 2 * 4096 * 4 and lib.segred_norm_grad_workspace(20000, 1) == 2 * 20000 * 4
     assert lib.segred_norm_grad_workspace(4096, 10 ** 9) == lib.segred_norm_grad_workspace(4096, 10 ** 6)
     assert lib.segred_cross_entropy_workspace(3, 64, 0, 10) == 0 and lib.segred_cross_entropy_workspace(0, 64, 1, 10) == 0
     assert lib.segred_cross_entropy_workspace(3, 64, 100, 6400) == 100 * 100 * 8

@@ -65,6 +65,19 @@ def test_kernels(t, n, k, v):
     _check(*_case(t, n, k, v, 20, seed=1), f"cross entropy {t} {n}x{k} vocab {v} picks 20", scale=0.5, weights_dtype=torch.float32)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("n,k,v", [(3, 2048, 6200), (16, 1024, 13001), (64, 1024, 13000), (250, 512, 25001)])
+def test_few_rows_and_many_weights(t, n, k, v):
+    """The weights' gradient from operands in the other order."""
+    _check(*_case(t, n, k, v), f"cross entropy {t} {n}x{k} vocab {v}")
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,picks", [(64, 16), (64, 17), (65, 2), (1, 1024), (1, 1025), (4096, 1), (4097, 1)])
+def test_rows_prepared_by_one_workgroup_or_more(t, n, picks):
+    _check(*_case(t, n, 72, 300, picks), f"cross entropy {t} {n}x72 vocab 300 picks {picks}")
+
+
 @pytest.mark.parametrize("t,n,k,v", [("bf16", 16500, 64, 9001), ("f16", 16500, 72, 8193), ("f32", 8200, 40, 9000),
                                      ("bf16", 16400, 65, 8300), ("bf16", 16389, 512, 8300), ("f16", 16389, 513, 8300)])
 def test_pieces(t, n, k, v):

@@ -56,6 +56,14 @@ def test_many_rows(t, n, k):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("k,n", [(100, 16), (96, 32), (100, 33), (512, 5), (512, 8), (1000, 9), (2048, 4), (2048, 8),
+                                 (2040, 9), (4096, 2), (4095, 3), (8192, 2), (16384, 2), (16384, 3), (17000, 1)])
+def test_few_rows(t, k, n):
+    """One workgroup leaves the parameters' gradients itself, two or more have them joined."""
+    _check(*_case(t, k, n, True, t, True, n), True, 1e-5, f"norm {t} {n}x{k}")
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("k", [96, 1024, 4096, 17000])
 def test_a_mean_far_from_zero(t, k):
     """The squares are taken around the mean, not subtracted from its square."""
