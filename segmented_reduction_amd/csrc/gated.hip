@@ -245,9 +245,9 @@ __global__ __launch_bounds__(kPhaseThreads) void seg_gated_many(GatedArgs a) {
 
 // Few rows per segment: 16 rows x 8 NT outputs per workgroup, the contraction
 // split over its waves.
-template <typename T, int NT, int NW, int STAGES, bool GRAD, bool ERF>
+template <typename T, int NT, int NW, int STAGES, bool DIRECT, bool GRAD, bool ERF>
 __global__ __launch_bounds__(64 * NW) void seg_gated_few(GatedArgs a) {
-    using Tile = FewTile<T, NT, NW, STAGES>;
+    using Tile = FewTile<T, NT, NW, STAGES, DIRECT>;
     __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
     lds_char *lds = (lds_char *)lds_mem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -309,11 +309,11 @@ int gated_many_launch(GatedArgs a, hipStream_t st) {
     timed_launch_ggl(true, (seg_gated_many<T, AH, GRAD, ERF>), grid, dim3(kPhaseThreads), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
-template <typename T, int NT, int NW, int STAGES, bool GRAD, bool ERF>
+template <typename T, int NT, int NW, int STAGES, bool DIRECT, bool GRAD, bool ERF>
 int gated_few_launch(GatedArgs a, hipStream_t st) {
     dim3 grid;
     if (!gated_grid(a, 4, 8 * NT, grid)) return SEGRED_ERR_UNSUPPORTED;
-    timed_launch_ggl(true, (seg_gated_few<T, NT, NW, STAGES, GRAD, ERF>), grid, dim3(64 * NW), 0, st, a);
+    timed_launch_ggl(true, (seg_gated_few<T, NT, NW, STAGES, DIRECT, GRAD, ERF>), grid, dim3(64 * NW), 0, st, a);
     return hipGetLastError() == hipSuccess ? SEGRED_OK : SEGRED_ERR_HIP;
 }
 
@@ -352,17 +352,20 @@ int gated_dispatch(const GatedArgs &a, bool direct, hipStream_t st) {
     const int64_t mean = a.N / a.S;
     if constexpr (sizeof(T) == 4) {
         const int64_t tiles = (a.N / 64 + a.S / 2) * ((2 * a.M + 127) / 128);
-        if (direct && mean <= kFewRows) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
+        if (direct && mean <= kFewRows) return gated_few_launch<T, 4, 4, 3, true, GRAD, ERF>(a, st);
         if (direct && (mean <= kSplitRows || tiles < kSplitTiles))
             return gated_launch<T, 32, 128, 1, 4, 3, true, GRAD, ERF>(a, st);
         if (mean <= kSplitRows) return gated_launch<T, 16, 128, 1, 4, 2, false, GRAD, ERF>(a, st);
         return gated_split_launch<64, 128, GRAD, ERF>(a, st);
     } else {
+        // waves that split the contraction where there are few workgroups (one
+        // segment of 16 rows, 4,096 x 4,096: 15 us against 23 of 64 x 32; of 4,095 x 4,095 68
+        // against 75 of 16 x 64, but 8 of 12 rows, 1,021 x 2,551, 53 against 39)
+        const bool few = mean <= 2 * kFewRows && a.S * ((a.M + 31) / 32) <= kFewGroups;
+        if (!direct && few) return gated_few_launch<T, 4, 4, 3, false, GRAD, ERF>(a, st);
         if (!direct && mean <= 2 * kFewRows) return gated_launch<T, 16, 128, 1, 4, 2, false, GRAD, ERF>(a, st);
         if (!direct) return gated_launch<T, 64, 128, 2, 2, 2, false, GRAD, ERF>(a, st);
-        // waves that split the contraction where there are few workgroups (one
-        // segment of 16 rows, 4,096 x 4,096: 15 us against 23 of 64 x 32)
-        if (mean <= 2 * kFewRows && a.S * ((a.M + 31) / 32) <= kFewGroups) return gated_few_launch<T, 4, 4, 3, GRAD, ERF>(a, st);
+        if (few) return gated_few_launch<T, 4, 4, 3, true, GRAD, ERF>(a, st);
         if (mean <= 2) return gated_launch<T, 32, 128, 1, 4, 3, true, GRAD, ERF>(a, st);
         switch (gated_kind(a, GRAD)) {
         case 0: return gated_many_launch<T, 2, GRAD, ERF>(a, st);

@@ -294,9 +294,9 @@ __global__ __launch_bounds__(kPhaseThreads) void loss_many(LossArgs a) {
 }
 
 // Up to 16 rows: 64 columns per workgroup, the contraction split over its waves.
-template <typename T, int NT, int NW, int STAGES, bool SLOPE>
+template <typename T, int NT, int NW, int STAGES, bool DIRECT, bool SLOPE>
 __global__ __launch_bounds__(64 * NW) void loss_few(LossArgs a) {
-    using Tile = FewTile<T, NT, NW, STAGES>;
+    using Tile = FewTile<T, NT, NW, STAGES, DIRECT>;
     static_assert(NT == NW, "a wave per block of columns");
     __shared__ __attribute__((aligned(1024))) char lds_mem[Tile::kLds];
     lds_char *lds = (lds_char *)lds_mem;
@@ -920,7 +920,7 @@ __global__ __launch_bounds__(kBackJoin) void loss_back_join(LossArgs a) {
 
 // Rows up to 2^27: 16 lanes prepare one, and a launch has fewer than 2^32; the products
 // over them count in 32 bits.
-constexpr int64_t kLossFewRows = 16, kLossRows = 1 << 27, kLossVocab = 1 << 30, kLossPicks = 4096;
+constexpr int64_t kLossFewRows = 16, kLossFewWords = 192 * 64, kLossRows = 1 << 27, kLossVocab = 1 << 30, kLossPicks = 4096;
 // Kernels of the tiles.  Times in us of the forward call (bfloat16, the joining
 // kernel's 6 to 10 among them):
 //
@@ -935,7 +935,7 @@ constexpr int64_t kLossFewRows = 16, kLossRows = 1 << 27, kLossVocab = 1 << 30, 
 // Up to 16 rows waves split the contraction, else the rule is the least of
 // tile_time(), less 3 us a round for the largest tiles (rows are not gathered and
 // need no search).
-enum LossKind { kLossFew, kLossSmall, kLossMiddle, kLossOne, kLossTwo, kLossSplit, kLossAny };
+enum LossKind { kLossFew, kLossSmall, kLossMiddle, kLossOne, kLossTwo, kLossSplit, kLossFewAny, kLossAny };
 LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) {
     if (dtype == SEGRED_F32) {
         // bf16 parts need tiles enough for every CU to be worth their splitting
@@ -943,7 +943,9 @@ LossKind loss_kind(int32_t dtype, int64_t n, int64_t k, int64_t v, bool direct) 
         if (n <= kLossFewRows) return kLossFew;
         return n <= 64 || ((n + 63) / 64) * ((v + 127) / 128) < 224 ? kLossSmall : kLossSplit;
     }
-    if (!direct) return kLossAny;
+    // (10 rows, k = 1,711, rows of no whole units: 7,143 entries 30 us against 44 in tiles of
+    // 64 x 128; 8 rows, k = 2,047, 32,000 entries 69 and 62)
+    if (!direct) return n <= kLossFewRows && v <= kLossFewWords ? kLossFewAny : kLossAny;
     if (n <= kLossFewRows) return kLossFew;
     constexpr LossKind kKinds[] = {kLossTwo, kLossOne, kLossMiddle, kLossSmall};
     auto time = [&](int i) {
@@ -962,20 +964,21 @@ int64_t loss_columns(LossKind kind) {
 
 template <typename T, bool SLOPE>
 int loss_tiles_launch(LossArgs a, LossKind kind, hipStream_t st) {
-    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne || kind == kLossMiddle ? 128 : kind == kLossFew ? 16 : sizeof(T) == 4 && kind == kLossSmall ? 32 : 64;
+    const int64_t bm = kind == kLossTwo ? 256 : kind == kLossOne || kind == kLossMiddle ? 128 : kind == kLossFew || kind == kLossFewAny ? 16 : sizeof(T) == 4 && kind == kLossSmall ? 32 : 64;
     const int64_t bn = kind == kLossSplit ? 128 : loss_columns(kind);
     a.mtiles = (a.N + bm - 1) / bm;
     a.ntiles = (a.vc + bn - 1) / bn;
     dim3 grid;
     if (!tile_grid(a.mtiles * a.ntiles, grid)) return SEGRED_ERR_UNSUPPORTED;
     if constexpr (sizeof(T) == 4) {
-        if (kind == kLossFew) timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a);
+        if (kind == kLossFew) timed_launch_ggl(true, (loss_few<T, 4, 4, 3, true, SLOPE>), grid, dim3(256), 0, st, a);
         else if (kind == kLossSmall) timed_launch_ggl(true, (loss_tiles<T, 32, 64, 1, 4, 4, true, SLOPE>), grid, dim3(256), 0, st, a);
         else if (a.K % 8 == 0) timed_launch_ggl(true, (loss_split<true, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
         else timed_launch_ggl(true, (loss_split<false, SLOPE>), grid, dim3(kRowSplitThreads), 0, st, a);
     } else {
         switch (kind) {
-        case kLossFew: timed_launch_ggl(true, (loss_few<T, 4, 4, 3, SLOPE>), grid, dim3(256), 0, st, a); break;
+        case kLossFew: timed_launch_ggl(true, (loss_few<T, 4, 4, 3, true, SLOPE>), grid, dim3(256), 0, st, a); break;
+        case kLossFewAny: timed_launch_ggl(true, (loss_few<T, 4, 4, 3, false, SLOPE>), grid, dim3(256), 0, st, a); break;
         case kLossSmall:
             timed_launch_ggl(true, (loss_tiles<T, 64, 64, 2, 2, 3, true, SLOPE>), grid, dim3(256), 0, st, a);
             break;
@@ -1287,7 +1290,7 @@ int loss_backward(LossArgs a, const LossPlan &p, LossKind kind, bool direct, int
         char *to = static_cast<char *>(grad_weights) + a.v0 * a.KO * ge;
         if constexpr (sizeof(T) == 2) {
             if (turn_rows) {
-                rc = loss_words_launch<T>(a, kind == kLossFew, to, ge == 4 ? 1 : 0, st);
+                rc = loss_words_launch<T>(a, kind == kLossFew || kind == kLossFewAny, to, ge == 4 ? 1 : 0, st);
                 continue;
             }
         }

@@ -172,26 +172,89 @@ struct SplitTile {
     }
 };
 
-// 16 rows x 16 NT columns, the contraction split over NW waves, rows of whole
-// units.  Each quad of four columns of all NT blocks belongs to one thread
-// afterwards: out(block j, row, column in the block, sum), j uniform in a wave.
-template <typename T, int NT, int NW, int STAGES>
+// 16 rows x 16 NT columns, the contraction split over NW waves.  Each quad of four
+// columns of all NT blocks belongs to one thread afterwards: out(block j, row, column
+// in the block, sum), j uniform in a wave.  DIRECT: rows of whole units, through LDS.
+// Otherwise (16-bit types) a lane loads its units of the operands, at any place, as the
+// matrix units take them, a step ahead (units that straddle words are slow, so only for
+// calls of few workgroups).
+template <typename T, int NT, int NW, int STAGES, bool DIRECT = true>
 struct FewTile {
     using AStage = RowStage<T, 16, 64, true>;
     using BStage = RowStage<T, 16 * NT, 64, true>;
     static constexpr int kThreads = 64 * NW;
     static constexpr int kStageBytes = AStage::kBytes + BStage::kBytes;
-    static constexpr int kLds = NW * STAGES * kStageBytes;
+    static constexpr int kSums = NW * NT * 1024, kLds = DIRECT ? NW * STAGES * kStageBytes : kSums + 1024;
+
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void any_steps(f32x4 (&acc)[NT], int K, int wave, int lane, FA arow, FB brow) {
+        static_assert(sizeof(T) == 2, "16-bit types");
+        uint64_t p[NT + 1];
+        int left[NT + 1];  // <= 0: a row of zeros
+#pragma unroll
+        for (int j = 0; j <= NT; ++j) {
+            const char *row = j < NT ? brow(16 * j + (lane & 15)) : arow(lane & 15);
+            p[j] = row ? (uint64_t)row + (lane >> 4) * 16 : (uint64_t)zero_unit();
+            left[j] = row ? K - (lane >> 4) * kUnit<T> : 0;
+        }
+        u32x4 next[2][NT + 1], cur[2][NT + 1];
+        // steps of 64 elements: whole ones without a bound, the last with one
+        const int whole = K / 64, t1 = (wave + 1) * whole / NW;
+        auto products = [&] {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[j] = mma<T>(cur[h][j], cur[h][NT], acc[j]);
+        };
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j <= NT; ++j) next[h][j] = load_whole<T>(p[j] + (left[j] > 0 ? t * 128 + h * 64 : 0));
+        };
+        auto take = [&] {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j <= NT; ++j) cur[h][j] = next[h][j];
+        };
+        int t = wave * whole / NW;
+        if (t < t1) fetch(t);
+        for (; t < t1; ++t) {
+            take();
+            if (t + 1 < t1) fetch(t + 1);
+            products();
+        }
+        if (wave == NW - 1 && whole * 64 < K) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j <= NT; ++j)
+                    cur[h][j] = load_unit<T>(p[j] + (left[j] > 0 ? whole * 128 + h * 64 : 0), left[j] - whole * 64 - h * 32);
+            products();
+        }
+    }
 
     // Leaves the waves' sums in LDS, each NT KiB: quad `lane` of block j of wave w
     // at (w * NT + j) * 1024 + lane * 16.
     template <typename FA, typename FB>
     static __device__ __forceinline__ void run(int K, lds_char *lds, int wave, int lane, FA arow, FB brow) {
+        f32x4 acc[1][NT] = {};
+        if constexpr (DIRECT) steps(acc, K, lds, wave, lane, arow, brow);
+        else any_steps(acc[0], K, wave, lane, arow, brow);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<__attribute__((address_space(3))) f32x4 *>(lds + (wave * NT + j) * 1024 + lane * 16) =
+                acc[0][j];
+        __syncthreads();
+    }
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void steps(f32x4 (&acc)[1][NT], int K, lds_char *lds, int wave, int lane, FA arow,
+                                                 FB brow) {
         AStage sa;
         BStage sb;
         sa.init(0, lane, K, arow);
         sb.init(0, lane, K, brow);
-        f32x4 acc[1][NT] = {};
         const int steps = (K + kStep<T> - 1) / kStep<T>;
         wave_steps<STAGES, true, AStage::kLoads + BStage::kLoads, kStageBytes>(
             lds + wave * STAGES * kStageBytes, wave * steps / NW, (wave + 1) * steps / NW,
@@ -205,11 +268,6 @@ struct FewTile {
                 step_products<T, 1, NT, false, 16, false, 16 * NT>(acc, buf, buf + AStage::kBytes, 0, 0, lane);
             },
             [] {});
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<__attribute__((address_space(3))) f32x4 *>(lds + (wave * NT + j) * 1024 + lane * 16) =
-                acc[0][j];
         __syncthreads();
     }
     // The sum of quad `lane` of block j, added in wave order.

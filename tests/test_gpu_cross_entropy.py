@@ -72,6 +72,13 @@ def test_few_rows_and_many_weights(t, n, k, v):
     _check(*_case(t, n, k, v), f"cross entropy {t} {n}x{k} vocab {v}")
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("n,k,v", [(1, 1, 1), (1, 31, 65), (7, 33, 200), (16, 95, 64), (16, 257, 1000), (10, 1711, 7143),
+                                   (3, 130, 12289), (13, 2047, 40)])
+def test_few_rows_that_are_no_whole_units(t, n, k, v):
+    _check(*_case(t, n, k, v, none=0.0), f"cross entropy {t} {n}x{k} vocab {v}")
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("n,picks", [(64, 16), (64, 17), (65, 2), (1, 1024), (1, 1025), (4096, 1), (4097, 1)])
 def test_rows_prepared_by_one_workgroup_or_more(t, n, picks):

@@ -69,6 +69,13 @@ KERNELS = [("bf16", [8] * 40, 256, 128), ("bf16", [60, 20, 0, 44, 30, 26], 512, 
            ("f32", [2000, 1000], 96, 130), ("bf16", [200, 111], 99, 65)]
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths,k,m", [([1], 1, 1), ([3, 16, 0, 1], 31, 5), ([17, 2], 33, 40), ([8] * 12, 257, 100),
+                                         ([8] * 40, 257, 200), ([16], 1023, 515)])
+def test_few_rows_that_are_no_whole_units(t, lengths, k, m):
+    _check(*_case(t, lengths, k, m, base=1, extra=2, gather=9), "gelu", f"gated {t} {lengths} {k}x{m}")
+
+
 @pytest.mark.parametrize("t,lengths,k,m", KERNELS)
 def test_kernels(t, lengths, k, m):
     n = sum(lengths)
