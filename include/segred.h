@@ -673,6 +673,10 @@ int segred_gated_grad(const void *grad, const void *values, int32_t dtype, int64
  * (x - m)^2, out = (x - m) / sqrt(v + eps) * weight + bias.  With center = 0 m is
  * 0 (the norm by the root mean square).
  *
+ * A row's mean takes no accuracy from the result: x - m is as exact for rows far from
+ * zero as for those around it, and zero in constant rows.  Squares are summed in float32:
+ * they overflow where |x - m| passes 1e19 (then 1 / sqrt is 0) and vanish below 1e-22.
+ *
  *   values        [rows, k] of type `dtype`.
  *   weight, bias  [k] of type `weight_dtype` (`dtype` or SEGRED_F32), or NULL: ones
  *                 and zeros.

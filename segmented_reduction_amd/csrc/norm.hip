@@ -6,9 +6,15 @@
 //   out = u w + b
 //   dx  = r (gw - mean(gw) - u mean(gw u)), gw = g w   (mean(gw) only if centered)
 //   dw  = sum over rows of g u, db = sum over rows of g.
+// A row's mean is no part of the result, so errors in proportion to it must not be one
+// either: a row is taken around a number near its mean, the shift (its first element +
+// the mean of the differences from it, so that a constant row gives zeros exactly), and
+// the sums of x - shift and of its squares then give what the shift misses the mean by,
+// and the squares around the mean.
 // Both directions move their rows once and are bound by memory: a row is held
-// in registers (up to 16,384 elements), the statistics are found there in two
-// passes (mean, then squares around it), and the gradient finds them again
+// in registers (up to 16,384 elements; the gradient of float32 rows above 8,192 spills
+// 36 to 49 of a lane's 256), the statistics are found there in two
+// passes (shift, then sums around it), and the gradient finds them again
 // instead of reading them.  (16,384 x 4,096 bfloat16 forward 50 us, 5.3 TB/s; 16,384 x
 // 2,048 forward 25 and gradient 38 + 5 for the join of the workgroups' sums, 5.3 TB/s.)
 #include <algorithm>
@@ -121,6 +127,14 @@ struct RowJoin {
     }
 };
 
+// The first element of a row, or of the wave's part of it, from its lane 0 of LW.
+template <int LW>
+__device__ __forceinline__ float norm_first(float v) {
+    static_assert(LW == 64 || LW == 16, "a wave, or a row of its lanes");
+    if constexpr (LW == 64) return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+    return dpp_take<kDppRowFirst>(v);
+}
+
 // Elements of a row that wave `part` of its L lanes holds.
 template <typename T, int L, int U>
 __device__ __forceinline__ int norm_part(int part, int K) {
@@ -128,6 +142,40 @@ __device__ __forceinline__ int norm_part(int part, int K) {
 #pragma unroll
     for (int u = 0; u < U; ++u) n += max(0, min(64 * kUnit<T>, K - norm_col<T, L>(u, part * 64)));
     return n;
+}
+
+// A number near the mean of a row (or part) of n elements, where 1 / n = per: `first`, its
+// first element, + the mean of the differences from that, so that it is `first` itself
+// where all are equal.  Of 16-bit elements (2,048 at most a wave) such a row's sum is exact, and
+// the differences' is found from it; float elements are subtracted one by one.
+template <typename T, int L, int U, bool WHOLE, typename F>
+__device__ __forceinline__ float norm_shift(float first, float n, float per, int l, int K, F x) {
+    constexpr int N = kUnit<T>, LW = L > 64 ? 64 : L;
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int left = K - norm_col<T, L>(u, l);
+        const float m = left > 0 ? first : 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum += sizeof(T) == 2 ? x(u, e) : x(u, e) - (WHOLE || e < left ? m : 0.f);
+    }
+    sum = lanes_sum<LW>(sum);
+    if constexpr (sizeof(T) == 2) sum = fmaf(-n, first, sum);
+    return fmaf(sum, per, first);
+}
+
+// The mean of a row from its parts, each with a shift and the sum of its elements'
+// differences from it, as the first part's shift and what the mean is above that.
+struct NormParts {
+    float base, mean;
+};
+template <typename T, int L, int U, int UNROLL, typename P>
+__device__ __forceinline__ NormParts norm_join_parts(P p, int K, float per) {
+    NormParts t{p[0][0], p[0][1]};
+#pragma unroll UNROLL
+    for (int q = 1; q < L / 64; ++q) t.mean += fmaf((float)norm_part<T, L, U>(q, K), p[q][0] - t.base, p[q][1]);
+    t.mean *= per;
+    return t;
 }
 
 // L lanes hold a row, E elements each.  A workgroup walks rows with its weight
@@ -156,10 +204,10 @@ template <typename T, int L, int E, bool WHOLE>
 __global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
     constexpr int kRows = kNormThreads<L> / L, N = kUnit<T>, U = E / N, W = L > 64 ? L / 64 : 1;
     constexpr int LW = L > 64 ? 64 : L;  // lanes of a row in one wave
-    __shared__ float s_join[2][kNormThreads<L> / 64][2];
+    __shared__ float s_join[2][kNormThreads<L> / 64][3];
     const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = a.K;
     const int part = wave % W;
-    RowJoin<L, 2> join{s_join};
+    RowJoin<L, 3> join{s_join};
     const float per = 1.f / (float)K;
     float w[U][N], b[U][N];
 #pragma unroll
@@ -168,7 +216,8 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
         param_unit<T>(w[u], a.weight, a.weight_f32, c, K - c, 1.f);
         param_unit<T>(b[u], a.bias, a.weight_f32, c, K - c, 0.f);
     }
-    const float own = 1.f / (float)max(norm_part<T, L, U>(part, K), 1);
+    const float count = W > 1 ? (float)norm_part<T, L, U>(part, K) : (float)K;
+    const float own = 1.f / fmaxf(count, 1.f);
 
     NormWalk<L> at(kRows, K, sizeof(T));
     u32x4 next[U];
@@ -179,58 +228,54 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
     };
     fetch(at.row);
     for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.N; first += at.step, at.row += at.step) {
-        float x[U][N], sum = 0.f, mean = 0.f, m2 = 0.f;
+        float x[U][N], shift = 0.f, over = 0.f, m2 = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < N; ++e) x[u][e] = element<T>(next[u], e);
         fetch(at.row + at.step);
         if (a.center) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < N; ++e) sum += x[u][e];
-            sum = lanes_sum<LW>(sum);
-            mean = sum * (W > 1 ? own : per);
+            shift = norm_shift<T, L, U, WHOLE>(norm_first<LW>(x[0][0]), count, W > 1 ? own : per, l, K,
+                                               [&](int u, int e) { return x[u][e]; });
         }
-        const float shift = mean;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int left = K - norm_col<T, L>(u, l);
-            const float m = left > 0 ? mean : 0.f;
+            const float m = left > 0 ? shift : 0.f;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 x[u][e] -= WHOLE || e < left ? m : 0.f;
+                over += x[u][e];
                 m2 = fmaf(x[u][e], x[u][e], m2);
             }
         }
         m2 = lanes_sum<LW>(m2);
+        over = a.center ? lanes_sum<LW>(over) : 0.f;
+        float rest = -over * per;  // the shift less the mean
         if constexpr (W > 1) {
-            // the parts' means and squares around them, joined
-            const float v[2] = {sum, m2};
+            // the parts' sums around shifts of their own, joined
+            const float v[3] = {shift, over, m2};
             const auto p = join.meet(v, wave, lane);
-            m2 = mean = 0.f;
-            if (a.center) {
-#pragma unroll
-                for (int q = 0; q < W; ++q) mean += p[q][0];
-                mean *= per;
-            }
+            const NormParts t = norm_join_parts<T, L, U, W>(p, K, per);
+            m2 = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) {
-                const float n = (float)norm_part<T, L, U>(q, K);
-                const float d = a.center && n > 0.f ? p[q][0] / n - mean : 0.f;
-                m2 += fmaf(n * d, d, p[q][1]);
+                const float d = p[q][0] - t.base - t.mean;
+                m2 += fmaf(d, fmaf((float)norm_part<T, L, U>(q, K), d, 2.f * p[q][1]), p[q][2]);
             }
+            rest = shift - t.base - t.mean;
+        } else {
+            m2 = fmaf(over, rest, m2);
         }
         const float r = 1.f / sqrtf(fmaf(m2, per, a.eps));
-        const float rest = (shift - mean) * r;  // the part's mean was taken off before
+        rest *= r;
         const uint64_t to = at.of(a.out, at.row, a.N);
         if (to != 0)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float y[N];
 #pragma unroll
-                for (int e = 0; e < N; ++e) y[e] = fmaf(W > 1 ? fmaf(x[u][e], r, rest) : x[u][e] * r, w[u][e], b[u][e]);
+                for (int e = 0; e < N; ++e) y[e] = fmaf(fmaf(x[u][e], r, rest), w[u][e], b[u][e]);
                 norm_store<T, L, WHOLE>(to, u, l, K, y);
             }
     }
@@ -238,17 +283,22 @@ __global__ __launch_bounds__(kNormThreads<L>) void norm_rows(NormArgs a) {
 
 // The gradient.  A workgroup walks rows as above and adds up g u and g of its
 // columns in registers; at the end its parts go to `partial`.  One exchange a
-// row between waves: besides the mean and the squares, sum gw and the sum of
-// gw (x - mean of this wave's part), which is corrected for the row's mean.
+// row between waves: besides the shift, the sum and the squares, sum gw and the sum
+// of gw (x - shift of this wave's part), which is corrected for the row's mean.
 template <typename T, int L, int E, bool WHOLE>
-__global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __is_same(T, __bf16) ? 4 : 1) void norm_grad_rows(NormArgs a) {
+__global__ __launch_bounds__(kNormThreads<L>) void norm_grad_rows(NormArgs a) {
     constexpr int kThreads = kNormThreads<L>, kRows = kThreads / L, N = kUnit<T>, U = E / N, W = L > 64 ? L / 64 : 1;
     constexpr int LW = L > 64 ? 64 : L;
-    __shared__ float s_join[2][kThreads / 64][4];
+    // Eight parts one at a time, except beside bfloat16 rows of whole units: the 40 numbers at
+    // once do not fit the registers with a row's sums (k = 16,384, us at once / one at a time:
+    // float32 105 / 86, float16 89 / 68, bfloat16 62 / 67; the forward call, which has none of
+    // these sums, 25 / 31).
+    constexpr int kTurn = W > 4 && !(WHOLE && __is_same(T, __bf16)) ? 1 : W;
+    __shared__ float s_join[2][kThreads / 64][5];
     __shared__ float s_sums[kRows > 1 ? 2 * L * E : 1];
     const int l = threadIdx.x % L, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = a.K;
     const int part = wave % W;
-    RowJoin<L, 4> join{s_join};
+    RowJoin<L, 5> join{s_join};
     const float per = 1.f / (float)K;
     float w[U][N], dw[U][N], db[U][N];
 #pragma unroll
@@ -258,7 +308,8 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[u][e] = db[u][e] = 0.f;
     }
-    const float own = 1.f / (float)max(norm_part<T, L, U>(part, K), 1);
+    const float count = W > 1 ? (float)norm_part<T, L, U>(part, K) : (float)K;
+    const float own = 1.f / fmaxf(count, 1.f);
 
     NormWalk<L> at(kRows, K, sizeof(T));
     u32x4 next_x[U], next_g[U];
@@ -279,23 +330,20 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
             g[u] = next_g[u];
         }
         fetch(at.row + at.step);
-        float sum = 0.f, mean = 0.f, m2 = 0.f, c1 = 0.f, c2 = 0.f;
+        float shift = 0.f, over = 0.f, m2 = 0.f, c1 = 0.f, c2 = 0.f;
         if (a.center) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < N; ++e) sum += element<T>(x[u], e);
-            sum = lanes_sum<LW>(sum);
-            mean = sum * (W > 1 ? own : per);
+            shift = norm_shift<T, L, U, WHOLE>(norm_first<LW>(element<T>(x[0], 0)), count, W > 1 ? own : per, l, K,
+                                               [&](int u, int e) { return element<T>(x[u], e); });
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int left = K - norm_col<T, L>(u, l);
-            const float m = left > 0 ? mean : 0.f;
+            const float m = left > 0 ? shift : 0.f;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float d = element<T>(x[u], e) - (WHOLE || e < left ? m : 0.f);
                 const float gw = element<T>(g[u], e) * w[u][e];
+                over += d;
                 m2 = fmaf(d, d, m2);
                 c1 += gw;
                 c2 = fmaf(gw, d, c2);
@@ -304,27 +352,29 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
         m2 = lanes_sum<LW>(m2);
         c1 = lanes_sum<LW>(c1);
         c2 = lanes_sum<LW>(c2);
+        over = a.center ? lanes_sum<LW>(over) : 0.f;
+        float rest = -over * per;  // the shift less the mean
         if constexpr (W > 1) {
-            const float v[4] = {sum, m2, c1, c2};
+            const float v[5] = {shift, over, m2, c1, c2};
             const auto p = join.meet(v, wave, lane);
-            m2 = c1 = c2 = mean = 0.f;
-            if (a.center) {
-#pragma unroll
-                for (int q = 0; q < W; ++q) mean += p[q][0];
-                mean *= per;
-            }
-#pragma unroll
+            const NormParts t = norm_join_parts<T, L, U, kTurn>(p, K, per);
+            m2 = c1 = c2 = 0.f;
+#pragma unroll kTurn
             for (int q = 0; q < W; ++q) {
-                const float n = (float)norm_part<T, L, U>(q, K);
-                const float d = a.center && n > 0.f ? p[q][0] / n - mean : 0.f;
-                m2 += fmaf(n * d, d, p[q][1]);
-                c1 += p[q][2];
-                c2 += fmaf(p[q][2], d, p[q][3]);
+                const float d = p[q][0] - t.base - t.mean;
+                m2 += fmaf(d, fmaf((float)norm_part<T, L, U>(q, K), d, 2.f * p[q][1]), p[q][2]);
+                c1 += p[q][3];
+                c2 += fmaf(p[q][3], d, p[q][4]);
             }
+            rest = shift - t.base - t.mean;
+        } else {
+            m2 = fmaf(over, rest, m2);
+            c2 = fmaf(c1, rest, c2);
         }
         const float r = 1.f / sqrtf(fmaf(m2, per, a.eps));
         const float along = c2 * r * per * r;               // mean(gw u) r
         const float level = a.center ? c1 * per * r : 0.f;  // mean(gw) r
+        rest *= r;
         const uint64_t to = at.of(a.out, at.row, a.N);
         if (to != 0)  // past the last row g is 0, but r may be infinite
 #pragma unroll
@@ -332,7 +382,7 @@ __global__ __launch_bounds__(kNormThreads<L>, E == 16 && L <= 256 && WHOLE && __
                 float y[N];
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float unit = (element<T>(x[u], e) - mean) * r, ge = element<T>(g[u], e);
+                    const float unit = fmaf(element<T>(x[u], e) - shift, r, rest), ge = element<T>(g[u], e);
                     y[e] = fmaf(ge * r, w[u][e], -fmaf(unit, along, level));
                     dw[u][e] = fmaf(ge, unit, dw[u][e]);
                     db[u][e] += ge;
@@ -407,13 +457,16 @@ __global__ __launch_bounds__(kLongThreads) void norm_long(NormArgs a) {
         const T *x = reinterpret_cast<const T *>(a.values) + row * K;
         const T *g = reinterpret_cast<const T *>(a.grad) + row * K;
         T *out = reinterpret_cast<T *>(a.out) + row * K;
-        float mean = 0.f, m2 = 0.f, c1 = 0.f, c2 = 0.f;
+        float shift = 0.f, over = 0.f, m2 = 0.f, c1 = 0.f, c2 = 0.f;
         if (a.center) {
-            for (int c = threadIdx.x; c < K; c += kLongThreads) mean += (float)x[c];
-            mean = long_sum(mean, s, wave, lane) * per;
+            const float first = (float)x[0];
+            float sum = 0.f;
+            for (int c = threadIdx.x; c < K; c += kLongThreads) sum += (float)x[c] - first;
+            shift = fmaf(long_sum(sum, s, wave, lane), per, first);
         }
         for (int c = threadIdx.x; c < K; c += kLongThreads) {
-            const float d = (float)x[c] - mean;
+            const float d = (float)x[c] - shift;
+            over += d;
             m2 = fmaf(d, d, m2);
             if constexpr (GRAD) {
                 const float gw = (float)g[c] * (a.weight ? param<T>(a.weight, a.weight_f32, c) : 1.f);
@@ -421,12 +474,16 @@ __global__ __launch_bounds__(kLongThreads) void norm_long(NormArgs a) {
                 c2 = fmaf(gw, d, c2);
             }
         }
-        const float r = 1.f / sqrtf(fmaf(long_sum(m2, s, wave, lane), per, a.eps));
+        over = a.center ? long_sum(over, s, wave, lane) : 0.f;
+        const float rest = -over * per;
+        m2 = fmaf(over, rest, long_sum(m2, s, wave, lane));
+        const float r = 1.f / sqrtf(fmaf(m2, per, a.eps));
         if constexpr (GRAD) {
-            const float level = a.center ? long_sum(c1, s, wave, lane) * per : 0.f;
-            const float along = long_sum(c2, s, wave, lane) * r * per;
+            c1 = long_sum(c1, s, wave, lane);
+            const float level = a.center ? c1 * per : 0.f;
+            const float along = fmaf(c1, rest, long_sum(c2, s, wave, lane)) * r * per;
             for (int c = threadIdx.x; c < K; c += kLongThreads) {
-                const float unit = ((float)x[c] - mean) * r, ge = (float)g[c];
+                const float unit = fmaf((float)x[c] - shift, r, rest * r), ge = (float)g[c];
                 const float w = a.weight ? param<T>(a.weight, a.weight_f32, c) : 1.f;
                 out[c] = (T)(r * (fmaf(ge, w, -level) - unit * along));
                 if (part) {
@@ -437,7 +494,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long(NormArgs a) {
         } else {
             for (int c = threadIdx.x; c < K; c += kLongThreads) {
                 const float w = a.weight ? param<T>(a.weight, a.weight_f32, c) : 1.f;
-                out[c] = (T)fmaf(((float)x[c] - mean) * r, w, a.bias ? param<T>(a.bias, a.weight_f32, c) : 0.f);
+                out[c] = (T)fmaf(fmaf((float)x[c] - shift, r, rest * r), w, a.bias ? param<T>(a.bias, a.weight_f32, c) : 0.f);
             }
         }
     }
@@ -476,7 +533,17 @@ __global__ __launch_bounds__(kNormJoinCols *kNormJoinParts) void norm_join(NormA
 //                     30 / 64   24 / 49                                 128 lanes (8, 16 each)
 //                               29 / 65   43 / 83   30 / 77             twice the lanes, half the elements
 //
-// and of 16.8M float32 with k = 2,048 the gradient 43 by 128 lanes, 47 by 64.
+// and of 16.8M float32 with k = 2,048 the gradient 43 by 128 lanes, 47 by 64.  The chosen
+// ones once more, with the sums around a shift and parameters in float32 (of float32 16.8M):
+//
+//   k            512       1024      2048      4096      8192      16384     96        333
+//   bfloat16     23 / 43   23 / 40   23 / 44   23 / 48   24 / 51   25 / 62   25 / 49   37 / 146
+//   float16      23 / 44   23 / 41   22 / 44   23 / 47   24 / 51   25 / 68   24 / 49   38 / 145
+//   float32      22 / 39   22 / 38   22 / 39   22 / 43   23 / 43   25 / 86   22 / 38   23 / 45
+//
+// (with sums around a rounded mean, whose errors grow with it, 22 / 44 of 96 and 34 / 144 of
+// 333 bfloat16 elements; wide rows are not slower).  Held to 128 registers and so 4 waves a SIMD
+// the gradient of 1,024 bfloat16 elements took 40.6 us, left alone 40.4.
 struct NormShape {
     int lanes, elements;  // lanes 0: too long for registers
 };

@@ -99,7 +99,7 @@ __device__ __forceinline__ void seg_scan_wave(T &x, bool &f, T id, Comb comb) {
 // The sum (or the largest) over each L neighbouring lanes (8, 16, 32 or 64, at a
 // multiple of L), in all of them and in the same order every time: exchanges
 // inside a row of 16 lanes by DPP, between rows by the swaps of gfx950.
-enum : int { kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140 };
+enum : int { kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140, kDppRowFirst = 0x150 };
 template <int CTRL>
 __device__ __forceinline__ float dpp_take(float v) {  // every lane has a source; becomes part of the instruction that uses it
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
