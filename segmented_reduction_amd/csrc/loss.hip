@@ -890,6 +890,23 @@ __global__ __launch_bounds__(256) void loss_pad(const T *in, int64_t rows, int64
     out[i] = load_unit<T>((uint64_t)(in + r * cols + u * 8), (int)min(cols - u * 8, (int64_t)8));
 }
 
+// Four neighbouring sums of dx from element i on, zeros in rows without a target: their dz is
+// zero, but a product with an infinite weight or a NaN is not.
+__device__ __forceinline__ f32x4 loss_live(const LossArgs &a, int64_t i, f32x4 s) {
+    int64_t r = a.N * a.KO <= UINT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)a.KO) : i / a.KO, left = (r + 1) * a.KO - i;
+    bool live = a.live[r] >= 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (e == left) {
+            if (++r >= a.N) break;
+            left += a.KO;
+            live = a.live[r] >= 0;
+        }
+        s[e] = live ? s[e] : 0.f;
+    }
+    return s;
+}
+
 // Adds the cuts' sums and rounds once: PARTS threads share four elements, each
 // adds its part of the cuts in order, and these sums are added in order.  (8 rows of
 // 2,048 from 32 cuts: 4.8 us by four threads, 10.5 by one; 4,096 rows of 1,024 from 4
@@ -913,7 +930,7 @@ __global__ __launch_bounds__(kBackJoin) void loss_back_join(LossArgs a) {
 #pragma unroll
         for (int q = 0; q < PARTS - 1; ++q) s += s_part[q][at];
     }
-    if (i < all) store_four<T>(static_cast<T *>(a.grad_values), i, all, s * (a.factor ? a.factor[1] : 1.f));
+    if (i < all) store_four<T>(static_cast<T *>(a.grad_values), i, all, loss_live(a, i, s) * (a.factor ? a.factor[1] : 1.f));
 }
 
 // --------------------------------------------------------------------- host
