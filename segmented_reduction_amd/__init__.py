@@ -811,7 +811,9 @@ def gated_grad(grad: torch.Tensor, values: torch.Tensor, weights: torch.Tensor, 
 
     ``matmul(pair, weights, offsets)`` is then the gradient of the (gathered)
     rows, ``outer(pair, values, offsets, right_rows=rows)`` that of the weights.
-    Rows of no segment are left as they were.
+    The pair is rounded to the values' type; where that is too coarse for the two
+    products, make all of these calls in float32.  Rows of no segment are left as
+    they were.
     """
     dev, code, act, s, n, k, m = _check_gated(values, weights, offsets, activation, rows)
     _beside(dev, "grad", grad)
@@ -966,6 +968,8 @@ def cross_entropy_grad(grad: torch.Tensor, values: torch.Tensor, weights: torch.
 
     lse, picked    what ``cross_entropy`` returned for the same arguments.
     weights_dtype  type of the weights' gradient: theirs (default) or float32.
+    The logits' gradient is rounded to the values' type before both products; with
+    ``values.float()`` and ``weights.float()`` nothing is.
     Returns (grad_values [N, K] or None, grad_weights [V, K] or None).
     """
     dev, code, picks = _check_entropy(values, weights, target, probs)
