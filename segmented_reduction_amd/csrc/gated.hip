@@ -12,8 +12,9 @@
 // operations to form them again (8,192 rows, 1,024 -> 2 x 2,560: 336 MB, 65 us at the
 // rate of a copy, against 90).
 // Few rows per segment are bound by the weights (64 rows over 64 segments, 2,048 x
-// 1,024: 5 TB/s), many by the matrix units (64 segments of 512 rows on average: 312 us,
-// 880 TFLOP/s; one segment of 8,192, 4,096 x 4,096: 1,340).
+// 1,024: 5 TB/s), many by the matrix units (64 segments of 512 rows on average: 312 to 321 us,
+// 855 to 880 TFLOP/s; one segment of 8,192, 4,096 x 4,096: 1,340; float32, 8 segments of 1,024
+// rows, 1,024 -> 2 x 2,560: 505 us and the gradient 544, 170 and 158 by bf16 parts).
 #include <algorithm>
 
 #include "internal.hpp"
@@ -356,7 +357,17 @@ int gated_kind(const GatedArgs &a, bool grad) {
     return best;
 }
 
-// Float: segred_matmul's rule with 2 m outputs.
+// Float: segred_matmul's rule with 2 m outputs.  Times in us (forward):
+//
+//   segments, k, m      8, 1024, 512                       64, 1024, 512                1, 2048, 2048
+//   mean rows           1    8   16   24   64  128  512    1    8   16   24   64  128   1    8   24  128  512
+//   few                11   11   11   19   28   44  141   55   60   65   88  162  305  16   16   17   44  150
+//   32 x 128           27   27   27   27   28   44  108   66   78   75   89  123  207  49   50   50   52   86
+//   16 x 128, any      29   28   27   28   35   47  127   66   70   75   98  138  241  55   52   52   50  113
+//   64 x 128 in parts  40   40   40   40   40   40   70   67   76   77   75   99  132  76   76   76   75   76
+//
+// (8 segments, 128 x 128: all within 8 to 10 us.)  From 9 to 63 rows a segment the first would
+// be faster than the second where workgroups are few.
 constexpr int64_t kFewRows = 8, kFewGroups = 192, kSplitRows = 24, kSplitTiles = 224;
 template <typename T, bool GRAD, bool ERF>
 int gated_dispatch(const GatedArgs &a, bool direct, hipStream_t st) {

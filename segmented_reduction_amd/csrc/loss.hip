@@ -11,11 +11,15 @@
 // dz of them, then the two products of dz.  dz is rounded to the inputs' type, which
 // the matrix units take: half a step of each term, which adds about as much to the
 // results as their own rounding does (bfloat16: 0.0024 off 64 bits in all, 0.0017
-// with dz in 32 bits); float32 stays float32.  dx is added up in float32 over the
+// with dz in 32 bits; a caller who wants that calls with float32 values and weights, 1,256
+// us against 268 for 4,096 rows x 1,024, 8,192 entries); float32 stays float32.  dx is added up in float32 over the
 // pieces and rounded at the end.
 // Many rows are bound by the matrix units (4,096 rows x 2,048, 65,536 entries,
-// bfloat16: 820 us forward, 1,340 TFLOP/s; 2,780 back for three products, 1,190), few
-// by the weights (8 rows, 32,000 entries: 27 us, 4.9 TB/s).
+// bfloat16: 820 to 860 us forward, 1,280 to 1,340 TFLOP/s; 2,780 to 2,880 back for three
+// products, 1,150 to 1,190), few by the weights (8 rows x 2,048, 32,000 entries: 28 us, 4.6
+// TB/s; float32 55, 4.8).  Float32, 256 rows x 1,024, 32,000 entries: 105 us forward and 331
+// back, what float products take at the rate of a large one; 4,096 rows, 8,192 entries 374
+// and 1,214, 184 TFLOP/s by bf16 parts.
 // Exponentials are powers of two: z scale log2(e) minus the base in one fma.
 #include <algorithm>
 #include <cmath>
@@ -1056,6 +1060,21 @@ LossArgs loss_args(const void *values, int64_t k, int64_t rows, const void *weig
 // kernels several times slower (4,096 rows, 32,000 entries, bfloat16: k = 2,047 took
 // 1,156 us forward and 5,787 back, 2,048 472 and 1,445).  Few rows go as they are
 // in the forward call (1 row: 65 us against 33 and 65 for the copy).
+//
+// A piece: 256 MiB of dz, and 4,096 entries at least.  The gradient call in us:
+//
+//   MiB                                       32    64   128   256   512
+//   bfloat16  4,096 x 2,048, 65,536         3416  2998  2926  2872  2829
+//   bfloat16 16,384 x 1,024, 32,000         4298  4296  4292  3341  3014
+//   float16   1,500 x 1,024, 32,011, 32      445   427   389   389   389
+//   bfloat16  2,166 x 88, 54,570, 16         447   367   287   225   224
+//   float32   4,096 x 1,024, 32,000         5062  5056  4896  4850  4945
+//   entries at least                         256  1024  2048  4096  8192
+//   bfloat16 65,536 x 512, 16,000           6574  6565  6567  5184  4706
+//   float32  32,768 x 256, 16,000           5685  5759  5742  5650  5920
+//
+// (equal times on the left: the piece has the least 4,096 entries already).  Twice the memory
+// would gain 0 to 10 %; dz may have a turned copy beside it, so a call holds up to two pieces.
 constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096, kPadRows = 256;
 bool loss_padded(int32_t dtype, int64_t k) { return dtype != SEGRED_F32 && k % 8 != 0; }
 template <typename T>
@@ -1146,6 +1165,12 @@ LossPlan loss_plan(int32_t dtype, int64_t columns, int64_t n, int64_t v, int64_t
     // values turned, 22 / 27 / 39 without; 8 x 1,024 x 32,000 65 and 70, 64 x 2,048 x 16,000 68
     // and 75; 1,024 x 512 x 4,000 55 and 64)
     p.turn_rows = whole && (p.pad || (n <= 256 ? k >= 128 && k * v >= kTurnWords : k >= 512 || (n <= 512 && k >= 128)));
+    // (32,000 entries, bfloat16, the call without / with the weights turned:
+    //   rows    512        1,024      1,500      2,048      3,000        4,096
+    //   k 512   100 / 122  158 / 181  221 / 254  283 / 310  417 / 429    528 / 516
+    //   1,024   156 / 188  253 / 284  353 / 381  451 / 459  709 / 665    833 / 806
+    //   2,048   253 / 313  427 / 459  661 / 623  787 / 772  1281 / 1176  1499 / 1418
+    // so 1,500 x 2,048 and 3,000 x 1,024 would be 6 % faster on the other side)
     p.turn_words = whole && n >= 2048 && ((n + 255) / 256) * ((k + 255) / 256) >= 64;
     const int64_t tiles = p.turn_words ? ((n + 255) / 256) * ((k + 255) / 256)
                           : p.many     ? ((n + 127) / 128) * ((k + 255) / 256)

@@ -16,7 +16,7 @@
 // 36 to 49 of a lane's 256), the statistics are found there in two
 // passes (shift, then sums around it), and the gradient finds them again
 // instead of reading them.  (16,384 x 4,096 bfloat16 forward 50 us, 5.3 TB/s; 16,384 x
-// 2,048 forward 25 and gradient 38 + 5 for the join of the workgroups' sums, 5.3 TB/s.)
+// 2,048 forward 26 and gradient 39 + 5 for the join of the workgroups' sums, 5.3 TB/s.)
 #include <algorithm>
 #include <cmath>
 
