@@ -1073,7 +1073,8 @@ LossArgs loss_args(const void *values, int64_t k, int64_t rows, const void *weig
 //   bfloat16 65,536 x 512, 16,000           6574  6565  6567  5184  4706
 //   float32  32,768 x 256, 16,000           5685  5759  5742  5650  5920
 //
-// (equal times on the left: the piece has the least 4,096 entries already).  Twice the memory
+// (equal times on the left: a piece has the least 4,096 entries already, or, below, the 2,048
+// that 256 MiB hold).  Twice the memory
 // would gain 0 to 10 %; dz may have a turned copy beside it, so a call holds up to two pieces.
 constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceLeast = 4096, kPadRows = 256;
 bool loss_padded(int32_t dtype, int64_t k) { return dtype != SEGRED_F32 && k % 8 != 0; }
